@@ -72,6 +72,8 @@ extern "C" {
 /* Device status bits (see mla_verify_read_status). */
 #define MLA_VERIFY_DEV_BAD_ROW 0x1u /* some resolved pool row was outside [0, pool_rows) */
 #define MLA_VERIFY_DEV_TIMEOUT 0x2u /* a pipeline wait gave up; that CTA's partial is invalid */
+#define MLA_VERIFY_DEV_NO_PAGE 0x4u /* a slot-map build ran out of free pages or of block-table columns */
+#define MLA_VERIFY_DEV_CAPACITY 0x8u /* a slot map was longer than its array; the rest was not written */
 
 /* Plan flags. */
 #define MLA_VERIFY_FORCE_SIMT 0x1 /* use the CUDA-core (warp-shuffle) split kernel for every shape */
@@ -90,6 +92,30 @@ extern "C" {
  * each key gathered once per row group).  Results agree within rounding;
  * the flag exists to compare the two modes. */
 #define MLA_VERIFY_REFETCH_VALUES 0x4
+/* The pool holds 4-bit rows: uint8 [pool_rows, 384], 16-byte aligned, in
+ * place of bf16 [pool_rows, 576], in every call of the plan that takes
+ * kv_pool (run, run_varlen, split, run_noalloc, relocate_kv, and store_kv4 and
+ * load_kv4, which take only such a plan).  A row is 640 codes of 4 bits --
+ * 512 latent channels, 64 RoPE channels, the RoPE channels' 64 residuals --
+ * and one power-of-two scale per 16 codes:
+ *
+ *   value = +-{0, 0.5, 1, 1.5, 2, 3, 4, 6} * 2^e, e in [-13, 13];
+ *   bytes 64m .. 64m+63, m = 0..4: codes 128m .. 128m+127, 8 per 32-bit
+ *     little-endian word; code i of a word has its magnitude's index in bits
+ *     4i..4i+2; the signs of codes 0..3 are bits 7, 15, 23, 31, those of codes
+ *     4..7 bits 3, 11, 19, 27;
+ *   byte 320 + 16q + 2m + h: e + 127 of codes 128m + 32q + 16h .. + 15
+ *     (q = 0..3, h = 0, 1); the other bytes are 0.
+ *
+ * A key's RoPE value is the sum of its code's and its residual's.  Attention
+ * over a 4-bit pool is the operation above on these values: the queries stay
+ * bf16, the scores, softmax and sums fp32, and the values enter the products
+ * exactly.  A row that a call references must have been stored (or be masked:
+ * unlike a bf16 row, a masked 4-bit row may hold any bytes).  Each query value
+ * must be finite.  A 4-bit row takes a third of a bf16 row's memory.
+ * With MLA_VERIFY_FUSED_MERGE or MLA_VERIFY_REFETCH_VALUES: EINVAL. */
+#define MLA_VERIFY_KV4 0x10
+#define MLA_VERIFY_KV4_ROW_BYTES 384
 /* Test only: the tensor-core split kernel's gather never signals its first
  * block, so every CTA's bounded pipeline waits run out (about 2 s), the CTAs
  * drain and return, and the call reports MLA_VERIFY_DEV_TIMEOUT; its outputs
@@ -115,7 +141,7 @@ typedef struct {
   int32_t d_latent;   /* must be 512 */
   int32_t d_rope;     /* must be 64 */
   int32_t flags;      /* OR of MLA_VERIFY_FORCE_SIMT, MLA_VERIFY_FUSED_MERGE, MLA_VERIFY_REFETCH_VALUES,
-                       * MLA_VERIFY_TEST_STALL_GATHER */
+                       * MLA_VERIFY_KV4, MLA_VERIFY_TEST_STALL_GATHER */
 } mla_verify_params;
 
 /* What a plan chose (for tests, benchmarks and logs). */
@@ -296,6 +322,7 @@ int mla_verify_build_tree_mask_varlen(mla_verify_plan_t plan, const int32_t* par
  * allocation, no host synchronisation.
  *
  *  kv_pool      bf16 [pool_rows, 576], 16-byte aligned; read and written
+ *               (a MLA_VERIFY_KV4 plan: uint8 [pool_rows, 384])
  *  kv_indptr    int32 [batch+1], non-decreasing: request b's prefix keys are
  *               kv_indices[kv_indptr[b] .. kv_indptr[b+1])
  *  kv_indices   int32, read and rewritten in place
@@ -350,6 +377,82 @@ int mla_verify_run_noalloc(mla_verify_plan_t plan, const void* q_nope_absorbed, 
                            const int32_t* out_cache_loc, const uint8_t* custom_mask,
                            const int32_t* mask_indptr, int32_t batch, float sm_scale, int32_t nsplit,
                            void* o, float* lse, void* stream);
+
+/*
+ * Store n tokens into a 4-bit pool (MLA_VERIFY_KV4 has the row's format).  One
+ * kernel on `stream`, no allocation, no host synchronisation.
+ *
+ *  latent, rope   bf16 [n, 512] and [n, 64] with row strides of latent_stride
+ *                 and rope_stride elements (e.g. the two column ranges of one
+ *                 [n, 576] projection output); base pointers 16-byte aligned,
+ *                 strides multiples of 8, at least 512 and 64
+ *  slots          int32 [n]: pool row of each token (out_cache_loc); -1 skips
+ *                 the token; no row may be named twice in one call
+ *  n              >= 0 (0 enqueues nothing)
+ *  kv_pool        uint8 [pool_rows, 384], written
+ *  workspace      the plan's workspace (only its status word is used)
+ *
+ * Per group of 16 values e is the least integer with max |x| <= 6 * 2^e,
+ * held in [-13, 13]; a value becomes the nearest code, ties to the one of even
+ * index, at most 6 * 2^e.  The RoPE residual is x minus its value, coded the
+ * same way.  A NaN is stored as 0, an infinity as the largest value.  A slot
+ * outside [0, pool_rows) other than -1 skips the token and raises
+ * MLA_VERIFY_DEV_BAD_ROW.  Errors: EINVAL (NULL or misaligned pointer, stride,
+ * n < 0, a plan without MLA_VERIFY_KV4), EWORKSPACE, EUNSUPPORTED, ECUDA.
+ */
+int mla_verify_store_kv4(mla_verify_plan_t plan, const void* latent, int64_t latent_stride, const void* rope,
+                         int64_t rope_stride, const int32_t* slots, int64_t n, void* kv_pool, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/*
+ * Load rows of a 4-bit pool back as bf16 (e.g. a shared prefix for a kernel
+ * that reads bf16).  Row slots[i] goes to row i of latent and rope; latents
+ * are exact, RoPE values (code plus residual) are rounded to nearest-even.
+ * -1 gives zeros; another slot outside [0, pool_rows) gives zeros and raises
+ * MLA_VERIFY_DEV_BAD_ROW.  A row may be named any number of times.  Arguments
+ * and errors otherwise as mla_verify_store_kv4.
+ */
+int mla_verify_load_kv4(mla_verify_plan_t plan, const void* kv_pool, const int32_t* slots, int64_t n, void* latent,
+                        int64_t latent_stride, void* rope, int64_t rope_stride, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/*
+ * Build a step's block tables and slot maps on the device from the requests'
+ * lengths: every index array that store_kv4, build_tree_mask_varlen and
+ * run_varlen take.  One kernel on `stream`, no allocation, no host
+ * synchronisation.  For a pool of any row format.
+ *
+ *  seq_lens       int32 [batch]: tokens P_b of each request already cached
+ *                 (a negative length counts as 0)
+ *  new_lens       int32 [batch]: tokens T_b that the step adds (drafts, or a
+ *                 prompt of any length), or NULL: the plan's q_len each
+ *  batch          0 <= batch <= min(max_batch, 4096) (0 enqueues nothing)
+ *  page_size      rows per page (>= 1): page p is pool rows [p*page_size, (p+1)*page_size)
+ *  block_table    int32 [batch, max_pages]: request b's first ceil(P_b / page_size)
+ *                 entries are its pages; the entries of the fresh pages that
+ *                 P_b + T_b tokens need are written after them
+ *  free_pages     int32 [num_free]: taken from the front, in request order
+ *  pages_used     int32 [1] output: how many were taken
+ *  kv_indptr      int32 [batch+1] output: exclusive scan of P_b
+ *  kv_indices     int32 [kv_capacity] output: pool rows of the cached tokens
+ *  qo_indptr      int32 [batch+1] output: exclusive scan of T_b
+ *  out_cache_loc  int32 [loc_capacity] output: pool rows of the new tokens
+ *  workspace      the plan's workspace (only its status word is used)
+ *
+ * A token whose page is missing (free_pages used up, more than max_pages
+ * columns) gets row -1, its page's table entry (if it has one) -1, and the call
+ * raises MLA_VERIFY_DEV_NO_PAGE; one whose page is negative or outside the pool
+ * gets row -1 and raises MLA_VERIFY_DEV_BAD_ROW.  Entries past an array's
+ * capacity are not written and raise MLA_VERIFY_DEV_CAPACITY (sums stop at
+ * 2^31 - 1).  Entries past the totals are left as they were.  The arrays must
+ * not overlap.  Errors: EINVAL (NULL or misaligned pointer, sizes), EWORKSPACE,
+ * EUNSUPPORTED, ECUDA.
+ */
+int mla_verify_build_slots(mla_verify_plan_t plan, const int32_t* seq_lens, const int32_t* new_lens, int32_t batch,
+                           int32_t page_size, int32_t* block_table, int32_t max_pages, const int32_t* free_pages,
+                           int32_t num_free, int32_t* pages_used, int32_t* kv_indptr, int32_t* kv_indices,
+                           int64_t kv_capacity, int32_t* qo_indptr, int32_t* out_cache_loc, int64_t loc_capacity,
+                           void* workspace, size_t workspace_bytes, void* stream);
 
 /* Free the plan (NULL is accepted).  Returns MLA_VERIFY_OK. */
 int mla_verify_destroy(mla_verify_plan_t plan);

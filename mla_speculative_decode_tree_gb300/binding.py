@@ -22,15 +22,20 @@ MLA_VERIFY_EWORKSPACE = 3
 MLA_VERIFY_ECUDA = 4
 MLA_VERIFY_DEV_BAD_ROW = 0x1
 MLA_VERIFY_DEV_TIMEOUT = 0x2
+MLA_VERIFY_DEV_NO_PAGE = 0x4
+MLA_VERIFY_DEV_CAPACITY = 0x8
 MLA_VERIFY_FORCE_SIMT = 0x1
 MLA_VERIFY_FUSED_MERGE = 0x2
 MLA_VERIFY_REFETCH_VALUES = 0x4
+MLA_VERIFY_KV4 = 0x10
+MLA_VERIFY_KV4_ROW_BYTES = 384
 MLA_VERIFY_TEST_STALL_GATHER = 0x100
 
 EXPORTED = ("mla_verify_plan", "mla_verify_plan_describe", "mla_verify_run", "mla_verify_split",
             "mla_verify_merge", "mla_verify_workspace_init", "mla_verify_read_status", "mla_verify_destroy",
             "mla_verify_strerror", "mla_verify_run_noalloc", "mla_verify_build_tree_mask",
-            "mla_verify_run_varlen", "mla_verify_relocate_kv", "mla_verify_build_tree_mask_varlen")
+            "mla_verify_run_varlen", "mla_verify_relocate_kv", "mla_verify_build_tree_mask_varlen",
+            "mla_verify_store_kv4", "mla_verify_load_kv4", "mla_verify_build_slots")
 
 
 class MlaVerifyParams(ctypes.Structure):
@@ -78,6 +83,9 @@ def load(path: str = LIB_PATH):
     lib.mla_verify_build_tree_mask.argtypes = [P, P, P, i32, P, sz, P, P]
     lib.mla_verify_relocate_kv.argtypes = [P, P, P, P, P, i32, P, sz, P]
     lib.mla_verify_build_tree_mask_varlen.argtypes = [P, P, P, P, i32, P, sz, P, P]
+    lib.mla_verify_store_kv4.argtypes = [P, P, i64, P, i64, P, i64, P, P, sz, P]
+    lib.mla_verify_load_kv4.argtypes = [P, P, P, i64, P, i64, P, i64, P, sz, P]
+    lib.mla_verify_build_slots.argtypes = [P, P, P, i32, i32, P, i32, P, i32, P, P, P, i64, P, P, i64, P, sz, P]
     lib.mla_verify_read_status.argtypes = [P, P, P, ctypes.POINTER(ctypes.c_uint32)]
     lib.mla_verify_destroy.argtypes = [P]
     lib.mla_verify_strerror.argtypes = [ctypes.c_int]
@@ -237,6 +245,64 @@ def mla_verify_build_tree_mask_varlen(plan: Plan, parents, kv_indptr, qo_indptr,
                                                   _ptr(qo_indptr), int(batch), _ptr(custom_mask), int(nbytes),
                                                   _ptr(mask_indptr), _stream(stream))
     _check(rc, "mla_verify_build_tree_mask_varlen")
+
+
+def _rows_of(x, width: int, n: int, what: str) -> int:
+    """Row stride in elements of a bf16 [n, width] tensor (any row stride, contiguous rows)."""
+    import torch
+    if x.dtype != torch.bfloat16 or x.dim() != 2 or tuple(x.shape) != (n, width) or (n > 0 and x.stride(1) != 1):
+        raise ValueError("%s: bf16 [%d, %d] with contiguous rows expected, got %s %s strides %s"
+                         % (what, n, width, x.dtype, tuple(x.shape), x.stride()))
+    return x.stride(0) if n > 1 else max(width, x.stride(0))
+
+
+def _int32(x, what: str):
+    import torch
+    if x.dtype != torch.int32 or not x.is_contiguous():
+        raise ValueError("%s: a contiguous int32 tensor expected, got %s strides %s" % (what, x.dtype, x.stride()))
+
+
+def mla_verify_store_kv4(plan: Plan, latent, rope, slots, kv_pool, workspace, stream=None):
+    """Code tokens (latent bf16 [n, 512], rope bf16 [n, 64], any row strides) into rows ``slots`` of a 4-bit pool."""
+    n = slots.numel()
+    _int32(slots, "slots")
+    rc = load().mla_verify_store_kv4(ctypes.c_void_p(plan.handle), _ptr(latent), _rows_of(latent, 512, n, "latent"),
+                                     _ptr(rope), _rows_of(rope, 64, n, "rope"), _ptr(slots), n, _ptr(kv_pool),
+                                     _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(rc, "mla_verify_store_kv4")
+
+
+def mla_verify_load_kv4(plan: Plan, kv_pool, slots, latent, rope, workspace, stream=None):
+    """Rows ``slots`` of a 4-bit pool as bf16, into latent [n, 512] and rope [n, 64] (any row strides)."""
+    n = slots.numel()
+    _int32(slots, "slots")
+    rc = load().mla_verify_load_kv4(ctypes.c_void_p(plan.handle), _ptr(kv_pool), _ptr(slots), n, _ptr(latent),
+                                    _rows_of(latent, 512, n, "latent"), _ptr(rope), _rows_of(rope, 64, n, "rope"),
+                                    _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(rc, "mla_verify_load_kv4")
+
+
+def mla_verify_build_slots(plan: Plan, seq_lens, new_lens, batch: int, page_size: int, block_table, free_pages,
+                           pages_used, kv_indptr, kv_indices, qo_indptr, out_cache_loc, workspace, stream=None):
+    """Block tables and slot maps of a step from the requests' lengths (new_lens None: the plan's q_len each).
+
+    block_table is int32 [>= batch, max_pages]; the capacities are the index tensors' lengths."""
+    for name, x in (("seq_lens", seq_lens), ("new_lens", new_lens), ("block_table", block_table),
+                    ("free_pages", free_pages), ("pages_used", pages_used), ("kv_indptr", kv_indptr),
+                    ("kv_indices", kv_indices), ("qo_indptr", qo_indptr), ("out_cache_loc", out_cache_loc)):
+        if x is not None:
+            _int32(x, name)
+    if block_table.dim() != 2 or min(block_table.shape[0], seq_lens.numel(), kv_indptr.numel() - 1,
+                                     qo_indptr.numel() - 1) < batch or (new_lens is not None
+                                                                        and new_lens.numel() < batch):
+        raise ValueError("an array is too short for %d requests" % batch)
+    rc = load().mla_verify_build_slots(ctypes.c_void_p(plan.handle), _ptr(seq_lens), _ptr(new_lens), int(batch),
+                                       int(page_size), _ptr(block_table), block_table.shape[1], _ptr(free_pages),
+                                       free_pages.numel(), _ptr(pages_used), _ptr(kv_indptr), _ptr(kv_indices),
+                                       kv_indices.numel(), _ptr(qo_indptr), _ptr(out_cache_loc),
+                                       out_cache_loc.numel(), _ptr(workspace),
+                                       workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(rc, "mla_verify_build_slots")
 
 
 def mla_verify_workspace_init(plan: Plan, workspace, stream=None):

@@ -11,7 +11,7 @@
 #include <new>
 
 #include "../../include/mla_verify.h"
-#include "common.cuh"
+#include "kv4.cuh"
 
 using namespace mlav;
 
@@ -30,6 +30,7 @@ struct mla_verify_plan_s {
   int merge_blocks;
   bool merge_quarter;  // merge with four warps per row (at most one wave of rows)
   int smem;
+  bool kv4;  // the pool holds 4-bit rows (MLA_VERIFY_KV4)
 };
 
 namespace {
@@ -154,6 +155,62 @@ cudaError_t tc_launch(int nq, bool res, const SplitArgs& a, const TcMaps& m, dim
     case 64: return launch_split_tc_64(a, m, grid, st, res);
     default: return launch_split_tc_96(a, m, grid, st, res);
   }
+}
+
+// ---- 4-bit pool: row-group size and split count ------------------------------
+const int kKv4NqChoices[] = {16, 32, 48, 64};
+
+int kv4_smem(int nq) {
+  switch (nq) {
+    case 16: return split_kv4_smem_16();
+    case 32: return split_kv4_smem_32();
+    case 48: return split_kv4_smem_48();
+    default: return split_kv4_smem_64();
+  }
+}
+
+cudaError_t kv4_launch(int nq, const SplitArgs& a, dim3 grid, cudaStream_t st) {
+  switch (nq) {
+    case 16: return launch_split_kv4_16(a, grid, st);
+    case 32: return launch_split_kv4_32(a, grid, st);
+    case 48: return launch_split_kv4_48(a, grid, st);
+    default: return launch_split_kv4_64(a, grid, st);
+  }
+}
+
+// The time model of est_us with the 4-bit kernel's times.
+double kv4_tile_us(int nq) { return nq >= 64 ? 2.2 : nq >= 48 ? 1.7 : 1.5; }
+
+Choice choose_kv4(int64_t rows_b, int64_t max_kv_len, int max_batch, int nsplit) {
+  constexpr double kCtaUs = 5.0, kMergeUs = 2.0, kMergeBytesPerUs = 3.0e6;
+  const double sms = (double)device_sm_count();
+  const int64_t tiles_max = (max_kv_len + kKeysPerTile - 1) / kKeysPerTile;
+  const int64_t n_lo = nsplit > 0 ? nsplit : 1;
+  const int64_t n_hi = nsplit > 0 ? nsplit : std::min<int64_t>(tiles_max, 4096);
+  Choice best{false, 64, (int)n_lo};
+  double t_best = -1.0;
+  for (int nq : kKv4NqChoices) {
+    const double groups = (double)((rows_b + nq - 1) / nq);
+    const double tu = kv4_tile_us(nq);
+    for (int64_t n = n_lo; n <= n_hi; ++n) {
+      if (nsplit == 0 && n > 1 && (tiles_max + n - 2) / (n - 1) == (tiles_max + n - 1) / n)
+        continue;  // same chunks as n - 1 splits, only more partials
+      const int64_t chunk = chunk_len(max_kv_len, (int)n, kMinChunk);
+      const double per = (double)(chunk / kKeysPerTile);
+      const double splits = (double)((max_kv_len + chunk - 1) / chunk);
+      double t;
+      if (max_batch == 1)
+        t = std::ceil(groups * splits / sms) * (per * tu + kCtaUs);
+      else
+        t = (groups * max_batch * tiles_max / 2.0 / sms + per) * tu + groups * max_batch * splits * kCtaUs / sms;
+      t += kMergeUs + splits * rows_b * max_batch * 2048.0 / kMergeBytesPerUs;
+      if (t_best < 0 || t < t_best) {
+        t_best = t;
+        best = {false, nq, (int)n};
+      }
+    }
+  }
+  return best;
 }
 
 // ---- TMA descriptors --------------------------------------------------------
@@ -285,8 +342,10 @@ int mla_verify_plan(const mla_verify_params* params, size_t* workspace_bytes, ml
       p.pool_rows < 1 || p.max_kv_len < p.q_len)
     return MLA_VERIFY_EINVAL;
   if (p.d_latent != kDLatent || p.d_rope != kDRope) return MLA_VERIFY_EUNSUPPORTED;
-  if ((p.flags & ~(MLA_VERIFY_FORCE_SIMT | MLA_VERIFY_FUSED_MERGE | MLA_VERIFY_REFETCH_VALUES |
+  if ((p.flags & ~(MLA_VERIFY_FORCE_SIMT | MLA_VERIFY_FUSED_MERGE | MLA_VERIFY_REFETCH_VALUES | MLA_VERIFY_KV4 |
                    MLA_VERIFY_TEST_STALL_GATHER)) != 0)
+    return MLA_VERIFY_EINVAL;
+  if ((p.flags & MLA_VERIFY_KV4) && (p.flags & (MLA_VERIFY_FUSED_MERGE | MLA_VERIFY_REFETCH_VALUES)))
     return MLA_VERIFY_EINVAL;
   const int64_t rows_b = (int64_t)p.q_len * p.num_heads;
   const int64_t rows_max = rows_b * p.max_batch;
@@ -302,7 +361,13 @@ int mla_verify_plan(const mla_verify_params* params, size_t* workspace_bytes, ml
   // than the CUDA-core kernel (16 requests x 8 heads x 1 token over 1k-33k
   // keys: 146 against 1064 us per call).
   pl->kernel = (p.flags & MLA_VERIFY_FORCE_SIMT) ? 0 : 1;
-  if (pl->kernel) {
+  pl->kv4 = (p.flags & MLA_VERIFY_KV4) != 0;
+  if (pl->kernel && pl->kv4) {
+    const Choice c = choose_kv4(rows_b, p.max_kv_len, p.max_batch, p.nsplit);
+    pl->resident = true;  // each key is read once per CTA
+    pl->nq = c.nq;
+    pl->splits = c.splits;
+  } else if (pl->kernel) {
     // The mode (resident tile, unless MLA_VERIFY_REFETCH_VALUES), the row-group
     // size and, for nsplit = 0, the split count, from the time model.
     const Choice c = choose(rows_b, p.max_kv_len, p.max_batch, p.nsplit, !(p.flags & MLA_VERIFY_REFETCH_VALUES));
@@ -325,7 +390,8 @@ int mla_verify_plan(const mla_verify_params* params, size_t* workspace_bytes, ml
   // keys at nsplit 16: 35.1 -> 34.3 us per call); whole tiles otherwise, where
   // the extra chunks measured slower (value refetch over 65,545 keys at
   // nsplit 64: 204.5 -> 207.5 us; 16 ragged decode requests +0.5 %).
-  pl->chunk_granule = (pl->kernel == 1 && pl->resident && p.max_batch == 1) ? kHalfTile : kKeysPerTile;
+  // A 4-bit tile costs its MMAs, not its landing, so it is never halved.
+  pl->chunk_granule = (pl->kernel == 1 && pl->resident && p.max_batch == 1 && !pl->kv4) ? kHalfTile : kKeysPerTile;
   // Chunks are never shorter than half the longest request's chunk: a
   // request much shorter than max_kv_len then takes fewer, longer chunks and
   // writes fewer partials, while the longest request -- the launch's
@@ -336,7 +402,7 @@ int mla_verify_plan(const mla_verify_params* params, size_t* workspace_bytes, ml
     pl->min_chunk = (int)(half < kMinChunk ? kMinChunk : half);
   }
   pl->groups = (int)((rows_b + pl->nq - 1) / pl->nq);
-  pl->smem = pl->kernel ? tc_smem(pl->nq, pl->resident) : 0;
+  pl->smem = !pl->kernel ? 0 : pl->kv4 ? kv4_smem(pl->nq) : tc_smem(pl->nq, pl->resident);
 
   pl->fused = pl->kernel == 1 && (p.flags & MLA_VERIFY_FUSED_MERGE);
   pl->off_cnt = kWsHeader;
@@ -388,7 +454,8 @@ int split_impl(mla_verify_plan_t pl, const void* q_nope_absorbed, const void* q_
   SplitArgs a = {};
   a.q_nope = static_cast<const __nv_bfloat16*>(q_nope_absorbed);
   a.q_rope = static_cast<const __nv_bfloat16*>(q_rope);
-  a.kv_pool = static_cast<const __nv_bfloat16*>(kv_pool);
+  a.kv_pool = pl->kv4 ? nullptr : static_cast<const __nv_bfloat16*>(kv_pool);
+  a.kv4_pool = pl->kv4 ? static_cast<const uint8_t*>(kv_pool) : nullptr;
   a.kv_indptr = kv_indptr;
   a.kv_indices = kv_indices;
   a.out_cache_loc = out_cache_loc;
@@ -416,7 +483,9 @@ int split_impl(mla_verify_plan_t pl, const void* q_nope_absorbed, const void* q_
   const dim3 grid(pl->groups, pl->splits, pl->p.max_batch);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
-  if (pl->kernel) {
+  if (pl->kernel && pl->kv4) {
+    e = kv4_launch(pl->nq, a, grid, st);
+  } else if (pl->kernel) {
     // Descriptors are plain host structs passed by value with the launch: no
     // device work, so this stays capture-safe.
     EncodeTiledFn enc;
@@ -554,8 +623,97 @@ int mla_verify_relocate_kv(mla_verify_plan_t pl, void* kv_pool, const int32_t* k
   int rc;
   if ((rc = check_device()) != MLA_VERIFY_OK) return rc;
   const int64_t max_keys = (int64_t)pl->p.max_batch * pl->p.max_kv_len;
-  cudaError_t e = mlav::launch_relocate(kv_pool, kv_indptr, kv_indices, dst_start, batch, pl->p.pool_rows, max_keys,
+  cudaError_t e = mlav::launch_relocate(kv_pool, pl->kv4 ? kKv4RowBytes : kRowBytes, kv_indptr, kv_indices, dst_start, batch, pl->p.pool_rows, max_keys,
                                         reinterpret_cast<uint32_t*>(workspace), static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MLA_VERIFY_OK : cuda_fail(e);
+}
+
+namespace {
+
+// The arguments that the store and the load of 4-bit rows share.
+int check_kv4_rows(const mla_verify_plan_s* pl, const void* latent, int64_t latent_stride, const void* rope,
+                   int64_t rope_stride, const int32_t* slots, int64_t n, const void* kv_pool, const void* workspace,
+                   size_t workspace_bytes) {
+  if (!pl || !pl->kv4 || n < 0) return MLA_VERIFY_EINVAL;
+  if (n == 0) return MLA_VERIFY_OK;
+  if (!latent || !rope || !slots || !kv_pool || !aligned(latent, 16) || !aligned(rope, 16) || !aligned(slots, 4) ||
+      !aligned(kv_pool, 16))
+    return MLA_VERIFY_EINVAL;
+  // rows are moved in 16-byte pieces; more than 2^31 - 1 rows never fit a pool
+  if (latent_stride < kDLatent || rope_stride < kDRope || latent_stride % 8 || rope_stride % 8 ||
+      latent_stride > ((int64_t)1 << 31) || rope_stride > ((int64_t)1 << 31) || n > ((int64_t)1 << 31) - 1)
+    return MLA_VERIFY_EINVAL;
+  if (!workspace || workspace_bytes < pl->ws_bytes) return MLA_VERIFY_EWORKSPACE;
+  if (!aligned(workspace, 256)) return MLA_VERIFY_EINVAL;
+  return check_device();
+}
+
+}  // namespace
+
+int mla_verify_store_kv4(mla_verify_plan_t pl, const void* latent, int64_t latent_stride, const void* rope,
+                         int64_t rope_stride, const int32_t* slots, int64_t n, void* kv_pool, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  const int rc = check_kv4_rows(pl, latent, latent_stride, rope, rope_stride, slots, n, kv_pool, workspace,
+                                workspace_bytes);
+  if (rc != MLA_VERIFY_OK || n == 0) return rc;
+  cudaError_t e = launch_store_kv4(latent, latent_stride, rope, rope_stride, slots, n, kv_pool, pl->p.pool_rows,
+                                   static_cast<uint32_t*>(workspace), static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MLA_VERIFY_OK : cuda_fail(e);
+}
+
+int mla_verify_load_kv4(mla_verify_plan_t pl, const void* kv_pool, const int32_t* slots, int64_t n, void* latent,
+                        int64_t latent_stride, void* rope, int64_t rope_stride, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+  const int rc = check_kv4_rows(pl, latent, latent_stride, rope, rope_stride, slots, n, kv_pool, workspace,
+                                workspace_bytes);
+  if (rc != MLA_VERIFY_OK || n == 0) return rc;
+  cudaError_t e = launch_load_kv4(kv_pool, pl->p.pool_rows, slots, n, latent, latent_stride, rope, rope_stride,
+                                  static_cast<uint32_t*>(workspace), static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MLA_VERIFY_OK : cuda_fail(e);
+}
+
+int mla_verify_build_slots(mla_verify_plan_t pl, const int32_t* seq_lens, const int32_t* new_lens, int32_t batch,
+                           int32_t page_size, int32_t* block_table, int32_t max_pages, const int32_t* free_pages,
+                           int32_t num_free, int32_t* pages_used, int32_t* kv_indptr, int32_t* kv_indices,
+                           int64_t kv_capacity, int32_t* qo_indptr, int32_t* out_cache_loc, int64_t loc_capacity,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  if (!pl || batch < 0 || batch > pl->p.max_batch || batch > kMaxSlotsBatch) return MLA_VERIFY_EINVAL;
+  if (batch == 0) return MLA_VERIFY_OK;
+  if (page_size < 1 || max_pages < 1 || num_free < 0 || kv_capacity < 0 || loc_capacity < 0) return MLA_VERIFY_EINVAL;
+  if (!seq_lens || !block_table || !pages_used || !kv_indptr || !qo_indptr || (num_free > 0 && !free_pages) ||
+      (kv_capacity > 0 && !kv_indices) || (loc_capacity > 0 && !out_cache_loc))
+    return MLA_VERIFY_EINVAL;
+  const void* words[] = {seq_lens, new_lens,  block_table, free_pages,   pages_used,
+                         kv_indptr, kv_indices, qo_indptr,  out_cache_loc};
+  for (const void* w : words)
+    if (!aligned(w, 4)) return MLA_VERIFY_EINVAL;
+  if (!workspace || workspace_bytes < pl->ws_bytes) return MLA_VERIFY_EWORKSPACE;
+  if (!aligned(workspace, 256)) return MLA_VERIFY_EINVAL;
+  int rc;
+  if ((rc = check_device()) != MLA_VERIFY_OK) return rc;
+  SlotsArgs a = {};
+  a.seq_lens = seq_lens;
+  a.new_lens = new_lens;
+  a.block_table = block_table;
+  a.free_pages = free_pages;
+  a.pages_used = pages_used;
+  a.kv_indptr = kv_indptr;
+  a.kv_indices = kv_indices;
+  a.qo_indptr = qo_indptr;
+  a.out_cache_loc = out_cache_loc;
+  a.status = static_cast<uint32_t*>(workspace);
+  a.pool_rows = pl->p.pool_rows;
+  a.kv_capacity = kv_capacity;
+  a.loc_capacity = loc_capacity;
+  a.batch = batch;
+  a.q_len = pl->p.q_len;
+  a.page_size = page_size;
+  a.page_shift = -1;
+  for (int s = 0; s < 31; ++s)
+    if (page_size == (1 << s)) a.page_shift = s;
+  a.max_pages = max_pages;
+  a.num_free = num_free;
+  cudaError_t e = launch_slots(a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MLA_VERIFY_OK : cuda_fail(e);
 }
 

@@ -21,11 +21,14 @@ constexpr int kWsHeader = 256;            // bytes: [0] status accumulated by sp
 // Status bits (mirror MLA_VERIFY_DEV_* in mla_verify.h).
 constexpr uint32_t kStatusBadRow = 0x1u;
 constexpr uint32_t kStatusTimeout = 0x2u;
+constexpr uint32_t kStatusNoPage = 0x4u;
+constexpr uint32_t kStatusCapacity = 0x8u;
 
 struct SplitArgs {
   const __nv_bfloat16* q_nope;   // [B*T, H, 512]
   const __nv_bfloat16* q_rope;   // [B*T, H, 64]
-  const __nv_bfloat16* kv_pool;  // [pool_rows, 576]
+  const __nv_bfloat16* kv_pool;  // [pool_rows, 576]; null with a 4-bit pool
+  const uint8_t* kv4_pool;       // [pool_rows, 384] 4-bit rows (kv4.cuh), or null
   const int32_t* kv_indptr;      // [B+1]
   const int32_t* kv_indices;
   const int32_t* out_cache_loc;  // [B*T]
@@ -241,13 +244,40 @@ MLAV_DECLARE_TC(48)
 MLAV_DECLARE_TC(64)
 MLAV_DECLARE_TC(96)
 #undef MLAV_DECLARE_TC
+// The same over a 4-bit pool (split_kv4.cuh).
+#define MLAV_DECLARE_KV4(NQ)                                                         \
+  cudaError_t launch_split_kv4_##NQ(const SplitArgs& a, dim3 grid, cudaStream_t stream); \
+  int split_kv4_smem_##NQ();
+MLAV_DECLARE_KV4(16)
+MLAV_DECLARE_KV4(32)
+MLAV_DECLARE_KV4(48)
+MLAV_DECLARE_KV4(64)
+#undef MLAV_DECLARE_KV4
 cudaError_t launch_merge(const MergeArgs& a, cudaStream_t stream);
 constexpr int kMaxTreeMaskVarlenBatch = 1024;  // requests of a varlen mask build
 cudaError_t launch_tree_mask(const int32_t* parents, const int32_t* kv_indptr, const int32_t* qo_indptr, int batch,
                              int T, uint8_t* mask, int64_t mask_bytes, int32_t* mask_indptr, int64_t max_bytes,
                              cudaStream_t stream);
-cudaError_t launch_relocate(void* pool, const int32_t* kv_indptr, int32_t* kv_indices, const int32_t* dst_start,
-                            int batch, int64_t pool_rows, int64_t max_keys, uint32_t* status, cudaStream_t stream);
+cudaError_t launch_relocate(void* pool, int row_bytes, const int32_t* kv_indptr, int32_t* kv_indices,
+                            const int32_t* dst_start, int batch, int64_t pool_rows, int64_t max_keys, uint32_t* status,
+                            cudaStream_t stream);
+// One slot-map build (slots.cu).
+struct SlotsArgs {
+  const int32_t* seq_lens;    // [batch] cached tokens P_b
+  const int32_t* new_lens;    // [batch] new tokens T_b, or null: q_len each
+  int32_t* block_table;       // [batch, max_pages]; fresh entries are written
+  const int32_t* free_pages;  // [num_free]
+  int32_t* pages_used;        // [1]
+  int32_t* kv_indptr;         // [batch+1]
+  int32_t* kv_indices;        // [kv_capacity]
+  int32_t* qo_indptr;         // [batch+1]
+  int32_t* out_cache_loc;     // [loc_capacity]
+  uint32_t* status;           // workspace header word 0
+  int64_t pool_rows, kv_capacity, loc_capacity;
+  int32_t batch, q_len, page_size, page_shift, max_pages, num_free;  // page_shift: log2, or -1
+};
+constexpr int kMaxSlotsBatch = 4096;  // requests of one slot-map build
+cudaError_t launch_slots(const SlotsArgs& a, cudaStream_t stream);
 int merge_blocks(int rows, bool quarter);
 bool merge_quarter_fits(int64_t rows, int sms);
 

@@ -17,16 +17,14 @@
 // read once and every destination row written once, so loads and stores are
 // marked streaming (evict-first) and each warp keeps kRows rows (4.5 KB) in
 // flight; a row is 72 16-byte pieces, lane l moving pieces l, l+32 and (for
-// l < 8) l+64.
-#include "common.cuh"
+// l < 8) l+64.  Rows of a 4-bit pool (384 bytes) are 24 pieces, one per lane.
+#include "kv4.cuh"
 
 namespace mlav {
 namespace {
 
 constexpr int kThreads = 256;
 constexpr int kRows = 4;                       // rows per warp per iteration
-constexpr int kPieces = kRowBytes / 16;        // 16-byte pieces per row (72)
-constexpr int kPerLane = (kPieces + 31) / 32;  // 3
 
 // The request owning flat key k: the last b with kv_indptr[b] <= k.
 __device__ __forceinline__ int owner_of(const int32_t* kv_indptr, int batch, int64_t k) {
@@ -41,6 +39,7 @@ __device__ __forceinline__ int owner_of(const int32_t* kv_indptr, int batch, int
   return lo;
 }
 
+template <int kPieces>  // 16-byte pieces per row
 __global__ void __launch_bounds__(kThreads) relocate_kernel(uint4* pool, const int32_t* kv_indptr,
                                                             int32_t* kv_indices, const int32_t* dst_start,
                                                             int batch, int64_t pool_rows, uint32_t* status) {
@@ -49,6 +48,7 @@ __global__ void __launch_bounds__(kThreads) relocate_kernel(uint4* pool, const i
   const int64_t nwarps = ((int64_t)gridDim.x * kThreads) >> 5;
   const int64_t k_begin = kv_indptr[0], k_end = kv_indptr[batch];
   constexpr int64_t kRowVec = kPieces;  // uint4 per row
+  constexpr int kPerLane = (kPieces + 31) / 32;
   uint32_t bad = 0;
 #pragma unroll 1
   for (int64_t base = k_begin + warp * kRows; base < k_end; base += nwarps * kRows) {
@@ -96,8 +96,9 @@ __global__ void __launch_bounds__(kThreads) relocate_kernel(uint4* pool, const i
 
 }  // namespace
 
-cudaError_t launch_relocate(void* pool, const int32_t* kv_indptr, int32_t* kv_indices, const int32_t* dst_start,
-                            int batch, int64_t pool_rows, int64_t max_keys, uint32_t* status, cudaStream_t stream) {
+cudaError_t launch_relocate(void* pool, int row_bytes, const int32_t* kv_indptr, int32_t* kv_indices,
+                            const int32_t* dst_start, int batch, int64_t pool_rows, int64_t max_keys, uint32_t* status,
+                            cudaStream_t stream) {
   if (batch <= 0 || max_keys <= 0) return cudaSuccess;
   int sms = 0, dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -107,8 +108,9 @@ cudaError_t launch_relocate(void* pool, const int32_t* kv_indptr, int32_t* kv_in
   const int64_t want = (max_keys + (int64_t)kRows * (kThreads / 32) - 1) / ((int64_t)kRows * (kThreads / 32));
   const int64_t cap = (int64_t)sms * (2048 / kThreads);
   const int grid = (int)(want < cap ? (want > 0 ? want : 1) : cap);
-  relocate_kernel<<<grid, kThreads, 0, stream>>>(static_cast<uint4*>(pool), kv_indptr, kv_indices, dst_start, batch,
-                                                   pool_rows, status);
+  auto kernel = row_bytes == kKv4RowBytes ? relocate_kernel<kKv4RowBytes / 16> : relocate_kernel<kRowBytes / 16>;
+  kernel<<<grid, kThreads, 0, stream>>>(static_cast<uint4*>(pool), kv_indptr, kv_indices, dst_start, batch, pool_rows,
+                                        status);
   return cudaGetLastError();
 }
 

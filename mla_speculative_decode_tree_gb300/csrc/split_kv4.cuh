@@ -1,0 +1,780 @@
+// Tensor-core (tcgen05) split kernel over a 4-bit latent cache (kv4.cuh).
+//
+// The split kernel's job and orientation are those of split_tc.cuh: one CTA
+// takes one request, one chunk of its keys and one group of NQ query rows;
+// 128 keys per tile lie on the MMA's M, the query rows on N; it leaves a
+// normalised partial O and an LSE per row for the merge kernel.  What differs
+// is the operand type.  A 4-bit value with a power-of-two scale is an exact
+// e5m2 float, so a tile is expanded to 8 bits, not 16: 80 KB for 128 keys,
+// half the shared memory, half the stores, and K = 32 per MMA.  The bf16
+// queries and the fp32 weights P become pairs of e4m3 floats:
+//
+//   q * 2^x = q_hi + q_lo / 32     (x per row: the row's largest |q| in [128, 256))
+//   S^T     = K . [q_hi | q_lo]^T  one MMA chain with N = 2 NQ; s = (S_hi + S_lo / 32) * c,
+//             c = 2^-x * sm_scale * log2(e)
+//   p       = p_hi + p_lo          O^T += V^T . p_hi, V^T . p_lo
+//
+// e4m3 carries 4 significant bits, so q_hi takes a bf16 value's upper four and
+// q_lo the other four exactly (down to 2^-15 of the row's largest value, below
+// which the error is under 2^-23 of it): scores are as exact as with bf16
+// operands.  p_hi + p_lo keeps 8 to 9 bits, as much as a bf16 P would, down
+// to 2^-18 of the row's largest weight.  The products and sums are fp32.
+//
+// The RoPE residual codes are 64 more K columns against a second copy of
+// q_rope, so a key is 640 codes: five blocks of 128, 20 k-steps of 32.
+//
+// NQ <= 48: p_hi and 16 * p_lo sit side by side on N as well and O^T keeps
+// both halves in tensor memory (4 x 2 NQ columns), added in the epilogue.  An
+// M = 128 MMA costs ~64 cycles up to N = 96 -- it is bound by reading its 4 KB
+// A operand from shared memory -- so the second half is nearly free.  NQ = 64:
+// both halves accumulate into one O^T (tensor memory holds 512 columns).
+//
+// Warp roles:
+//   warps 0..4CG-1      softmax (CG column groups of HC query columns).  They
+//                       first turn the CTA's queries into q_hi, q_lo.
+//   warp 4CG            tensor memory, and the one thread that issues MMAs
+//   8 warps after it    expansion.  A thread owns quarter q (32 codes) of each
+//                       block of two keys.  It loads the next tile's codes
+//                       into registers as it finishes this tile's blocks, so
+//                       every global load has a whole tile's time to land and
+//                       no packed staging passes through shared memory.
+//
+// Slots.  A ring of 16 KB slots (128 keys x 128 channels, 8 bits, in the
+// 128-byte-swizzle atom of 8 keys x 128 bytes) takes the blocks of the tiles in
+// order.  The same bytes are the K-major A operand of S^T and the MN-major A
+// operand of O^T.  A tile's RoPE block is free after S^T, its value block m
+// after O^T block m.  MMA order: S^T(t+1) as far as the ring reaches past tile
+// t, then O^T(t), then the rest of S^T(t+1) -- so the softmax of tile t runs
+// beside S^T(t+1), and the expansion of t+1 beside O^T(t).
+//
+// P^T is written MN-major (a thread owns one key, its columns are contiguous:
+// 16-byte stores), in the unswizzled layout of 16 columns x 8 keys cores.
+//
+// Waits are bounded as in split_tc.cuh.
+#pragma once
+
+#include "kv4.cuh"
+#include "tc_ptx.cuh"
+
+namespace mlav {
+
+constexpr float kKv4Top = 4.0f;   // base 2: the running max maps to p = 2^4 ...
+constexpr float kKv4Tau = 4.0f;   // ... and is raised when a score passes it by this much (p <= 2^8 < 448)
+constexpr float kQLoScale = 32.f;
+constexpr float kPLoScale = 16.f;  // concatenated halves only
+
+template <int NQ>
+struct Kv4Cfg {
+  static_assert(NQ == 16 || NQ == 32 || NQ == 48 || NQ == 64, "row-group sizes built");
+  static constexpr bool kConcat = NQ <= 48;
+  static constexpr int kKeys = kKeysPerTile;
+  static constexpr int kHC = NQ == 64 ? 32 : 16;  // query columns per softmax thread
+  static constexpr int kCG = NQ / kHC;
+  static constexpr int kSoftmaxWarps = 4 * kCG;
+  static constexpr int kSoftmaxThreads = 32 * kSoftmaxWarps;
+  static constexpr int kMmaWarp = kSoftmaxWarps;
+  static constexpr int kExpandWarp = kSoftmaxWarps + 1;
+  static constexpr int kExpandWarps = 8;
+  static constexpr int kThreads = 32 * (kExpandWarp + kExpandWarps);
+  static constexpr int kQBlock = 2 * NQ * 128;  // one 128-channel block of q_hi rows, then q_lo rows
+  static constexpr int kQBytes = kKv4Blocks * kQBlock;
+  static constexpr int kPCore = kKeys * 16;     // 16 query columns x 128 keys of P^T
+  static constexpr int kPBytes = 2 * NQ * kKeys;
+  static constexpr int kPBufs = NQ == 64 ? 1 : 2;
+  static constexpr int kSlotBytes = kKeys * 128;
+  static constexpr int kSlots = NQ <= 16 ? 12 : NQ <= 32 ? 10 : 8;
+  static constexpr int kAhead = kSlots - kKv4Blocks < kKv4Blocks ? kSlots - kKv4Blocks : kKv4Blocks;
+  static constexpr int kOffP = kQBytes;
+  static constexpr int kOffRing = kOffP + kPBufs * kPBytes;
+  static constexpr int kOffCtl = kOffRing + kSlots * kSlotBytes;
+  static constexpr int kOStride = kConcat ? 2 * NQ : NQ;  // tensor-memory columns per O^T block
+  static constexpr int kColS = 4 * kOStride;
+  static_assert(kColS + 2 * NQ <= 512, "tensor memory budget");
+  static_assert(kOffRing % 1024 == 0, "slots are 1024-byte aligned");
+};
+
+template <int NQ>
+struct Kv4Ctl {
+  uint64_t full[Kv4Cfg<NQ>::kSlots];
+  uint64_t empty[Kv4Cfg<NQ>::kSlots];
+  uint64_t q_full, s_full, s_free, p_full[2], pv_done[2], mma_idle;
+  uint32_t tmem_base;
+  int abort;
+  int flag[2][Kv4Cfg<NQ>::kSoftmaxWarps];
+  int rflag[2];
+  alignas(16) float cscale[NQ];  // raw score -> base-2 score
+  alignas(16) float mtau[NQ];    // running max + kKv4Tau; -inf before any visible key
+  alignas(16) float muse[NQ];    // running max - kKv4Top, 0 while it is -inf
+  alignas(16) float alpha[NQ];   // rescale factor of the tile; 1/l in the epilogue
+  alignas(16) float red[4][NQ];
+  uint32_t colmask[kMaxQLen][Kv4Cfg<NQ>::kCG];  // per token: which of a column group's columns are its
+};
+
+template <int NQ>
+constexpr int kv4_smem_bytes() {
+  return Kv4Cfg<NQ>::kOffCtl + (int)sizeof(Kv4Ctl<NQ>);
+}
+
+namespace kv4 {
+
+// kind::f8f6f4, fp32 accumulator: bits 4-5 D (1 = f32) | 7-9 A, 10-12 B format
+// (0 = e4m3, 1 = e5m2) | 15, 16 A, B major (1 = MN) | 17-22 N>>3 | 24-28 M>>4
+__host__ __device__ constexpr uint32_t idesc_f8(int M, int N, int afmt, int bfmt, bool a_mn, bool b_mn) {
+  return (1u << 4) | ((uint32_t)afmt << 7) | ((uint32_t)bfmt << 10) | ((a_mn ? 1u : 0u) << 15) |
+         ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+constexpr int kE4M3 = 0, kE5M2 = 1;
+
+__device__ __forceinline__ void mma_f8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// Two floats -> two 8-bit floats (a in the low byte) and back to halves.
+__device__ __forceinline__ uint32_t cvt_e4m3x2(float a, float b) {
+  uint16_t d;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(b), "f"(a));
+  return d;
+}
+__device__ __forceinline__ uint32_t cvt_e4m3x2_f16x2(uint32_t h2) {
+  uint16_t d;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(d) : "r"(h2));
+  return d;
+}
+__device__ __forceinline__ uint32_t cvt_e5m2x2_f16x2(uint32_t h2) {
+  uint16_t d;
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(d) : "r"(h2));
+  return d;
+}
+__device__ __forceinline__ uint32_t cvt_f16x2_e4m3x2(uint32_t v) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"((uint16_t)v));
+  return d;
+}
+__device__ __forceinline__ uint32_t cvt_f16x2(float a, float b) {  // a in the low half
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(b), "f"(a));
+  return d;
+}
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+__device__ __forceinline__ uint4 ldg_stream(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// One word of 8 codes -> two words of 4 e5m2 values.  lo, hi: the eight
+// magnitudes times the group's scale, one byte each.
+__device__ __forceinline__ void expand8(uint32_t w, uint32_t lo, uint32_t hi, uint32_t& o0, uint32_t& o1) {
+  const uint32_t sel = w & 0x77777777u;
+  o0 = __byte_perm(lo, hi, sel) | (w & 0x80808080u);
+  o1 = __byte_perm(lo, hi, sel >> 16) | ((w << 4) & 0x80808080u);
+}
+
+// The scaled magnitudes 0, .5, 1, 1.5, 2, 3, 4, 6 as e5m2 bytes: exponent
+// field + e for all but the zero.
+__device__ __forceinline__ void scale_table(uint32_t scale_byte, uint32_t& lo, uint32_t& hi) {
+  const uint32_t a = (uint32_t)(4 * kv4_exponent(scale_byte));
+  lo = 0x3E3C3800u + a * 0x01010100u;
+  hi = 0x46444240u + a * 0x01010101u;
+}
+
+// Bounded wait that ignores the abort flag (teardown only).
+__device__ __forceinline__ void wait_teardown(uint64_t* bar, uint32_t parity) {
+  const uint64_t t0 = global_timer_ns();
+  for (uint32_t it = 0; it < (1u << 30); ++it) {
+    if (mbar_try_wait(bar, parity)) return;
+    if ((it & 63u) == 0 && global_timer_ns() - t0 > kWaitLimitNs) return;
+  }
+}
+
+// Max (or sum) of v[0..15] over the warp, index by index: lane l returns that
+// of index l / 2.
+template <bool kMax>
+__device__ __forceinline__ float reduce16(float (&v)[16], int lane) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) {
+    const bool upper = (lane & (2 * o)) != 0;
+#pragma unroll
+    for (int m = 0; m < o; ++m) {
+      const float send = upper ? v[m] : v[m + o];
+      const float keep = upper ? v[m + o] : v[m];
+      const float got = __shfl_xor_sync(0xffffffffu, send, 2 * o);
+      v[m] = kMax ? fmaxf(keep, got) : keep + got;
+    }
+  }
+  const float got = __shfl_xor_sync(0xffffffffu, v[0], 1);
+  return kMax ? fmaxf(v[0], got) : v[0] + got;
+}
+
+template <int HC, bool kMax>
+__device__ __forceinline__ void columns_to_smem(const float (&x)[HC], float* dst, int lane) {
+#pragma unroll
+  for (int g = 0; g < HC / 16; ++g) {
+    float v[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) v[k] = x[16 * g + k];
+    const float r = reduce16<kMax>(v, lane);
+    if ((lane & 1) == 0) dst[16 * g + (lane >> 1)] = r;
+  }
+}
+
+}  // namespace kv4
+
+template <int NQ>
+__global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(const __grid_constant__ SplitArgs a) {
+  using Cfg = Kv4Cfg<NQ>;
+  constexpr int kKeys = Cfg::kKeys;
+  constexpr int S = Cfg::kSlots;
+  constexpr int HC = Cfg::kHC;
+  constexpr int CG = Cfg::kCG;
+  constexpr int kSoftmaxWarps = Cfg::kSoftmaxWarps;
+  constexpr int kSoftmaxThreads = Cfg::kSoftmaxThreads;
+  const int b = blockIdx.z;
+  if (b >= a.batch) return;
+  const int tid = threadIdx.x;
+  const int warp = tid >> 5;
+  const int lane = tid & 31;
+  const int s_idx = blockIdx.y;
+  const int g = blockIdx.x;
+
+  const int64_t kv_base = a.kv_indptr[b];
+  const int64_t P = (int64_t)a.kv_indptr[b + 1] - kv_base;
+  const RequestTokens rq = request_tokens(a, b);
+  const int64_t L = P + rq.n;
+  const int64_t chunk = chunk_len(L, a.nsplit, a.min_chunk, a.chunk_granule);
+  const int64_t j0 = (int64_t)s_idx * chunk;
+  const int64_t j1 = (j0 + chunk < L) ? j0 + chunk : L;
+  const int rows_b = rq.n * a.H;
+  const int r0 = g * NQ;
+  if (r0 >= rows_b) return;
+  const int nrows = (rows_b - r0 < NQ) ? rows_b - r0 : NQ;
+  const int64_t grow0 = rq.q0 * a.H + r0;  // global row of the group's first row
+  float* lse_out = a.part_lse + (int64_t)s_idx * a.rows_max + grow0;
+  if (j0 >= j1) {
+    for (int n = tid; n < nrows; n += Cfg::kThreads) lse_out[n] = -INFINITY;
+    return;
+  }
+  const int nt = (int)((j1 - j0 + kKeys - 1) / kKeys);
+  const int i0 = r0 / a.H;
+  const int ntok = (r0 + nrows - 1) / a.H - i0 + 1;
+  // Row group g starts g tiles into the split: the groups of a split read the
+  // same keys, and staggered they read them from L2 one after the other.
+  const int rot = g % nt;
+  auto tile_at = [&](int t) -> int { return t + rot < nt ? t + rot : t + rot - nt; };
+
+  extern __shared__ __align__(1024) uint8_t kv4_smem[];  // the swizzle atoms are 1024-byte aligned
+  const uint32_t sQ = smem_u32(kv4_smem), sP = sQ + Cfg::kOffP, sRing = sQ + Cfg::kOffRing;
+  Kv4Ctl<NQ>& ctl = *reinterpret_cast<Kv4Ctl<NQ>*>(kv4_smem + Cfg::kOffCtl);
+
+  // ---- set-up ---------------------------------------------------------------
+  if (tid == 0) {
+    for (int k = 0; k < S; ++k) {
+      mbar_init(&ctl.full[k], Cfg::kExpandWarps);
+      mbar_init(&ctl.empty[k], 1);
+    }
+    mbar_init(&ctl.q_full, kSoftmaxWarps);
+    mbar_init(&ctl.s_full, 1);
+    mbar_init(&ctl.s_free, kSoftmaxWarps);
+    // two: the softmax may finish the next tile before the MMA thread has seen this one's
+    mbar_init(&ctl.p_full[0], kSoftmaxWarps);
+    mbar_init(&ctl.p_full[1], kSoftmaxWarps);
+    mbar_init(&ctl.pv_done[0], 1);
+    mbar_init(&ctl.pv_done[1], 1);
+    mbar_init(&ctl.mma_idle, 1);
+    ctl.abort = 0;
+    ctl.rflag[0] = ctl.rflag[1] = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == Cfg::kMmaWarp) {
+    tc::tmem_alloc(&ctl.tmem_base, 512);
+    tc::tmem_relinquish();
+  }
+  if (tid < kSoftmaxThreads) {
+    for (int n = tid; n < NQ; n += kSoftmaxThreads) {
+      ctl.mtau[n] = -INFINITY;
+      ctl.muse[n] = 0.f;
+    }
+    for (int t = tid; t < ntok * CG; t += kSoftmaxThreads) {
+      const int tok = t / CG, h = t % CG;
+      uint32_t bits = 0;
+      for (int c = 0; c < HC; ++c) {
+        const int n = h * HC + c;
+        if (n < nrows && (r0 + n) / a.H == i0 + tok) bits |= 1u << c;
+      }
+      ctl.colmask[tok][h] = bits;
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = ctl.tmem_base;
+
+  if (warp >= Cfg::kExpandWarp) {
+    // =========================== expansion ===================================
+    // Thread (warp w, lane) owns codes 32q..32q+31 of each block of keys
+    // 8w + lane/4 and 64 + 8w + lane/4, q = lane % 4: a warp's load of one
+    // block covers 8 rows x 64 contiguous bytes, and its 16-byte stores reach
+    // all 32 banks (8 lanes = 2 keys x 4 chunks of opposite parity).
+    const int w = warp - Cfg::kExpandWarp;
+    const int q = lane & 3;
+    const int key0 = 8 * w + (lane >> 2);
+    uint32_t bad = 0;
+    // Raw row id of own key h of tile t (-1 past the chunk's end).
+    auto load_id = [&](int t, int h) -> int64_t {
+      const int64_t j = j0 + (int64_t)tile_at(t < nt ? t : 0) * kKeys + key0 + 64 * h;
+      if (t >= nt || j >= j1) return -1;
+      const int32_t r = load_row_id(a, rq.q0, P, kv_base, j);
+      if (r >= 0 && r < a.pool_rows) return r;
+      bad = 1;  // left out: expands to zeros, masked by the softmax
+      return -1;
+    };
+    const uint8_t* row[2];
+    uint4 code[2][kKv4Blocks], scale[2];
+    auto set_rows = [&](int t) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int64_t r = load_id(t, h);
+        row[h] = r >= 0 ? a.kv4_pool + r * kKv4RowBytes + 16 * q : nullptr;
+      }
+    };
+    auto load_block = [&](int m) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        code[h][m] = row[h] ? kv4::ldg_stream(row[h] + 64 * m) : make_uint4(0, 0, 0, 0);
+    };
+    auto load_scales = [&](uint4 (&to)[2]) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) to[h] = row[h] ? kv4::ldg_stream(row[h] + kKv4ScaleOff) : make_uint4(0, 0, 0, 0);
+    };
+    set_rows(0);
+    load_scales(scale);
+#pragma unroll
+    for (int m = 0; m < kKv4Blocks; ++m) load_block(m);
+    set_rows(1);
+    int slot = 0;
+    uint32_t phase = 1;  // the first pass over the ring finds every slot empty
+    bool stop = false;
+#pragma unroll 1
+    for (int t = 0; t < nt && !stop; ++t) {
+      uint4 next_scale[2];
+      load_scales(next_scale);
+#pragma unroll
+      for (int m = 0; m < kKv4Blocks; ++m) {
+        if (!stop) {
+          const bool got = mbar_wait(&ctl.empty[slot], phase, &ctl.abort, a.status);
+          if (!__all_sync(0xffffffffu, got)) stop = true;
+        }
+        if (!stop) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t sw = m < 2 ? scale[h].x : m < 4 ? scale[h].y : scale[h].z;
+            uint32_t lo[2], hi[2], o[8];
+            kv4::scale_table((sw >> (16 * (m & 1))) & 0xFFu, lo[0], hi[0]);
+            kv4::scale_table((sw >> (16 * (m & 1) + 8)) & 0xFFu, lo[1], hi[1]);
+            kv4::expand8(code[h][m].x, lo[0], hi[0], o[0], o[1]);
+            kv4::expand8(code[h][m].y, lo[0], hi[0], o[2], o[3]);
+            kv4::expand8(code[h][m].z, lo[1], hi[1], o[4], o[5]);
+            kv4::expand8(code[h][m].w, lo[1], hi[1], o[6], o[7]);
+            const int key = key0 + 64 * h;
+            const uint32_t dst = sRing + slot * Cfg::kSlotBytes + key * 128;
+            kv4::sts128(dst + (((2 * q) ^ (key & 7)) << 4), o[0], o[1], o[2], o[3]);
+            kv4::sts128(dst + (((2 * q + 1) ^ (key & 7)) << 4), o[4], o[5], o[6], o[7]);
+          }
+          load_block(m);  // tile t+1
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && !(a.test_stall && t == 0 && m == 0)) mbar_arrive(&ctl.full[slot]);
+          if (++slot == S) {
+            slot = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      scale[0] = next_scale[0];
+      scale[1] = next_scale[1];
+      set_rows(t + 2);
+    }
+    if (bad) atomicOr(a.status, kStatusBadRow);
+  } else if (warp == Cfg::kMmaWarp) {
+    // ============================ MMA issue ==================================
+    if (lane == 0) {
+      constexpr uint32_t idesc_qk = kv4::idesc_f8(kKeys, 2 * NQ, kv4::kE5M2, kv4::kE4M3, false, false);
+      constexpr uint32_t idesc_pv =
+          kv4::idesc_f8(128, Cfg::kConcat ? 2 * NQ : NQ, kv4::kE5M2, kv4::kE4M3, true, true);
+      constexpr uint32_t idesc_lo = kv4::idesc_f8(128, NQ, kv4::kE5M2, kv4::kE5M2, true, true);
+      int used = 0;  // blocks of the ring consumed by S^T so far
+      bool ok = mbar_wait_spin(&ctl.q_full, 0, &ctl.abort, a.status);
+      // S^T += K block blk . Q block blk^T for blocks [blk0, blk1) of the next tile
+      auto qk = [&](int blk0, int blk1) {
+#pragma unroll 1
+        for (int blk = blk0; blk < blk1 && ok; ++blk) {
+          const int slot = used % S;
+          if (!(ok = mbar_wait_spin(&ctl.full[slot], (used / S) & 1, &ctl.abort, a.status))) return;
+          tc::fence_after_sync();
+          ++used;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint64_t ad = tc::smem_desc(sRing + slot * Cfg::kSlotBytes + k * 32, 16, 1024, tc::kSwizzle128B);
+            const uint64_t bd = tc::smem_desc(sQ + blk * Cfg::kQBlock + k * 32, 16, 1024, tc::kSwizzle128B);
+            kv4::mma_f8_ss(tmem + Cfg::kColS, ad, bd, idesc_qk, (blk == 0 && k == 0) ? 0u : 1u);
+          }
+          if (blk == kKv4Blocks - 1) tc::mma_commit(&ctl.empty[slot]);  // the RoPE block is done with
+        }
+      };
+      qk(0, kKv4Blocks);
+      if (ok) tc::mma_commit(&ctl.s_full);
+#pragma unroll 1
+      for (int t = 0; t < nt && ok; ++t) {
+        const bool more = t + 1 < nt;
+        if (more) {
+          ok = mbar_wait_spin(&ctl.s_free, t & 1, &ctl.abort, a.status);
+          tc::fence_after_sync();
+          if (ok) qk(0, Cfg::kAhead);
+          if (ok && Cfg::kAhead == kKv4Blocks) tc::mma_commit(&ctl.s_full);
+        }
+        if (!ok || !(ok = mbar_wait_spin(&ctl.p_full[t & 1], (t >> 1) & 1, &ctl.abort, a.status))) break;
+        tc::fence_after_sync();
+        const uint32_t pbuf = sP + (t % Cfg::kPBufs) * Cfg::kPBytes;
+#pragma unroll 1
+        for (int m = 0; m < 4; ++m) {
+          const int slot = (kKv4Blocks * t + m) % S;
+          const uint32_t d = tmem + m * Cfg::kOStride;
+#pragma unroll
+          for (int k = 0; k < kKeys / 32; ++k) {
+            const uint64_t ad =
+                tc::smem_desc(sRing + slot * Cfg::kSlotBytes + k * 4096, Cfg::kSlotBytes, 1024, tc::kSwizzle128B);
+            const uint32_t acc = (t == 0 && k == 0) ? 0u : 1u;
+            kv4::mma_f8_ss(d, ad, tc::smem_desc(pbuf + k * 512, 128, Cfg::kPCore, 0), idesc_pv, acc);
+            if (!Cfg::kConcat)
+              kv4::mma_f8_ss(d, ad, tc::smem_desc(pbuf + (NQ / 16) * Cfg::kPCore + k * 512, 128, Cfg::kPCore, 0),
+                             idesc_lo, 1u);
+          }
+          tc::mma_commit(&ctl.empty[slot]);
+        }
+        tc::mma_commit(&ctl.pv_done[t & 1]);
+        if (more && Cfg::kAhead < kKv4Blocks) {
+          qk(Cfg::kAhead, kKv4Blocks);
+          if (ok) tc::mma_commit(&ctl.s_full);
+        }
+      }
+      // Every MMA this thread issued has completed before tensor memory is freed.
+      tc::mma_commit(&ctl.mma_idle);
+      kv4::wait_teardown(&ctl.mma_idle, 0);
+    }
+    __syncwarp();
+  } else {
+    // ============================ softmax ====================================
+    // Queries: warp w turns rows w, w + warps, ... into q_hi and q_lo.  Lane l
+    // holds channels 8l..8l+7 and 256+8l.., lanes 0-7 also RoPE channels 8l...
+#pragma unroll 1
+    for (int n = warp; n < NQ; n += kSoftmaxWarps) {
+      uint4 v[3];
+      v[0] = v[1] = v[2] = make_uint4(0, 0, 0, 0);
+      if (n < nrows) {
+        const uint4* qn = reinterpret_cast<const uint4*>(a.q_nope + (grow0 + n) * kDLatent);
+        v[0] = __ldg(qn + lane);
+        v[1] = __ldg(qn + 32 + lane);
+        if (lane < 8) v[2] = __ldg(reinterpret_cast<const uint4*>(a.q_rope + (grow0 + n) * kDRope) + lane);
+      }
+      uint32_t top = 0;  // largest |q| as bits: bf16 magnitudes order as integers
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        const uint32_t u[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = max(top, max(u[i] & 0x7FFFu, (u[i] >> 16) & 0x7FFFu));
+      }
+      top = __reduce_max_sync(0xffffffffu, top);
+      const int ex = (int)(top >> 7);  // biased exponent of the largest value
+      // 2^x brings it into [128, 256); rows of zeros or denormals use the largest x
+      int x = 7 + 127 - ex;
+      x = x > 126 ? 126 : x;
+      const float up = pow2f(x);
+      if (lane == 0) {
+        // a row with an infinity or a NaN scores NaN
+        const float c = ex == 255 ? NAN : a.scale_log2 * pow2f(-x);
+        ctl.cscale[n] = c;
+      }
+      auto put = [&](int chunk8, const uint4& bits) {  // 8 channels -> 8 bytes of q_hi and of q_lo
+        const uint32_t u[4] = {bits.x, bits.y, bits.z, bits.w};
+        uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float f0 = __uint_as_float(u[i] << 16) * up, f1 = __uint_as_float(u[i] & 0xFFFF0000u) * up;
+          const uint32_t h = kv4::cvt_e4m3x2(f0, f1);
+          const uint32_t hf = kv4::cvt_f16x2_e4m3x2(h);
+          const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hf));
+          const uint32_t l = kv4::cvt_e4m3x2((f0 - back.x) * kQLoScale, (f1 - back.y) * kQLoScale);
+          hi[i >> 1] |= h << (16 * (i & 1));
+          lo[i >> 1] |= l << (16 * (i & 1));
+        }
+        const int blk = chunk8 >> 4, c16 = (chunk8 & 15) >> 1;
+        const uint32_t at = sQ + blk * Cfg::kQBlock + ((c16 ^ (n & 7)) << 4) + 8 * (chunk8 & 1);
+        asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at + n * 128), "r"(hi[0]), "r"(hi[1]) : "memory");
+        asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at + (NQ + n) * 128), "r"(lo[0]), "r"(lo[1]) : "memory");
+      };
+      static_assert(NQ % 8 == 0, "q_lo row n swizzles as q_hi row n");
+      put(lane, v[0]);
+      put(32 + lane, v[1]);
+      if (lane < 8) {
+        put(64 + lane, v[2]);
+        put(72 + lane, v[2]);  // against the RoPE residual codes
+      }
+    }
+    fence_proxy_async_smem();
+    named_bar_sync(1, kSoftmaxThreads);  // cscale
+    if (lane == 0) mbar_arrive(&ctl.q_full);
+
+    const int quad = warp & 3;
+    const int half = warp >> 2;      // column group
+    const int j = 32 * quad + lane;  // key within the tile == TMEM lane
+    const int c0 = half * HC;        // first query column of this thread
+    const uint32_t t_lane = tmem + ((uint32_t)(32 * quad) << 16);
+    const int64_t mask_base = (int64_t)a.mask_indptr[b] + (int64_t)i0 * L;
+    float acc[HC];  // sum of p over this thread's keys
+#pragma unroll
+    for (int k = 0; k < HC; ++k) acc[k] = 0.f;
+    bool my_abort = false;
+#pragma unroll 1
+    for (int t = 0; t < nt; ++t) {
+      const int64_t key = j0 + (int64_t)tile_at(t) * kKeys + j;
+      uint32_t vis = 0;
+      if (key < j1 && resolve_row(a, rq.q0, P, kv_base, key) >= 0) {  // rows outside the pool are left out
+        for (int tl = 0; tl < ntok; ++tl)
+          if (mask_bit(a.mask, mask_base + (int64_t)tl * L + key)) vis |= ctl.colmask[tl][half];
+      }
+      float s[HC];
+      if (!my_abort) my_abort = !mbar_wait(&ctl.s_full, t & 1, &ctl.abort, a.status);
+      my_abort = __any_sync(0xffffffffu, my_abort);  // tcgen05.ld below is warp-collective
+      tc::fence_after_sync();
+      if (!my_abort) {
+#pragma unroll
+        for (int c = 0; c < HC / 16; ++c) {
+          float lo[16];
+          kv4::tmem_ld16(t_lane + Cfg::kColS + c0 + 16 * c, &s[16 * c]);
+          kv4::tmem_ld16(t_lane + Cfg::kColS + NQ + c0 + 16 * c, lo);
+          tc::tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 16; ++k) s[16 * c + k] = fmaf(lo[k], 1.f / kQLoScale, s[16 * c + k]);
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < HC; ++k) s[k] = 0.f;
+      }
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0 && !my_abort) mbar_arrive(&ctl.s_free);  // S^T may be overwritten
+
+      bool need = false;
+      const float4* mt4 = reinterpret_cast<const float4*>(&ctl.mtau[c0]);
+      const float4* cs4 = reinterpret_cast<const float4*>(&ctl.cscale[c0]);
+#pragma unroll
+      for (int k4 = 0; k4 < HC / 4; ++k4) {
+        const float4 mt = mt4[k4], cs = cs4[k4];
+        const float mtk[4] = {mt.x, mt.y, mt.z, mt.w}, csk[4] = {cs.x, cs.y, cs.z, cs.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int k = 4 * k4 + i;
+          s[k] = ((vis >> k) & 1u) ? s[k] * csk[i] : -INFINITY;
+          need |= s[k] > mtk[i];
+        }
+      }
+      const bool warp_need = __any_sync(0xffffffffu, need);
+      const bool warp_abort = __any_sync(0xffffffffu, my_abort) || ctl.abort;
+      if (lane == 0) ctl.flag[t & 1][warp] = (warp_need ? 1 : 0) | (warp_abort ? 2 : 0);
+      named_bar_sync(1, kSoftmaxThreads);
+      int f = 0;
+#pragma unroll
+      for (int w = 0; w < kSoftmaxWarps; ++w) f |= ctl.flag[t & 1][w];
+      if (tid == 0) ctl.rflag[(t + 1) & 1] = 0;
+      if (f & 2) {
+        my_abort = true;
+        break;
+      }
+      bool rescale = false;
+      if (f & 1) {
+        // Exact column max over the tile's 128 keys; raise the running max
+        // where it passed by more than kKv4Tau.
+        kv4::columns_to_smem<HC, true>(s, &ctl.red[quad][c0], lane);
+        named_bar_sync(1, kSoftmaxThreads);
+        if (tid < NQ) {
+          const float cm = fmaxf(fmaxf(ctl.red[0][tid], ctl.red[1][tid]), fmaxf(ctl.red[2][tid], ctl.red[3][tid]));
+          const float old = ctl.mtau[tid];  // -inf or max + kKv4Tau
+          float al = 1.f;
+          if (cm > old) {
+            al = (old == -INFINITY) ? 0.f : ex2_approx(old - kKv4Tau - cm);
+            ctl.mtau[tid] = cm + kKv4Tau;
+            ctl.muse[tid] = cm - kKv4Top;
+            ctl.rflag[t & 1] = 1;
+          }
+          ctl.alpha[tid] = al;
+        }
+        named_bar_sync(1, kSoftmaxThreads);
+#pragma unroll
+        for (int k = 0; k < HC; ++k) acc[k] *= ctl.alpha[c0 + k];
+        rescale = (t > 0) && ctl.rflag[t & 1];
+      }
+      // P^T(t) overwrites what O^T(t - kPBufs) read; a rescale of O^T needs all of them done.
+      if (t >= Cfg::kPBufs && !my_abort)
+        my_abort = !mbar_wait(&ctl.pv_done[(t - Cfg::kPBufs) & 1], ((t - Cfg::kPBufs) >> 1) & 1, &ctl.abort, a.status);
+      if (Cfg::kPBufs > 1 && rescale && !my_abort)
+        my_abort = !mbar_wait(&ctl.pv_done[(t - 1) & 1], ((t - 1) >> 1) & 1, &ctl.abort, a.status);
+      my_abort = __any_sync(0xffffffffu, my_abort);
+      tc::fence_after_sync();
+      if (!my_abort && rescale) {
+#pragma unroll 1
+        for (int m = 0; m < 4 * (Cfg::kConcat ? 2 : 1); ++m) {
+          const uint32_t col = Cfg::kConcat ? (m >> 1) * Cfg::kOStride + (m & 1) * NQ : m * Cfg::kOStride;
+#pragma unroll
+          for (int c = 0; c < HC / 8; ++c) {
+            float v[8];
+            tc::tmem_ld8(t_lane + col + c0 + 8 * c, v);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] *= ctl.alpha[c0 + 8 * c + k];
+            tc::tmem_st8(t_lane + col + c0 + 8 * c, v);
+          }
+        }
+        tc::tmem_wait_st();
+      }
+      if (!my_abort) {
+        const uint32_t dst = sP + (t % Cfg::kPBufs) * Cfg::kPBytes + j * 16;
+        const float4* mu4 = reinterpret_cast<const float4*>(&ctl.muse[c0]);
+#pragma unroll
+        for (int c = 0; c < HC / 16; ++c) {
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int k4 = 0; k4 < 4; ++k4) {
+            const float4 mu = mu4[4 * c + k4];
+            const int k = 16 * c + 4 * k4;
+            const float p0 = ex2_approx(s[k + 0] - mu.x);  // s = -inf (masked) gives 0
+            const float p1 = ex2_approx(s[k + 1] - mu.y);
+            const float p2 = ex2_approx(s[k + 2] - mu.z);
+            const float p3 = ex2_approx(s[k + 3] - mu.w);
+            acc[k + 0] += p0;
+            acc[k + 1] += p1;
+            acc[k + 2] += p2;
+            acc[k + 3] += p3;
+            // through halves: 11 bits, far finer than the 8 to 9 kept
+            const uint32_t h01 = kv4::cvt_f16x2(p0, p1), h23 = kv4::cvt_f16x2(p2, p3);
+            const uint32_t u01 = kv4::cvt_e4m3x2_f16x2(h01), u23 = kv4::cvt_e4m3x2_f16x2(h23);
+            uint32_t r01 = kv4::sub_f16x2(h01, kv4::cvt_f16x2_e4m3x2(u01));
+            uint32_t r23 = kv4::sub_f16x2(h23, kv4::cvt_f16x2_e4m3x2(u23));
+            hi[k4] = u01 | (u23 << 16);
+            if constexpr (Cfg::kConcat) {
+              r01 = kv4::mul_f16x2(r01, 0x4C004C00u);  // 16: kPLoScale
+              r23 = kv4::mul_f16x2(r23, 0x4C004C00u);
+              lo[k4] = kv4::cvt_e4m3x2_f16x2(r01) | (kv4::cvt_e4m3x2_f16x2(r23) << 16);
+            } else {
+              lo[k4] = kv4::cvt_e5m2x2_f16x2(r01) | (kv4::cvt_e5m2x2_f16x2(r23) << 16);
+            }
+          }
+          kv4::sts128(dst + (c0 / 16 + c) * Cfg::kPCore, hi[0], hi[1], hi[2], hi[3]);
+          kv4::sts128(dst + ((NQ + c0) / 16 + c) * Cfg::kPCore, lo[0], lo[1], lo[2], lo[3]);
+        }
+      }
+      fence_proxy_async_smem();
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0 && !my_abort) mbar_arrive(&ctl.p_full[t & 1]);
+    }
+
+    // ---- epilogue: l, LSE, O = O^T / l ----------------------------------------
+    kv4::columns_to_smem<HC, false>(acc, &ctl.red[quad][c0], lane);
+    if (!my_abort) my_abort = !mbar_wait(&ctl.pv_done[(nt - 1) & 1], ((nt - 1) >> 1) & 1, &ctl.abort, a.status);
+    tc::fence_after_sync();
+    const bool wa = __any_sync(0xffffffffu, my_abort) || ctl.abort;
+    if (lane == 0) ctl.flag[nt & 1][warp] = wa ? 2 : 0;
+    named_bar_sync(1, kSoftmaxThreads);
+    int f = 0;
+#pragma unroll
+    for (int w = 0; w < kSoftmaxWarps; ++w) f |= ctl.flag[nt & 1][w];
+    if (tid < NQ) {
+      const float l = (ctl.red[0][tid] + ctl.red[1][tid]) + (ctl.red[2][tid] + ctl.red[3][tid]);
+      ctl.alpha[tid] = l == 0.f ? 0.f : 1.f / l;
+      if (!(f & 2) && tid < nrows)
+        lse_out[tid] = l == 0.f ? -INFINITY : (ctl.muse[tid] + __log2f(l)) * 0.69314718055994530942f;
+    }
+    named_bar_sync(1, kSoftmaxThreads);
+    if (!(f & 2)) {
+      // Thread (quad, lane) holds latent column 128m + j of rows c0..c0+HC: a
+      // warp store writes 128 contiguous bytes of one row.  Rows with nothing
+      // visible are not written (their LSE is -inf).
+      float* ocol = a.part_o + ((int64_t)s_idx * a.rows_max + grow0) * kDLatent + j;
+#pragma unroll 1
+      for (int m = 0; m < 4; ++m) {
+#pragma unroll
+        for (int c = 0; c < HC / 16; ++c) {
+          float v[16];
+          kv4::tmem_ld16(t_lane + m * Cfg::kOStride + c0 + 16 * c, v);
+          if constexpr (Cfg::kConcat) {
+            float lo[16];
+            kv4::tmem_ld16(t_lane + m * Cfg::kOStride + NQ + c0 + 16 * c, lo);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) v[k] = fmaf(lo[k], 1.f / kPLoScale, v[k]);
+          } else {
+            tc::tmem_wait_ld();
+          }
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const int n = c0 + 16 * c + k;
+            const float inv = ctl.alpha[n];
+            if (n < nrows && inv != 0.f) ocol[(int64_t)n * kDLatent + 128 * m] = v[k] * inv;
+          }
+        }
+      }
+    }
+    tc::fence_before_sync();
+  }
+
+  // ---- teardown ---------------------------------------------------------------
+  __syncthreads();
+  if (warp == Cfg::kMmaWarp) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int NQ>
+cudaError_t launch_split_kv4_nq(const SplitArgs& a, dim3 grid, cudaStream_t stream) {
+  constexpr int smem = kv4_smem_bytes<NQ>();
+  static_assert(smem <= 232448, "shared memory budget exceeded");
+  cudaError_t e = cudaFuncSetAttribute(split_kv4_kernel<NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  split_kv4_kernel<NQ><<<grid, Kv4Cfg<NQ>::kThreads, smem, stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace mlav

@@ -1,0 +1,9 @@
+// 4-bit-cache split kernel instantiated for 48 query rows per CTA.
+#include "split_kv4.cuh"
+
+namespace mlav {
+cudaError_t launch_split_kv4_48(const SplitArgs& a, dim3 grid, cudaStream_t stream) {
+  return launch_split_kv4_nq<48>(a, grid, stream);
+}
+int split_kv4_smem_48() { return kv4_smem_bytes<48>(); }
+}  // namespace mlav

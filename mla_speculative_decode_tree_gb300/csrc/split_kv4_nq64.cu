@@ -1,0 +1,9 @@
+// 4-bit-cache split kernel instantiated for 64 query rows per CTA.
+#include "split_kv4.cuh"
+
+namespace mlav {
+cudaError_t launch_split_kv4_64(const SplitArgs& a, dim3 grid, cudaStream_t stream) {
+  return launch_split_kv4_nq<64>(a, grid, stream);
+}
+int split_kv4_smem_64() { return kv4_smem_bytes<64>(); }
+}  // namespace mlav

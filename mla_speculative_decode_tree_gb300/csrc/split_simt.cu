@@ -10,7 +10,11 @@
 // key row is fetched with 128-bit loads [Capture Safety to MoE Ceiling,
 // §"Vectorized Loads: The Final Push"; Custom sm_120 Verify Kernel, §"The
 // Float4 Vectorization"].
-#include "common.cuh"
+//
+// kKv4: the rows of a 4-bit pool (kv4.cuh).  The lanes own the same columns:
+// the words of 8 codes l and l+32 of the latent, and, lanes 0-7, word l of the
+// RoPE codes and of their residuals.
+#include "kv4.cuh"
 
 namespace mlav {
 namespace {
@@ -26,6 +30,59 @@ __device__ __forceinline__ void bf16x8_to_f32(uint4 u, float (&f)[8]) {
   }
 }
 
+// What a lane holds of one key row, and its values.
+template <bool kKv4>
+struct LaneRow;
+
+template <>
+struct LaneRow<false> {
+  uint4 a, b, r;
+  __device__ __forceinline__ void clear() { a = b = r = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void load(const SplitArgs& args, int64_t row, int lane) {
+    const uint4* kv = reinterpret_cast<const uint4*>(args.kv_pool + row * kDRow);
+    a = __ldg(kv + lane);
+    b = __ldg(kv + 32 + lane);
+    if (lane < 8) r = __ldg(kv + 64 + lane);
+  }
+  __device__ __forceinline__ void latent(float (&fa)[8], float (&fb)[8]) const {
+    bf16x8_to_f32(a, fa);
+    bf16x8_to_f32(b, fb);
+  }
+  __device__ __forceinline__ void rope(float (&fr)[8]) const { bf16x8_to_f32(r, fr); }
+};
+
+template <>
+struct LaneRow<true> {
+  uint32_t w[4];  // latent words lane, lane + 32; RoPE, residual
+  float s[4];     // their scales
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] = 0, s[k] = 1.f;
+  }
+  __device__ __forceinline__ void load(const SplitArgs& args, int64_t row, int lane) {
+    const uint8_t* kv = args.kv4_pool + row * kKv4RowBytes;
+    const int first[4] = {8 * lane, 256 + 8 * lane, 512 + 8 * lane, 576 + 8 * lane};
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (k < 2 || lane < 8) {
+        w[k] = __ldg(reinterpret_cast<const uint32_t*>(kv + first[k] / 2));
+        s[k] = pow2f(kv4_exponent(__ldg(kv + kv4_scale_at(first[k]))));
+      }
+  }
+  __device__ __forceinline__ void latent(float (&fa)[8], float (&fb)[8]) const {
+    kv4_decode8(w[0], s[0], fa);
+    kv4_decode8(w[1], s[1], fb);
+  }
+  __device__ __forceinline__ void rope(float (&fr)[8]) const {
+    float rest[8];
+    kv4_decode8(w[2], s[2], fr);
+    kv4_decode8(w[3], s[3], rest);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) fr[k] += rest[k];
+  }
+};
+
+template <bool kKv4>
 __global__ void __launch_bounds__(32 * kSimtRowsPerCta) split_simt_kernel(SplitArgs a) {
   const int b = blockIdx.z;
   if (b >= a.batch) return;
@@ -68,20 +125,17 @@ __global__ void __launch_bounds__(32 * kSimtRowsPerCta) split_simt_kernel(SplitA
   for (int k = 0; k < 8; ++k) acc_a[k] = acc_b[k] = 0.f;
 
   for (int64_t jb = j0; jb < j1; jb += kKeysPerStep) {
-    uint4 va[kKeysPerStep], vb[kKeysPerStep], vr[kKeysPerStep];
+    LaneRow<kKv4> key[kKeysPerStep];
     bool vis[kKeysPerStep];
 #pragma unroll
     for (int u = 0; u < kKeysPerStep; ++u) {
       const int64_t j = jb + u;
       vis[u] = (j < j1) && mask_bit(a.mask, mask_row + j);
-      va[u] = vb[u] = vr[u] = make_uint4(0, 0, 0, 0);
+      key[u].clear();
       if (vis[u]) {
         const int64_t row = resolve_row(a, rq.q0, P, kv_base, j);
         if (row >= 0) {
-          const uint4* kv = reinterpret_cast<const uint4*>(a.kv_pool + row * kDRow);
-          va[u] = __ldg(kv + lane);
-          vb[u] = __ldg(kv + 32 + lane);
-          if (lane < 8) vr[u] = __ldg(kv + 64 + lane);
+          key[u].load(a, row, lane);
         } else {  // a row outside the pool excludes the key
           vis[u] = false;
           if (lane == 0) atomicOr(a.status, kStatusBadRow);
@@ -92,9 +146,8 @@ __global__ void __launch_bounds__(32 * kSimtRowsPerCta) split_simt_kernel(SplitA
 #pragma unroll
     for (int u = 0; u < kKeysPerStep; ++u) {
       float fa[8], fb[8], fr[8];
-      bf16x8_to_f32(va[u], fa);
-      bf16x8_to_f32(vb[u], fb);
-      bf16x8_to_f32(vr[u], fr);
+      key[u].latent(fa, fb);
+      key[u].rope(fr);
       float d = 0.f;
 #pragma unroll
       for (int k = 0; k < 8; ++k) d = fmaf(qa[k], fa[k], fmaf(qb[k], fb[k], fmaf(qr[k], fr[k], d)));
@@ -120,8 +173,7 @@ __global__ void __launch_bounds__(32 * kSimtRowsPerCta) split_simt_kernel(SplitA
       }
       const float p = ex2_approx(sv - m);
       float fa[8], fb[8];
-      bf16x8_to_f32(va[u], fa);
-      bf16x8_to_f32(vb[u], fb);
+      key[u].latent(fa, fb);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         acc_a[k] = fmaf(p, fa[k], acc_a[k]);
@@ -147,7 +199,10 @@ __global__ void __launch_bounds__(32 * kSimtRowsPerCta) split_simt_kernel(SplitA
 }  // namespace
 
 cudaError_t launch_split_simt(const SplitArgs& a, dim3 grid, cudaStream_t stream) {
-  split_simt_kernel<<<grid, 32 * kSimtRowsPerCta, 0, stream>>>(a);
+  if (a.kv4_pool)
+    split_simt_kernel<true><<<grid, 32 * kSimtRowsPerCta, 0, stream>>>(a);
+  else
+    split_simt_kernel<false><<<grid, 32 * kSimtRowsPerCta, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
