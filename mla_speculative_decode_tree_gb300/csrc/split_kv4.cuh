@@ -32,7 +32,7 @@
 // Warp roles:
 //   warps 0..4CG-1      softmax (CG column groups of HC query columns).  They
 //                       first turn the CTA's queries into q_hi, q_lo.
-//   warp 4CG            tensor memory, and the one thread that issues MMAs
+//   warp 4CG            tensor memory, and the MMAs
 //   8 warps after it    expansion.  A thread owns quarter q (32 codes) of each
 //                       block of two keys.  It loads the next tile's codes
 //                       into registers as it finishes this tile's blocks, so
@@ -208,6 +208,12 @@ __device__ __forceinline__ void scale_table(uint32_t scale_byte, uint32_t& lo, u
   const uint32_t a = (uint32_t)(4 * kv4_exponent(scale_byte));
   lo = 0x3E3C3800u + a * 0x01010100u;
   hi = 0x46444240u + a * 0x01010101u;
+}
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
 }
 
 // Bounded wait that ignores the abort flag (teardown only).
@@ -429,67 +435,85 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
     if (bad) atomicOr(a.status, kStatusBadRow);
   } else if (warp == Cfg::kMmaWarp) {
     // ============================ MMA issue ==================================
-    if (lane == 0) {
-      constexpr uint32_t idesc_qk = kv4::idesc_f8(kKeys, 2 * NQ, kv4::kE5M2, kv4::kE4M3, false, false);
-      constexpr uint32_t idesc_pv =
-          kv4::idesc_f8(128, Cfg::kConcat ? 2 * NQ : NQ, kv4::kE5M2, kv4::kE4M3, true, true);
-      constexpr uint32_t idesc_lo = kv4::idesc_f8(128, NQ, kv4::kE5M2, kv4::kE5M2, true, true);
-      int used = 0;  // blocks of the ring consumed by S^T so far
-      bool ok = mbar_wait_spin(&ctl.q_full, 0, &ctl.abort, a.status);
-      // S^T += K block blk . Q block blk^T for blocks [blk0, blk1) of the next tile
-      auto qk = [&](int blk0, int blk1) {
+    // The whole warp runs the loop and one elected lane issues: the loop's
+    // values then stay warp-uniform, where an MMA takes its descriptors from.
+    // With a single thread running it every MMA cost ~160 cycles to issue,
+    // against 32 + N/4 (N <= 128) that the tensor core needs for one.
+    constexpr uint32_t idesc_qk = kv4::idesc_f8(kKeys, 2 * NQ, kv4::kE5M2, kv4::kE4M3, false, false);
+    constexpr uint32_t idesc_pv =
+        kv4::idesc_f8(128, Cfg::kConcat ? 2 * NQ : NQ, kv4::kE5M2, kv4::kE4M3, true, true);
+    constexpr uint32_t idesc_lo = kv4::idesc_f8(128, NQ, kv4::kE5M2, kv4::kE5M2, true, true);
+    const bool leader = kv4::elect_one();
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+      const bool got = mbar_wait_spin(bar, parity, &ctl.abort, a.status);
+      const bool all = __all_sync(0xffffffffu, got);
+      tc::fence_after_sync();
+      return all;
+    };
+    const uint64_t desc_k = tc::smem_desc(sRing, 16, 1024, tc::kSwizzle128B);                // A of S^T
+    const uint64_t desc_q = tc::smem_desc(sQ, 16, 1024, tc::kSwizzle128B);                   // B of S^T
+    const uint64_t desc_v = tc::smem_desc(sRing, Cfg::kSlotBytes, 1024, tc::kSwizzle128B);   // A of O^T
+    const uint64_t desc_p = tc::smem_desc(sP, 128, Cfg::kPCore, 0);                          // B of O^T
+    int qk_slot = 0, pv_slot = 0;  // ring positions of the next block of S^T and of O^T
+    uint32_t qk_phase = 0;
+    bool ok = wait(&ctl.q_full, 0);
+    // S^T += K block blk . Q block blk^T for blocks [blk0, blk1) of the next tile
+    auto qk = [&](int blk0, int blk1) {
 #pragma unroll 1
-        for (int blk = blk0; blk < blk1 && ok; ++blk) {
-          const int slot = used % S;
-          if (!(ok = mbar_wait_spin(&ctl.full[slot], (used / S) & 1, &ctl.abort, a.status))) return;
-          tc::fence_after_sync();
-          ++used;
+      for (int blk = blk0; blk < blk1; ++blk) {
+        if (!(ok = wait(&ctl.full[qk_slot], qk_phase))) return;
+        const uint64_t ad = desc_k + (uint32_t)(qk_slot * (Cfg::kSlotBytes >> 4));
+        const uint64_t bd = desc_q + (uint32_t)(blk * (Cfg::kQBlock >> 4));
+        if (leader) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint64_t ad = tc::smem_desc(sRing + slot * Cfg::kSlotBytes + k * 32, 16, 1024, tc::kSwizzle128B);
-            const uint64_t bd = tc::smem_desc(sQ + blk * Cfg::kQBlock + k * 32, 16, 1024, tc::kSwizzle128B);
-            kv4::mma_f8_ss(tmem + Cfg::kColS, ad, bd, idesc_qk, (blk == 0 && k == 0) ? 0u : 1u);
-          }
-          if (blk == kKv4Blocks - 1) tc::mma_commit(&ctl.empty[slot]);  // the RoPE block is done with
+          for (int k = 0; k < 4; ++k)
+            kv4::mma_f8_ss(tmem + Cfg::kColS, ad + 2 * k, bd + 2 * k, idesc_qk, (blk == 0 && k == 0) ? 0u : 1u);
+          if (blk == kKv4Blocks - 1) tc::mma_commit(&ctl.empty[qk_slot]);  // the RoPE block is done with
         }
-      };
-      qk(0, kKv4Blocks);
-      if (ok) tc::mma_commit(&ctl.s_full);
-#pragma unroll 1
-      for (int t = 0; t < nt && ok; ++t) {
-        const bool more = t + 1 < nt;
-        if (more) {
-          ok = mbar_wait_spin(&ctl.s_free, t & 1, &ctl.abort, a.status);
-          tc::fence_after_sync();
-          if (ok) qk(0, Cfg::kAhead);
-          if (ok && Cfg::kAhead == kKv4Blocks) tc::mma_commit(&ctl.s_full);
-        }
-        if (!ok || !(ok = mbar_wait_spin(&ctl.p_full[t & 1], (t >> 1) & 1, &ctl.abort, a.status))) break;
-        tc::fence_after_sync();
-        const uint32_t pbuf = sP + (t % Cfg::kPBufs) * Cfg::kPBytes;
-#pragma unroll 1
-        for (int m = 0; m < 4; ++m) {
-          const int slot = (kKv4Blocks * t + m) % S;
-          const uint32_t d = tmem + m * Cfg::kOStride;
-#pragma unroll
-          for (int k = 0; k < kKeys / 32; ++k) {
-            const uint64_t ad =
-                tc::smem_desc(sRing + slot * Cfg::kSlotBytes + k * 4096, Cfg::kSlotBytes, 1024, tc::kSwizzle128B);
-            const uint32_t acc = (t == 0 && k == 0) ? 0u : 1u;
-            kv4::mma_f8_ss(d, ad, tc::smem_desc(pbuf + k * 512, 128, Cfg::kPCore, 0), idesc_pv, acc);
-            if (!Cfg::kConcat)
-              kv4::mma_f8_ss(d, ad, tc::smem_desc(pbuf + (NQ / 16) * Cfg::kPCore + k * 512, 128, Cfg::kPCore, 0),
-                             idesc_lo, 1u);
-          }
-          tc::mma_commit(&ctl.empty[slot]);
-        }
-        tc::mma_commit(&ctl.pv_done[t & 1]);
-        if (more && Cfg::kAhead < kKv4Blocks) {
-          qk(Cfg::kAhead, kKv4Blocks);
-          if (ok) tc::mma_commit(&ctl.s_full);
+        __syncwarp();
+        if (++qk_slot == S) {
+          qk_slot = 0;
+          qk_phase ^= 1;
         }
       }
-      // Every MMA this thread issued has completed before tensor memory is freed.
+    };
+    if (ok) qk(0, kKv4Blocks);
+    if (ok && leader) tc::mma_commit(&ctl.s_full);
+#pragma unroll 1
+    for (int t = 0; t < nt && ok; ++t) {
+      const bool more = t + 1 < nt;
+      if (more) {
+        if (!(ok = wait(&ctl.s_free, t & 1))) break;
+        qk(0, Cfg::kAhead);
+        if (ok && leader && Cfg::kAhead == kKv4Blocks) tc::mma_commit(&ctl.s_full);
+      }
+      if (!ok || !(ok = wait(&ctl.p_full[t & 1], (t >> 1) & 1))) break;
+      const uint64_t pd = desc_p + (uint32_t)((t % Cfg::kPBufs) * (Cfg::kPBytes >> 4));
+#pragma unroll 1
+      for (int m = 0; m < 4; ++m) {
+        const uint64_t ad = desc_v + (uint32_t)(pv_slot * (Cfg::kSlotBytes >> 4));
+        const uint32_t d = tmem + m * Cfg::kOStride;
+        if (leader) {
+#pragma unroll
+          for (int k = 0; k < kKeys / 32; ++k) {
+            kv4::mma_f8_ss(d, ad + k * (4096 >> 4), pd + k * (512 >> 4), idesc_pv, (t == 0 && k == 0) ? 0u : 1u);
+            if (!Cfg::kConcat)
+              kv4::mma_f8_ss(d, ad + k * (4096 >> 4), pd + ((NQ / 16) * Cfg::kPCore + k * 512 >> 4), idesc_lo, 1u);
+          }
+          tc::mma_commit(&ctl.empty[pv_slot]);
+          if (m == 3) tc::mma_commit(&ctl.pv_done[t & 1]);
+        }
+        __syncwarp();
+        if (++pv_slot == S) pv_slot = 0;
+      }
+      if (++pv_slot == S) pv_slot = 0;  // past the RoPE block
+      if (more && Cfg::kAhead < kKv4Blocks) {
+        qk(Cfg::kAhead, kKv4Blocks);
+        if (ok && leader) tc::mma_commit(&ctl.s_full);
+      }
+    }
+    // Every MMA issued has completed before tensor memory is freed.
+    if (leader) {
       tc::mma_commit(&ctl.mma_idle);
       kv4::wait_teardown(&ctl.mma_idle, 0);
     }
