@@ -66,30 +66,37 @@ constexpr float kPLoScale = 16.f;  // concatenated halves only
 template <int NQ>
 struct Kv4Cfg {
   static_assert(NQ == 16 || NQ == 32 || NQ == 48 || NQ == 64, "row-group sizes built");
-  static constexpr bool kConcat = NQ <= 48;
+  static constexpr bool kConcat = NQ <= 32;
   static constexpr int kKeys = kKeysPerTile;
   static constexpr int kHC = NQ == 64 ? 32 : 16;  // query columns per softmax thread
   static constexpr int kCG = NQ / kHC;
   static constexpr int kSoftmaxWarps = 4 * kCG;
   static constexpr int kSoftmaxThreads = 32 * kSoftmaxWarps;
-  static constexpr int kMmaWarp = kSoftmaxWarps;
-  static constexpr int kExpandWarp = kSoftmaxWarps + 1;
+  static constexpr int kMmaWarp = kSoftmaxWarps;           // first warp of its warpgroup, the others idle
+  static constexpr int kExpandWarp = kSoftmaxWarps + 4;
   static constexpr int kExpandWarps = 8;
   static constexpr int kThreads = 32 * (kExpandWarp + kExpandWarps);
+  // Registers per thread by role.  A block starts with 65536 / kThreads rounded down to what its warps can all
+  // have (128, 96 or 80); the MMA warpgroup gives most of its share up: kCG * softmax + mma + 2 * expand is at
+  // most (kCG + 3) times the start's.
+  static constexpr int kRegsStart = kCG == 1 ? 128 : kCG == 2 ? 96 : 80;
+  static constexpr int kRegsMma = 32;
+  static constexpr int kRegsSoftmax = NQ == 64 ? 120 : kCG == 1 ? 128 : kCG == 2 ? 96 : 80;
+  static constexpr int kRegsExpand = kCG == 1 ? 128 : kCG == 2 && NQ != 64 ? 128 : 104;
+  static_assert(kCG * kRegsSoftmax + kRegsMma + 2 * kRegsExpand <= (kCG + 3) * kRegsStart, "register shares");
   static constexpr int kQBlock = 2 * NQ * 128;  // one 128-channel block of q_hi rows, then q_lo rows
   static constexpr int kQBytes = kKv4Blocks * kQBlock;
   static constexpr int kPCore = kKeys * 16;     // 16 query columns x 128 keys of P^T
   static constexpr int kPBytes = 2 * NQ * kKeys;
   static constexpr int kPBufs = NQ == 64 ? 1 : 2;
   static constexpr int kSlotBytes = kKeys * 128;
-  static constexpr int kSlots = NQ <= 16 ? 12 : NQ <= 32 ? 10 : 8;
-  static constexpr int kAhead = kSlots - kKv4Blocks < kKv4Blocks ? kSlots - kKv4Blocks : kKv4Blocks;
+  static constexpr int kSlots = 8;
   static constexpr int kOffP = kQBytes;
   static constexpr int kOffRing = kOffP + kPBufs * kPBytes;
   static constexpr int kOffCtl = kOffRing + kSlots * kSlotBytes;
   static constexpr int kOStride = kConcat ? 2 * NQ : NQ;  // tensor-memory columns per O^T block
-  static constexpr int kColS = 4 * kOStride;
-  static_assert(kColS + 2 * NQ <= 512, "tensor memory budget");
+  static constexpr int kColS = 4 * kOStride;              // two S^T buffers of 2 NQ columns
+  static_assert(kColS + 4 * NQ <= 512, "tensor memory budget");
   static_assert(kOffRing % 1024 == 0, "slots are 1024-byte aligned");
 };
 
@@ -97,14 +104,14 @@ template <int NQ>
 struct Kv4Ctl {
   uint64_t full[Kv4Cfg<NQ>::kSlots];
   uint64_t empty[Kv4Cfg<NQ>::kSlots];
-  uint64_t q_full, s_full, s_free, p_full[2], pv_done[2], mma_idle;
+  // Two of each, by tile parity: the column groups and the MMAs may be a tile apart.
+  uint64_t s_full[2], s_free[2], p_full[2], pv_done[2];
+  uint64_t q_full, mma_idle;
   uint32_t tmem_base;
   int abort;
-  int flag[2][Kv4Cfg<NQ>::kSoftmaxWarps];
-  int rflag[2];
+  int flag[Kv4Cfg<NQ>::kSoftmaxWarps];
   alignas(16) float cscale[NQ];  // raw score -> base-2 score
-  alignas(16) float mtau[NQ];    // running max + kKv4Tau; -inf before any visible key
-  alignas(16) float muse[NQ];    // running max - kKv4Top, 0 while it is -inf
+  alignas(16) float nmu[NQ];     // -(running max - kKv4Top); +inf before any visible key
   alignas(16) float alpha[NQ];   // rescale factor of the tile; 1/l in the epilogue
   alignas(16) float red[4][NQ];
   uint32_t colmask[kMaxQLen][Kv4Cfg<NQ>::kCG];  // per token: which of a column group's columns are its
@@ -183,6 +190,52 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   return d;
 }
 
+// Pairs of fp32 in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
+      "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+// Barrier of `nthreads` threads that tells each whether any of them said yes.
+__device__ __forceinline__ bool bar_any(int id, int nthreads, bool mine) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+      "barrier.cta.red.or.pred p, %2, %3, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(any)
+      : "r"((uint32_t)mine), "r"(id), "r"(nthreads)
+      : "memory");
+  return any != 0;
+}
+
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int kFrom, int kTo>
+__device__ __forceinline__ void regs_to() {
+  if constexpr (kTo > kFrom) regs_inc<kTo>();
+  if constexpr (kTo < kFrom) regs_dec<kTo>();
+}
+
 __device__ __forceinline__ uint4 ldg_stream(const void* p) {
   uint4 v;
   asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
@@ -215,6 +268,15 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
   return p != 0;
 }
+
+// The ring.  Tile t's blocks pass through slots 4(t%2) .. 4(t%2)+3 in the order
+// RoPE, 0, 1, 2, 3: value block m stays in slot m until O^T is done with it, and
+// the RoPE block, which only S^T reads, uses slot 3 before block 3 does.  So
+// eight slots hold one tile's values and all of the next tile's S^T.
+__host__ __device__ constexpr int block_of(int u) { return u == 0 ? 4 : u - 1; }
+__host__ __device__ constexpr int slot_of(int u) { return u == 0 ? 3 : u - 1; }
+// Parity of the fill of a slot: slots 0..2 are filled every other tile, slot 3 twice then.
+__host__ __device__ constexpr uint32_t slot_use(int t, int u) { return u == 0 ? 0u : u == 4 ? 1u : (t >> 1) & 1u; }
 
 // Bounded wait that ignores the abort flag (teardown only).
 __device__ __forceinline__ void wait_teardown(uint64_t* bar, uint32_t parity) {
@@ -310,17 +372,15 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
       mbar_init(&ctl.full[k], Cfg::kExpandWarps);
       mbar_init(&ctl.empty[k], 1);
     }
+    for (int k = 0; k < 2; ++k) {
+      mbar_init(&ctl.s_full[k], 1);
+      mbar_init(&ctl.s_free[k], kSoftmaxWarps);
+      mbar_init(&ctl.p_full[k], kSoftmaxWarps);
+      mbar_init(&ctl.pv_done[k], 1);
+    }
     mbar_init(&ctl.q_full, kSoftmaxWarps);
-    mbar_init(&ctl.s_full, 1);
-    mbar_init(&ctl.s_free, kSoftmaxWarps);
-    // two: the softmax may finish the next tile before the MMA thread has seen this one's
-    mbar_init(&ctl.p_full[0], kSoftmaxWarps);
-    mbar_init(&ctl.p_full[1], kSoftmaxWarps);
-    mbar_init(&ctl.pv_done[0], 1);
-    mbar_init(&ctl.pv_done[1], 1);
     mbar_init(&ctl.mma_idle, 1);
     ctl.abort = 0;
-    ctl.rflag[0] = ctl.rflag[1] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == Cfg::kMmaWarp) {
@@ -328,10 +388,7 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
     tc::tmem_relinquish();
   }
   if (tid < kSoftmaxThreads) {
-    for (int n = tid; n < NQ; n += kSoftmaxThreads) {
-      ctl.mtau[n] = -INFINITY;
-      ctl.muse[n] = 0.f;
-    }
+    for (int n = tid; n < NQ; n += kSoftmaxThreads) ctl.nmu[n] = INFINITY;
     for (int t = tid; t < ntok * CG; t += kSoftmaxThreads) {
       const int tok = t / CG, h = t % CG;
       uint32_t bits = 0;
@@ -353,26 +410,30 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
     // 8w + lane/4 and 64 + 8w + lane/4, q = lane % 4: a warp's load of one
     // block covers 8 rows x 64 contiguous bytes, and its 16-byte stores reach
     // all 32 banks (8 lanes = 2 keys x 4 chunks of opposite parity).
+    kv4::regs_to<Cfg::kRegsStart, Cfg::kRegsExpand>();
     const int w = warp - Cfg::kExpandWarp;
     const int q = lane & 3;
     const int key0 = 8 * w + (lane >> 2);
     uint32_t bad = 0;
-    // Raw row id of own key h of tile t (-1 past the chunk's end).
-    auto load_id = [&](int t, int h) -> int64_t {
-      const int64_t j = j0 + (int64_t)tile_at(t < nt ? t : 0) * kKeys + key0 + 64 * h;
-      if (t >= nt || j >= j1) return -1;
-      const int32_t r = load_row_id(a, rq.q0, P, kv_base, j);
-      if (r >= 0 && r < a.pool_rows) return r;
-      bad = 1;  // left out: expands to zeros, masked by the softmax
-      return -1;
+    // Raw row ids of the own keys of tile t (-1 past the chunk's end); loaded
+    // a tile before their rows are.
+    int32_t id[2];
+    auto load_ids = [&](int t) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int64_t j = j0 + (int64_t)tile_at(t < nt ? t : 0) * kKeys + key0 + 64 * h;
+        id[h] = (t < nt && j < j1) ? load_row_id(a, rq.q0, P, kv_base, j) : INT32_MIN;
+      }
     };
     const uint8_t* row[2];
     uint4 code[2][kKv4Blocks], scale[2];
-    auto set_rows = [&](int t) {
+    auto set_rows = [&]() {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int64_t r = load_id(t, h);
-        row[h] = r >= 0 ? a.kv4_pool + r * kKv4RowBytes + 16 * q : nullptr;
+        const bool in = id[h] >= 0 && id[h] < a.pool_rows;
+        // a row outside the pool expands to zeros; the softmax leaves it out
+        if (!in && id[h] != INT32_MIN) bad = 1;
+        row[h] = in ? a.kv4_pool + (int64_t)id[h] * kKv4RowBytes + 16 * q : nullptr;
       }
     };
     auto load_block = [&](int m) {
@@ -384,22 +445,25 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
 #pragma unroll
       for (int h = 0; h < 2; ++h) to[h] = row[h] ? kv4::ldg_stream(row[h] + kKv4ScaleOff) : make_uint4(0, 0, 0, 0);
     };
-    set_rows(0);
+    load_ids(0);
+    set_rows();
+    load_ids(1);
     load_scales(scale);
 #pragma unroll
-    for (int m = 0; m < kKv4Blocks; ++m) load_block(m);
-    set_rows(1);
-    int slot = 0;
-    uint32_t phase = 1;  // the first pass over the ring finds every slot empty
+    for (int u = 0; u < kKv4Blocks; ++u) load_block(kv4::block_of(u));
     bool stop = false;
 #pragma unroll 1
     for (int t = 0; t < nt && !stop; ++t) {
       uint4 next_scale[2];
+      set_rows();  // tile t+1
       load_scales(next_scale);
+      load_ids(t + 2);
 #pragma unroll
-      for (int m = 0; m < kKv4Blocks; ++m) {
+      for (int u = 0; u < kKv4Blocks; ++u) {
+        const int m = kv4::block_of(u);
+        const int slot = 4 * (t & 1) + kv4::slot_of(u);
         if (!stop) {
-          const bool got = mbar_wait(&ctl.empty[slot], phase, &ctl.abort, a.status);
+          const bool got = mbar_wait(&ctl.empty[slot], kv4::slot_use(t, u) ^ 1, &ctl.abort, a.status);
           if (!__all_sync(0xffffffffu, got)) stop = true;
         }
         if (!stop) {
@@ -421,159 +485,155 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
           load_block(m);  // tile t+1
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0 && !(a.test_stall && t == 0 && m == 0)) mbar_arrive(&ctl.full[slot]);
-          if (++slot == S) {
-            slot = 0;
-            phase ^= 1;
-          }
+          if (lane == 0 && !(a.test_stall && t == 0 && u == 0)) mbar_arrive(&ctl.full[slot]);
         }
       }
       scale[0] = next_scale[0];
       scale[1] = next_scale[1];
-      set_rows(t + 2);
     }
     if (bad) atomicOr(a.status, kStatusBadRow);
-  } else if (warp == Cfg::kMmaWarp) {
+  } else if (warp >= Cfg::kMmaWarp) {
     // ============================ MMA issue ==================================
     // The whole warp runs the loop and one elected lane issues: the loop's
     // values then stay warp-uniform, where an MMA takes its descriptors from.
     // With a single thread running it every MMA cost ~160 cycles to issue,
     // against 32 + N/4 (N <= 128) that the tensor core needs for one.
-    constexpr uint32_t idesc_qk = kv4::idesc_f8(kKeys, 2 * NQ, kv4::kE5M2, kv4::kE4M3, false, false);
-    constexpr uint32_t idesc_pv =
-        kv4::idesc_f8(128, Cfg::kConcat ? 2 * NQ : NQ, kv4::kE5M2, kv4::kE4M3, true, true);
-    constexpr uint32_t idesc_lo = kv4::idesc_f8(128, NQ, kv4::kE5M2, kv4::kE5M2, true, true);
-    const bool leader = kv4::elect_one();
-    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-      const bool got = mbar_wait_spin(bar, parity, &ctl.abort, a.status);
-      const bool all = __all_sync(0xffffffffu, got);
-      tc::fence_after_sync();
-      return all;
-    };
-    const uint64_t desc_k = tc::smem_desc(sRing, 16, 1024, tc::kSwizzle128B);                // A of S^T
-    const uint64_t desc_q = tc::smem_desc(sQ, 16, 1024, tc::kSwizzle128B);                   // B of S^T
-    const uint64_t desc_v = tc::smem_desc(sRing, Cfg::kSlotBytes, 1024, tc::kSwizzle128B);   // A of O^T
-    const uint64_t desc_p = tc::smem_desc(sP, 128, Cfg::kPCore, 0);                          // B of O^T
-    int qk_slot = 0, pv_slot = 0;  // ring positions of the next block of S^T and of O^T
-    uint32_t qk_phase = 0;
-    bool ok = wait(&ctl.q_full, 0);
-    // S^T += K block blk . Q block blk^T for blocks [blk0, blk1) of the next tile
-    auto qk = [&](int blk0, int blk1) {
+    kv4::regs_to<Cfg::kRegsStart, Cfg::kRegsMma>();
+    if (warp == Cfg::kMmaWarp) {
+      constexpr uint32_t idesc_qk = kv4::idesc_f8(kKeys, 2 * NQ, kv4::kE5M2, kv4::kE4M3, false, false);
+      constexpr uint32_t idesc_pv =
+          kv4::idesc_f8(128, Cfg::kConcat ? 2 * NQ : NQ, kv4::kE5M2, kv4::kE4M3, true, true);
+      constexpr uint32_t idesc_lo = kv4::idesc_f8(128, NQ, kv4::kE5M2, kv4::kE5M2, true, true);
+      const bool leader = kv4::elect_one();
+      auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        const bool got = mbar_wait_spin(bar, parity, &ctl.abort, a.status);
+        const bool all = __all_sync(0xffffffffu, got);
+        tc::fence_after_sync();
+        return all;
+      };
+      const uint64_t desc_k = tc::smem_desc(sRing, 16, 1024, tc::kSwizzle128B);               // A of S^T
+      const uint64_t desc_q = tc::smem_desc(sQ, 16, 1024, tc::kSwizzle128B);                  // B of S^T
+      const uint64_t desc_v = tc::smem_desc(sRing, Cfg::kSlotBytes, 1024, tc::kSwizzle128B);  // A of O^T
+      const uint64_t desc_p = tc::smem_desc(sP, 128, Cfg::kPCore, 0);                         // B of O^T
+      bool ok = wait(&ctl.q_full, 0);
+      // S^T(t) = sum over blocks of K block . Q block^T
+      auto qk = [&](int t) {
+        const uint32_t d = tmem + Cfg::kColS + (t & 1) * 2 * NQ;
 #pragma unroll 1
-      for (int blk = blk0; blk < blk1; ++blk) {
-        if (!(ok = wait(&ctl.full[qk_slot], qk_phase))) return;
-        const uint64_t ad = desc_k + (uint32_t)(qk_slot * (Cfg::kSlotBytes >> 4));
-        const uint64_t bd = desc_q + (uint32_t)(blk * (Cfg::kQBlock >> 4));
-        if (leader) {
+        for (int u = 0; u < kKv4Blocks; ++u) {
+          const int slot = 4 * (t & 1) + kv4::slot_of(u);
+          if (!(ok = wait(&ctl.full[slot], kv4::slot_use(t, u)))) return;
+          const uint64_t ad = desc_k + (uint32_t)(slot * (Cfg::kSlotBytes >> 4));
+          const uint64_t bd = desc_q + (uint32_t)(kv4::block_of(u) * (Cfg::kQBlock >> 4));
+          if (leader) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            kv4::mma_f8_ss(tmem + Cfg::kColS, ad + 2 * k, bd + 2 * k, idesc_qk, (blk == 0 && k == 0) ? 0u : 1u);
-          if (blk == kKv4Blocks - 1) tc::mma_commit(&ctl.empty[qk_slot]);  // the RoPE block is done with
-        }
-        __syncwarp();
-        if (++qk_slot == S) {
-          qk_slot = 0;
-          qk_phase ^= 1;
-        }
-      }
-    };
-    if (ok) qk(0, kKv4Blocks);
-    if (ok && leader) tc::mma_commit(&ctl.s_full);
-#pragma unroll 1
-    for (int t = 0; t < nt && ok; ++t) {
-      const bool more = t + 1 < nt;
-      if (more) {
-        if (!(ok = wait(&ctl.s_free, t & 1))) break;
-        qk(0, Cfg::kAhead);
-        if (ok && leader && Cfg::kAhead == kKv4Blocks) tc::mma_commit(&ctl.s_full);
-      }
-      if (!ok || !(ok = wait(&ctl.p_full[t & 1], (t >> 1) & 1))) break;
-      const uint64_t pd = desc_p + (uint32_t)((t % Cfg::kPBufs) * (Cfg::kPBytes >> 4));
-#pragma unroll 1
-      for (int m = 0; m < 4; ++m) {
-        const uint64_t ad = desc_v + (uint32_t)(pv_slot * (Cfg::kSlotBytes >> 4));
-        const uint32_t d = tmem + m * Cfg::kOStride;
-        if (leader) {
-#pragma unroll
-          for (int k = 0; k < kKeys / 32; ++k) {
-            kv4::mma_f8_ss(d, ad + k * (4096 >> 4), pd + k * (512 >> 4), idesc_pv, (t == 0 && k == 0) ? 0u : 1u);
-            if (!Cfg::kConcat)
-              kv4::mma_f8_ss(d, ad + k * (4096 >> 4), pd + ((NQ / 16) * Cfg::kPCore + k * 512 >> 4), idesc_lo, 1u);
+            for (int k = 0; k < 4; ++k)
+              kv4::mma_f8_ss(d, ad + 2 * k, bd + 2 * k, idesc_qk, (u == 0 && k == 0) ? 0u : 1u);
+            if (u == 0) tc::mma_commit(&ctl.empty[slot]);  // the RoPE block is done with
+            if (u == kKv4Blocks - 1) tc::mma_commit(&ctl.s_full[t & 1]);
           }
-          tc::mma_commit(&ctl.empty[pv_slot]);
-          if (m == 3) tc::mma_commit(&ctl.pv_done[t & 1]);
+          __syncwarp();
         }
-        __syncwarp();
-        if (++pv_slot == S) pv_slot = 0;
+      };
+      if (ok) qk(0);
+#pragma unroll 1
+      for (int t = 0; t < nt && ok; ++t) {
+        if (t + 1 < nt) {
+          if (t >= 1 && !(ok = wait(&ctl.s_free[(t + 1) & 1], ((t - 1) >> 1) & 1))) break;
+          qk(t + 1);
+        }
+        if (!ok || !(ok = wait(&ctl.p_full[t & 1], (t >> 1) & 1))) break;
+        const uint64_t pd = desc_p + (uint32_t)((t % Cfg::kPBufs) * (Cfg::kPBytes >> 4));
+#pragma unroll 1
+        for (int m = 0; m < 4; ++m) {
+          const int slot = 4 * (t & 1) + m;
+          const uint64_t ad = desc_v + (uint32_t)(slot * (Cfg::kSlotBytes >> 4));
+          const uint32_t d = tmem + m * Cfg::kOStride;
+          if (leader) {
+#pragma unroll
+            for (int k = 0; k < kKeys / 32; ++k) {
+              kv4::mma_f8_ss(d, ad + k * (4096 >> 4), pd + k * (512 >> 4), idesc_pv, (t == 0 && k == 0) ? 0u : 1u);
+              if (!Cfg::kConcat)
+                kv4::mma_f8_ss(d, ad + k * (4096 >> 4), pd + (((NQ / 16) * Cfg::kPCore + k * 512) >> 4), idesc_lo, 1u);
+            }
+            tc::mma_commit(&ctl.empty[slot]);
+            if (m == 3) tc::mma_commit(&ctl.pv_done[t & 1]);
+          }
+          __syncwarp();
+        }
       }
-      if (++pv_slot == S) pv_slot = 0;  // past the RoPE block
-      if (more && Cfg::kAhead < kKv4Blocks) {
-        qk(Cfg::kAhead, kKv4Blocks);
-        if (ok && leader) tc::mma_commit(&ctl.s_full);
+      // Every MMA issued has completed before tensor memory is freed.
+      if (leader) {
+        tc::mma_commit(&ctl.mma_idle);
+        kv4::wait_teardown(&ctl.mma_idle, 0);
       }
+      __syncwarp();
     }
-    // Every MMA issued has completed before tensor memory is freed.
-    if (leader) {
-      tc::mma_commit(&ctl.mma_idle);
-      kv4::wait_teardown(&ctl.mma_idle, 0);
-    }
-    __syncwarp();
   } else {
     // ============================ softmax ====================================
-    // Queries: warp w turns rows w, w + warps, ... into q_hi and q_lo.  Lane l
-    // holds channels 8l..8l+7 and 256+8l.., lanes 0-7 also RoPE channels 8l...
+    kv4::regs_to<Cfg::kRegsStart, Cfg::kRegsSoftmax>();
+    // Queries: warp w turns rows w, w + warps, ... into q_hi and q_lo, four at
+    // a time so that their loads overlap.  Lane l holds channels 8l..8l+7 and
+    // 256+8l.., lanes 0-7 also RoPE channels 8l...
+    constexpr int kRowsAtOnce = 4;
+    static_assert(NQ % (kSoftmaxWarps * kRowsAtOnce) == 0, "whole rounds of query rows");
 #pragma unroll 1
-    for (int n = warp; n < NQ; n += kSoftmaxWarps) {
-      uint4 v[3];
-      v[0] = v[1] = v[2] = make_uint4(0, 0, 0, 0);
-      if (n < nrows) {
-        const uint4* qn = reinterpret_cast<const uint4*>(a.q_nope + (grow0 + n) * kDLatent);
-        v[0] = __ldg(qn + lane);
-        v[1] = __ldg(qn + 32 + lane);
-        if (lane < 8) v[2] = __ldg(reinterpret_cast<const uint4*>(a.q_rope + (grow0 + n) * kDRope) + lane);
-      }
-      uint32_t top = 0;  // largest |q| as bits: bf16 magnitudes order as integers
+    for (int base = warp; base < NQ; base += kSoftmaxWarps * kRowsAtOnce) {
+      uint4 v[kRowsAtOnce][3];
 #pragma unroll
-      for (int k = 0; k < 3; ++k) {
-        const uint32_t u[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) top = max(top, max(u[i] & 0x7FFFu, (u[i] >> 16) & 0x7FFFu));
-      }
-      top = __reduce_max_sync(0xffffffffu, top);
-      const int ex = (int)(top >> 7);  // biased exponent of the largest value
-      // 2^x brings it into [128, 256); rows of zeros or denormals use the largest x
-      int x = 7 + 127 - ex;
-      x = x > 126 ? 126 : x;
-      const float up = pow2f(x);
-      if (lane == 0) {
-        // a row with an infinity or a NaN scores NaN
-        const float c = ex == 255 ? NAN : a.scale_log2 * pow2f(-x);
-        ctl.cscale[n] = c;
-      }
-      auto put = [&](int chunk8, const uint4& bits) {  // 8 channels -> 8 bytes of q_hi and of q_lo
-        const uint32_t u[4] = {bits.x, bits.y, bits.z, bits.w};
-        uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float f0 = __uint_as_float(u[i] << 16) * up, f1 = __uint_as_float(u[i] & 0xFFFF0000u) * up;
-          const uint32_t h = kv4::cvt_e4m3x2(f0, f1);
-          const uint32_t hf = kv4::cvt_f16x2_e4m3x2(h);
-          const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hf));
-          const uint32_t l = kv4::cvt_e4m3x2((f0 - back.x) * kQLoScale, (f1 - back.y) * kQLoScale);
-          hi[i >> 1] |= h << (16 * (i & 1));
-          lo[i >> 1] |= l << (16 * (i & 1));
+      for (int i = 0; i < kRowsAtOnce; ++i) {
+        const int n = base + i * kSoftmaxWarps;
+        v[i][0] = v[i][1] = v[i][2] = make_uint4(0, 0, 0, 0);
+        if (n < nrows) {
+          const uint4* qn = reinterpret_cast<const uint4*>(a.q_nope + (grow0 + n) * kDLatent);
+          v[i][0] = __ldg(qn + lane);
+          v[i][1] = __ldg(qn + 32 + lane);
+          if (lane < 8) v[i][2] = __ldg(reinterpret_cast<const uint4*>(a.q_rope + (grow0 + n) * kDRope) + lane);
         }
-        const int blk = chunk8 >> 4, c16 = (chunk8 & 15) >> 1;
-        const uint32_t at = sQ + blk * Cfg::kQBlock + ((c16 ^ (n & 7)) << 4) + 8 * (chunk8 & 1);
-        asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at + n * 128), "r"(hi[0]), "r"(hi[1]) : "memory");
-        asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at + (NQ + n) * 128), "r"(lo[0]), "r"(lo[1]) : "memory");
-      };
-      static_assert(NQ % 8 == 0, "q_lo row n swizzles as q_hi row n");
-      put(lane, v[0]);
-      put(32 + lane, v[1]);
-      if (lane < 8) {
-        put(64 + lane, v[2]);
-        put(72 + lane, v[2]);  // against the RoPE residual codes
+      }
+#pragma unroll
+      for (int i = 0; i < kRowsAtOnce; ++i) {
+        const int n = base + i * kSoftmaxWarps;
+        uint32_t top = 0;  // largest |q| as bits: bf16 magnitudes order as integers
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+          const uint32_t u[4] = {v[i][k].x, v[i][k].y, v[i][k].z, v[i][k].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = max(top, max(u[e] & 0x7FFFu, (u[e] >> 16) & 0x7FFFu));
+        }
+        top = __reduce_max_sync(0xffffffffu, top);
+        const int ex = (int)(top >> 7);  // biased exponent of the largest value
+        // 2^x brings it into [128, 256); rows of zeros or denormals use the largest x
+        int x = 7 + 127 - ex;
+        x = x > 126 ? 126 : x;
+        const float up = pow2f(x);
+        // a row with an infinity or a NaN scores NaN
+        if (lane == 0) ctl.cscale[n] = ex == 255 ? NAN : a.scale_log2 * pow2f(-x);
+        auto put = [&](int chunk8, const uint4& bits) {  // 8 channels -> 8 bytes of q_hi and of q_lo
+          const uint32_t u[4] = {bits.x, bits.y, bits.z, bits.w};
+          uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float f0 = __uint_as_float(u[e] << 16) * up, f1 = __uint_as_float(u[e] & 0xFFFF0000u) * up;
+            const uint32_t h = kv4::cvt_e4m3x2(f0, f1);
+            const uint32_t hf = kv4::cvt_f16x2_e4m3x2(h);
+            const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hf));
+            const uint32_t l = kv4::cvt_e4m3x2((f0 - back.x) * kQLoScale, (f1 - back.y) * kQLoScale);
+            hi[e >> 1] |= h << (16 * (e & 1));
+            lo[e >> 1] |= l << (16 * (e & 1));
+          }
+          const int blk = chunk8 >> 4, c16 = (chunk8 & 15) >> 1;
+          const uint32_t at = sQ + blk * Cfg::kQBlock + ((c16 ^ (n & 7)) << 4) + 8 * (chunk8 & 1);
+          asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at + n * 128), "r"(hi[0]), "r"(hi[1]) : "memory");
+          asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at + (NQ + n) * 128), "r"(lo[0]), "r"(lo[1]) : "memory");
+        };
+        static_assert(NQ % 8 == 0, "q_lo row n swizzles as q_hi row n");
+        put(lane, v[i][0]);
+        put(32 + lane, v[i][1]);
+        if (lane < 8) {
+          put(64 + lane, v[i][2]);
+          put(72 + lane, v[i][2]);  // against the RoPE residual codes
+        }
       }
     }
     fence_proxy_async_smem();
@@ -584,93 +644,134 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
     const int half = warp >> 2;      // column group
     const int j = 32 * quad + lane;  // key within the tile == TMEM lane
     const int c0 = half * HC;        // first query column of this thread
+    const int bar_id = 2 + half;     // the group's four warps (quads) share its columns
     const uint32_t t_lane = tmem + ((uint32_t)(32 * quad) << 16);
     const int64_t mask_base = (int64_t)a.mask_indptr[b] + (int64_t)i0 * L;
+    // Visibility, a tile ahead of its use.  Lane i fetches the 32 mask bits of
+    // tokens i and i + 32 for this warp's 32 keys, and its own key's row id.
+    uint32_t bits[2] = {0, 0};
+    int32_t my_id = -1;
+    auto fetch_vis = [&](int t) {
+      const int64_t k0 = j0 + (int64_t)tile_at(t < nt ? t : 0) * kKeys + 32 * quad;
+      const int64_t n = t < nt ? (j1 - k0 < 32 ? j1 - k0 : 32) : 0;  // keys of this warp inside the chunk
+      my_id = lane < n ? load_row_id(a, rq.q0, P, kv_base, k0 + lane) : -1;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int tok = lane + 32 * i;
+        uint64_t v = 0;
+        if (tok < ntok && n > 0) {
+          const int64_t bit = mask_base + (int64_t)tok * L + k0;
+          const uint8_t* p = a.mask + (bit >> 3);
+          const int last = (int)(((bit & 7) + n - 1) >> 3);  // bytes that hold the n bits
+#pragma unroll
+          for (int k = 0; k < 5; ++k)
+            if (k <= last) v |= (uint64_t)__ldg(p + k) << (8 * k);
+          v >>= bit & 7;
+        }
+        bits[i] = (uint32_t)v;
+      }
+    };
+    fetch_vis(0);
     float acc[HC];  // sum of p over this thread's keys
 #pragma unroll
     for (int k = 0; k < HC; ++k) acc[k] = 0.f;
     bool my_abort = false;
 #pragma unroll 1
     for (int t = 0; t < nt; ++t) {
-      const int64_t key = j0 + (int64_t)tile_at(t) * kKeys + j;
       uint32_t vis = 0;
-      if (key < j1 && resolve_row(a, rq.q0, P, kv_base, key) >= 0) {  // rows outside the pool are left out
-        for (int tl = 0; tl < ntok; ++tl)
-          if (mask_bit(a.mask, mask_base + (int64_t)tl * L + key)) vis |= ctl.colmask[tl][half];
+      for (int tl = 0; tl < ntok; ++tl) {
+        const uint32_t w = __shfl_sync(0xffffffffu, tl < 32 ? bits[0] : bits[1], tl & 31);
+        if ((w >> lane) & 1u) vis |= ctl.colmask[tl][half];
       }
-      float s[HC];
-      if (!my_abort) my_abort = !mbar_wait(&ctl.s_full, t & 1, &ctl.abort, a.status);
+      if (my_id < 0 || my_id >= a.pool_rows) vis = 0;  // past the chunk's end, or a row outside the pool
+      fetch_vis(t + 1);
+      const bool all_vis = __all_sync(0xffffffffu, vis == (uint32_t)((1ull << HC) - 1));
+      const uint32_t t_s = t_lane + Cfg::kColS + (t & 1) * 2 * NQ + c0;
+
+      if (!my_abort) my_abort = !mbar_wait(&ctl.s_full[t & 1], (t >> 1) & 1, &ctl.abort, a.status);
       my_abort = __any_sync(0xffffffffu, my_abort);  // tcgen05.ld below is warp-collective
       tc::fence_after_sync();
-      if (!my_abort) {
+      // x = base-2 score + `add`, -inf where masked
+      float x[HC];
+      auto load_scores = [&](bool with_mu) {
 #pragma unroll
         for (int c = 0; c < HC / 16; ++c) {
           float lo[16];
-          kv4::tmem_ld16(t_lane + Cfg::kColS + c0 + 16 * c, &s[16 * c]);
-          kv4::tmem_ld16(t_lane + Cfg::kColS + NQ + c0 + 16 * c, lo);
+          kv4::tmem_ld16(t_s + 16 * c, &x[16 * c]);
+          kv4::tmem_ld16(t_s + NQ + 16 * c, lo);
+          const float4* cs4 = reinterpret_cast<const float4*>(&ctl.cscale[c0 + 16 * c]);
+          const float4* nm4 = reinterpret_cast<const float4*>(&ctl.nmu[c0 + 16 * c]);
           tc::tmem_wait_ld();
 #pragma unroll
-          for (int k = 0; k < 16; ++k) s[16 * c + k] = fmaf(lo[k], 1.f / kQLoScale, s[16 * c + k]);
+          for (int k4 = 0; k4 < 4; ++k4) {
+            const float4 cs = cs4[k4];
+            const float4 nm = with_mu ? nm4[k4] : make_float4(0.f, 0.f, 0.f, 0.f);
+            const float2 inv = make_float2(1.f / kQLoScale, 1.f / kQLoScale);
+            float* xs = &x[16 * c + 4 * k4];
+            const float* ls = &lo[4 * k4];
+            float2 u = kv4::fma2(make_float2(ls[0], ls[1]), inv, make_float2(xs[0], xs[1]));
+            float2 v = kv4::fma2(make_float2(ls[2], ls[3]), inv, make_float2(xs[2], xs[3]));
+            u = kv4::fma2(u, make_float2(cs.x, cs.y), make_float2(nm.x, nm.y));
+            v = kv4::fma2(v, make_float2(cs.z, cs.w), make_float2(nm.z, nm.w));
+            xs[0] = u.x;
+            xs[1] = u.y;
+            xs[2] = v.x;
+            xs[3] = v.y;
+          }
         }
+        if (!all_vis) {
+#pragma unroll
+          for (int k = 0; k < HC; ++k) x[k] = ((vis >> k) & 1u) ? x[k] : -INFINITY;
+        }
+      };
+      bool need = false;
+      if (!my_abort) {
+        load_scores(true);
+        float top = x[0];
+#pragma unroll
+        for (int k = 1; k < HC; ++k) top = fmaxf(top, x[k]);
+        need = top > kKv4Top + kKv4Tau;
       } else {
 #pragma unroll
-        for (int k = 0; k < HC; ++k) s[k] = 0.f;
+        for (int k = 0; k < HC; ++k) x[k] = -INFINITY;
+      }
+      bool rescale = false;
+      if (kv4::bar_any(bar_id, 128, need || my_abort || ctl.abort)) {
+        // Rare: a score passed the running max by more than kKv4Tau, a column
+        // saw its first key, or a wait gave up.
+        const bool ab = __any_sync(0xffffffffu, my_abort) || ctl.abort;
+        if (lane == 0) ctl.flag[warp] = ab ? 1 : 0;
+        if (!my_abort) load_scores(false);
+        kv4::columns_to_smem<HC, true>(x, &ctl.red[quad][c0], lane);
+        named_bar_sync(bar_id, 128);
+        my_abort = (ctl.flag[4 * half] | ctl.flag[4 * half + 1] | ctl.flag[4 * half + 2] | ctl.flag[4 * half + 3]) != 0;
+        if (my_abort) break;
+        bool raised = false;
+        if (j < HC) {
+          const int n = c0 + j;
+          const float cm = fmaxf(fmaxf(ctl.red[0][n], ctl.red[1][n]), fmaxf(ctl.red[2][n], ctl.red[3][n]));
+          const float old = ctl.nmu[n];
+          float al = 1.f;
+          if (cm + old > kKv4Top + kKv4Tau) {  // old = +inf: the first visible key (cm = -inf gives NaN, no)
+            const float nm = kKv4Top - cm;
+            al = old == INFINITY ? 0.f : ex2_approx(nm - old);
+            ctl.nmu[n] = nm;
+            raised = true;
+          }
+          ctl.alpha[n] = al;
+        }
+        rescale = kv4::bar_any(bar_id, 128, raised) && t > 0;
+#pragma unroll
+        for (int k = 0; k < HC; ++k) {
+          acc[k] *= ctl.alpha[c0 + k];
+          x[k] += ctl.nmu[c0 + k] == INFINITY ? 0.f : ctl.nmu[c0 + k];
+        }
       }
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0 && !my_abort) mbar_arrive(&ctl.s_free);  // S^T may be overwritten
-
-      bool need = false;
-      const float4* mt4 = reinterpret_cast<const float4*>(&ctl.mtau[c0]);
-      const float4* cs4 = reinterpret_cast<const float4*>(&ctl.cscale[c0]);
-#pragma unroll
-      for (int k4 = 0; k4 < HC / 4; ++k4) {
-        const float4 mt = mt4[k4], cs = cs4[k4];
-        const float mtk[4] = {mt.x, mt.y, mt.z, mt.w}, csk[4] = {cs.x, cs.y, cs.z, cs.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int k = 4 * k4 + i;
-          s[k] = ((vis >> k) & 1u) ? s[k] * csk[i] : -INFINITY;
-          need |= s[k] > mtk[i];
-        }
-      }
-      const bool warp_need = __any_sync(0xffffffffu, need);
-      const bool warp_abort = __any_sync(0xffffffffu, my_abort) || ctl.abort;
-      if (lane == 0) ctl.flag[t & 1][warp] = (warp_need ? 1 : 0) | (warp_abort ? 2 : 0);
-      named_bar_sync(1, kSoftmaxThreads);
-      int f = 0;
-#pragma unroll
-      for (int w = 0; w < kSoftmaxWarps; ++w) f |= ctl.flag[t & 1][w];
-      if (tid == 0) ctl.rflag[(t + 1) & 1] = 0;
-      if (f & 2) {
-        my_abort = true;
-        break;
-      }
-      bool rescale = false;
-      if (f & 1) {
-        // Exact column max over the tile's 128 keys; raise the running max
-        // where it passed by more than kKv4Tau.
-        kv4::columns_to_smem<HC, true>(s, &ctl.red[quad][c0], lane);
-        named_bar_sync(1, kSoftmaxThreads);
-        if (tid < NQ) {
-          const float cm = fmaxf(fmaxf(ctl.red[0][tid], ctl.red[1][tid]), fmaxf(ctl.red[2][tid], ctl.red[3][tid]));
-          const float old = ctl.mtau[tid];  // -inf or max + kKv4Tau
-          float al = 1.f;
-          if (cm > old) {
-            al = (old == -INFINITY) ? 0.f : ex2_approx(old - kKv4Tau - cm);
-            ctl.mtau[tid] = cm + kKv4Tau;
-            ctl.muse[tid] = cm - kKv4Top;
-            ctl.rflag[t & 1] = 1;
-          }
-          ctl.alpha[tid] = al;
-        }
-        named_bar_sync(1, kSoftmaxThreads);
-#pragma unroll
-        for (int k = 0; k < HC; ++k) acc[k] *= ctl.alpha[c0 + k];
-        rescale = (t > 0) && ctl.rflag[t & 1];
-      }
+      if (lane == 0) mbar_arrive(&ctl.s_free[t & 1]);  // the S^T buffer may be overwritten
       // P^T(t) overwrites what O^T(t - kPBufs) read; a rescale of O^T needs all of them done.
-      if (t >= Cfg::kPBufs && !my_abort)
+      if (t >= Cfg::kPBufs)
         my_abort = !mbar_wait(&ctl.pv_done[(t - Cfg::kPBufs) & 1], ((t - Cfg::kPBufs) >> 1) & 1, &ctl.abort, a.status);
       if (Cfg::kPBufs > 1 && rescale && !my_abort)
         my_abort = !mbar_wait(&ctl.pv_done[(t - 1) & 1], ((t - 1) >> 1) & 1, &ctl.abort, a.status);
@@ -694,22 +795,22 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
       }
       if (!my_abort) {
         const uint32_t dst = sP + (t % Cfg::kPBufs) * Cfg::kPBytes + j * 16;
-        const float4* mu4 = reinterpret_cast<const float4*>(&ctl.muse[c0]);
 #pragma unroll
         for (int c = 0; c < HC / 16; ++c) {
           uint32_t hi[4], lo[4];
 #pragma unroll
           for (int k4 = 0; k4 < 4; ++k4) {
-            const float4 mu = mu4[4 * c + k4];
             const int k = 16 * c + 4 * k4;
-            const float p0 = ex2_approx(s[k + 0] - mu.x);  // s = -inf (masked) gives 0
-            const float p1 = ex2_approx(s[k + 1] - mu.y);
-            const float p2 = ex2_approx(s[k + 2] - mu.z);
-            const float p3 = ex2_approx(s[k + 3] - mu.w);
-            acc[k + 0] += p0;
-            acc[k + 1] += p1;
-            acc[k + 2] += p2;
-            acc[k + 3] += p3;
+            const float p0 = ex2_approx(x[k + 0]);  // x = -inf (masked) gives 0
+            const float p1 = ex2_approx(x[k + 1]);
+            const float p2 = ex2_approx(x[k + 2]);
+            const float p3 = ex2_approx(x[k + 3]);
+            const float2 a01 = kv4::add2(make_float2(acc[k], acc[k + 1]), make_float2(p0, p1));
+            const float2 a23 = kv4::add2(make_float2(acc[k + 2], acc[k + 3]), make_float2(p2, p3));
+            acc[k + 0] = a01.x;
+            acc[k + 1] = a01.y;
+            acc[k + 2] = a23.x;
+            acc[k + 3] = a23.y;
             // through halves: 11 bits, far finer than the 8 to 9 kept
             const uint32_t h01 = kv4::cvt_f16x2(p0, p1), h23 = kv4::cvt_f16x2(p2, p3);
             const uint32_t u01 = kv4::cvt_e4m3x2_f16x2(h01), u23 = kv4::cvt_e4m3x2_f16x2(h23);
@@ -735,23 +836,20 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
     }
 
     // ---- epilogue: l, LSE, O = O^T / l ----------------------------------------
+    named_bar_sync(bar_id, 128);  // (a raise of the last tile has read red)
     kv4::columns_to_smem<HC, false>(acc, &ctl.red[quad][c0], lane);
     if (!my_abort) my_abort = !mbar_wait(&ctl.pv_done[(nt - 1) & 1], ((nt - 1) >> 1) & 1, &ctl.abort, a.status);
     tc::fence_after_sync();
-    const bool wa = __any_sync(0xffffffffu, my_abort) || ctl.abort;
-    if (lane == 0) ctl.flag[nt & 1][warp] = wa ? 2 : 0;
-    named_bar_sync(1, kSoftmaxThreads);
-    int f = 0;
-#pragma unroll
-    for (int w = 0; w < kSoftmaxWarps; ++w) f |= ctl.flag[nt & 1][w];
-    if (tid < NQ) {
-      const float l = (ctl.red[0][tid] + ctl.red[1][tid]) + (ctl.red[2][tid] + ctl.red[3][tid]);
-      ctl.alpha[tid] = l == 0.f ? 0.f : 1.f / l;
-      if (!(f & 2) && tid < nrows)
-        lse_out[tid] = l == 0.f ? -INFINITY : (ctl.muse[tid] + __log2f(l)) * 0.69314718055994530942f;
+    const bool failed = kv4::bar_any(bar_id, 128, my_abort || ctl.abort);
+    if (j < HC) {
+      const int n = c0 + j;
+      const float l = (ctl.red[0][n] + ctl.red[1][n]) + (ctl.red[2][n] + ctl.red[3][n]);
+      ctl.alpha[n] = l == 0.f ? 0.f : 1.f / l;
+      if (!failed && n < nrows)
+        lse_out[n] = l == 0.f ? -INFINITY : (__log2f(l) - ctl.nmu[n]) * 0.69314718055994530942f;
     }
-    named_bar_sync(1, kSoftmaxThreads);
-    if (!(f & 2)) {
+    named_bar_sync(bar_id, 128);
+    if (!failed) {
       // Thread (quad, lane) holds latent column 128m + j of rows c0..c0+HC: a
       // warp store writes 128 contiguous bytes of one row.  Rows with nothing
       // visible are not written (their LSE is -inf).
