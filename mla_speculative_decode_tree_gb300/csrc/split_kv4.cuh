@@ -72,7 +72,10 @@ struct Kv4Cfg {
   static constexpr int kCG = NQ / kHC;
   static constexpr int kSoftmaxWarps = 4 * kCG;
   static constexpr int kSoftmaxThreads = 32 * kSoftmaxWarps;
-  static constexpr int kMmaWarp = kSoftmaxWarps;           // first warp of its warpgroup, the others idle
+  static constexpr int kMmaWarp = kSoftmaxWarps;           // first warp of its warpgroup
+  static constexpr int kIndexWarp = kSoftmaxWarps + 1;     // the other three
+  static constexpr int kIndexWarps = 3;
+  static constexpr int kIndexRing = 4;                     // tiles of row ids and mask words in flight
   static constexpr int kExpandWarp = kSoftmaxWarps + 4;
   static constexpr int kExpandWarps = 8;
   static constexpr int kThreads = 32 * (kExpandWarp + kExpandWarps);
@@ -80,17 +83,26 @@ struct Kv4Cfg {
   // have (128, 96 or 80); the MMA warpgroup gives most of its share up: kCG * softmax + mma + 2 * expand is at
   // most (kCG + 3) times the start's.
   static constexpr int kRegsStart = kCG == 1 ? 128 : kCG == 2 ? 96 : 80;
-  static constexpr int kRegsMma = 32;
+  static constexpr int kRegsMma = 48;
   static constexpr int kRegsSoftmax = NQ == 64 ? 120 : kCG == 1 ? 128 : kCG == 2 ? 96 : 80;
-  static constexpr int kRegsExpand = kCG == 1 ? 128 : kCG == 2 && NQ != 64 ? 128 : 104;
+  static constexpr int kRegsExpand = kCG == 1 ? 128 : kCG == 2 && NQ != 64 ? 120 : 96;
   static_assert(kCG * kRegsSoftmax + kRegsMma + 2 * kRegsExpand <= (kCG + 3) * kRegsStart, "register shares");
   static constexpr int kQBlock = 2 * NQ * 128;  // one 128-channel block of q_hi rows, then q_lo rows
-  static constexpr int kQBytes = kKv4Blocks * kQBlock;
+  static constexpr int kQRope = 2 * NQ * 64;    // RoPE channels, once: the residual codes meet the same bytes
+  static constexpr int kQBytes = 4 * kQBlock + kQRope;
   static constexpr int kPCore = kKeys * 16;     // 16 query columns x 128 keys of P^T
   static constexpr int kPBytes = 2 * NQ * kKeys;
-  static constexpr int kPBufs = NQ == 64 ? 1 : 2;
+  static constexpr int kPBufs = NQ >= 48 ? 1 : 2;
   static constexpr int kSlotBytes = kKeys * 128;
-  static constexpr int kSlots = 8;
+  static constexpr bool kRopeSlot = NQ <= 48;
+  static constexpr int kSlots = kRopeSlot ? 9 : 8;
+  // Slot of the u-th block of tile t, and the parity of its fill there.
+  __host__ __device__ static constexpr int slot(int t, int u) {
+    return u < 3 ? 4 * (t & 1) + u : u == 3 && kRopeSlot ? 8 : 4 * (t & 1) + 3;
+  }
+  __host__ __device__ static constexpr uint32_t fill(int t, int u) {
+    return u < 3 ? (t >> 1) & 1u : kRopeSlot ? (u == 3 ? t & 1u : (t >> 1) & 1u) : (u == 3 ? 0u : 1u);
+  }
   static constexpr int kOffP = kQBytes;
   static constexpr int kOffRing = kOffP + kPBufs * kPBytes;
   static constexpr int kOffCtl = kOffRing + kSlots * kSlotBytes;
@@ -106,6 +118,7 @@ struct Kv4Ctl {
   uint64_t empty[Kv4Cfg<NQ>::kSlots];
   // Two of each, by tile parity: the column groups and the MMAs may be a tile apart.
   uint64_t s_full[2], s_free[2], p_full[2], pv_done[2];
+  uint64_t idx_full[Kv4Cfg<NQ>::kIndexRing], idx_empty[Kv4Cfg<NQ>::kIndexRing];
   uint64_t q_full, mma_idle;
   uint32_t tmem_base;
   int abort;
@@ -115,6 +128,9 @@ struct Kv4Ctl {
   alignas(16) float alpha[NQ];   // rescale factor of the tile; 1/l in the epilogue
   alignas(16) float red[4][NQ];
   uint32_t colmask[kMaxQLen][Kv4Cfg<NQ>::kCG];  // per token: which of a column group's columns are its
+  int32_t row_id[Kv4Cfg<NQ>::kIndexRing][kKeysPerTile];      // pool row of each key, 0 where there is none
+  uint32_t see[Kv4Cfg<NQ>::kIndexRing][4][kMaxQLen];         // per 32 keys and token: which keys it sees
+  uint32_t see_all[Kv4Cfg<NQ>::kIndexRing][4];               // every token sees all 32
 };
 
 template <int NQ>
@@ -131,6 +147,7 @@ __host__ __device__ constexpr uint32_t idesc_f8(int M, int N, int afmt, int bfmt
          ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 constexpr int kE4M3 = 0, kE5M2 = 1;
+constexpr uint64_t kSwizzle64B = 4;
 
 __device__ __forceinline__ void mma_f8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                           uint32_t accumulate) {
@@ -210,6 +227,12 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return d;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // Barrier of `nthreads` threads that tells each whether any of them said yes.
 __device__ __forceinline__ bool bar_any(int id, int nthreads, bool mine) {
   uint32_t any;
@@ -269,14 +292,11 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-// The ring.  Tile t's blocks pass through slots 4(t%2) .. 4(t%2)+3 in the order
-// RoPE, 0, 1, 2, 3: value block m stays in slot m until O^T is done with it, and
-// the RoPE block, which only S^T reads, uses slot 3 before block 3 does.  So
-// eight slots hold one tile's values and all of the next tile's S^T.
-__host__ __device__ constexpr int block_of(int u) { return u == 0 ? 4 : u - 1; }
-__host__ __device__ constexpr int slot_of(int u) { return u == 0 ? 3 : u - 1; }
-// Parity of the fill of a slot: slots 0..2 are filled every other tile, slot 3 twice then.
-__host__ __device__ constexpr uint32_t slot_use(int t, int u) { return u == 0 ? 0u : u == 4 ? 1u : (t >> 1) & 1u; }
+// Slots.  Tile t's value blocks 0..3 stay in slots 4(t%2) .. 4(t%2)+3 until O^T
+// is done with them.  The RoPE block, which only S^T reads, has slot 8 where
+// shared memory has room for nine; else it passes through slot 3 of the tile's
+// set before block 3 does.  Order of expansion and of S^T: u = 0..4.
+__host__ __device__ constexpr int block_of(int u) { return u < 3 ? u : u == 3 ? 4 : 3; }
 
 // Bounded wait that ignores the abort flag (teardown only).
 __device__ __forceinline__ void wait_teardown(uint64_t* bar, uint32_t parity) {
@@ -378,6 +398,10 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
       mbar_init(&ctl.p_full[k], kSoftmaxWarps);
       mbar_init(&ctl.pv_done[k], 1);
     }
+    for (int k = 0; k < Cfg::kIndexRing; ++k) {
+      mbar_init(&ctl.idx_full[k], 1);
+      mbar_init(&ctl.idx_empty[k], kSoftmaxWarps + Cfg::kExpandWarps);
+    }
     mbar_init(&ctl.q_full, kSoftmaxWarps);
     mbar_init(&ctl.mma_idle, 1);
     ctl.abort = 0;
@@ -414,56 +438,48 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
     const int w = warp - Cfg::kExpandWarp;
     const int q = lane & 3;
     const int key0 = 8 * w + (lane >> 2);
-    uint32_t bad = 0;
-    // Raw row ids of the own keys of tile t (-1 past the chunk's end); loaded
-    // a tile before their rows are.
-    int32_t id[2];
-    auto load_ids = [&](int t) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int64_t j = j0 + (int64_t)tile_at(t < nt ? t : 0) * kKeys + key0 + 64 * h;
-        id[h] = (t < nt && j < j1) ? load_row_id(a, rq.q0, P, kv_base, j) : INT32_MIN;
-      }
-    };
+    const uint32_t off0 = key0 * 128 + (((2 * q) ^ (key0 & 7)) << 4);
+    const uint32_t off1 = key0 * 128 + (((2 * q + 1) ^ (key0 & 7)) << 4);
     const uint8_t* row[2];
     uint4 code[2][kKv4Blocks], scale[2];
-    auto set_rows = [&]() {
+    bool stop = false;
+    // Rows of tile t.  (A key without one reads row 0: its weight is 0, and a
+    // 4-bit value is finite whatever the bytes.)
+    auto set_rows = [&](int t) {
+      const int r = t % Cfg::kIndexRing;
+      const bool got = mbar_wait(&ctl.idx_full[r], (t / Cfg::kIndexRing) & 1, &ctl.abort, a.status);
+      stop = !__all_sync(0xffffffffu, got);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const bool in = id[h] >= 0 && id[h] < a.pool_rows;
-        // a row outside the pool expands to zeros; the softmax leaves it out
-        if (!in && id[h] != INT32_MIN) bad = 1;
-        row[h] = in ? a.kv4_pool + (int64_t)id[h] * kKv4RowBytes + 16 * q : nullptr;
-      }
+      for (int h = 0; h < 2; ++h)
+        row[h] = a.kv4_pool + (int64_t)(stop ? 0 : ctl.row_id[r][key0 + 64 * h]) * kKv4RowBytes + 16 * q;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl.idx_empty[r]);
     };
     auto load_block = [&](int m) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        code[h][m] = row[h] ? kv4::ldg_stream(row[h] + 64 * m) : make_uint4(0, 0, 0, 0);
+      for (int h = 0; h < 2; ++h) code[h][m] = kv4::ldg_stream(row[h] + 64 * m);
     };
     auto load_scales = [&](uint4 (&to)[2]) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) to[h] = row[h] ? kv4::ldg_stream(row[h] + kKv4ScaleOff) : make_uint4(0, 0, 0, 0);
+      for (int h = 0; h < 2; ++h) to[h] = kv4::ldg_stream(row[h] + kKv4ScaleOff);
     };
-    load_ids(0);
-    set_rows();
-    load_ids(1);
+    set_rows(0);
     load_scales(scale);
 #pragma unroll
     for (int u = 0; u < kKv4Blocks; ++u) load_block(kv4::block_of(u));
-    bool stop = false;
 #pragma unroll 1
     for (int t = 0; t < nt && !stop; ++t) {
-      uint4 next_scale[2];
-      set_rows();  // tile t+1
-      load_scales(next_scale);
-      load_ids(t + 2);
+      const bool more = t + 1 < nt;
+      uint4 next_scale[2] = {scale[0], scale[1]};
+      if (more) {
+        set_rows(t + 1);
+        load_scales(next_scale);
+      }
 #pragma unroll
       for (int u = 0; u < kKv4Blocks; ++u) {
-        const int m = kv4::block_of(u);
-        const int slot = 4 * (t & 1) + kv4::slot_of(u);
+        const int m = kv4::block_of(u), sl = Cfg::slot(t, u);
         if (!stop) {
-          const bool got = mbar_wait(&ctl.empty[slot], kv4::slot_use(t, u) ^ 1, &ctl.abort, a.status);
+          const bool got = mbar_wait(&ctl.empty[sl], Cfg::fill(t, u) ^ 1, &ctl.abort, a.status);
           if (!__all_sync(0xffffffffu, got)) stop = true;
         }
         if (!stop) {
@@ -477,21 +493,19 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
             kv4::expand8(code[h][m].y, lo[0], hi[0], o[2], o[3]);
             kv4::expand8(code[h][m].z, lo[1], hi[1], o[4], o[5]);
             kv4::expand8(code[h][m].w, lo[1], hi[1], o[6], o[7]);
-            const int key = key0 + 64 * h;
-            const uint32_t dst = sRing + slot * Cfg::kSlotBytes + key * 128;
-            kv4::sts128(dst + (((2 * q) ^ (key & 7)) << 4), o[0], o[1], o[2], o[3]);
-            kv4::sts128(dst + (((2 * q + 1) ^ (key & 7)) << 4), o[4], o[5], o[6], o[7]);
+            const uint32_t dst = sRing + sl * Cfg::kSlotBytes + h * 64 * 128;
+            kv4::sts128(dst + off0, o[0], o[1], o[2], o[3]);
+            kv4::sts128(dst + off1, o[4], o[5], o[6], o[7]);
           }
-          load_block(m);  // tile t+1
+          if (more) load_block(m);  // tile t+1
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0 && !(a.test_stall && t == 0 && u == 0)) mbar_arrive(&ctl.full[slot]);
+          if (lane == 0 && !(a.test_stall && t == 0 && u == 0)) mbar_arrive(&ctl.full[sl]);
         }
       }
       scale[0] = next_scale[0];
       scale[1] = next_scale[1];
     }
-    if (bad) atomicOr(a.status, kStatusBadRow);
   } else if (warp >= Cfg::kMmaWarp) {
     // ============================ MMA issue ==================================
     // The whole warp runs the loop and one elected lane issues: the loop's
@@ -511,56 +525,82 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
         tc::fence_after_sync();
         return all;
       };
+      auto all_ready = [&](uint64_t* bar, uint32_t parity) -> bool {
+        const bool r = __all_sync(0xffffffffu, mbar_test_wait(bar, parity));
+        if (r) tc::fence_after_sync();
+        return r;
+      };
       const uint64_t desc_k = tc::smem_desc(sRing, 16, 1024, tc::kSwizzle128B);               // A of S^T
       const uint64_t desc_q = tc::smem_desc(sQ, 16, 1024, tc::kSwizzle128B);                  // B of S^T
+      const uint64_t desc_r = tc::smem_desc(sQ + 4 * Cfg::kQBlock, 16, 512, kv4::kSwizzle64B);  // its RoPE part
       const uint64_t desc_v = tc::smem_desc(sRing, Cfg::kSlotBytes, 1024, tc::kSwizzle128B);  // A of O^T
       const uint64_t desc_p = tc::smem_desc(sP, 128, Cfg::kPCore, 0);                         // B of O^T
       bool ok = wait(&ctl.q_full, 0);
-      // S^T(t) = sum over blocks of K block . Q block^T
-      auto qk = [&](int t) {
-        const uint32_t d = tmem + Cfg::kColS + (t & 1) * 2 * NQ;
+      // Two products compete for the tensor core: block u of S^T(tq), ready when
+      // it is expanded and its S^T buffer is read out, and O^T(tp), ready when
+      // P^T(tp) is written.  O^T goes first -- it frees the slots the expansion
+      // waits for -- and S^T runs up to one tile ahead of it.
+      int tq = 0, u = 0, tp = 0;
+      uint64_t t_idle = global_timer_ns();
+      uint32_t polls = 0;
 #pragma unroll 1
-        for (int u = 0; u < kKv4Blocks; ++u) {
-          const int slot = 4 * (t & 1) + kv4::slot_of(u);
-          if (!(ok = wait(&ctl.full[slot], kv4::slot_use(t, u)))) return;
+      while (ok && tp < nt) {
+        if (tp < tq && all_ready(&ctl.p_full[tp & 1], (tp >> 1) & 1)) {
+          const uint64_t pd = desc_p + (uint32_t)((tp % Cfg::kPBufs) * (Cfg::kPBytes >> 4));
+#pragma unroll 1
+          for (int m = 0; m < 4; ++m) {
+            const int slot = 4 * (tp & 1) + m;
+            const uint64_t ad = desc_v + (uint32_t)(slot * (Cfg::kSlotBytes >> 4));
+            const uint32_t d = tmem + m * Cfg::kOStride;
+            if (leader) {
+#pragma unroll
+              for (int k = 0; k < kKeys / 32; ++k) {
+                kv4::mma_f8_ss(d, ad + k * (4096 >> 4), pd + k * (512 >> 4), idesc_pv, (tp == 0 && k == 0) ? 0u : 1u);
+                if (!Cfg::kConcat)
+                  kv4::mma_f8_ss(d, ad + k * (4096 >> 4), pd + (((NQ / 16) * Cfg::kPCore + k * 512) >> 4), idesc_lo,
+                                 1u);
+              }
+              tc::mma_commit(&ctl.empty[slot]);
+              if (m == 3) tc::mma_commit(&ctl.pv_done[tp & 1]);
+            }
+            __syncwarp();
+          }
+          ++tp;
+        } else if (tq < nt && tq <= tp + 1 &&
+                   (u > 0 || tq < 2 || all_ready(&ctl.s_free[tq & 1], ((tq - 2) >> 1) & 1)) &&
+                   all_ready(&ctl.full[Cfg::slot(tq, u)], Cfg::fill(tq, u))) {
+          const int slot = Cfg::slot(tq, u);
+          const uint32_t d = tmem + Cfg::kColS + (tq & 1) * 2 * NQ;
           const uint64_t ad = desc_k + (uint32_t)(slot * (Cfg::kSlotBytes >> 4));
-          const uint64_t bd = desc_q + (uint32_t)(kv4::block_of(u) * (Cfg::kQBlock >> 4));
-          if (leader) {
+          const int blk = kv4::block_of(u);
+          if (leader && blk == kKv4Blocks - 1) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) kv4::mma_f8_ss(d, ad + 2 * k, desc_r + 2 * (k & 1), idesc_qk, 1u);
+            tc::mma_commit(&ctl.empty[slot]);  // only S^T reads the RoPE block
+          } else if (leader) {
+            const uint64_t bd = desc_q + (uint32_t)(blk * (Cfg::kQBlock >> 4));
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               kv4::mma_f8_ss(d, ad + 2 * k, bd + 2 * k, idesc_qk, (u == 0 && k == 0) ? 0u : 1u);
-            if (u == 0) tc::mma_commit(&ctl.empty[slot]);  // the RoPE block is done with
-            if (u == kKv4Blocks - 1) tc::mma_commit(&ctl.s_full[t & 1]);
+            if (u == kKv4Blocks - 1) tc::mma_commit(&ctl.s_full[tq & 1]);
           }
           __syncwarp();
-        }
-      };
-      if (ok) qk(0);
-#pragma unroll 1
-      for (int t = 0; t < nt && ok; ++t) {
-        if (t + 1 < nt) {
-          if (t >= 1 && !(ok = wait(&ctl.s_free[(t + 1) & 1], ((t - 1) >> 1) & 1))) break;
-          qk(t + 1);
-        }
-        if (!ok || !(ok = wait(&ctl.p_full[t & 1], (t >> 1) & 1))) break;
-        const uint64_t pd = desc_p + (uint32_t)((t % Cfg::kPBufs) * (Cfg::kPBytes >> 4));
-#pragma unroll 1
-        for (int m = 0; m < 4; ++m) {
-          const int slot = 4 * (t & 1) + m;
-          const uint64_t ad = desc_v + (uint32_t)(slot * (Cfg::kSlotBytes >> 4));
-          const uint32_t d = tmem + m * Cfg::kOStride;
-          if (leader) {
-#pragma unroll
-            for (int k = 0; k < kKeys / 32; ++k) {
-              kv4::mma_f8_ss(d, ad + k * (4096 >> 4), pd + k * (512 >> 4), idesc_pv, (t == 0 && k == 0) ? 0u : 1u);
-              if (!Cfg::kConcat)
-                kv4::mma_f8_ss(d, ad + k * (4096 >> 4), pd + (((NQ / 16) * Cfg::kPCore + k * 512) >> 4), idesc_lo, 1u);
+          if (++u == kKv4Blocks) {
+            u = 0;
+            ++tq;
+          }
+        } else {  // nothing ready: the bounds of mbar_wait
+          if ((++polls & 255u) == 0) {
+            const bool late = __any_sync(0xffffffffu, global_timer_ns() - t_idle > kWaitLimitNs);
+            if (late && leader) {
+              *(volatile int*)&ctl.abort = 1;
+              atomicOr(a.status, kStatusTimeout);
             }
-            tc::mma_commit(&ctl.empty[slot]);
-            if (m == 3) tc::mma_commit(&ctl.pv_done[t & 1]);
+            ok = __all_sync(0xffffffffu, !late && !*(volatile int*)&ctl.abort);
           }
-          __syncwarp();
+          continue;
         }
+        t_idle = global_timer_ns();
       }
       // Every MMA issued has completed before tensor memory is freed.
       if (leader) {
@@ -568,6 +608,80 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
         kv4::wait_teardown(&ctl.mma_idle, 0);
       }
       __syncwarp();
+    } else {
+      // ========================= row ids and mask ============================
+      // Warp i takes tiles i, i + 3, ...: the pool rows of the tile's keys, and
+      // per 32 keys and token the mask's bits, less keys that have no row.
+      uint32_t bad = 0;
+      const int n_keys = (int)(j1 - j0);
+      const int pre = (int)(P - j0 < n_keys ? (P > j0 ? P - j0 : 0) : n_keys);  // keys of the chunk in the prefix
+      const int32_t* pre_ids = a.kv_indices + kv_base + j0;
+      const int32_t* new_ids = a.out_cache_loc + rq.q0 + (j0 - P);
+      const int64_t block0 = (int64_t)a.mask_indptr[b];
+      const uint8_t* mask_lo = a.mask + (block0 >> 3);  // the request's mask block, in whole bytes
+      const uint8_t* mask_hi = a.mask + ((block0 + (int64_t)rq.n * L + 7) >> 3);
+      // An aligned word of the mask; bytes outside the block read as 0.
+      auto mask_word = [&](const uint8_t* p) -> uint32_t {
+        if (p >= mask_lo && p + 4 <= mask_hi) return __ldg(reinterpret_cast<const uint32_t*>(p));
+        uint32_t v = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (p + k >= mask_lo && p + k < mask_hi) v |= (uint32_t)__ldg(p + k) << (8 * k);
+        return v;
+      };
+#pragma unroll 1
+      for (int t = warp - Cfg::kIndexWarp; t < nt; t += Cfg::kIndexWarps) {
+        const int r = t % Cfg::kIndexRing;
+        const int key0 = tile_at(t) * kKeys;
+        int32_t id[4];
+        uint32_t w[5];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int key = key0 + 32 * k + lane;
+          id[k] = key < pre ? __ldg(pre_ids + key) : key < n_keys ? __ldg(new_ids + key) : -1;
+        }
+        const int64_t bit0 = block0 + (int64_t)i0 * L + j0 + key0;  // the first token's, key 0 of the tile
+        auto load_mask = [&](int tok) {
+          const uintptr_t p = reinterpret_cast<uintptr_t>(a.mask + ((bit0 + (int64_t)tok * L) >> 3)) & ~(uintptr_t)3;
+#pragma unroll
+          for (int k = 0; k < 5; ++k) w[k] = tok < ntok ? mask_word(reinterpret_cast<const uint8_t*>(p) + 4 * k) : 0u;
+        };
+        load_mask(lane);
+        const bool got = mbar_wait(&ctl.idx_empty[r], ((t / Cfg::kIndexRing) & 1) ^ 1, &ctl.abort, a.status);
+        if (!__all_sync(0xffffffffu, got)) break;
+        uint32_t valid[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const bool in = id[k] >= 0 && id[k] < a.pool_rows;
+          if (!in && key0 + 32 * k + lane < n_keys) bad = 1;  // left out, and reported
+          valid[k] = __ballot_sync(0xffffffffu, in);
+          ctl.row_id[r][32 * k + lane] = in ? id[k] : 0;
+        }
+        bool all[4] = {true, true, true, true};
+#pragma unroll 1
+        for (int tok = lane;; tok += 32) {
+          const uintptr_t p = reinterpret_cast<uintptr_t>(a.mask + ((bit0 + (int64_t)tok * L) >> 3));
+          const int shift = 8 * (int)(p & 3) + (int)((bit0 + (int64_t)tok * L) & 7);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t v = __funnelshift_r(w[k], w[k + 1], shift) & valid[k];
+            if (tok < ntok) {
+              ctl.see[r][k][tok] = v;
+              all[k] = all[k] && v == 0xffffffffu;
+            }
+          }
+          if (tok - lane + 32 >= ntok) break;
+          load_mask(tok + 32);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const bool every = __all_sync(0xffffffffu, all[k]);
+          if (lane == 0) ctl.see_all[r][k] = every;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl.idx_full[r]);
+      }
+      if (bad) atomicOr(a.status, kStatusBadRow);
     }
   } else {
     // ============================ softmax ====================================
@@ -609,7 +723,8 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
         const float up = pow2f(x);
         // a row with an infinity or a NaN scores NaN
         if (lane == 0) ctl.cscale[n] = ex == 255 ? NAN : a.scale_log2 * pow2f(-x);
-        auto put = [&](int chunk8, const uint4& bits) {  // 8 channels -> 8 bytes of q_hi and of q_lo
+        // 8 channels -> 8 bytes of q_hi (at `at`) and of q_lo (`lo_off` further on)
+        auto put = [&](uint32_t at, uint32_t lo_off, const uint4& bits) {
           const uint32_t u[4] = {bits.x, bits.y, bits.z, bits.w};
           uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
 #pragma unroll
@@ -622,18 +737,16 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
             hi[e >> 1] |= h << (16 * (e & 1));
             lo[e >> 1] |= l << (16 * (e & 1));
           }
-          const int blk = chunk8 >> 4, c16 = (chunk8 & 15) >> 1;
-          const uint32_t at = sQ + blk * Cfg::kQBlock + ((c16 ^ (n & 7)) << 4) + 8 * (chunk8 & 1);
-          asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at + n * 128), "r"(hi[0]), "r"(hi[1]) : "memory");
-          asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at + (NQ + n) * 128), "r"(lo[0]), "r"(lo[1]) : "memory");
+          asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at), "r"(hi[0]), "r"(hi[1]) : "memory");
+          asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at + lo_off), "r"(lo[0]), "r"(lo[1]) : "memory");
         };
         static_assert(NQ % 8 == 0, "q_lo row n swizzles as q_hi row n");
-        put(lane, v[i][0]);
-        put(32 + lane, v[i][1]);
-        if (lane < 8) {
-          put(64 + lane, v[i][2]);
-          put(72 + lane, v[i][2]);  // against the RoPE residual codes
-        }
+        const uint32_t in_block = (((lane & 15) >> 1) ^ (n & 7)) << 4;  // 16-byte chunk, 128-byte swizzle
+        const uint32_t at = sQ + (lane >> 4) * Cfg::kQBlock + n * 128 + in_block + 8 * (lane & 1);
+        put(at, NQ * 128, v[i][0]);
+        put(at + 2 * Cfg::kQBlock, NQ * 128, v[i][1]);
+        if (lane < 8)  // RoPE: rows of 64 bytes, 64-byte swizzle
+          put(sQ + 4 * Cfg::kQBlock + n * 64 + (((lane >> 1) ^ ((n >> 1) & 3)) << 4) + 8 * (lane & 1), NQ * 64, v[i][2]);
       }
     }
     fence_proxy_async_smem();
@@ -646,46 +759,24 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
     const int c0 = half * HC;        // first query column of this thread
     const int bar_id = 2 + half;     // the group's four warps (quads) share its columns
     const uint32_t t_lane = tmem + ((uint32_t)(32 * quad) << 16);
-    const int64_t mask_base = (int64_t)a.mask_indptr[b] + (int64_t)i0 * L;
-    // Visibility, a tile ahead of its use.  Lane i fetches the 32 mask bits of
-    // tokens i and i + 32 for this warp's 32 keys, and its own key's row id.
-    uint32_t bits[2] = {0, 0};
-    int32_t my_id = -1;
-    auto fetch_vis = [&](int t) {
-      const int64_t k0 = j0 + (int64_t)tile_at(t < nt ? t : 0) * kKeys + 32 * quad;
-      const int64_t n = t < nt ? (j1 - k0 < 32 ? j1 - k0 : 32) : 0;  // keys of this warp inside the chunk
-      my_id = lane < n ? load_row_id(a, rq.q0, P, kv_base, k0 + lane) : -1;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int tok = lane + 32 * i;
-        uint64_t v = 0;
-        if (tok < ntok && n > 0) {
-          const int64_t bit = mask_base + (int64_t)tok * L + k0;
-          const uint8_t* p = a.mask + (bit >> 3);
-          const int last = (int)(((bit & 7) + n - 1) >> 3);  // bytes that hold the n bits
-#pragma unroll
-          for (int k = 0; k < 5; ++k)
-            if (k <= last) v |= (uint64_t)__ldg(p + k) << (8 * k);
-          v >>= bit & 7;
-        }
-        bits[i] = (uint32_t)v;
-      }
-    };
-    fetch_vis(0);
     float acc[HC];  // sum of p over this thread's keys
 #pragma unroll
     for (int k = 0; k < HC; ++k) acc[k] = 0.f;
     bool my_abort = false;
 #pragma unroll 1
     for (int t = 0; t < nt; ++t) {
-      uint32_t vis = 0;
-      for (int tl = 0; tl < ntok; ++tl) {
-        const uint32_t w = __shfl_sync(0xffffffffu, tl < 32 ? bits[0] : bits[1], tl & 31);
-        if ((w >> lane) & 1u) vis |= ctl.colmask[tl][half];
+      // Which of its columns see this thread's key.
+      uint32_t vis = 0xffffffffu;
+      const int r = t % Cfg::kIndexRing;
+      if (!my_abort) my_abort = !mbar_wait(&ctl.idx_full[r], (t / Cfg::kIndexRing) & 1, &ctl.abort, a.status);
+      const bool all_vis = ctl.see_all[r][quad] != 0;
+      if (!all_vis) {
+        vis = 0;
+        for (int tl = 0; tl < ntok; ++tl)
+          if ((ctl.see[r][quad][tl] >> lane) & 1u) vis |= ctl.colmask[tl][half];
       }
-      if (my_id < 0 || my_id >= a.pool_rows) vis = 0;  // past the chunk's end, or a row outside the pool
-      fetch_vis(t + 1);
-      const bool all_vis = __all_sync(0xffffffffu, vis == (uint32_t)((1ull << HC) - 1));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl.idx_empty[r]);
       const uint32_t t_s = t_lane + Cfg::kColS + (t & 1) * 2 * NQ + c0;
 
       if (!my_abort) my_abort = !mbar_wait(&ctl.s_full[t & 1], (t >> 1) & 1, &ctl.abort, a.status);
@@ -727,9 +818,9 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
       bool need = false;
       if (!my_abort) {
         load_scores(true);
-        float top = x[0];
+        float top = fmaxf(x[0], x[1]);
 #pragma unroll
-        for (int k = 1; k < HC; ++k) top = fmaxf(top, x[k]);
+        for (int k = 2; k < HC; k += 2) top = kv4::max3(top, x[k], x[k + 1]);
         need = top > kKv4Top + kKv4Tau;
       } else {
 #pragma unroll
