@@ -58,8 +58,10 @@
 
 namespace mlav {
 
-constexpr float kKv4Top = 4.0f;   // base 2: the running max maps to p = 2^4 ...
-constexpr float kKv4Tau = 4.0f;   // ... and is raised when a score passes it by this much (p <= 2^8 < 448)
+// Base 2.  The running max of a column maps to p = 2^kKv4Top, the first one it
+// sees to 2^kKv4First (scores usually grow for a while), and it is raised when
+// a score would pass 2^kKv4Limit (e4m3 ends at 448).
+constexpr float kKv4First = 2.0f, kKv4Top = 4.0f, kKv4Limit = 8.0f;
 constexpr float kQLoScale = 32.f;
 constexpr float kPLoScale = 16.f;  // concatenated halves only
 
@@ -72,9 +74,9 @@ struct Kv4Cfg {
   static constexpr int kCG = NQ / kHC;
   static constexpr int kSoftmaxWarps = 4 * kCG;
   static constexpr int kSoftmaxThreads = 32 * kSoftmaxWarps;
-  static constexpr int kMmaWarp = kSoftmaxWarps;           // first warp of its warpgroup
-  static constexpr int kIndexWarp = kSoftmaxWarps + 1;     // the other three
-  static constexpr int kIndexWarps = 3;
+  static constexpr int kMmaWarp = kSoftmaxWarps;           // S^T, and the next one O^T
+  static constexpr int kIndexWarp = kSoftmaxWarps + 2;     // the other two of that warpgroup
+  static constexpr int kIndexWarps = 2;
   static constexpr int kIndexRing = 4;                     // tiles of row ids and mask words in flight
   static constexpr int kExpandWarp = kSoftmaxWarps + 4;
   static constexpr int kExpandWarps = 8;
@@ -98,10 +100,10 @@ struct Kv4Cfg {
   static constexpr int kSlots = kRopeSlot ? 9 : 8;
   // Slot of the u-th block of tile t, and the parity of its fill there.
   __host__ __device__ static constexpr int slot(int t, int u) {
-    return u < 3 ? 4 * (t & 1) + u : u == 3 && kRopeSlot ? 8 : 4 * (t & 1) + 3;
+    return u == 0 && kRopeSlot ? 8 : 4 * (t & 1) + (u & 3);
   }
   __host__ __device__ static constexpr uint32_t fill(int t, int u) {
-    return u < 3 ? (t >> 1) & 1u : kRopeSlot ? (u == 3 ? t & 1u : (t >> 1) & 1u) : (u == 3 ? 0u : 1u);
+    return !kRopeSlot && (u & 3) == 0 ? (u == 4 ? 1u : 0u) : kRopeSlot && u == 0 ? t & 1u : (t >> 1) & 1u;
   }
   static constexpr int kOffP = kQBytes;
   static constexpr int kOffRing = kOffP + kPBufs * kPBytes;
@@ -119,12 +121,12 @@ struct Kv4Ctl {
   // Two of each, by tile parity: the column groups and the MMAs may be a tile apart.
   uint64_t s_full[2], s_free[2], p_full[2], pv_done[2];
   uint64_t idx_full[Kv4Cfg<NQ>::kIndexRing], idx_empty[Kv4Cfg<NQ>::kIndexRing];
-  uint64_t q_full, mma_idle;
+  uint64_t q_full, mma_idle[2];
   uint32_t tmem_base;
   int abort;
   int flag[Kv4Cfg<NQ>::kSoftmaxWarps];
   alignas(16) float cscale[NQ];  // raw score -> base-2 score
-  alignas(16) float nmu[NQ];     // -(running max - kKv4Top); +inf before any visible key
+  alignas(16) float nmu[NQ];     // what turns a score into log2 p; +inf before any visible key
   alignas(16) float alpha[NQ];   // rescale factor of the tile; 1/l in the epilogue
   alignas(16) float red[4][NQ];
   uint32_t colmask[kMaxQLen][Kv4Cfg<NQ>::kCG];  // per token: which of a column group's columns are its
@@ -294,9 +296,9 @@ __device__ __forceinline__ bool elect_one() {
 
 // Slots.  Tile t's value blocks 0..3 stay in slots 4(t%2) .. 4(t%2)+3 until O^T
 // is done with them.  The RoPE block, which only S^T reads, has slot 8 where
-// shared memory has room for nine; else it passes through slot 3 of the tile's
-// set before block 3 does.  Order of expansion and of S^T: u = 0..4.
-__host__ __device__ constexpr int block_of(int u) { return u < 3 ? u : u == 3 ? 4 : 3; }
+// shared memory has room for nine; else it passes through slot 0 of the tile's
+// set before block 0 does.  Order of expansion and of S^T: RoPE, 1, 2, 3, 0.
+__host__ __device__ constexpr int block_of(int u) { return u == 0 ? 4 : u & 3; }
 
 // Bounded wait that ignores the abort flag (teardown only).
 __device__ __forceinline__ void wait_teardown(uint64_t* bar, uint32_t parity) {
@@ -403,7 +405,8 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
       mbar_init(&ctl.idx_empty[k], kSoftmaxWarps + Cfg::kExpandWarps);
     }
     mbar_init(&ctl.q_full, kSoftmaxWarps);
-    mbar_init(&ctl.mma_idle, 1);
+    mbar_init(&ctl.mma_idle[0], 1);
+    mbar_init(&ctl.mma_idle[1], 1);
     ctl.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -441,19 +444,26 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
     const uint32_t off0 = key0 * 128 + (((2 * q) ^ (key0 & 7)) << 4);
     const uint32_t off1 = key0 * 128 + (((2 * q + 1) ^ (key0 & 7)) << 4);
     const uint8_t* row[2];
+    int32_t id[2];
     uint4 code[2][kKv4Blocks], scale[2];
     bool stop = false;
-    // Rows of tile t.  (A key without one reads row 0: its weight is 0, and a
-    // 4-bit value is finite whatever the bytes.)
-    auto set_rows = [&](int t) {
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      const bool got = mbar_wait(bar, parity, &ctl.abort, a.status);
+      if (!__all_sync(0xffffffffu, got)) stop = true;
+    };
+    // Pool rows of the own keys of tile t.  (A key without one reads row 0: its
+    // weight is 0, and a 4-bit value is finite whatever the bytes.)
+    auto read_ids = [&](int t, bool ready) {
       const int r = t % Cfg::kIndexRing;
-      const bool got = mbar_wait(&ctl.idx_full[r], (t / Cfg::kIndexRing) & 1, &ctl.abort, a.status);
-      stop = !__all_sync(0xffffffffu, got);
+      if (!ready) wait(&ctl.idx_full[r], (t / Cfg::kIndexRing) & 1);
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        row[h] = a.kv4_pool + (int64_t)(stop ? 0 : ctl.row_id[r][key0 + 64 * h]) * kKv4RowBytes + 16 * q;
+      for (int h = 0; h < 2; ++h) id[h] = stop ? 0 : ctl.row_id[r][key0 + 64 * h];
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl.idx_empty[r]);
+    };
+    auto set_rows = [&]() {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) row[h] = a.kv4_pool + (int64_t)id[h] * kKv4RowBytes + 16 * q;
     };
     auto load_block = [&](int m) {
 #pragma unroll
@@ -463,25 +473,37 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
 #pragma unroll
       for (int h = 0; h < 2; ++h) to[h] = kv4::ldg_stream(row[h] + kKv4ScaleOff);
     };
-    set_rows(0);
+    read_ids(0, false);
+    set_rows();
     load_scales(scale);
 #pragma unroll
     for (int u = 0; u < kKv4Blocks; ++u) load_block(kv4::block_of(u));
+    if (nt > 1) read_ids(1, false);
 #pragma unroll 1
     for (int t = 0; t < nt && !stop; ++t) {
       const bool more = t + 1 < nt;
+      // A barrier takes ~200 cycles to ask here, so the tile asks all of its
+      // own at once, a lane each: its slots, and the row ids of tile t+2.
+      uint32_t ready;
+      {
+        uint64_t* bar = lane < kKv4Blocks ? &ctl.empty[Cfg::slot(t, lane)] : &ctl.idx_full[(t + 2) % Cfg::kIndexRing];
+        const uint32_t par =
+            lane < kKv4Blocks ? Cfg::fill(t, lane) ^ 1 : (uint32_t)((t + 2) / Cfg::kIndexRing) & 1;
+        // (not for block 0 in a slot that the RoPE block passes through first: a parity tells
+        // a fill from the one before it only once that one is consumed)
+        const bool ask = lane <= kKv4Blocks && (Cfg::kRopeSlot || lane != kKv4Blocks - 1);
+        ready = __ballot_sync(0xffffffffu, ask && mbar_test_wait(bar, par));
+      }
       uint4 next_scale[2] = {scale[0], scale[1]};
       if (more) {
-        set_rows(t + 1);
+        set_rows();
         load_scales(next_scale);
+        if (t + 2 < nt) read_ids(t + 2, (ready >> kKv4Blocks) & 1);
       }
 #pragma unroll
       for (int u = 0; u < kKv4Blocks; ++u) {
         const int m = kv4::block_of(u), sl = Cfg::slot(t, u);
-        if (!stop) {
-          const bool got = mbar_wait(&ctl.empty[sl], Cfg::fill(t, u) ^ 1, &ctl.abort, a.status);
-          if (!__all_sync(0xffffffffu, got)) stop = true;
-        }
+        if (!stop && !((ready >> u) & 1)) wait(&ctl.empty[sl], Cfg::fill(t, u) ^ 1);
         if (!stop) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -498,7 +520,6 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
             kv4::sts128(dst + off1, o[4], o[5], o[6], o[7]);
           }
           if (more) load_block(m);  // tile t+1
-          fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0 && !(a.test_stall && t == 0 && u == 0)) mbar_arrive(&ctl.full[sl]);
         }
@@ -508,104 +529,88 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
     }
   } else if (warp >= Cfg::kMmaWarp) {
     // ============================ MMA issue ==================================
-    // The whole warp runs the loop and one elected lane issues: the loop's
-    // values then stay warp-uniform, where an MMA takes its descriptors from.
-    // With a single thread running it every MMA cost ~160 cycles to issue,
-    // against 32 + N/4 (N <= 128) that the tensor core needs for one.
+    // Two warps, one for each product, so that neither waits behind the other:
+    // the tensor core takes their MMAs as they come.  The whole warp runs the
+    // loop and one elected lane issues: the loop's values then stay
+    // warp-uniform, where an MMA takes its descriptors from.  With a single
+    // thread running it every MMA cost ~160 cycles to issue, against 32 + N/4
+    // (N <= 128) that the tensor core needs for one.  The writers' generic
+    // stores are ordered before the MMAs' reads by a proxy fence here, after
+    // the wait: at the writers it held each block up until its stores landed.
     kv4::regs_to<Cfg::kRegsStart, Cfg::kRegsMma>();
-    if (warp == Cfg::kMmaWarp) {
-      constexpr uint32_t idesc_qk = kv4::idesc_f8(kKeys, 2 * NQ, kv4::kE5M2, kv4::kE4M3, false, false);
-      constexpr uint32_t idesc_pv =
-          kv4::idesc_f8(128, Cfg::kConcat ? 2 * NQ : NQ, kv4::kE5M2, kv4::kE4M3, true, true);
-      constexpr uint32_t idesc_lo = kv4::idesc_f8(128, NQ, kv4::kE5M2, kv4::kE5M2, true, true);
+    if (warp < Cfg::kIndexWarp) {
       const bool leader = kv4::elect_one();
       auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-        const bool got = mbar_wait_spin(bar, parity, &ctl.abort, a.status);
+        const bool got = mbar_wait(bar, parity, &ctl.abort, a.status);
         const bool all = __all_sync(0xffffffffu, got);
+        fence_proxy_async_smem();
         tc::fence_after_sync();
         return all;
       };
-      auto all_ready = [&](uint64_t* bar, uint32_t parity) -> bool {
-        const bool r = __all_sync(0xffffffffu, mbar_test_wait(bar, parity));
-        if (r) tc::fence_after_sync();
-        return r;
-      };
-      const uint64_t desc_k = tc::smem_desc(sRing, 16, 1024, tc::kSwizzle128B);               // A of S^T
-      const uint64_t desc_q = tc::smem_desc(sQ, 16, 1024, tc::kSwizzle128B);                  // B of S^T
-      const uint64_t desc_r = tc::smem_desc(sQ + 4 * Cfg::kQBlock, 16, 512, kv4::kSwizzle64B);  // its RoPE part
-      const uint64_t desc_v = tc::smem_desc(sRing, Cfg::kSlotBytes, 1024, tc::kSwizzle128B);  // A of O^T
-      const uint64_t desc_p = tc::smem_desc(sP, 128, Cfg::kPCore, 0);                         // B of O^T
-      bool ok = wait(&ctl.q_full, 0);
-      // Two products compete for the tensor core: block u of S^T(tq), ready when
-      // it is expanded and its S^T buffer is read out, and O^T(tp), ready when
-      // P^T(tp) is written.  O^T goes first -- it frees the slots the expansion
-      // waits for -- and S^T runs up to one tile ahead of it.
-      int tq = 0, u = 0, tp = 0;
-      uint64_t t_idle = global_timer_ns();
-      uint32_t polls = 0;
+      if (warp == Cfg::kMmaWarp) {
+        constexpr uint32_t idesc = kv4::idesc_f8(kKeys, 2 * NQ, kv4::kE5M2, kv4::kE4M3, false, false);
+        const uint64_t desc_k = tc::smem_desc(sRing, 16, 1024, tc::kSwizzle128B);
+        const uint64_t desc_q = tc::smem_desc(sQ, 16, 1024, tc::kSwizzle128B);
+        const uint64_t desc_r = tc::smem_desc(sQ + 4 * Cfg::kQBlock, 16, 512, kv4::kSwizzle64B);  // RoPE part
+        bool ok = wait(&ctl.q_full, 0);
 #pragma unroll 1
-      while (ok && tp < nt) {
-        if (tp < tq && all_ready(&ctl.p_full[tp & 1], (tp >> 1) & 1)) {
-          const uint64_t pd = desc_p + (uint32_t)((tp % Cfg::kPBufs) * (Cfg::kPBytes >> 4));
+        for (int t = 0; t < nt && ok; ++t) {
+          if (t >= 2 && !(ok = wait(&ctl.s_free[t & 1], ((t - 2) >> 1) & 1))) break;
+          const uint32_t d = tmem + Cfg::kColS + (t & 1) * 2 * NQ;
+#pragma unroll 1
+          for (int u = 0; u < kKv4Blocks; ++u) {
+            const int slot = Cfg::slot(t, u);
+            if (!(ok = wait(&ctl.full[slot], Cfg::fill(t, u)))) break;
+            const uint64_t ad = desc_k + (uint32_t)(slot * (Cfg::kSlotBytes >> 4));
+            if (leader && u == 0) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                kv4::mma_f8_ss(d, ad + 2 * k, desc_r + 2 * (k & 1), idesc, k == 0 ? 0u : 1u);
+              tc::mma_commit(&ctl.empty[slot]);  // only S^T reads the RoPE block
+            } else if (leader) {
+              const uint64_t bd = desc_q + (uint32_t)(kv4::block_of(u) * (Cfg::kQBlock >> 4));
+#pragma unroll
+              for (int k = 0; k < 4; ++k) kv4::mma_f8_ss(d, ad + 2 * k, bd + 2 * k, idesc, 1u);
+              if (u == kKv4Blocks - 1) tc::mma_commit(&ctl.s_full[t & 1]);
+            }
+            __syncwarp();
+          }
+        }
+      } else {
+        constexpr uint32_t idesc =
+            kv4::idesc_f8(128, Cfg::kConcat ? 2 * NQ : NQ, kv4::kE5M2, kv4::kE4M3, true, true);
+        constexpr uint32_t idesc_lo = kv4::idesc_f8(128, NQ, kv4::kE5M2, kv4::kE5M2, true, true);
+        const uint64_t desc_v = tc::smem_desc(sRing, Cfg::kSlotBytes, 1024, tc::kSwizzle128B);
+        const uint64_t desc_p = tc::smem_desc(sP, 128, Cfg::kPCore, 0);
+#pragma unroll 1
+        for (int t = 0; t < nt; ++t) {
+          // (P^T(t) was written after S^T(t), so its value blocks are there too)
+          if (!wait(&ctl.p_full[t & 1], (t >> 1) & 1)) break;
+          const uint64_t pd = desc_p + (uint32_t)((t % Cfg::kPBufs) * (Cfg::kPBytes >> 4));
 #pragma unroll 1
           for (int m = 0; m < 4; ++m) {
-            const int slot = 4 * (tp & 1) + m;
+            const int slot = 4 * (t & 1) + m;
             const uint64_t ad = desc_v + (uint32_t)(slot * (Cfg::kSlotBytes >> 4));
             const uint32_t d = tmem + m * Cfg::kOStride;
             if (leader) {
 #pragma unroll
               for (int k = 0; k < kKeys / 32; ++k) {
-                kv4::mma_f8_ss(d, ad + k * (4096 >> 4), pd + k * (512 >> 4), idesc_pv, (tp == 0 && k == 0) ? 0u : 1u);
+                kv4::mma_f8_ss(d, ad + k * (4096 >> 4), pd + k * (512 >> 4), idesc, (t == 0 && k == 0) ? 0u : 1u);
                 if (!Cfg::kConcat)
                   kv4::mma_f8_ss(d, ad + k * (4096 >> 4), pd + (((NQ / 16) * Cfg::kPCore + k * 512) >> 4), idesc_lo,
                                  1u);
               }
               tc::mma_commit(&ctl.empty[slot]);
-              if (m == 3) tc::mma_commit(&ctl.pv_done[tp & 1]);
+              if (m == 3) tc::mma_commit(&ctl.pv_done[t & 1]);
             }
             __syncwarp();
           }
-          ++tp;
-        } else if (tq < nt && tq <= tp + 1 &&
-                   (u > 0 || tq < 2 || all_ready(&ctl.s_free[tq & 1], ((tq - 2) >> 1) & 1)) &&
-                   all_ready(&ctl.full[Cfg::slot(tq, u)], Cfg::fill(tq, u))) {
-          const int slot = Cfg::slot(tq, u);
-          const uint32_t d = tmem + Cfg::kColS + (tq & 1) * 2 * NQ;
-          const uint64_t ad = desc_k + (uint32_t)(slot * (Cfg::kSlotBytes >> 4));
-          const int blk = kv4::block_of(u);
-          if (leader && blk == kKv4Blocks - 1) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) kv4::mma_f8_ss(d, ad + 2 * k, desc_r + 2 * (k & 1), idesc_qk, 1u);
-            tc::mma_commit(&ctl.empty[slot]);  // only S^T reads the RoPE block
-          } else if (leader) {
-            const uint64_t bd = desc_q + (uint32_t)(blk * (Cfg::kQBlock >> 4));
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              kv4::mma_f8_ss(d, ad + 2 * k, bd + 2 * k, idesc_qk, (u == 0 && k == 0) ? 0u : 1u);
-            if (u == kKv4Blocks - 1) tc::mma_commit(&ctl.s_full[tq & 1]);
-          }
-          __syncwarp();
-          if (++u == kKv4Blocks) {
-            u = 0;
-            ++tq;
-          }
-        } else {  // nothing ready: the bounds of mbar_wait
-          if ((++polls & 255u) == 0) {
-            const bool late = __any_sync(0xffffffffu, global_timer_ns() - t_idle > kWaitLimitNs);
-            if (late && leader) {
-              *(volatile int*)&ctl.abort = 1;
-              atomicOr(a.status, kStatusTimeout);
-            }
-            ok = __all_sync(0xffffffffu, !late && !*(volatile int*)&ctl.abort);
-          }
-          continue;
         }
-        t_idle = global_timer_ns();
       }
-      // Every MMA issued has completed before tensor memory is freed.
+      // Every MMA this warp issued has completed before tensor memory is freed.
       if (leader) {
-        tc::mma_commit(&ctl.mma_idle);
-        kv4::wait_teardown(&ctl.mma_idle, 0);
+        tc::mma_commit(&ctl.mma_idle[warp - Cfg::kMmaWarp]);
+        kv4::wait_teardown(&ctl.mma_idle[warp - Cfg::kMmaWarp], 0);
       }
       __syncwarp();
     } else {
@@ -780,6 +785,9 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
       const uint32_t t_s = t_lane + Cfg::kColS + (t & 1) * 2 * NQ + c0;
 
       if (!my_abort) my_abort = !mbar_wait(&ctl.s_full[t & 1], (t >> 1) & 1, &ctl.abort, a.status);
+      // (asked now, so that the answer is there by the time P^T is written)
+      const bool p_free = t < Cfg::kPBufs ||
+                          mbar_test_wait(&ctl.pv_done[(t - Cfg::kPBufs) & 1], ((t - Cfg::kPBufs) >> 1) & 1);
       my_abort = __any_sync(0xffffffffu, my_abort);  // tcgen05.ld below is warp-collective
       tc::fence_after_sync();
       // x = base-2 score + `add`, -inf where masked
@@ -821,14 +829,14 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
         float top = fmaxf(x[0], x[1]);
 #pragma unroll
         for (int k = 2; k < HC; k += 2) top = kv4::max3(top, x[k], x[k + 1]);
-        need = top > kKv4Top + kKv4Tau;
+        need = top > kKv4Limit;
       } else {
 #pragma unroll
         for (int k = 0; k < HC; ++k) x[k] = -INFINITY;
       }
       bool rescale = false;
       if (kv4::bar_any(bar_id, 128, need || my_abort || ctl.abort)) {
-        // Rare: a score passed the running max by more than kKv4Tau, a column
+        // Rare: a score passed the running max by too much, a column
         // saw its first key, or a wait gave up.
         const bool ab = __any_sync(0xffffffffu, my_abort) || ctl.abort;
         if (lane == 0) ctl.flag[warp] = ab ? 1 : 0;
@@ -843,8 +851,8 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
           const float cm = fmaxf(fmaxf(ctl.red[0][n], ctl.red[1][n]), fmaxf(ctl.red[2][n], ctl.red[3][n]));
           const float old = ctl.nmu[n];
           float al = 1.f;
-          if (cm + old > kKv4Top + kKv4Tau) {  // old = +inf: the first visible key (cm = -inf gives NaN, no)
-            const float nm = kKv4Top - cm;
+          if (cm + old > kKv4Limit) {  // old = +inf: the first visible key (cm = -inf gives NaN, no)
+            const float nm = (old == INFINITY ? kKv4First : kKv4Top) - cm;
             al = old == INFINITY ? 0.f : ex2_approx(nm - old);
             ctl.nmu[n] = nm;
             raised = true;
@@ -862,7 +870,7 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl.s_free[t & 1]);  // the S^T buffer may be overwritten
       // P^T(t) overwrites what O^T(t - kPBufs) read; a rescale of O^T needs all of them done.
-      if (t >= Cfg::kPBufs)
+      if (!p_free)
         my_abort = !mbar_wait(&ctl.pv_done[(t - Cfg::kPBufs) & 1], ((t - Cfg::kPBufs) >> 1) & 1, &ctl.abort, a.status);
       if (Cfg::kPBufs > 1 && rescale && !my_abort)
         my_abort = !mbar_wait(&ctl.pv_done[(t - 1) & 1], ((t - 1) >> 1) & 1, &ctl.abort, a.status);
@@ -920,7 +928,6 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
           kv4::sts128(dst + ((NQ + c0) / 16 + c) * Cfg::kPCore, lo[0], lo[1], lo[2], lo[3]);
         }
       }
-      fence_proxy_async_smem();
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0 && !my_abort) mbar_arrive(&ctl.p_full[t & 1]);
