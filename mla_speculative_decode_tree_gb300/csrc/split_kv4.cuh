@@ -70,7 +70,7 @@ struct Kv4Cfg {
   static_assert(NQ == 16 || NQ == 32 || NQ == 48 || NQ == 64, "row-group sizes built");
   static constexpr bool kConcat = NQ <= 32;
   static constexpr int kKeys = kKeysPerTile;
-  static constexpr int kHC = NQ == 64 ? 32 : 16;  // query columns per softmax thread
+  static constexpr int kHC = 16;  // query columns per softmax thread
   static constexpr int kCG = NQ / kHC;
   static constexpr int kSoftmaxWarps = 4 * kCG;
   static constexpr int kSoftmaxThreads = 32 * kSoftmaxWarps;
@@ -82,12 +82,11 @@ struct Kv4Cfg {
   static constexpr int kExpandWarps = 8;
   static constexpr int kThreads = 32 * (kExpandWarp + kExpandWarps);
   // Registers per thread by role.  A block starts with 65536 / kThreads rounded down to what its warps can all
-  // have (128, 96 or 80); the MMA warpgroup gives most of its share up: kCG * softmax + mma + 2 * expand is at
-  // most (kCG + 3) times the start's.
-  static constexpr int kRegsStart = kCG == 1 ? 128 : kCG == 2 ? 96 : 80;
+  // have (128, 96, 80 or 72); the shares together are at most the start's, or the last warps would wait for ever.
+  static constexpr int kRegsStart = kCG == 1 ? 128 : kCG == 2 ? 96 : kCG == 3 ? 80 : 72;
   static constexpr int kRegsMma = 48;
-  static constexpr int kRegsSoftmax = NQ == 64 ? 120 : kCG == 1 ? 128 : kCG == 2 ? 96 : 80;
-  static constexpr int kRegsExpand = kCG == 1 ? 128 : kCG == 2 && NQ != 64 ? 120 : 96;
+  static constexpr int kRegsSoftmax = kCG == 1 ? 128 : kCG == 2 ? 96 : kCG == 3 ? 80 : 64;
+  static constexpr int kRegsExpand = kCG == 1 ? 128 : kCG == 2 ? 120 : 96;
   static_assert(kCG * kRegsSoftmax + kRegsMma + 2 * kRegsExpand <= (kCG + 3) * kRegsStart, "register shares");
   static constexpr int kQBlock = 2 * NQ * 128;  // one 128-channel block of q_hi rows, then q_lo rows
   static constexpr int kQRope = 2 * NQ * 64;    // RoPE channels, once: the residual codes meet the same bytes
@@ -272,20 +271,49 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, ui
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
+// Bytes of (a, b) chosen by the four nibbles of the low half of sel, each 0..7
+// (a plain permute: __byte_perm would mask the nibbles once more).
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+  uint32_t d;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
+  return d;
+}
+
 // One word of 8 codes -> two words of 4 e5m2 values.  lo, hi: the eight
 // magnitudes times the group's scale, one byte each.
 __device__ __forceinline__ void expand8(uint32_t w, uint32_t lo, uint32_t hi, uint32_t& o0, uint32_t& o1) {
   const uint32_t sel = w & 0x77777777u;
-  o0 = __byte_perm(lo, hi, sel) | (w & 0x80808080u);
-  o1 = __byte_perm(lo, hi, sel >> 16) | ((w << 4) & 0x80808080u);
+  o0 = prmt(lo, hi, sel) | (w & 0x80808080u);
+  o1 = prmt(lo, hi, sel >> 16) | ((w << 4) & 0x80808080u);
 }
 
 // The scaled magnitudes 0, .5, 1, 1.5, 2, 3, 4, 6 as e5m2 bytes: exponent
-// field + e for all but the zero.
+// field + e for all but the zero.  The scale byte is a valid one.
 __device__ __forceinline__ void scale_table(uint32_t scale_byte, uint32_t& lo, uint32_t& hi) {
-  const uint32_t a = (uint32_t)(4 * kv4_exponent(scale_byte));
-  lo = 0x3E3C3800u + a * 0x01010100u;
-  hi = 0x46444240u + a * 0x01010101u;
+  lo = scale_byte * 0x04040400u + (0x3E3C3800u - 127u * 0x04040400u);
+  hi = scale_byte * 0x04040404u + (0x46444240u - 127u * 0x04040404u);
+}
+
+// The ten scale bytes of a quarter row: x, y and the low half of z.  A row that
+// was never stored may hold bytes outside the format; they are clamped to it, so
+// that every code expands to a finite value.  The check of all at once is a
+// third of what clamping each as it is used would cost.
+__device__ __forceinline__ bool scales_valid(const uint4& s) {
+  // valid: byte - 114 is 0 .. 26 (the first byte that is not spoils the ones after it, no matter)
+  const uint32_t x = s.x - 0x72727272u, y = s.y - 0x72727272u, z = ((s.z & 0xFFFFu) | 0x72720000u) - 0x72727272u;
+  return (((x | (x + 0x05050505u)) | (y | (y + 0x05050505u)) | (z | (z + 0x05050505u))) & 0xE0E0E0E0u) == 0;
+}
+__device__ __forceinline__ uint32_t clamp_scales(uint32_t w) {
+  uint32_t r = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) r |= (uint32_t)(kv4_exponent((w >> (8 * k)) & 0xFFu) + 127) << (8 * k);
+  return r;
+}
+__device__ __forceinline__ void make_valid(uint4& s) {
+  if (scales_valid(s)) return;
+  s.x = clamp_scales(s.x);
+  s.y = clamp_scales(s.y);
+  s.z = clamp_scales(s.z);
 }
 
 __device__ __forceinline__ bool elect_one() {
@@ -300,13 +328,20 @@ __device__ __forceinline__ bool elect_one() {
 // set before block 0 does.  Order of expansion and of S^T: RoPE, 1, 2, 3, 0.
 __host__ __device__ constexpr int block_of(int u) { return u == 0 ? 4 : u & 3; }
 
-// Bounded wait that ignores the abort flag (teardown only).
-__device__ __forceinline__ void wait_teardown(uint64_t* bar, uint32_t parity) {
-  const uint64_t t0 = global_timer_ns();
-  for (uint32_t it = 0; it < (1u << 30); ++it) {
-    if (mbar_try_wait(bar, parity)) return;
-    if ((it & 63u) == 0 && global_timer_ns() - t0 > kWaitLimitNs) return;
+// Bounded wait for phase `parity` of `bar`: at most kWaitTries tries, each of
+// which the hardware suspends for at most 20 us (mbar_try_wait), 2.6 s in all.
+// Gives up as well once another thread of the CTA has raised *abort, and raises
+// it when it gives up.  Short code on purpose: it stands at many places, and
+// what the roles' loops take of the instruction cache counts (see below).
+constexpr int kWaitTries = 1 << 17;
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+#pragma unroll 1
+  for (int tries = kWaitTries; tries > 0; --tries) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort) return false;
   }
+  *abort = 1;
+  return false;
 }
 
 // Max (or sum) of v[0..15] over the warp, index by index: lane l returns that
@@ -363,7 +398,9 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
   const int64_t P = (int64_t)a.kv_indptr[b + 1] - kv_base;
   const RequestTokens rq = request_tokens(a, b);
   const int64_t L = P + rq.n;
-  const int64_t chunk = chunk_len(L, a.nsplit, a.min_chunk, a.chunk_granule);
+  // chunk_len in 32 bits (a request has fewer than 2^31 keys, whole tiles per chunk)
+  const uint32_t per = ((uint32_t)L + (uint32_t)a.nsplit - 1u) / (uint32_t)a.nsplit;
+  const int64_t chunk = max((int64_t)((per + kKeys - 1u) & ~(uint32_t)(kKeys - 1)), (int64_t)a.min_chunk);
   const int64_t j0 = (int64_t)s_idx * chunk;
   const int64_t j1 = (j0 + chunk < L) ? j0 + chunk : L;
   const int rows_b = rq.n * a.H;
@@ -446,84 +483,66 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
     const uint8_t* row[2];
     int32_t id[2];
     uint4 code[2][kKv4Blocks], scale[2];
-    bool stop = false;
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-      const bool got = mbar_wait(bar, parity, &ctl.abort, a.status);
-      if (!__all_sync(0xffffffffu, got)) stop = true;
-    };
+    bool ok = true;
     // Pool rows of the own keys of tile t.  (A key without one reads row 0: its
     // weight is 0, and a 4-bit value is finite whatever the bytes.)
-    auto read_ids = [&](int t, bool ready) {
+    auto read_ids = [&](int t) {
       const int r = t % Cfg::kIndexRing;
-      if (!ready) wait(&ctl.idx_full[r], (t / Cfg::kIndexRing) & 1);
+      ok = __all_sync(0xffffffffu, kv4::wait(&ctl.idx_full[r], (t / Cfg::kIndexRing) & 1, &ctl.abort));
 #pragma unroll
-      for (int h = 0; h < 2; ++h) id[h] = stop ? 0 : ctl.row_id[r][key0 + 64 * h];
+      for (int h = 0; h < 2; ++h) id[h] = ok ? ctl.row_id[r][key0 + 64 * h] : 0;
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl.idx_empty[r]);
     };
-    auto set_rows = [&]() {
+    read_ids(0);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) row[h] = a.kv4_pool + (int64_t)id[h] * kKv4RowBytes + 16 * q;
-    };
-    auto load_block = [&](int m) {
+    for (int h = 0; h < 2; ++h) {
+      row[h] = a.kv4_pool + (int64_t)id[h] * kKv4RowBytes + 16 * q;
+      scale[h] = kv4::ldg_stream(row[h] + kKv4ScaleOff);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) code[h][m] = kv4::ldg_stream(row[h] + 64 * m);
-    };
-    auto load_scales = [&](uint4 (&to)[2]) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) to[h] = kv4::ldg_stream(row[h] + kKv4ScaleOff);
-    };
-    read_ids(0, false);
-    set_rows();
-    load_scales(scale);
-#pragma unroll
-    for (int u = 0; u < kKv4Blocks; ++u) load_block(kv4::block_of(u));
-    if (nt > 1) read_ids(1, false);
+      for (int u = 0; u < kKv4Blocks; ++u) code[h][kv4::block_of(u)] = kv4::ldg_stream(row[h] + 64 * kv4::block_of(u));
+    }
+    if (ok && nt > 1) read_ids(1);
 #pragma unroll 1
-    for (int t = 0; t < nt && !stop; ++t) {
-      const bool more = t + 1 < nt;
-      // A barrier takes ~200 cycles to ask here, so the tile asks all of its
-      // own at once, a lane each: its slots, and the row ids of tile t+2.
-      uint32_t ready;
-      {
-        uint64_t* bar = lane < kKv4Blocks ? &ctl.empty[Cfg::slot(t, lane)] : &ctl.idx_full[(t + 2) % Cfg::kIndexRing];
-        const uint32_t par =
-            lane < kKv4Blocks ? Cfg::fill(t, lane) ^ 1 : (uint32_t)((t + 2) / Cfg::kIndexRing) & 1;
-        // (not for block 0 in a slot that the RoPE block passes through first: a parity tells
-        // a fill from the one before it only once that one is consumed)
-        const bool ask = lane <= kKv4Blocks && (Cfg::kRopeSlot || lane != kKv4Blocks - 1);
-        ready = __ballot_sync(0xffffffffu, ask && mbar_test_wait(bar, par));
-      }
-      uint4 next_scale[2] = {scale[0], scale[1]};
-      if (more) {
-        set_rows();
-        load_scales(next_scale);
-        if (t + 2 < nt) read_ids(t + 2, (ready >> kKv4Blocks) & 1);
+    for (int t = 0; t < nt && ok; ++t) {
+      // Loads of tile t+1 follow the use of their registers in tile t; after the
+      // last tile they repeat its own.
+      uint4 next_scale[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        kv4::make_valid(scale[h]);
+        row[h] = a.kv4_pool + (int64_t)id[h] * kKv4RowBytes + 16 * q;
+        next_scale[h] = kv4::ldg_stream(row[h] + kKv4ScaleOff);
       }
 #pragma unroll
       for (int u = 0; u < kKv4Blocks; ++u) {
         const int m = kv4::block_of(u), sl = Cfg::slot(t, u);
-        if (!stop && !((ready >> u) & 1)) wait(&ctl.empty[sl], Cfg::fill(t, u) ^ 1);
-        if (!stop) {
-#pragma unroll
+        ok = ok && __all_sync(0xffffffffu, kv4::wait(&ctl.empty[sl], Cfg::fill(t, u) ^ 1, &ctl.abort));
+        if (ok) {
+          // (one copy of the code for both keys, see the note on code size)
+#pragma unroll 1
           for (int h = 0; h < 2; ++h) {
-            const uint32_t sw = m < 2 ? scale[h].x : m < 4 ? scale[h].y : scale[h].z;
+            const uint4 c = h ? code[1][m] : code[0][m];
+            uint32_t sw = h ? (m < 2 ? scale[1].x : m < 4 ? scale[1].y : scale[1].z)
+                            : (m < 2 ? scale[0].x : m < 4 ? scale[0].y : scale[0].z);
             uint32_t lo[2], hi[2], o[8];
             kv4::scale_table((sw >> (16 * (m & 1))) & 0xFFu, lo[0], hi[0]);
             kv4::scale_table((sw >> (16 * (m & 1) + 8)) & 0xFFu, lo[1], hi[1]);
-            kv4::expand8(code[h][m].x, lo[0], hi[0], o[0], o[1]);
-            kv4::expand8(code[h][m].y, lo[0], hi[0], o[2], o[3]);
-            kv4::expand8(code[h][m].z, lo[1], hi[1], o[4], o[5]);
-            kv4::expand8(code[h][m].w, lo[1], hi[1], o[6], o[7]);
+            kv4::expand8(c.x, lo[0], hi[0], o[0], o[1]);
+            kv4::expand8(c.y, lo[0], hi[0], o[2], o[3]);
+            kv4::expand8(c.z, lo[1], hi[1], o[4], o[5]);
+            kv4::expand8(c.w, lo[1], hi[1], o[6], o[7]);
             const uint32_t dst = sRing + sl * Cfg::kSlotBytes + h * 64 * 128;
             kv4::sts128(dst + off0, o[0], o[1], o[2], o[3]);
             kv4::sts128(dst + off1, o[4], o[5], o[6], o[7]);
           }
-          if (more) load_block(m);  // tile t+1
           __syncwarp();
-          if (lane == 0 && !(a.test_stall && t == 0 && u == 0)) mbar_arrive(&ctl.full[sl]);
+          if (lane == 0 && !(a.test_stall && t + u == 0)) mbar_arrive(&ctl.full[sl]);
+          code[0][m] = kv4::ldg_stream(row[0] + 64 * m);
+          code[1][m] = kv4::ldg_stream(row[1] + 64 * m);
         }
       }
+      if (ok && t + 2 < nt) read_ids(t + 2);
       scale[0] = next_scale[0];
       scale[1] = next_scale[1];
     }
@@ -541,7 +560,7 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
     if (warp < Cfg::kIndexWarp) {
       const bool leader = kv4::elect_one();
       auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-        const bool got = mbar_wait(bar, parity, &ctl.abort, a.status);
+        const bool got = kv4::wait(bar, parity, &ctl.abort);
         const bool all = __all_sync(0xffffffffu, got);
         fence_proxy_async_smem();
         tc::fence_after_sync();
@@ -610,13 +629,14 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
       // Every MMA this warp issued has completed before tensor memory is freed.
       if (leader) {
         tc::mma_commit(&ctl.mma_idle[warp - Cfg::kMmaWarp]);
-        kv4::wait_teardown(&ctl.mma_idle[warp - Cfg::kMmaWarp], 0);
+        int never = 0;  // (also after an abort)
+        kv4::wait(&ctl.mma_idle[warp - Cfg::kMmaWarp], 0, &never);
       }
       __syncwarp();
     } else {
       // ========================= row ids and mask ============================
-      // Warp i takes tiles i, i + 3, ...: the pool rows of the tile's keys, and
-      // per 32 keys and token the mask's bits, less keys that have no row.
+      // The two warps take turns at the tiles: the pool rows of the tile's keys,
+      // and per 32 keys and token the mask's bits, less keys that have no row.
       uint32_t bad = 0;
       const int n_keys = (int)(j1 - j0);
       const int pre = (int)(P - j0 < n_keys ? (P > j0 ? P - j0 : 0) : n_keys);  // keys of the chunk in the prefix
@@ -625,64 +645,54 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
       const int64_t block0 = (int64_t)a.mask_indptr[b];
       const uint8_t* mask_lo = a.mask + (block0 >> 3);  // the request's mask block, in whole bytes
       const uint8_t* mask_hi = a.mask + ((block0 + (int64_t)rq.n * L + 7) >> 3);
-      // An aligned word of the mask; bytes outside the block read as 0.
-      auto mask_word = [&](const uint8_t* p) -> uint32_t {
-        if (p >= mask_lo && p + 4 <= mask_hi) return __ldg(reinterpret_cast<const uint32_t*>(p));
-        uint32_t v = 0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (p + k >= mask_lo && p + k < mask_hi) v |= (uint32_t)__ldg(p + k) << (8 * k);
-        return v;
-      };
 #pragma unroll 1
       for (int t = warp - Cfg::kIndexWarp; t < nt; t += Cfg::kIndexWarps) {
         const int r = t % Cfg::kIndexRing;
         const int key0 = tile_at(t) * kKeys;
-        int32_t id[4];
-        uint32_t w[5];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int key = key0 + 32 * k + lane;
-          id[k] = key < pre ? __ldg(pre_ids + key) : key < n_keys ? __ldg(new_ids + key) : -1;
-        }
-        const int64_t bit0 = block0 + (int64_t)i0 * L + j0 + key0;  // the first token's, key 0 of the tile
-        auto load_mask = [&](int tok) {
-          const uintptr_t p = reinterpret_cast<uintptr_t>(a.mask + ((bit0 + (int64_t)tok * L) >> 3)) & ~(uintptr_t)3;
-#pragma unroll
-          for (int k = 0; k < 5; ++k) w[k] = tok < ntok ? mask_word(reinterpret_cast<const uint8_t*>(p) + 4 * k) : 0u;
-        };
-        load_mask(lane);
-        const bool got = mbar_wait(&ctl.idx_empty[r], ((t / Cfg::kIndexRing) & 1) ^ 1, &ctl.abort, a.status);
+        const bool got = kv4::wait(&ctl.idx_empty[r], ((t / Cfg::kIndexRing) & 1) ^ 1, &ctl.abort);
         if (!__all_sync(0xffffffffu, got)) break;
         uint32_t valid[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const bool in = id[k] >= 0 && id[k] < a.pool_rows;
-          if (!in && key0 + 32 * k + lane < n_keys) bad = 1;  // left out, and reported
+          const int key = key0 + 32 * k + lane;
+          const int32_t id = key < pre ? __ldg(pre_ids + key) : key < n_keys ? __ldg(new_ids + key) : -1;
+          const bool in = id >= 0 && id < a.pool_rows;
+          if (!in && key < n_keys) bad = 1;  // left out, and reported
           valid[k] = __ballot_sync(0xffffffffu, in);
-          ctl.row_id[r][32 * k + lane] = in ? id[k] : 0;
+          ctl.row_id[r][32 * k + lane] = in ? id : 0;
         }
-        bool all[4] = {true, true, true, true};
+        uint32_t blind = 0;  // bit k: some token does not see all of the k-th 32 keys
 #pragma unroll 1
-        for (int tok = lane;; tok += 32) {
-          const uintptr_t p = reinterpret_cast<uintptr_t>(a.mask + ((bit0 + (int64_t)tok * L) >> 3));
-          const int shift = 8 * (int)(p & 3) + (int)((bit0 + (int64_t)tok * L) & 7);
+        for (int tok = lane; tok - lane < ntok; tok += 32) {
+          const int64_t bit = block0 + (int64_t)(i0 + tok) * L + j0 + key0;
+          const uintptr_t byte = reinterpret_cast<uintptr_t>(a.mask + (bit >> 3));
+          const uint8_t* p = reinterpret_cast<const uint8_t*>(byte & ~(uintptr_t)3);
+          const int shift = 8 * (int)(byte & 3) + (int)(bit & 7);
+          const bool whole = p >= mask_lo && p + 20 <= mask_hi;
+          uint32_t w[5] = {0, 0, 0, 0, 0};
+          if (tok < ntok) {
+            if (whole) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t v = __funnelshift_r(w[k], w[k + 1], shift) & valid[k];
-            if (tok < ntok) {
+              for (int k = 0; k < 5; ++k) w[k] = __ldg(reinterpret_cast<const uint32_t*>(p) + k);
+            } else {  // at an end of the mask block: only its own bytes are read
+#pragma unroll 1
+              for (int k = 0; k < 20; ++k) {
+                const uint32_t v = p + k >= mask_lo && p + k < mask_hi ? __ldg(p + k) : 0u;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 8);
+                w[4] = (w[4] >> 8) | (v << 24);
+              }
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t v = __funnelshift_r(w[k], w[k + 1], shift) & valid[k];
               ctl.see[r][k][tok] = v;
-              all[k] = all[k] && v == 0xffffffffu;
+              if (v != 0xffffffffu) blind |= 1u << k;
             }
           }
-          if (tok - lane + 32 >= ntok) break;
-          load_mask(tok + 32);
         }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const bool every = __all_sync(0xffffffffu, all[k]);
-          if (lane == 0) ctl.see_all[r][k] = every;
-        }
+        blind = __reduce_or_sync(0xffffffffu, blind);
+        if (lane < 4) ctl.see_all[r][lane] = !((blind >> lane) & 1);
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl.idx_full[r]);
       }
@@ -694,7 +704,7 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
     // Queries: warp w turns rows w, w + warps, ... into q_hi and q_lo, four at
     // a time so that their loads overlap.  Lane l holds channels 8l..8l+7 and
     // 256+8l.., lanes 0-7 also RoPE channels 8l...
-    constexpr int kRowsAtOnce = 4;
+    constexpr int kRowsAtOnce = 2;
     static_assert(NQ % (kSoftmaxWarps * kRowsAtOnce) == 0, "whole rounds of query rows");
 #pragma unroll 1
     for (int base = warp; base < NQ; base += kSoftmaxWarps * kRowsAtOnce) {
@@ -773,7 +783,7 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
       // Which of its columns see this thread's key.
       uint32_t vis = 0xffffffffu;
       const int r = t % Cfg::kIndexRing;
-      if (!my_abort) my_abort = !mbar_wait(&ctl.idx_full[r], (t / Cfg::kIndexRing) & 1, &ctl.abort, a.status);
+      if (!my_abort) my_abort = !kv4::wait(&ctl.idx_full[r], (t / Cfg::kIndexRing) & 1, &ctl.abort);
       const bool all_vis = ctl.see_all[r][quad] != 0;
       if (!all_vis) {
         vis = 0;
@@ -784,7 +794,7 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
       if (lane == 0) mbar_arrive(&ctl.idx_empty[r]);
       const uint32_t t_s = t_lane + Cfg::kColS + (t & 1) * 2 * NQ + c0;
 
-      if (!my_abort) my_abort = !mbar_wait(&ctl.s_full[t & 1], (t >> 1) & 1, &ctl.abort, a.status);
+      if (!my_abort) my_abort = !kv4::wait(&ctl.s_full[t & 1], (t >> 1) & 1, &ctl.abort);
       // (asked now, so that the answer is there by the time P^T is written)
       const bool p_free = t < Cfg::kPBufs ||
                           mbar_test_wait(&ctl.pv_done[(t - Cfg::kPBufs) & 1], ((t - Cfg::kPBufs) >> 1) & 1);
@@ -871,9 +881,9 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
       if (lane == 0) mbar_arrive(&ctl.s_free[t & 1]);  // the S^T buffer may be overwritten
       // P^T(t) overwrites what O^T(t - kPBufs) read; a rescale of O^T needs all of them done.
       if (!p_free)
-        my_abort = !mbar_wait(&ctl.pv_done[(t - Cfg::kPBufs) & 1], ((t - Cfg::kPBufs) >> 1) & 1, &ctl.abort, a.status);
+        my_abort = !kv4::wait(&ctl.pv_done[(t - Cfg::kPBufs) & 1], ((t - Cfg::kPBufs) >> 1) & 1, &ctl.abort);
       if (Cfg::kPBufs > 1 && rescale && !my_abort)
-        my_abort = !mbar_wait(&ctl.pv_done[(t - 1) & 1], ((t - 1) >> 1) & 1, &ctl.abort, a.status);
+        my_abort = !kv4::wait(&ctl.pv_done[(t - 1) & 1], ((t - 1) >> 1) & 1, &ctl.abort);
       my_abort = __any_sync(0xffffffffu, my_abort);
       tc::fence_after_sync();
       if (!my_abort && rescale) {
@@ -936,7 +946,7 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
     // ---- epilogue: l, LSE, O = O^T / l ----------------------------------------
     named_bar_sync(bar_id, 128);  // (a raise of the last tile has read red)
     kv4::columns_to_smem<HC, false>(acc, &ctl.red[quad][c0], lane);
-    if (!my_abort) my_abort = !mbar_wait(&ctl.pv_done[(nt - 1) & 1], ((nt - 1) >> 1) & 1, &ctl.abort, a.status);
+    if (!my_abort) my_abort = !kv4::wait(&ctl.pv_done[(nt - 1) & 1], ((nt - 1) >> 1) & 1, &ctl.abort);
     tc::fence_after_sync();
     const bool failed = kv4::bar_any(bar_id, 128, my_abort || ctl.abort);
     if (j < HC) {
@@ -981,6 +991,7 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
 
   // ---- teardown ---------------------------------------------------------------
   __syncthreads();
+  if (tid == 0 && ctl.abort) atomicOr(a.status, kStatusTimeout);
   if (warp == Cfg::kMmaWarp) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, 512);
