@@ -85,8 +85,8 @@ struct Kv4Cfg {
   // have (128, 96, 80 or 72); the shares together are at most the start's, or the last warps would wait for ever.
   static constexpr int kRegsStart = kCG == 1 ? 128 : kCG == 2 ? 96 : kCG == 3 ? 80 : 72;
   static constexpr int kRegsMma = 48;
-  static constexpr int kRegsSoftmax = kCG == 1 ? 128 : kCG == 2 ? 96 : kCG == 3 ? 80 : 64;
-  static constexpr int kRegsExpand = kCG == 1 ? 128 : kCG == 2 ? 120 : 96;
+  static constexpr int kRegsSoftmax = kCG == 1 ? 128 : kCG == 2 ? 96 : kCG == 3 ? 80 : 72;
+  static constexpr int kRegsExpand = kCG == 1 ? 128 : kCG == 2 ? 120 : kCG == 3 ? 96 : 80;
   static_assert(kCG * kRegsSoftmax + kRegsMma + 2 * kRegsExpand <= (kCG + 3) * kRegsStart, "register shares");
   static constexpr int kQBlock = 2 * NQ * 128;  // one 128-channel block of q_hi rows, then q_lo rows
   static constexpr int kQRope = 2 * NQ * 64;    // RoPE channels, once: the residual codes meet the same bytes
