@@ -31,6 +31,8 @@ struct mla_verify_plan_s {
   bool merge_quarter;  // merge with four warps per row (at most one wave of rows)
   int smem;
   bool kv4;  // the pool holds 4-bit rows (MLA_VERIFY_KV4)
+  int pieces;  // > 0: the 4-bit kernel's CTAs, which take the work in equal pieces (nsplit = 0)
+  int seg_cost;  // its start and end of a row group, in tiles
 };
 
 namespace {
@@ -178,36 +180,33 @@ cudaError_t kv4_launch(int nq, const SplitArgs& a, dim3 grid, cudaStream_t st) {
   }
 }
 
-// The time model of est_us with the 4-bit kernel's times.
-double kv4_tile_us(int nq) { return nq >= 64 ? 2.2 : nq >= 48 ? 1.7 : 1.5; }
+// Times of the 4-bit kernel on GB300 (clocks near 1.95 GHz): a tile, and what a
+// row group's start and end (queries in, outputs out) add, in tiles.
+double kv4_tile_us(int nq) { return nq >= 64 ? 3.1 : nq >= 48 ? 2.7 : nq >= 32 ? 2.4 : 2.2; }
+constexpr int kKv4SegCost = 2;
 
-Choice choose_kv4(int64_t rows_b, int64_t max_kv_len, int max_batch, int nsplit) {
-  constexpr double kCtaUs = 5.0, kMergeUs = 2.0, kMergeBytesPerUs = 3.0e6;
+// Row-group size: the least modelled time of a CTA's equal piece of the work
+// (nsplit = 0), or of the chunk grid's waves.  Several requests: lengths are
+// unknown at plan time and taken as half of max_kv_len.
+int choose_kv4(int64_t rows_b, int64_t max_kv_len, int max_batch, int nsplit) {
+  constexpr double kCtaUs = 5.0;
   const double sms = (double)device_sm_count();
-  const int64_t tiles_max = (max_kv_len + kKeysPerTile - 1) / kKeysPerTile;
-  const int64_t n_lo = nsplit > 0 ? nsplit : 1;
-  const int64_t n_hi = nsplit > 0 ? nsplit : std::min<int64_t>(tiles_max, 4096);
-  Choice best{false, 64, (int)n_lo};
+  int best = 64;
   double t_best = -1.0;
   for (int nq : kKv4NqChoices) {
-    const double groups = (double)((rows_b + nq - 1) / nq);
-    const double tu = kv4_tile_us(nq);
-    for (int64_t n = n_lo; n <= n_hi; ++n) {
-      if (nsplit == 0 && n > 1 && (tiles_max + n - 2) / (n - 1) == (tiles_max + n - 1) / n)
-        continue;  // same chunks as n - 1 splits, only more partials
-      const int64_t chunk = chunk_len(max_kv_len, (int)n, kMinChunk);
-      const double per = (double)(chunk / kKeysPerTile);
-      const double splits = (double)((max_kv_len + chunk - 1) / chunk);
-      double t;
-      if (max_batch == 1)
-        t = std::ceil(groups * splits / sms) * (per * tu + kCtaUs);
-      else
-        t = (groups * max_batch * tiles_max / 2.0 / sms + per) * tu + groups * max_batch * splits * kCtaUs / sms;
-      t += kMergeUs + splits * rows_b * max_batch * 2048.0 / kMergeBytesPerUs;
-      if (t_best < 0 || t < t_best) {
-        t_best = t;
-        best = {false, nq, (int)n};
-      }
+    const double groups = (double)((rows_b + nq - 1) / nq) * max_batch;
+    const double tiles = (double)((max_kv_len + kKeysPerTile - 1) / kKeysPerTile) / (max_batch > 1 ? 2.0 : 1.0);
+    double t;
+    if (nsplit == 0) {
+      t = std::ceil(groups * (tiles + kKv4SegCost) / sms) * kv4_tile_us(nq);
+    } else {
+      const double per = (double)(chunk_len(max_kv_len, nsplit, kMinChunk) / kKeysPerTile);
+      t = max_batch > 1 ? (groups * tiles / sms + per) * kv4_tile_us(nq) + groups * nsplit * kCtaUs / sms
+                        : std::ceil(groups * nsplit / sms) * (per * kv4_tile_us(nq) + kCtaUs);
+    }
+    if (t_best < 0 || t < t_best * 0.999) {
+      t_best = t;
+      best = nq;
     }
   }
   return best;
@@ -363,10 +362,11 @@ int mla_verify_plan(const mla_verify_params* params, size_t* workspace_bytes, ml
   pl->kernel = (p.flags & MLA_VERIFY_FORCE_SIMT) ? 0 : 1;
   pl->kv4 = (p.flags & MLA_VERIFY_KV4) != 0;
   if (pl->kernel && pl->kv4) {
-    const Choice c = choose_kv4(rows_b, p.max_kv_len, p.max_batch, p.nsplit);
-    pl->resident = true;  // each key is read once per CTA
-    pl->nq = c.nq;
-    pl->splits = c.splits;
+    pl->resident = true;  // each key is read once per row group
+    pl->nq = choose_kv4(rows_b, p.max_kv_len, p.max_batch, p.nsplit);
+    pl->splits = p.nsplit > 0 ? p.nsplit : 1;
+    pl->pieces = p.nsplit > 0 ? 0 : device_sm_count();
+    pl->seg_cost = kKv4SegCost;
   } else if (pl->kernel) {
     // The mode (resident tile, unless MLA_VERIFY_REFETCH_VALUES), the row-group
     // size and, for nsplit = 0, the split count, from the time model.
@@ -412,6 +412,17 @@ int mla_verify_plan(const mla_verify_params* params, size_t* workspace_bytes, ml
   pl->ws_bytes = pl->off_o + sizeof(float) * (size_t)pl->splits * (size_t)rows_max * kDLatent;
   pl->merge_quarter = merge_quarter_fits(rows_max, device_sm_count());
   pl->merge_blocks = pl->fused ? 0 : merge_blocks((int)rows_max, pl->merge_quarter);
+  if (pl->pieces) {
+    // The table of the row groups' partials, then the partials: every piece end
+    // and every row group ends one (nq rows each).
+    const size_t spans = (size_t)p.max_batch * pl->groups;
+    const size_t rows = (spans + pl->pieces) * pl->nq;
+    pl->off_lse = round_up(kWsHeader + sizeof(int2) * spans, 256);
+    pl->off_o = round_up(pl->off_lse + sizeof(float) * rows, 256);
+    pl->ws_bytes = pl->off_o + sizeof(float) * rows * kDLatent;
+    const int per_block = pl->merge_quarter ? 2 : 4;
+    pl->merge_blocks = (int)((rows_b + per_block - 1) / per_block) * p.max_batch;
+  }
   *workspace_bytes = pl->ws_bytes;
   *out = pl;
   return MLA_VERIFY_OK;
@@ -423,9 +434,9 @@ int mla_verify_plan_describe(mla_verify_plan_t pl, mla_verify_plan_info* info) {
   info->rows_per_cta = pl->nq;
   info->resident_tile = pl->resident ? 1 : 0;
   info->keys_per_tile = kKeysPerTile;
-  info->grid_x = pl->groups;
+  info->grid_x = pl->pieces ? pl->pieces : pl->groups;
   info->grid_y = pl->splits;
-  info->grid_z = pl->p.max_batch;
+  info->grid_z = pl->pieces ? 1 : pl->p.max_batch;
   info->merge_blocks = pl->merge_blocks;
   info->smem_bytes = pl->smem;
   info->min_chunk = pl->min_chunk;
@@ -480,7 +491,12 @@ int split_impl(mla_verify_plan_t pl, const void* q_nope_absorbed, const void* q_
   a.o = pl->fused ? static_cast<__nv_bfloat16*>(o) : nullptr;
   a.lse = pl->fused ? lse : nullptr;
 
-  const dim3 grid(pl->groups, pl->splits, pl->p.max_batch);
+  if (pl->pieces) {
+    a.seg_table = reinterpret_cast<int2*>(ws + kWsHeader);
+    a.seg_cost = pl->seg_cost;
+    a.groups_max = pl->groups;
+  }
+  const dim3 grid = pl->pieces ? dim3(pl->pieces, 1, 1) : dim3(pl->groups, pl->splits, pl->p.max_batch);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (pl->kernel && pl->kv4) {
@@ -529,7 +545,14 @@ int merge_impl(mla_verify_plan_t pl, int32_t batch, int32_t nsplit, const int32_
   m.quarter = pl->merge_quarter ? 1 : 0;
   m.speculative =
       m.quarter && (uint64_t)pl->splits * (uint64_t)pl->rows_max * kDLatent * sizeof(float) <= (48ull << 20) ? 1 : 0;
-  cudaError_t e = launch_merge(m, static_cast<cudaStream_t>(stream));
+  if (pl->pieces) {
+    m.seg_table = reinterpret_cast<const int2*>(ws + kWsHeader);
+    m.nq = pl->nq;
+    m.groups_max = pl->groups;
+    m.T = pl->p.q_len;
+  }
+  cudaError_t e = pl->pieces ? launch_merge_pieces(m, static_cast<cudaStream_t>(stream))
+                             : launch_merge(m, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MLA_VERIFY_OK : cuda_fail(e);
 }
 

@@ -52,6 +52,11 @@ struct SplitArgs {
   uint32_t* merge_count;         // [max_batch, groups]
   __nv_bfloat16* o;              // [rows, 512]
   float* lse;                    // [rows]
+  // 4-bit pool, work in equal pieces (split_kv4.cuh): per (request, row group)
+  // the first of its partials and their number; null: chunks by the grid.
+  int2* seg_table;
+  int32_t seg_cost;              // start and end of a row group, in tiles
+  int32_t groups_max;            // row groups of a request of T tokens
 };
 
 // TMA descriptors of one call: the pool for row gathers (box 64 columns x 1
@@ -71,6 +76,8 @@ struct MergeArgs {
   __nv_bfloat16* o;  // [rows, 512]
   float* lse;        // [rows]
   uint32_t* status;  // header words 0 (accumulated) and 1 (last call)
+  const int2* seg_table;  // work in equal pieces: see SplitArgs; T tokens per request or qo_indptr
+  int32_t nq, groups_max, T;
   int32_t quarter;      // four warps per row (few rows) instead of two
   int32_t speculative;  // quarter layout: load the first 16 splits' partials before their LSEs
 };
@@ -254,6 +261,7 @@ MLAV_DECLARE_KV4(48)
 MLAV_DECLARE_KV4(64)
 #undef MLAV_DECLARE_KV4
 cudaError_t launch_merge(const MergeArgs& a, cudaStream_t stream);
+cudaError_t launch_merge_pieces(const MergeArgs& a, cudaStream_t stream);
 constexpr int kMaxTreeMaskVarlenBatch = 1024;  // requests of a varlen mask build
 cudaError_t launch_tree_mask(const int32_t* parents, const int32_t* kv_indptr, const int32_t* qo_indptr, int batch,
                              int T, uint8_t* mask, int64_t mask_bytes, int32_t* mask_indptr, int64_t max_bytes,

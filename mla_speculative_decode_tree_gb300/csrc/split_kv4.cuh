@@ -113,6 +113,29 @@ struct Kv4Cfg {
   static_assert(kOffRing % 1024 == 0, "slots are 1024-byte aligned");
 };
 
+// What a CTA does: segments, each a range of tiles of one row group of one
+// request, one after the other.  nt = 0 ends the list.
+struct Kv4Segment {
+  int32_t nt;          // tiles
+  int32_t tile0;       // the first one
+  int32_t rot;         // tile t of the segment is tile0 + (t + rot) % nt
+  int32_t batch;       // request
+  int32_t n_tokens;    // its query tokens
+  int32_t i0, ntok;    // tokens the row group spans
+  int32_t r0, nrows;   // its rows within the request
+  int32_t keys;        // L: keys of the request
+  int64_t q0;          // first token row of the request
+  int64_t prow;        // row of the partial outputs
+};
+// Where the hand-out of segments stands (kv4::next_segment).
+struct Kv4Cursor {
+  int64_t x, x_end, piece;  // own piece of the axis
+  int64_t carry;            // axis before request `base`
+  int32_t base;
+  int32_t done;
+};
+constexpr uint32_t kTileFirst = 1, kTileEnd = 2;  // first tile of a segment; no tile, the end of all
+
 template <int NQ>
 struct Kv4Ctl {
   uint64_t full[Kv4Cfg<NQ>::kSlots];
@@ -120,7 +143,8 @@ struct Kv4Ctl {
   // Two of each, by tile parity: the column groups and the MMAs may be a tile apart.
   uint64_t s_full[2], s_free[2], p_full[2], pv_done[2];
   uint64_t idx_full[Kv4Cfg<NQ>::kIndexRing], idx_empty[Kv4Cfg<NQ>::kIndexRing];
-  uint64_t q_full, mma_idle[2];
+  uint64_t seg_full[2], seg_empty[2];
+  uint64_t q_full, sm_sync, mma_idle[2];
   uint32_t tmem_base;
   int abort;
   int flag[Kv4Cfg<NQ>::kSoftmaxWarps];
@@ -129,6 +153,9 @@ struct Kv4Ctl {
   alignas(16) float alpha[NQ];   // rescale factor of the tile; 1/l in the epilogue
   alignas(16) float red[4][NQ];
   uint32_t colmask[kMaxQLen][Kv4Cfg<NQ>::kCG];  // per token: which of a column group's columns are its
+  Kv4Segment seg[2];
+  Kv4Cursor cursor;
+  uint32_t tile[Kv4Cfg<NQ>::kIndexRing];                     // kTile* bits
   int32_t row_id[Kv4Cfg<NQ>::kIndexRing][kKeysPerTile];      // pool row of each key, 0 where there is none
   uint32_t see[Kv4Cfg<NQ>::kIndexRing][4][kMaxQLen];         // per 32 keys and token: which keys it sees
   uint32_t see_all[Kv4Cfg<NQ>::kIndexRing][4];               // every token sees all 32
@@ -375,6 +402,147 @@ __device__ __forceinline__ void columns_to_smem(const float (&x)[HC], float* dst
   }
 }
 
+// Hands a CTA its segments (one full warp calls it).
+//
+// Flat (a.seg_table set): the work of the call -- for each request and row group
+// seg_cost units of start and end, then one per tile -- lies on one axis, and
+// the CTAs take equal pieces of it, so they end together whatever the requests'
+// lengths are.  A piece that ends inside a row group's keys leaves a partial;
+// the partials of group g of request b are numbered from (CTA that has its
+// first tile) + b * groups_max + g on, by CTA, which no two segments share.
+// Otherwise: one chunk of one row group per CTA (the grid), or none.
+struct Schedule {
+  // Query tokens and keys of request b, and its length on the axis.
+  struct Req {
+    int64_t q0;
+    int n, keys, tiles, groups;
+    int64_t cost;
+  };
+  static __device__ __forceinline__ Req request(const SplitArgs& a, int nq, int b) {
+    Req r = {};
+    if (b < a.batch) {
+      const RequestTokens rq = request_tokens(a, b);
+      r.q0 = rq.q0;
+      r.n = rq.n;
+      r.keys = a.kv_indptr[b + 1] - a.kv_indptr[b] + rq.n;
+      r.tiles = (r.keys + kKeysPerTile - 1) / kKeysPerTile;
+      r.groups = (rq.n * a.H + nq - 1) / nq;
+      r.cost = (int64_t)r.groups * (r.tiles + a.seg_cost);
+    }
+    return r;
+  }
+  static __device__ __forceinline__ int64_t scan(int64_t v, int lane) {  // inclusive, over the warp
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += y;
+    }
+    return v;
+  }
+
+  static __device__ __forceinline__ void start(const SplitArgs& a, int nq, int lane, Kv4Cursor& c) {
+    int64_t total = 0, piece = 1;
+    if (a.seg_table) {
+#pragma unroll 1
+      for (int b = 0; b < a.batch; b += 32)
+        total += __shfl_sync(0xffffffffu, scan(request(a, nq, b + lane).cost, lane), 31);
+      piece = (total + gridDim.x - 1) / gridDim.x;
+      piece = piece < 1 ? 1 : piece;
+    }
+    if (lane == 0) {
+      const int64_t x = blockIdx.x * piece;
+      c = {x, x + piece < total ? x + piece : total, piece, 0, 0, 0};
+    }
+    __syncwarp();
+  }
+
+  static __device__ __forceinline__ void rows(const SplitArgs& a, int nq, int g, Kv4Segment& s) {
+    s.r0 = g * nq;
+    s.nrows = s.n_tokens * a.H - s.r0 < nq ? s.n_tokens * a.H - s.r0 : nq;
+    s.i0 = s.r0 / a.H;
+    s.ntok = (s.r0 + s.nrows - 1) / a.H - s.i0 + 1;
+  }
+
+  // The next segment, or one of no tiles, in s (a register copy in every lane).
+  static __device__ __forceinline__ void next(const SplitArgs& a, int nq, int lane, Kv4Cursor& c, Kv4Segment& s) {
+    s.nt = 0;
+    if (!a.seg_table) {
+      const int b = blockIdx.z, g = blockIdx.x;
+      const bool done = c.done != 0;
+      __syncwarp();
+      if (done || b >= a.batch) return;
+      if (lane == 0) c.done = 1;
+      const Req r = request(a, nq, b);
+      if (g >= r.groups) return;
+      s.batch = b;
+      s.q0 = r.q0;
+      s.n_tokens = r.n;
+      s.keys = r.keys;
+      rows(a, nq, g, s);
+      s.prow = (int64_t)blockIdx.y * a.rows_max + r.q0 * a.H + s.r0;
+      // chunk_len, in tiles
+      const int per = (int)(((uint32_t)r.keys + (uint32_t)a.nsplit - 1u) / (uint32_t)a.nsplit);
+      int chunk = (per + kKeysPerTile - 1) / kKeysPerTile;
+      chunk = chunk < a.min_chunk / kKeysPerTile ? a.min_chunk / kKeysPerTile : chunk;
+      const int64_t t0 = (int64_t)blockIdx.y * chunk;
+      if (t0 >= r.tiles) {  // an empty chunk
+        for (int n = lane; n < s.nrows; n += 32) a.part_lse[s.prow + n] = -INFINITY;
+        return;
+      }
+      s.tile0 = (int)t0;
+      s.nt = r.tiles - s.tile0 < chunk ? r.tiles - s.tile0 : chunk;
+      // The row groups of a chunk read the same keys; staggered they read them
+      // from L2 one after the other.
+      s.rot = g % s.nt;
+      return;
+    }
+    int64_t x = c.x, carry = c.carry;
+    int base = c.base;
+    const int64_t x_end = c.x_end;
+    __syncwarp();
+#pragma unroll 1
+    while (x < x_end) {
+      const Req r = request(a, nq, base + lane);
+      const int64_t incl = carry + scan(r.cost, lane);
+      const uint32_t past = __ballot_sync(0xffffffffu, incl > x);
+      if (!past) {
+        carry = __shfl_sync(0xffffffffu, incl, 31);
+        base += 32;
+        continue;
+      }
+      const int l = __ffs(past) - 1;
+      s.batch = base + l;
+      s.q0 = __shfl_sync(0xffffffffu, r.q0, l);
+      s.n_tokens = __shfl_sync(0xffffffffu, r.n, l);
+      s.keys = __shfl_sync(0xffffffffu, r.keys, l);
+      const int tiles = __shfl_sync(0xffffffffu, r.tiles, l);
+      const int64_t from = __shfl_sync(0xffffffffu, incl - r.cost, l);  // the request's place on the axis
+      const int g = (int)((x - from) / (tiles + a.seg_cost));
+      const int64_t first = from + (int64_t)g * (tiles + a.seg_cost) + a.seg_cost;  // the group's first tile
+      const int64_t end = first + tiles;
+      const int64_t t0 = x > first ? x - first : 0;
+      x = x_end < end ? x_end : end;
+      if (x - first <= t0) continue;  // only of the group's start
+      rows(a, nq, g, s);
+      const int slot = s.batch * a.groups_max + g;
+      s.prow = (int64_t)(blockIdx.x + slot) * nq;
+      s.tile0 = (int)t0;
+      s.nt = (int)(x - first - t0);
+      s.rot = 0;
+      if (lane == 0) {
+        // where the merge finds the group's partials, and how many
+        if (t0 == 0)
+          a.seg_table[slot] = make_int2(blockIdx.x + slot, (int)((end - 1) / c.piece) - (int)blockIdx.x + 1);
+        c.x = x;
+        c.carry = carry;
+        c.base = base;
+      }
+      __syncwarp();
+      return;
+    }
+  }
+};
+
 }  // namespace kv4
 
 template <int NQ>
@@ -386,41 +554,9 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
   constexpr int CG = Cfg::kCG;
   constexpr int kSoftmaxWarps = Cfg::kSoftmaxWarps;
   constexpr int kSoftmaxThreads = Cfg::kSoftmaxThreads;
-  const int b = blockIdx.z;
-  if (b >= a.batch) return;
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
   const int lane = tid & 31;
-  const int s_idx = blockIdx.y;
-  const int g = blockIdx.x;
-
-  const int64_t kv_base = a.kv_indptr[b];
-  const int64_t P = (int64_t)a.kv_indptr[b + 1] - kv_base;
-  const RequestTokens rq = request_tokens(a, b);
-  const int64_t L = P + rq.n;
-  // chunk_len in 32 bits (a request has fewer than 2^31 keys, whole tiles per chunk)
-  const uint32_t per = ((uint32_t)L + (uint32_t)a.nsplit - 1u) / (uint32_t)a.nsplit;
-  const int64_t chunk = max((int64_t)((per + kKeys - 1u) & ~(uint32_t)(kKeys - 1)), (int64_t)a.min_chunk);
-  const int64_t j0 = (int64_t)s_idx * chunk;
-  const int64_t j1 = (j0 + chunk < L) ? j0 + chunk : L;
-  const int rows_b = rq.n * a.H;
-  const int r0 = g * NQ;
-  if (r0 >= rows_b) return;
-  const int nrows = (rows_b - r0 < NQ) ? rows_b - r0 : NQ;
-  const int64_t grow0 = rq.q0 * a.H + r0;  // global row of the group's first row
-  float* lse_out = a.part_lse + (int64_t)s_idx * a.rows_max + grow0;
-  if (j0 >= j1) {
-    for (int n = tid; n < nrows; n += Cfg::kThreads) lse_out[n] = -INFINITY;
-    return;
-  }
-  const int nt = (int)((j1 - j0 + kKeys - 1) / kKeys);
-  const int i0 = r0 / a.H;
-  const int ntok = (r0 + nrows - 1) / a.H - i0 + 1;
-  // Row group g starts g tiles into the split: the groups of a split read the
-  // same keys, and staggered they read them from L2 one after the other.
-  const int rot = g % nt;
-  auto tile_at = [&](int t) -> int { return t + rot < nt ? t + rot : t + rot - nt; };
-
   extern __shared__ __align__(1024) uint8_t kv4_smem[];  // the swizzle atoms are 1024-byte aligned
   const uint32_t sQ = smem_u32(kv4_smem), sP = sQ + Cfg::kOffP, sRing = sQ + Cfg::kOffRing;
   Kv4Ctl<NQ>& ctl = *reinterpret_cast<Kv4Ctl<NQ>*>(kv4_smem + Cfg::kOffCtl);
@@ -436,14 +572,16 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
       mbar_init(&ctl.s_free[k], kSoftmaxWarps);
       mbar_init(&ctl.p_full[k], kSoftmaxWarps);
       mbar_init(&ctl.pv_done[k], 1);
+      mbar_init(&ctl.seg_full[k], 1);
+      mbar_init(&ctl.seg_empty[k], kSoftmaxWarps + Cfg::kIndexWarps);
+      mbar_init(&ctl.mma_idle[k], 1);
     }
     for (int k = 0; k < Cfg::kIndexRing; ++k) {
       mbar_init(&ctl.idx_full[k], 1);
-      mbar_init(&ctl.idx_empty[k], kSoftmaxWarps + Cfg::kExpandWarps);
+      mbar_init(&ctl.idx_empty[k], kSoftmaxWarps + Cfg::kExpandWarps + 2);
     }
     mbar_init(&ctl.q_full, kSoftmaxWarps);
-    mbar_init(&ctl.mma_idle[0], 1);
-    mbar_init(&ctl.mma_idle[1], 1);
+    mbar_init(&ctl.sm_sync, kSoftmaxWarps);
     ctl.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -451,22 +589,16 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
     tc::tmem_alloc(&ctl.tmem_base, 512);
     tc::tmem_relinquish();
   }
-  if (tid < kSoftmaxThreads) {
-    for (int n = tid; n < NQ; n += kSoftmaxThreads) ctl.nmu[n] = INFINITY;
-    for (int t = tid; t < ntok * CG; t += kSoftmaxThreads) {
-      const int tok = t / CG, h = t % CG;
-      uint32_t bits = 0;
-      for (int c = 0; c < HC; ++c) {
-        const int n = h * HC + c;
-        if (n < nrows && (r0 + n) / a.H == i0 + tok) bits |= 1u << c;
-      }
-      ctl.colmask[tok][h] = bits;
-    }
-  }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = ctl.tmem_base;
+  // Tiles are counted through all segments (t below, in the rings and their
+  // parities), so no role waits for the others at a segment's end: the rings
+  // just go on, with only the queries and O^T changing hands.
+  auto wait_warp = [&](uint64_t* bar, uint32_t parity) -> bool {
+    return __all_sync(0xffffffffu, kv4::wait(bar, parity, &ctl.abort));
+  };
 
   if (warp >= Cfg::kExpandWarp) {
     // =========================== expansion ===================================
@@ -483,30 +615,36 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
     const uint8_t* row[2];
     int32_t id[2];
     uint4 code[2][kKv4Blocks], scale[2];
-    bool ok = true;
-    // Pool rows of the own keys of tile t.  (A key without one reads row 0: its
-    // weight is 0, and a 4-bit value is finite whatever the bytes.)
+    bool ok = true, more = true;
+    // Pool rows of the own keys of tile t, if there is one.  (A key without a
+    // row reads row 0: its weight is 0, and a 4-bit value is finite whatever the
+    // bytes.)
     auto read_ids = [&](int t) {
       const int r = t % Cfg::kIndexRing;
-      ok = __all_sync(0xffffffffu, kv4::wait(&ctl.idx_full[r], (t / Cfg::kIndexRing) & 1, &ctl.abort));
+      ok = wait_warp(&ctl.idx_full[r], (t / Cfg::kIndexRing) & 1);
+      more = ok && !(ctl.tile[r] & kTileEnd);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) id[h] = ok ? ctl.row_id[r][key0 + 64 * h] : 0;
+      for (int h = 0; h < 2; ++h) id[h] = more ? ctl.row_id[r][key0 + 64 * h] : 0;
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl.idx_empty[r]);
     };
     read_ids(0);
+    if (more) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      row[h] = a.kv4_pool + (int64_t)id[h] * kKv4RowBytes + 16 * q;
-      scale[h] = kv4::ldg_stream(row[h] + kKv4ScaleOff);
+      for (int h = 0; h < 2; ++h) {
+        row[h] = a.kv4_pool + (int64_t)id[h] * kKv4RowBytes + 16 * q;
+        scale[h] = kv4::ldg_stream(row[h] + kKv4ScaleOff);
 #pragma unroll
-      for (int u = 0; u < kKv4Blocks; ++u) code[h][kv4::block_of(u)] = kv4::ldg_stream(row[h] + 64 * kv4::block_of(u));
+        for (int u = 0; u < kKv4Blocks; ++u)
+          code[h][kv4::block_of(u)] = kv4::ldg_stream(row[h] + 64 * kv4::block_of(u));
+      }
     }
-    if (ok && nt > 1) read_ids(1);
+    bool have = more;
+    if (have) read_ids(1);
 #pragma unroll 1
-    for (int t = 0; t < nt && ok; ++t) {
+    for (int t = 0; have && ok; ++t) {
       // Loads of tile t+1 follow the use of their registers in tile t; after the
-      // last tile they repeat its own.
+      // last tile they read row 0.
       uint4 next_scale[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -517,14 +655,15 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
 #pragma unroll
       for (int u = 0; u < kKv4Blocks; ++u) {
         const int m = kv4::block_of(u), sl = Cfg::slot(t, u);
-        ok = ok && __all_sync(0xffffffffu, kv4::wait(&ctl.empty[sl], Cfg::fill(t, u) ^ 1, &ctl.abort));
+        ok = ok && wait_warp(&ctl.empty[sl], Cfg::fill(t, u) ^ 1);
         if (ok) {
-          // (one copy of the code for both keys, see the note on code size)
+          // (one copy of the code for both keys: the roles' loops share the
+          // instruction cache)
 #pragma unroll 1
           for (int h = 0; h < 2; ++h) {
             const uint4 c = h ? code[1][m] : code[0][m];
-            uint32_t sw = h ? (m < 2 ? scale[1].x : m < 4 ? scale[1].y : scale[1].z)
-                            : (m < 2 ? scale[0].x : m < 4 ? scale[0].y : scale[0].z);
+            const uint32_t sw = h ? (m < 2 ? scale[1].x : m < 4 ? scale[1].y : scale[1].z)
+                                  : (m < 2 ? scale[0].x : m < 4 ? scale[0].y : scale[0].z);
             uint32_t lo[2], hi[2], o[8];
             kv4::scale_table((sw >> (16 * (m & 1))) & 0xFFu, lo[0], hi[0]);
             kv4::scale_table((sw >> (16 * (m & 1) + 8)) & 0xFFu, lo[1], hi[1]);
@@ -542,7 +681,8 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
           code[1][m] = kv4::ldg_stream(row[1] + 64 * m);
         }
       }
-      if (ok && t + 2 < nt) read_ids(t + 2);
+      have = more;
+      if (ok && more) read_ids(t + 2);
       scale[0] = next_scale[0];
       scale[1] = next_scale[1];
     }
@@ -559,27 +699,42 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
     kv4::regs_to<Cfg::kRegsStart, Cfg::kRegsMma>();
     if (warp < Cfg::kIndexWarp) {
       const bool leader = kv4::elect_one();
-      auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-        const bool got = kv4::wait(bar, parity, &ctl.abort);
-        const bool all = __all_sync(0xffffffffu, got);
+      auto wait_mma = [&](uint64_t* bar, uint32_t parity) -> bool {
+        const bool ok = wait_warp(bar, parity);
         fence_proxy_async_smem();
         tc::fence_after_sync();
-        return all;
+        return ok;
+      };
+      // Bits of tile t; kTileEnd after a wait that gave up.
+      auto tile_bits = [&](int t) -> uint32_t {
+        const int r = t % Cfg::kIndexRing;
+        if (!wait_warp(&ctl.idx_full[r], (t / Cfg::kIndexRing) & 1)) return kTileEnd;
+        const uint32_t bits = ctl.tile[r];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl.idx_empty[r]);
+        return bits;
       };
       if (warp == Cfg::kMmaWarp) {
         constexpr uint32_t idesc = kv4::idesc_f8(kKeys, 2 * NQ, kv4::kE5M2, kv4::kE4M3, false, false);
         const uint64_t desc_k = tc::smem_desc(sRing, 16, 1024, tc::kSwizzle128B);
         const uint64_t desc_q = tc::smem_desc(sQ, 16, 1024, tc::kSwizzle128B);
         const uint64_t desc_r = tc::smem_desc(sQ + 4 * Cfg::kQBlock, 16, 512, kv4::kSwizzle64B);  // RoPE part
-        bool ok = wait(&ctl.q_full, 0);
+        uint32_t q_phase = 0;
 #pragma unroll 1
-        for (int t = 0; t < nt && ok; ++t) {
-          if (t >= 2 && !(ok = wait(&ctl.s_free[t & 1], ((t - 2) >> 1) & 1))) break;
+        for (int t = 0;; ++t) {
+          const uint32_t bits = tile_bits(t);
+          if (bits & kTileEnd) break;
+          if (bits & kTileFirst) {
+            if (!wait_mma(&ctl.q_full, q_phase)) break;
+            q_phase ^= 1;
+          }
+          if (t >= 2 && !wait_mma(&ctl.s_free[t & 1], ((t - 2) >> 1) & 1)) break;
           const uint32_t d = tmem + Cfg::kColS + (t & 1) * 2 * NQ;
+          bool ok = true;
 #pragma unroll 1
           for (int u = 0; u < kKv4Blocks; ++u) {
             const int slot = Cfg::slot(t, u);
-            if (!(ok = wait(&ctl.full[slot], Cfg::fill(t, u)))) break;
+            if (!(ok = wait_mma(&ctl.full[slot], Cfg::fill(t, u)))) break;
             const uint64_t ad = desc_k + (uint32_t)(slot * (Cfg::kSlotBytes >> 4));
             if (leader && u == 0) {
 #pragma unroll
@@ -594,6 +749,7 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
             }
             __syncwarp();
           }
+          if (!ok) break;
         }
       } else {
         constexpr uint32_t idesc =
@@ -602,9 +758,12 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
         const uint64_t desc_v = tc::smem_desc(sRing, Cfg::kSlotBytes, 1024, tc::kSwizzle128B);
         const uint64_t desc_p = tc::smem_desc(sP, 128, Cfg::kPCore, 0);
 #pragma unroll 1
-        for (int t = 0; t < nt; ++t) {
-          // (P^T(t) was written after S^T(t), so its value blocks are there too)
-          if (!wait(&ctl.p_full[t & 1], (t >> 1) & 1)) break;
+        for (int t = 0;; ++t) {
+          const uint32_t bits = tile_bits(t);
+          if (bits & kTileEnd) break;
+          // (P^T(t) was written after S^T(t), so its value blocks are there too,
+          // and after the last segment's O^T was read out)
+          if (!wait_mma(&ctl.p_full[t & 1], (t >> 1) & 1)) break;
           const uint64_t pd = desc_p + (uint32_t)((t % Cfg::kPBufs) * (Cfg::kPBytes >> 4));
 #pragma unroll 1
           for (int m = 0; m < 4; ++m) {
@@ -614,7 +773,8 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
             if (leader) {
 #pragma unroll
               for (int k = 0; k < kKeys / 32; ++k) {
-                kv4::mma_f8_ss(d, ad + k * (4096 >> 4), pd + k * (512 >> 4), idesc, (t == 0 && k == 0) ? 0u : 1u);
+                kv4::mma_f8_ss(d, ad + k * (4096 >> 4), pd + k * (512 >> 4), idesc,
+                               k == 0 && (bits & kTileFirst) ? 0u : 1u);
                 if (!Cfg::kConcat)
                   kv4::mma_f8_ss(d, ad + k * (4096 >> 4), pd + (((NQ / 16) * Cfg::kPCore + k * 512) >> 4), idesc_lo,
                                  1u);
@@ -634,189 +794,258 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
       }
       __syncwarp();
     } else {
-      // ========================= row ids and mask ============================
-      // The two warps take turns at the tiles: the pool rows of the tile's keys,
-      // and per 32 keys and token the mask's bits, less keys that have no row.
+      // ================= segments, row ids and mask words =====================
+      // The first warp hands out the segments; the two take turns at the tiles:
+      // the pool rows of the tile's keys, and per 32 keys and token the mask's
+      // bits, less keys that have no row.
+      const int iw = warp - Cfg::kIndexWarp;
+      if (iw == 0) kv4::Schedule::start(a, NQ, lane, ctl.cursor);
       uint32_t bad = 0;
-      const int n_keys = (int)(j1 - j0);
-      const int pre = (int)(P - j0 < n_keys ? (P > j0 ? P - j0 : 0) : n_keys);  // keys of the chunk in the prefix
-      const int32_t* pre_ids = a.kv_indices + kv_base + j0;
-      const int32_t* new_ids = a.out_cache_loc + rq.q0 + (j0 - P);
-      const int64_t block0 = (int64_t)a.mask_indptr[b];
-      const uint8_t* mask_lo = a.mask + (block0 >> 3);  // the request's mask block, in whole bytes
-      const uint8_t* mask_hi = a.mask + ((block0 + (int64_t)rq.n * L + 7) >> 3);
+      int t_seg = 0;  // first tile of the segment in the count of all
+      bool ok = true;
 #pragma unroll 1
-      for (int t = warp - Cfg::kIndexWarp; t < nt; t += Cfg::kIndexWarps) {
-        const int r = t % Cfg::kIndexRing;
-        const int key0 = tile_at(t) * kKeys;
-        const bool got = kv4::wait(&ctl.idx_empty[r], ((t / Cfg::kIndexRing) & 1) ^ 1, &ctl.abort);
-        if (!__all_sync(0xffffffffu, got)) break;
-        uint32_t valid[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int key = key0 + 32 * k + lane;
-          const int32_t id = key < pre ? __ldg(pre_ids + key) : key < n_keys ? __ldg(new_ids + key) : -1;
-          const bool in = id >= 0 && id < a.pool_rows;
-          if (!in && key < n_keys) bad = 1;  // left out, and reported
-          valid[k] = __ballot_sync(0xffffffffu, in);
-          ctl.row_id[r][32 * k + lane] = in ? id : 0;
+      for (int k = 0; ok; ++k) {
+        if (iw == 0) {
+          Kv4Segment sg;
+          kv4::Schedule::next(a, NQ, lane, ctl.cursor, sg);
+          if (!(ok = wait_warp(&ctl.seg_empty[k & 1], ((k >> 1) & 1) ^ 1))) break;
+          if (lane == 0) {
+            ctl.seg[k & 1] = sg;
+            mbar_arrive(&ctl.seg_full[k & 1]);
+          }
+          __syncwarp();
         }
-        uint32_t blind = 0;  // bit k: some token does not see all of the k-th 32 keys
+        if (!(ok = wait_warp(&ctl.seg_full[k & 1], (k >> 1) & 1))) break;
+        const Kv4Segment& sg = ctl.seg[k & 1];
+        const int nt = sg.nt, b = sg.batch;
+        if (nt == 0) {
+          // the end, as one more tile
+          const int r = t_seg % Cfg::kIndexRing;
+          if (t_seg % Cfg::kIndexWarps == iw &&
+              wait_warp(&ctl.idx_empty[r], ((t_seg / Cfg::kIndexRing) & 1) ^ 1) && lane == 0) {
+            ctl.tile[r] = kTileEnd;
+            mbar_arrive(&ctl.idx_full[r]);
+          }
+          break;
+        }
+        const int tile0 = sg.tile0, rot = sg.rot, i0 = sg.i0, ntok = sg.ntok, L = sg.keys, n_tok = sg.n_tokens;
+        const int64_t q0 = sg.q0;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl.seg_empty[k & 1]);
+        const int64_t kv_base = a.kv_indptr[b];
+        const int P = (int)(a.kv_indptr[b + 1] - kv_base);
+        const int32_t* pre_ids = a.kv_indices + kv_base;
+        const int32_t* new_ids = a.out_cache_loc + q0 - P;
+        const int64_t block0 = (int64_t)a.mask_indptr[b];
+        const uint8_t* mask_lo = a.mask + (block0 >> 3);  // the request's mask block, in whole bytes
+        const uint8_t* mask_hi = a.mask + ((block0 + (int64_t)n_tok * L + 7) >> 3);
 #pragma unroll 1
-        for (int tok = lane; tok - lane < ntok; tok += 32) {
-          const int64_t bit = block0 + (int64_t)(i0 + tok) * L + j0 + key0;
-          const uintptr_t byte = reinterpret_cast<uintptr_t>(a.mask + (bit >> 3));
-          const uint8_t* p = reinterpret_cast<const uint8_t*>(byte & ~(uintptr_t)3);
-          const int shift = 8 * (int)(byte & 3) + (int)(bit & 7);
-          const bool whole = p >= mask_lo && p + 20 <= mask_hi;
-          uint32_t w[5] = {0, 0, 0, 0, 0};
-          if (tok < ntok) {
-            if (whole) {
+        for (int i = (iw - t_seg) & (Cfg::kIndexWarps - 1); i < nt; i += Cfg::kIndexWarps) {
+          const int t = t_seg + i;
+          const int r = t % Cfg::kIndexRing;
+          const int key0 = (tile0 + (i + rot < nt ? i + rot : i + rot - nt)) * kKeys;
+          if (!(ok = wait_warp(&ctl.idx_empty[r], ((t / Cfg::kIndexRing) & 1) ^ 1))) break;
+          uint32_t valid[4];
 #pragma unroll
-              for (int k = 0; k < 5; ++k) w[k] = __ldg(reinterpret_cast<const uint32_t*>(p) + k);
-            } else {  // at an end of the mask block: only its own bytes are read
+          for (int j = 0; j < 4; ++j) {
+            const int key = key0 + 32 * j + lane;
+            const int32_t id = key < P ? __ldg(pre_ids + key) : key < L ? __ldg(new_ids + key) : -1;
+            const bool in = id >= 0 && id < a.pool_rows;
+            if (!in && key < L) bad = 1;  // left out, and reported
+            valid[j] = __ballot_sync(0xffffffffu, in);
+            ctl.row_id[r][32 * j + lane] = in ? id : 0;
+          }
+          uint32_t blind = 0;  // bit j: some token does not see all of the j-th 32 keys
 #pragma unroll 1
-              for (int k = 0; k < 20; ++k) {
-                const uint32_t v = p + k >= mask_lo && p + k < mask_hi ? __ldg(p + k) : 0u;
+          for (int tok = lane; tok - lane < ntok; tok += 32) {
+            const int64_t bit = block0 + (int64_t)(i0 + tok) * L + key0;
+            const uintptr_t byte = reinterpret_cast<uintptr_t>(a.mask + (bit >> 3));
+            const uint8_t* p = reinterpret_cast<const uint8_t*>(byte & ~(uintptr_t)3);
+            const int shift = 8 * (int)(byte & 3) + (int)(bit & 7);
+            uint32_t w[5] = {0, 0, 0, 0, 0};
+            if (tok < ntok) {
+              if (p >= mask_lo && p + 20 <= mask_hi) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 8);
-                w[4] = (w[4] >> 8) | (v << 24);
+                for (int j = 0; j < 5; ++j) w[j] = __ldg(reinterpret_cast<const uint32_t*>(p) + j);
+              } else {  // at an end of the mask block: only its own bytes are read
+#pragma unroll 1
+                for (int n = 0; n < 20; ++n) {
+                  const uint32_t v = p + n >= mask_lo && p + n < mask_hi ? __ldg(p + n) : 0u;
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) w[j] = __funnelshift_r(w[j], w[j + 1], 8);
+                  w[4] = (w[4] >> 8) | (v << 24);
+                }
+              }
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const uint32_t v = __funnelshift_r(w[j], w[j + 1], shift) & valid[j];
+                ctl.see[r][j][tok] = v;
+                if (v != 0xffffffffu) blind |= 1u << j;
               }
             }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t v = __funnelshift_r(w[k], w[k + 1], shift) & valid[k];
-              ctl.see[r][k][tok] = v;
-              if (v != 0xffffffffu) blind |= 1u << k;
-            }
           }
+          blind = __reduce_or_sync(0xffffffffu, blind);
+          if (lane < 4) ctl.see_all[r][lane] = !((blind >> lane) & 1);
+          if (lane == 0) ctl.tile[r] = i == 0 ? kTileFirst : 0u;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl.idx_full[r]);
         }
-        blind = __reduce_or_sync(0xffffffffu, blind);
-        if (lane < 4) ctl.see_all[r][lane] = !((blind >> lane) & 1);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl.idx_full[r]);
+        t_seg += nt;
       }
       if (bad) atomicOr(a.status, kStatusBadRow);
     }
   } else {
     // ============================ softmax ====================================
     kv4::regs_to<Cfg::kRegsStart, Cfg::kRegsSoftmax>();
-    // Queries: warp w turns rows w, w + warps, ... into q_hi and q_lo, four at
-    // a time so that their loads overlap.  Lane l holds channels 8l..8l+7 and
-    // 256+8l.., lanes 0-7 also RoPE channels 8l...
-    constexpr int kRowsAtOnce = 2;
-    static_assert(NQ % (kSoftmaxWarps * kRowsAtOnce) == 0, "whole rounds of query rows");
-#pragma unroll 1
-    for (int base = warp; base < NQ; base += kSoftmaxWarps * kRowsAtOnce) {
-      uint4 v[kRowsAtOnce][3];
-#pragma unroll
-      for (int i = 0; i < kRowsAtOnce; ++i) {
-        const int n = base + i * kSoftmaxWarps;
-        v[i][0] = v[i][1] = v[i][2] = make_uint4(0, 0, 0, 0);
-        if (n < nrows) {
-          const uint4* qn = reinterpret_cast<const uint4*>(a.q_nope + (grow0 + n) * kDLatent);
-          v[i][0] = __ldg(qn + lane);
-          v[i][1] = __ldg(qn + 32 + lane);
-          if (lane < 8) v[i][2] = __ldg(reinterpret_cast<const uint4*>(a.q_rope + (grow0 + n) * kDRope) + lane);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < kRowsAtOnce; ++i) {
-        const int n = base + i * kSoftmaxWarps;
-        uint32_t top = 0;  // largest |q| as bits: bf16 magnitudes order as integers
-#pragma unroll
-        for (int k = 0; k < 3; ++k) {
-          const uint32_t u[4] = {v[i][k].x, v[i][k].y, v[i][k].z, v[i][k].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) top = max(top, max(u[e] & 0x7FFFu, (u[e] >> 16) & 0x7FFFu));
-        }
-        top = __reduce_max_sync(0xffffffffu, top);
-        const int ex = (int)(top >> 7);  // biased exponent of the largest value
-        // 2^x brings it into [128, 256); rows of zeros or denormals use the largest x
-        int x = 7 + 127 - ex;
-        x = x > 126 ? 126 : x;
-        const float up = pow2f(x);
-        // a row with an infinity or a NaN scores NaN
-        if (lane == 0) ctl.cscale[n] = ex == 255 ? NAN : a.scale_log2 * pow2f(-x);
-        // 8 channels -> 8 bytes of q_hi (at `at`) and of q_lo (`lo_off` further on)
-        auto put = [&](uint32_t at, uint32_t lo_off, const uint4& bits) {
-          const uint32_t u[4] = {bits.x, bits.y, bits.z, bits.w};
-          uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float f0 = __uint_as_float(u[e] << 16) * up, f1 = __uint_as_float(u[e] & 0xFFFF0000u) * up;
-            const uint32_t h = kv4::cvt_e4m3x2(f0, f1);
-            const uint32_t hf = kv4::cvt_f16x2_e4m3x2(h);
-            const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hf));
-            const uint32_t l = kv4::cvt_e4m3x2((f0 - back.x) * kQLoScale, (f1 - back.y) * kQLoScale);
-            hi[e >> 1] |= h << (16 * (e & 1));
-            lo[e >> 1] |= l << (16 * (e & 1));
-          }
-          asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at), "r"(hi[0]), "r"(hi[1]) : "memory");
-          asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at + lo_off), "r"(lo[0]), "r"(lo[1]) : "memory");
-        };
-        static_assert(NQ % 8 == 0, "q_lo row n swizzles as q_hi row n");
-        const uint32_t in_block = (((lane & 15) >> 1) ^ (n & 7)) << 4;  // 16-byte chunk, 128-byte swizzle
-        const uint32_t at = sQ + (lane >> 4) * Cfg::kQBlock + n * 128 + in_block + 8 * (lane & 1);
-        put(at, NQ * 128, v[i][0]);
-        put(at + 2 * Cfg::kQBlock, NQ * 128, v[i][1]);
-        if (lane < 8)  // RoPE: rows of 64 bytes, 64-byte swizzle
-          put(sQ + 4 * Cfg::kQBlock + n * 64 + (((lane >> 1) ^ ((n >> 1) & 3)) << 4) + 8 * (lane & 1), NQ * 64, v[i][2]);
-      }
-    }
-    fence_proxy_async_smem();
-    named_bar_sync(1, kSoftmaxThreads);  // cscale
-    if (lane == 0) mbar_arrive(&ctl.q_full);
-
     const int quad = warp & 3;
     const int half = warp >> 2;      // column group
     const int j = 32 * quad + lane;  // key within the tile == TMEM lane
     const int c0 = half * HC;        // first query column of this thread
     const int bar_id = 2 + half;     // the group's four warps (quads) share its columns
     const uint32_t t_lane = tmem + ((uint32_t)(32 * quad) << 16);
-    float acc[HC];  // sum of p over this thread's keys
-#pragma unroll
-    for (int k = 0; k < HC; ++k) acc[k] = 0.f;
+    int t = 0;  // tiles of all segments
     bool my_abort = false;
-#pragma unroll 1
-    for (int t = 0; t < nt; ++t) {
-      // Which of its columns see this thread's key.
-      uint32_t vis = 0xffffffffu;
-      const int r = t % Cfg::kIndexRing;
-      if (!my_abort) my_abort = !kv4::wait(&ctl.idx_full[r], (t / Cfg::kIndexRing) & 1, &ctl.abort);
-      const bool all_vis = ctl.see_all[r][quad] != 0;
-      if (!all_vis) {
-        vis = 0;
-        for (int tl = 0; tl < ntok; ++tl)
-          if ((ctl.see[r][quad][tl] >> lane) & 1u) vis |= ctl.colmask[tl][half];
-      }
+    // All softmax warps meet here, but a column group may have given up and left:
+    // so this wait is bounded too, and each group then decides as one.
+    uint32_t sync_phase = 0;
+    auto meet = [&](bool ok) -> bool {
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl.idx_empty[r]);
-      const uint32_t t_s = t_lane + Cfg::kColS + (t & 1) * 2 * NQ + c0;
-
-      if (!my_abort) my_abort = !kv4::wait(&ctl.s_full[t & 1], (t >> 1) & 1, &ctl.abort);
-      // (asked now, so that the answer is there by the time P^T is written)
-      const bool p_free = t < Cfg::kPBufs ||
-                          mbar_test_wait(&ctl.pv_done[(t - Cfg::kPBufs) & 1], ((t - Cfg::kPBufs) >> 1) & 1);
-      my_abort = __any_sync(0xffffffffu, my_abort);  // tcgen05.ld below is warp-collective
-      tc::fence_after_sync();
-      // x = base-2 score + `add`, -inf where masked
-      float x[HC];
-      auto load_scores = [&](bool with_mu) {
+      if (lane == 0) mbar_arrive(&ctl.sm_sync);
+      ok = wait_warp(&ctl.sm_sync, sync_phase) && ok;
+      sync_phase ^= 1;
+      return !kv4::bar_any(bar_id, 128, !ok);
+    };
+#pragma unroll 1
+    for (int k = 0;; ++k) {
+      // (every warp is done with the last segment's tables)
+      if (!meet(wait_warp(&ctl.seg_full[k & 1], (k >> 1) & 1))) break;
+      const Kv4Segment sg = ctl.seg[k & 1];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl.seg_empty[k & 1]);
+      if (sg.nt == 0) break;
+      const int nrows = sg.nrows;
+      const int64_t grow0 = sg.q0 * a.H + sg.r0;  // global row of the group's first row
+      const int t_end = t + sg.nt;
+      const int ntok = sg.ntok;
+      for (int n = tid; n < NQ; n += kSoftmaxThreads) ctl.nmu[n] = INFINITY;
+      for (int i = tid; i < ntok * CG; i += kSoftmaxThreads) {
+        const int tok = i / CG, h = i % CG;
+        // rows (tok + i0) * H .. + H of the request, as columns of the group
+        const int first = (sg.i0 + tok) * a.H - sg.r0 - h * HC;
+        const int lo = first < 0 ? 0 : first;
+        int hi = first + a.H < HC ? first + a.H : HC;
+        hi = nrows - h * HC < hi ? nrows - h * HC : hi;
+        ctl.colmask[tok][h] = hi > lo ? (0xFFFFFFFFu >> (32 - (hi - lo))) << lo : 0u;
+      }
+      // Queries: warp w turns rows w, w + warps, ... into q_hi and q_lo, two at
+      // a time so that their loads overlap.  Lane l holds channels 8l..8l+7 and
+      // 256+8l.., lanes 0-7 also RoPE channels 8l...  (The last segment's S^T
+      // is complete: this warp has read it.)
+      constexpr int kRowsAtOnce = 2;
+      static_assert(NQ % (kSoftmaxWarps * kRowsAtOnce) == 0, "whole rounds of query rows");
+#pragma unroll 1
+      for (int base = warp; base < NQ; base += kSoftmaxWarps * kRowsAtOnce) {
+        uint4 v[kRowsAtOnce][3];
 #pragma unroll
-        for (int c = 0; c < HC / 16; ++c) {
-          float lo[16];
-          kv4::tmem_ld16(t_s + 16 * c, &x[16 * c]);
-          kv4::tmem_ld16(t_s + NQ + 16 * c, lo);
-          const float4* cs4 = reinterpret_cast<const float4*>(&ctl.cscale[c0 + 16 * c]);
-          const float4* nm4 = reinterpret_cast<const float4*>(&ctl.nmu[c0 + 16 * c]);
+        for (int i = 0; i < kRowsAtOnce; ++i) {
+          const int n = base + i * kSoftmaxWarps;
+          v[i][0] = v[i][1] = v[i][2] = make_uint4(0, 0, 0, 0);
+          if (n < nrows) {
+            const uint4* qn = reinterpret_cast<const uint4*>(a.q_nope + (grow0 + n) * kDLatent);
+            v[i][0] = __ldg(qn + lane);
+            v[i][1] = __ldg(qn + 32 + lane);
+            if (lane < 8) v[i][2] = __ldg(reinterpret_cast<const uint4*>(a.q_rope + (grow0 + n) * kDRope) + lane);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kRowsAtOnce; ++i) {
+          const int n = base + i * kSoftmaxWarps;
+          uint32_t top = 0;  // largest |q| as bits: bf16 magnitudes order as integers
+#pragma unroll
+          for (int c = 0; c < 3; ++c) {
+            const uint32_t u[4] = {v[i][c].x, v[i][c].y, v[i][c].z, v[i][c].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = max(top, max(u[e] & 0x7FFFu, (u[e] >> 16) & 0x7FFFu));
+          }
+          top = __reduce_max_sync(0xffffffffu, top);
+          const int ex = (int)(top >> 7);  // biased exponent of the largest value
+          // 2^x brings it into [128, 256); rows of zeros or denormals use the largest x
+          int x = 7 + 127 - ex;
+          x = x > 126 ? 126 : x;
+          const float up = pow2f(x);
+          // a row with an infinity or a NaN scores NaN
+          if (lane == 0) ctl.cscale[n] = ex == 255 ? NAN : a.scale_log2 * pow2f(-x);
+          // 8 channels -> 8 bytes of q_hi (at `at`) and of q_lo (`lo_off` further on)
+          auto put = [&](uint32_t at, uint32_t lo_off, const uint4& bits) {
+            const uint32_t u[4] = {bits.x, bits.y, bits.z, bits.w};
+            uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float f0 = __uint_as_float(u[e] << 16) * up, f1 = __uint_as_float(u[e] & 0xFFFF0000u) * up;
+              const uint32_t h = kv4::cvt_e4m3x2(f0, f1);
+              const uint32_t hf = kv4::cvt_f16x2_e4m3x2(h);
+              const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hf));
+              const uint32_t l = kv4::cvt_e4m3x2((f0 - back.x) * kQLoScale, (f1 - back.y) * kQLoScale);
+              hi[e >> 1] |= h << (16 * (e & 1));
+              lo[e >> 1] |= l << (16 * (e & 1));
+            }
+            asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at), "r"(hi[0]), "r"(hi[1]) : "memory");
+            asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at + lo_off), "r"(lo[0]), "r"(lo[1]) : "memory");
+          };
+          static_assert(NQ % 8 == 0, "q_lo row n swizzles as q_hi row n");
+          const uint32_t in_block = (((lane & 15) >> 1) ^ (n & 7)) << 4;  // 16-byte chunk, 128-byte swizzle
+          const uint32_t at = sQ + (lane >> 4) * Cfg::kQBlock + n * 128 + in_block + 8 * (lane & 1);
+          put(at, NQ * 128, v[i][0]);
+          put(at + 2 * Cfg::kQBlock, NQ * 128, v[i][1]);
+          if (lane < 8)  // RoPE: rows of 64 bytes, 64-byte swizzle
+            put(sQ + 4 * Cfg::kQBlock + n * 64 + (((lane >> 1) ^ ((n >> 1) & 3)) << 4) + 8 * (lane & 1), NQ * 64,
+                v[i][2]);
+        }
+      }
+      if (!meet(true)) break;  // the tables are written
+      if (lane == 0) mbar_arrive(&ctl.q_full);
+
+      float acc[HC];  // sum of p over this thread's keys
+#pragma unroll
+      for (int c = 0; c < HC; ++c) acc[c] = 0.f;
+      const int t_first = t;
+#pragma unroll 1
+      for (; t < t_end; ++t) {
+        // Which of its columns see this thread's key.
+        uint32_t vis = 0xffffffffu;
+        const int r = t % Cfg::kIndexRing;
+        if (!my_abort) my_abort = !kv4::wait(&ctl.idx_full[r], (t / Cfg::kIndexRing) & 1, &ctl.abort);
+        const bool all_vis = ctl.see_all[r][quad] != 0;
+        if (!all_vis) {
+          vis = 0;
+          for (int tl = 0; tl < ntok; ++tl)
+            if ((ctl.see[r][quad][tl] >> lane) & 1u) vis |= ctl.colmask[tl][half];
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl.idx_empty[r]);
+        const uint32_t t_s = t_lane + Cfg::kColS + (t & 1) * 2 * NQ + c0;
+
+        if (!my_abort) my_abort = !kv4::wait(&ctl.s_full[t & 1], (t >> 1) & 1, &ctl.abort);
+        // (asked now, so that the answer is there by the time P^T is written)
+        const bool p_free = t < Cfg::kPBufs ||
+                            mbar_test_wait(&ctl.pv_done[(t - Cfg::kPBufs) & 1], ((t - Cfg::kPBufs) >> 1) & 1);
+        my_abort = __any_sync(0xffffffffu, my_abort);  // tcgen05.ld below is warp-collective
+        tc::fence_after_sync();
+        // x = base-2 score + nmu (or the score alone), -inf where masked
+        float x[HC];
+        auto load_scores = [&](bool with_mu) {
+          float lo[HC];
+          kv4::tmem_ld16(t_s, x);
+          kv4::tmem_ld16(t_s + NQ, lo);
+          const float4* cs4 = reinterpret_cast<const float4*>(&ctl.cscale[c0]);
+          const float4* nm4 = reinterpret_cast<const float4*>(&ctl.nmu[c0]);
           tc::tmem_wait_ld();
 #pragma unroll
-          for (int k4 = 0; k4 < 4; ++k4) {
+          for (int k4 = 0; k4 < HC / 4; ++k4) {
             const float4 cs = cs4[k4];
             const float4 nm = with_mu ? nm4[k4] : make_float4(0.f, 0.f, 0.f, 0.f);
             const float2 inv = make_float2(1.f / kQLoScale, 1.f / kQLoScale);
-            float* xs = &x[16 * c + 4 * k4];
+            float* xs = &x[4 * k4];
             const float* ls = &lo[4 * k4];
             float2 u = kv4::fma2(make_float2(ls[0], ls[1]), inv, make_float2(xs[0], xs[1]));
             float2 v = kv4::fma2(make_float2(ls[2], ls[3]), inv, make_float2(xs[2], xs[3]));
@@ -827,99 +1056,96 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
             xs[2] = v.x;
             xs[3] = v.y;
           }
-        }
-        if (!all_vis) {
+          if (!all_vis) {
 #pragma unroll
-          for (int k = 0; k < HC; ++k) x[k] = ((vis >> k) & 1u) ? x[k] : -INFINITY;
-        }
-      };
-      bool need = false;
-      if (!my_abort) {
-        load_scores(true);
-        float top = fmaxf(x[0], x[1]);
-#pragma unroll
-        for (int k = 2; k < HC; k += 2) top = kv4::max3(top, x[k], x[k + 1]);
-        need = top > kKv4Limit;
-      } else {
-#pragma unroll
-        for (int k = 0; k < HC; ++k) x[k] = -INFINITY;
-      }
-      bool rescale = false;
-      if (kv4::bar_any(bar_id, 128, need || my_abort || ctl.abort)) {
-        // Rare: a score passed the running max by too much, a column
-        // saw its first key, or a wait gave up.
-        const bool ab = __any_sync(0xffffffffu, my_abort) || ctl.abort;
-        if (lane == 0) ctl.flag[warp] = ab ? 1 : 0;
-        if (!my_abort) load_scores(false);
-        kv4::columns_to_smem<HC, true>(x, &ctl.red[quad][c0], lane);
-        named_bar_sync(bar_id, 128);
-        my_abort = (ctl.flag[4 * half] | ctl.flag[4 * half + 1] | ctl.flag[4 * half + 2] | ctl.flag[4 * half + 3]) != 0;
-        if (my_abort) break;
-        bool raised = false;
-        if (j < HC) {
-          const int n = c0 + j;
-          const float cm = fmaxf(fmaxf(ctl.red[0][n], ctl.red[1][n]), fmaxf(ctl.red[2][n], ctl.red[3][n]));
-          const float old = ctl.nmu[n];
-          float al = 1.f;
-          if (cm + old > kKv4Limit) {  // old = +inf: the first visible key (cm = -inf gives NaN, no)
-            const float nm = (old == INFINITY ? kKv4First : kKv4Top) - cm;
-            al = old == INFINITY ? 0.f : ex2_approx(nm - old);
-            ctl.nmu[n] = nm;
-            raised = true;
+            for (int c = 0; c < HC; ++c) x[c] = ((vis >> c) & 1u) ? x[c] : -INFINITY;
           }
-          ctl.alpha[n] = al;
-        }
-        rescale = kv4::bar_any(bar_id, 128, raised) && t > 0;
+        };
+        bool need = false;
+        if (!my_abort) {
+          load_scores(true);
+          float top = fmaxf(x[0], x[1]);
 #pragma unroll
-        for (int k = 0; k < HC; ++k) {
-          acc[k] *= ctl.alpha[c0 + k];
-          x[k] += ctl.nmu[c0 + k] == INFINITY ? 0.f : ctl.nmu[c0 + k];
+          for (int c = 2; c < HC; c += 2) top = kv4::max3(top, x[c], x[c + 1]);
+          need = top > kKv4Limit;
+        } else {
+#pragma unroll
+          for (int c = 0; c < HC; ++c) x[c] = -INFINITY;
         }
-      }
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl.s_free[t & 1]);  // the S^T buffer may be overwritten
-      // P^T(t) overwrites what O^T(t - kPBufs) read; a rescale of O^T needs all of them done.
-      if (!p_free)
-        my_abort = !kv4::wait(&ctl.pv_done[(t - Cfg::kPBufs) & 1], ((t - Cfg::kPBufs) >> 1) & 1, &ctl.abort);
-      if (Cfg::kPBufs > 1 && rescale && !my_abort)
-        my_abort = !kv4::wait(&ctl.pv_done[(t - 1) & 1], ((t - 1) >> 1) & 1, &ctl.abort);
-      my_abort = __any_sync(0xffffffffu, my_abort);
-      tc::fence_after_sync();
-      if (!my_abort && rescale) {
+        bool rescale = false;
+        if (kv4::bar_any(bar_id, 128, need || my_abort || ctl.abort)) {
+          // Rare: a score passed the running max by too much, a column
+          // saw its first key, or a wait gave up.
+          const bool ab = __any_sync(0xffffffffu, my_abort) || ctl.abort;
+          if (lane == 0) ctl.flag[warp] = ab ? 1 : 0;
+          if (!my_abort) load_scores(false);
+          kv4::columns_to_smem<HC, true>(x, &ctl.red[quad][c0], lane);
+          named_bar_sync(bar_id, 128);
+          my_abort =
+              (ctl.flag[4 * half] | ctl.flag[4 * half + 1] | ctl.flag[4 * half + 2] | ctl.flag[4 * half + 3]) != 0;
+          if (my_abort) break;
+          bool raised = false;
+          if (j < HC) {
+            const int n = c0 + j;
+            const float cm = fmaxf(fmaxf(ctl.red[0][n], ctl.red[1][n]), fmaxf(ctl.red[2][n], ctl.red[3][n]));
+            const float old = ctl.nmu[n];
+            float al = 1.f;
+            if (cm + old > kKv4Limit) {  // old = +inf: the first visible key (cm = -inf gives NaN, no)
+              const float nm = (old == INFINITY ? kKv4First : kKv4Top) - cm;
+              al = old == INFINITY ? 0.f : ex2_approx(nm - old);
+              ctl.nmu[n] = nm;
+              raised = true;
+            }
+            ctl.alpha[n] = al;
+          }
+          rescale = kv4::bar_any(bar_id, 128, raised) && t > t_first;
+#pragma unroll
+          for (int c = 0; c < HC; ++c) {
+            acc[c] *= ctl.alpha[c0 + c];
+            x[c] += ctl.nmu[c0 + c] == INFINITY ? 0.f : ctl.nmu[c0 + c];
+          }
+        }
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl.s_free[t & 1]);  // the S^T buffer may be overwritten
+        // P^T(t) overwrites what O^T(t - kPBufs) read; a rescale of O^T needs all of them done.
+        if (!p_free)
+          my_abort = !kv4::wait(&ctl.pv_done[(t - Cfg::kPBufs) & 1], ((t - Cfg::kPBufs) >> 1) & 1, &ctl.abort);
+        if (Cfg::kPBufs > 1 && rescale && !my_abort)
+          my_abort = !kv4::wait(&ctl.pv_done[(t - 1) & 1], ((t - 1) >> 1) & 1, &ctl.abort);
+        my_abort = __any_sync(0xffffffffu, my_abort);
+        tc::fence_after_sync();
+        if (!my_abort && rescale) {
 #pragma unroll 1
-        for (int m = 0; m < 4 * (Cfg::kConcat ? 2 : 1); ++m) {
-          const uint32_t col = Cfg::kConcat ? (m >> 1) * Cfg::kOStride + (m & 1) * NQ : m * Cfg::kOStride;
+          for (int m = 0; m < 4 * (Cfg::kConcat ? 2 : 1); ++m) {
+            const uint32_t col = Cfg::kConcat ? (m >> 1) * Cfg::kOStride + (m & 1) * NQ : m * Cfg::kOStride;
+#pragma unroll 1
+            for (int c = 0; c < HC; c += 8) {
+              float v[8];
+              tc::tmem_ld8(t_lane + col + c0 + c, v);
+              tc::tmem_wait_ld();
 #pragma unroll
-          for (int c = 0; c < HC / 8; ++c) {
-            float v[8];
-            tc::tmem_ld8(t_lane + col + c0 + 8 * c, v);
-            tc::tmem_wait_ld();
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] *= ctl.alpha[c0 + 8 * c + k];
-            tc::tmem_st8(t_lane + col + c0 + 8 * c, v);
+              for (int e = 0; e < 8; ++e) v[e] *= ctl.alpha[c0 + c + e];
+              tc::tmem_st8(t_lane + col + c0 + c, v);
+            }
           }
+          tc::tmem_wait_st();
         }
-        tc::tmem_wait_st();
-      }
-      if (!my_abort) {
-        const uint32_t dst = sP + (t % Cfg::kPBufs) * Cfg::kPBytes + j * 16;
-#pragma unroll
-        for (int c = 0; c < HC / 16; ++c) {
+        if (!my_abort) {
+          const uint32_t dst = sP + (t % Cfg::kPBufs) * Cfg::kPBytes + j * 16 + half * Cfg::kPCore;
           uint32_t hi[4], lo[4];
 #pragma unroll
           for (int k4 = 0; k4 < 4; ++k4) {
-            const int k = 16 * c + 4 * k4;
-            const float p0 = ex2_approx(x[k + 0]);  // x = -inf (masked) gives 0
-            const float p1 = ex2_approx(x[k + 1]);
-            const float p2 = ex2_approx(x[k + 2]);
-            const float p3 = ex2_approx(x[k + 3]);
-            const float2 a01 = kv4::add2(make_float2(acc[k], acc[k + 1]), make_float2(p0, p1));
-            const float2 a23 = kv4::add2(make_float2(acc[k + 2], acc[k + 3]), make_float2(p2, p3));
-            acc[k + 0] = a01.x;
-            acc[k + 1] = a01.y;
-            acc[k + 2] = a23.x;
-            acc[k + 3] = a23.y;
+            const float p0 = ex2_approx(x[4 * k4 + 0]);  // x = -inf (masked) gives 0
+            const float p1 = ex2_approx(x[4 * k4 + 1]);
+            const float p2 = ex2_approx(x[4 * k4 + 2]);
+            const float p3 = ex2_approx(x[4 * k4 + 3]);
+            const float2 a01 = kv4::add2(make_float2(acc[4 * k4], acc[4 * k4 + 1]), make_float2(p0, p1));
+            const float2 a23 = kv4::add2(make_float2(acc[4 * k4 + 2], acc[4 * k4 + 3]), make_float2(p2, p3));
+            acc[4 * k4 + 0] = a01.x;
+            acc[4 * k4 + 1] = a01.y;
+            acc[4 * k4 + 2] = a23.x;
+            acc[4 * k4 + 3] = a23.y;
             // through halves: 11 bits, far finer than the 8 to 9 kept
             const uint32_t h01 = kv4::cvt_f16x2(p0, p1), h23 = kv4::cvt_f16x2(p2, p3);
             const uint32_t u01 = kv4::cvt_e4m3x2_f16x2(h01), u23 = kv4::cvt_e4m3x2_f16x2(h23);
@@ -934,59 +1160,56 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
               lo[k4] = kv4::cvt_e5m2x2_f16x2(r01) | (kv4::cvt_e5m2x2_f16x2(r23) << 16);
             }
           }
-          kv4::sts128(dst + (c0 / 16 + c) * Cfg::kPCore, hi[0], hi[1], hi[2], hi[3]);
-          kv4::sts128(dst + ((NQ + c0) / 16 + c) * Cfg::kPCore, lo[0], lo[1], lo[2], lo[3]);
+          kv4::sts128(dst, hi[0], hi[1], hi[2], hi[3]);
+          kv4::sts128(dst + (NQ / 16) * Cfg::kPCore, lo[0], lo[1], lo[2], lo[3]);
         }
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0 && !my_abort) mbar_arrive(&ctl.p_full[t & 1]);
       }
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0 && !my_abort) mbar_arrive(&ctl.p_full[t & 1]);
-    }
 
-    // ---- epilogue: l, LSE, O = O^T / l ----------------------------------------
-    named_bar_sync(bar_id, 128);  // (a raise of the last tile has read red)
-    kv4::columns_to_smem<HC, false>(acc, &ctl.red[quad][c0], lane);
-    if (!my_abort) my_abort = !kv4::wait(&ctl.pv_done[(nt - 1) & 1], ((nt - 1) >> 1) & 1, &ctl.abort);
-    tc::fence_after_sync();
-    const bool failed = kv4::bar_any(bar_id, 128, my_abort || ctl.abort);
-    if (j < HC) {
-      const int n = c0 + j;
-      const float l = (ctl.red[0][n] + ctl.red[1][n]) + (ctl.red[2][n] + ctl.red[3][n]);
-      ctl.alpha[n] = l == 0.f ? 0.f : 1.f / l;
-      if (!failed && n < nrows)
-        lse_out[n] = l == 0.f ? -INFINITY : (__log2f(l) - ctl.nmu[n]) * 0.69314718055994530942f;
-    }
-    named_bar_sync(bar_id, 128);
-    if (!failed) {
+      // ---- the segment's end: l, LSE, O = O^T / l -----------------------------
+      named_bar_sync(bar_id, 128);  // (a raise of the last tile has read red)
+      kv4::columns_to_smem<HC, false>(acc, &ctl.red[quad][c0], lane);
+      if (!my_abort) my_abort = !kv4::wait(&ctl.pv_done[(t_end - 1) & 1], ((t_end - 1) >> 1) & 1, &ctl.abort);
+      tc::fence_after_sync();
+      if (kv4::bar_any(bar_id, 128, my_abort || ctl.abort)) {
+        my_abort = true;
+        break;
+      }
+      if (j < HC) {
+        const int n = c0 + j;
+        const float l = (ctl.red[0][n] + ctl.red[1][n]) + (ctl.red[2][n] + ctl.red[3][n]);
+        ctl.alpha[n] = l == 0.f ? 0.f : 1.f / l;
+        if (n < nrows)
+          a.part_lse[sg.prow + n] = l == 0.f ? -INFINITY : (__log2f(l) - ctl.nmu[n]) * 0.69314718055994530942f;
+      }
+      named_bar_sync(bar_id, 128);
       // Thread (quad, lane) holds latent column 128m + j of rows c0..c0+HC: a
       // warp store writes 128 contiguous bytes of one row.  Rows with nothing
       // visible are not written (their LSE is -inf).
-      float* ocol = a.part_o + ((int64_t)s_idx * a.rows_max + grow0) * kDLatent + j;
+      float* ocol = a.part_o + (sg.prow + c0) * kDLatent + j;
 #pragma unroll 1
-      for (int m = 0; m < 4; ++m) {
+      for (int m = 0; m < 4; ++m, ocol += 128) {
+        float v[16];
+        kv4::tmem_ld16(t_lane + m * Cfg::kOStride + c0, v);
+        if constexpr (Cfg::kConcat) {
+          float lo[16];
+          kv4::tmem_ld16(t_lane + m * Cfg::kOStride + NQ + c0, lo);
+          tc::tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < HC / 16; ++c) {
-          float v[16];
-          kv4::tmem_ld16(t_lane + m * Cfg::kOStride + c0 + 16 * c, v);
-          if constexpr (Cfg::kConcat) {
-            float lo[16];
-            kv4::tmem_ld16(t_lane + m * Cfg::kOStride + NQ + c0 + 16 * c, lo);
-            tc::tmem_wait_ld();
+          for (int c = 0; c < 16; ++c) v[c] = fmaf(lo[c], 1.f / kPLoScale, v[c]);
+        } else {
+          tc::tmem_wait_ld();
+        }
 #pragma unroll
-            for (int k = 0; k < 16; ++k) v[k] = fmaf(lo[k], 1.f / kPLoScale, v[k]);
-          } else {
-            tc::tmem_wait_ld();
-          }
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const int n = c0 + 16 * c + k;
-            const float inv = ctl.alpha[n];
-            if (n < nrows && inv != 0.f) ocol[(int64_t)n * kDLatent + 128 * m] = v[k] * inv;
-          }
+        for (int c = 0; c < 16; ++c) {
+          const float inv = ctl.alpha[c0 + c];
+          if (c0 + c < nrows && inv != 0.f) ocol[c * kDLatent] = v[c] * inv;
         }
       }
+      tc::fence_before_sync();  // O^T may be overwritten once P^T of the next tile is written
     }
-    tc::fence_before_sync();
   }
 
   // ---- teardown ---------------------------------------------------------------
