@@ -107,17 +107,32 @@ def _check(rc: int, what: str):
 
 
 def _ptr(t) -> Optional[int]:
-    if t is None:
-        return None
-    if isinstance(t, int):
+    try:
+        return t.data_ptr()
+    except AttributeError:  # None, or an address
         return t
-    return t.data_ptr()
+
+
+_torch = None
+_raw_stream = None
+
+
+def _load_torch():
+    global _torch, _raw_stream
+    import torch
+    # The current stream's handle without a Stream object around it (0.1 against 3 us per call on Grace).
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if _raw_stream is None:
+        def _raw_stream(device):
+            return torch.cuda.current_stream(device).cuda_stream
+    _torch = torch
+    return torch
 
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        torch = _torch or _load_torch()
+        return _raw_stream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -169,24 +184,25 @@ def mla_verify_plan_describe(plan: Plan) -> MlaVerifyPlanInfo:
 def mla_verify_run_varlen(plan: Plan, q_nope_absorbed, q_rope, kv_pool, kv_indptr, kv_indices, qo_indptr,
                           out_cache_loc, custom_mask, mask_indptr, batch: int, sm_scale: float, nsplit: int,
                           workspace, o, lse, stream=None, workspace_bytes: Optional[int] = None):
-    ws_bytes = plan.workspace_bytes if workspace_bytes is None else workspace_bytes
-    rc = load().mla_verify_run_varlen(ctypes.c_void_p(plan.handle), _ptr(q_nope_absorbed), _ptr(q_rope),
-                                      _ptr(kv_pool), _ptr(kv_indptr), _ptr(kv_indices), _ptr(qo_indptr),
-                                      _ptr(out_cache_loc), _ptr(custom_mask), _ptr(mask_indptr), int(batch),
-                                      float(sm_scale), int(nsplit), _ptr(workspace), int(ws_bytes), _ptr(o),
-                                      _ptr(lse), _stream(stream))
-    _check(rc, "mla_verify_run_varlen")
+    rc = (_lib or load()).mla_verify_run_varlen(
+        plan.handle, _ptr(q_nope_absorbed), _ptr(q_rope), _ptr(kv_pool), _ptr(kv_indptr), _ptr(kv_indices),
+        _ptr(qo_indptr), _ptr(out_cache_loc), _ptr(custom_mask), _ptr(mask_indptr), int(batch), float(sm_scale),
+        int(nsplit), _ptr(workspace), plan.workspace_bytes if workspace_bytes is None else int(workspace_bytes),
+        _ptr(o), _ptr(lse), _stream(stream))
+    if rc:
+        _check(rc, "mla_verify_run_varlen")
 
 
 def mla_verify_run(plan: Plan, q_nope_absorbed, q_rope, kv_pool, kv_indptr, kv_indices, out_cache_loc,
                    custom_mask, mask_indptr, batch: int, sm_scale: float, nsplit: int, workspace, o, lse,
                    stream=None, workspace_bytes: Optional[int] = None):
-    ws_bytes = plan.workspace_bytes if workspace_bytes is None else workspace_bytes
-    rc = load().mla_verify_run(ctypes.c_void_p(plan.handle), _ptr(q_nope_absorbed), _ptr(q_rope), _ptr(kv_pool),
-                               _ptr(kv_indptr), _ptr(kv_indices), _ptr(out_cache_loc), _ptr(custom_mask),
-                               _ptr(mask_indptr), int(batch), float(sm_scale), int(nsplit), _ptr(workspace),
-                               int(ws_bytes), _ptr(o), _ptr(lse), _stream(stream))
-    _check(rc, "mla_verify_run")
+    rc = (_lib or load()).mla_verify_run(
+        plan.handle, _ptr(q_nope_absorbed), _ptr(q_rope), _ptr(kv_pool), _ptr(kv_indptr), _ptr(kv_indices),
+        _ptr(out_cache_loc), _ptr(custom_mask), _ptr(mask_indptr), int(batch), float(sm_scale), int(nsplit),
+        _ptr(workspace), plan.workspace_bytes if workspace_bytes is None else int(workspace_bytes), _ptr(o),
+        _ptr(lse), _stream(stream))
+    if rc:
+        _check(rc, "mla_verify_run")
 
 
 def mla_verify_split(plan: Plan, q_nope_absorbed, q_rope, kv_pool, kv_indptr, kv_indices, out_cache_loc,
@@ -249,16 +265,16 @@ def mla_verify_build_tree_mask_varlen(plan: Plan, parents, kv_indptr, qo_indptr,
 
 def _rows_of(x, width: int, n: int, what: str) -> int:
     """Row stride in elements of a bf16 [n, width] tensor (any row stride, contiguous rows)."""
-    import torch
-    if x.dtype != torch.bfloat16 or x.dim() != 2 or tuple(x.shape) != (n, width) or (n > 0 and x.stride(1) != 1):
-        raise ValueError("%s: bf16 [%d, %d] with contiguous rows expected, got %s %s strides %s"
-                         % (what, n, width, x.dtype, tuple(x.shape), x.stride()))
-    return x.stride(0) if n > 1 else max(width, x.stride(0))
+    if x.dtype is (_torch or _load_torch()).bfloat16 and x.shape == (n, width):
+        row, col = x.stride()
+        if col == 1 or n == 0:
+            return row if n > 1 else max(width, row // 8 * 8)
+    raise ValueError("%s: bf16 [%d, %d] with contiguous rows expected, got %s %s strides %s"
+                     % (what, n, width, x.dtype, tuple(x.shape), x.stride()))
 
 
 def _int32(x, what: str):
-    import torch
-    if x.dtype != torch.int32 or not x.is_contiguous():
+    if x.dtype is not (_torch or _load_torch()).int32 or not x.is_contiguous():
         raise ValueError("%s: a contiguous int32 tensor expected, got %s strides %s" % (what, x.dtype, x.stride()))
 
 
@@ -266,20 +282,23 @@ def mla_verify_store_kv4(plan: Plan, latent, rope, slots, kv_pool, workspace, st
     """Code tokens (latent bf16 [n, 512], rope bf16 [n, 64], any row strides) into rows ``slots`` of a 4-bit pool."""
     n = slots.numel()
     _int32(slots, "slots")
-    rc = load().mla_verify_store_kv4(ctypes.c_void_p(plan.handle), _ptr(latent), _rows_of(latent, 512, n, "latent"),
-                                     _ptr(rope), _rows_of(rope, 64, n, "rope"), _ptr(slots), n, _ptr(kv_pool),
-                                     _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
-    _check(rc, "mla_verify_store_kv4")
+    rc = (_lib or load()).mla_verify_store_kv4(
+        plan.handle, latent.data_ptr(), _rows_of(latent, 512, n, "latent"), rope.data_ptr(),
+        _rows_of(rope, 64, n, "rope"), slots.data_ptr(), n, _ptr(kv_pool), workspace.data_ptr(), workspace.nbytes,
+        _stream(stream))
+    if rc:
+        _check(rc, "mla_verify_store_kv4")
 
 
 def mla_verify_load_kv4(plan: Plan, kv_pool, slots, latent, rope, workspace, stream=None):
     """Rows ``slots`` of a 4-bit pool as bf16, into latent [n, 512] and rope [n, 64] (any row strides)."""
     n = slots.numel()
     _int32(slots, "slots")
-    rc = load().mla_verify_load_kv4(ctypes.c_void_p(plan.handle), _ptr(kv_pool), _ptr(slots), n, _ptr(latent),
-                                    _rows_of(latent, 512, n, "latent"), _ptr(rope), _rows_of(rope, 64, n, "rope"),
-                                    _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
-    _check(rc, "mla_verify_load_kv4")
+    rc = (_lib or load()).mla_verify_load_kv4(
+        plan.handle, _ptr(kv_pool), slots.data_ptr(), n, latent.data_ptr(), _rows_of(latent, 512, n, "latent"),
+        rope.data_ptr(), _rows_of(rope, 64, n, "rope"), workspace.data_ptr(), workspace.nbytes, _stream(stream))
+    if rc:
+        _check(rc, "mla_verify_load_kv4")
 
 
 def mla_verify_build_slots(plan: Plan, seq_lens, new_lens, batch: int, page_size: int, block_table, free_pages,
@@ -287,22 +306,24 @@ def mla_verify_build_slots(plan: Plan, seq_lens, new_lens, batch: int, page_size
     """Block tables and slot maps of a step from the requests' lengths (new_lens None: the plan's q_len each).
 
     block_table is int32 [>= batch, max_pages]; the capacities are the index tensors' lengths."""
-    for name, x in (("seq_lens", seq_lens), ("new_lens", new_lens), ("block_table", block_table),
-                    ("free_pages", free_pages), ("pages_used", pages_used), ("kv_indptr", kv_indptr),
-                    ("kv_indices", kv_indices), ("qo_indptr", qo_indptr), ("out_cache_loc", out_cache_loc)):
-        if x is not None:
-            _int32(x, name)
-    if block_table.dim() != 2 or min(block_table.shape[0], seq_lens.numel(), kv_indptr.numel() - 1,
-                                     qo_indptr.numel() - 1) < batch or (new_lens is not None
-                                                                        and new_lens.numel() < batch):
+    i32 = (_torch or _load_torch()).int32
+    for x in (seq_lens, block_table, free_pages, pages_used, kv_indptr, kv_indices, qo_indptr, out_cache_loc):
+        if x.dtype is not i32 or not x.is_contiguous():
+            raise ValueError("contiguous int32 tensors expected, got %s strides %s" % (x.dtype, x.stride()))
+    if new_lens is not None:
+        _int32(new_lens, "new_lens")
+        if new_lens.numel() < batch:
+            raise ValueError("new_lens is too short for %d requests" % batch)
+    rows, max_pages = block_table.shape
+    if rows < batch or seq_lens.numel() < batch or kv_indptr.numel() <= batch or qo_indptr.numel() <= batch:
         raise ValueError("an array is too short for %d requests" % batch)
-    rc = load().mla_verify_build_slots(ctypes.c_void_p(plan.handle), _ptr(seq_lens), _ptr(new_lens), int(batch),
-                                       int(page_size), _ptr(block_table), block_table.shape[1], _ptr(free_pages),
-                                       free_pages.numel(), _ptr(pages_used), _ptr(kv_indptr), _ptr(kv_indices),
-                                       kv_indices.numel(), _ptr(qo_indptr), _ptr(out_cache_loc),
-                                       out_cache_loc.numel(), _ptr(workspace),
-                                       workspace.numel() * workspace.element_size(), _stream(stream))
-    _check(rc, "mla_verify_build_slots")
+    rc = (_lib or load()).mla_verify_build_slots(
+        plan.handle, seq_lens.data_ptr(), _ptr(new_lens), int(batch), int(page_size), block_table.data_ptr(),
+        max_pages, free_pages.data_ptr(), free_pages.numel(), pages_used.data_ptr(), kv_indptr.data_ptr(),
+        kv_indices.data_ptr(), kv_indices.numel(), qo_indptr.data_ptr(), out_cache_loc.data_ptr(),
+        out_cache_loc.numel(), workspace.data_ptr(), workspace.nbytes, _stream(stream))
+    if rc:
+        _check(rc, "mla_verify_build_slots")
 
 
 def mla_verify_workspace_init(plan: Plan, workspace, stream=None):

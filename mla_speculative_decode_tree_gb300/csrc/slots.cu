@@ -22,7 +22,7 @@ namespace mlav {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPerThread = 4;  // outputs per thread and pass, 32 apart within a warp's 128
+constexpr int kPerThread = 4;  // consecutive outputs per thread: a warp's pass covers 128
 
 struct SlotsDev {
   SlotsArgs a;
@@ -39,7 +39,9 @@ struct SlotsDev {
     return v > 0 ? v : 0;
   }
   __device__ __forceinline__ int64_t page_of(int64_t pos) const {
-    return a.page_shift >= 0 ? pos >> a.page_shift : (int64_t)((uint64_t)pos / (uint32_t)a.page_size);
+    if (a.page_shift >= 0) return pos >> a.page_shift;
+    if ((pos >> 32) == 0) return (uint32_t)pos / (uint32_t)a.page_size;
+    return (int64_t)((uint64_t)pos / (uint32_t)a.page_size);
   }
   __device__ __forceinline__ int64_t pages(int64_t tokens) const { return page_of(tokens + a.page_size - 1); }
 
@@ -56,81 +58,109 @@ struct SlotsDev {
     return lo;
   }
 
-  // Pool row of position pos of request b, -1 where there is none.
-  __device__ __forceinline__ int32_t row(int b, int64_t pos, uint32_t& status) const {
-    const int64_t c = page_of(pos);
+  // Pool row of position pos, which lies on `page`, the request's c-th; -1 where there is none.
+  __device__ __forceinline__ int32_t row_on(int32_t page, int64_t c, int64_t pos, uint32_t& status) const {
+    const int64_t r = (int64_t)page * a.page_size + (pos - c * a.page_size);
+    if (page >= 0 && r < a.pool_rows) return (int32_t)r;
+    status |= kStatusBadRow;
+    return -1;
+  }
+
+  // Where the page of position pos of request b is written, its c-th page; null where there is none.
+  __device__ __forceinline__ const int32_t* page_at(int b, int64_t pos, int64_t& c) const {
+    c = page_of(pos);
     const int64_t have = pages(kv[b + 1] - kv[b]);
-    int64_t page = -1;
-    if (c >= a.max_pages) {
-      status |= kStatusNoPage;
-    } else if (c < have) {
-      page = a.block_table[(int64_t)b * a.max_pages + c];
-      if (page < 0) status |= kStatusBadRow;
-    } else {
-      const int64_t f = (int64_t)fresh[b] + (c - have);
-      if (f < a.num_free) {
-        page = a.free_pages[f];
-        if (page < 0) status |= kStatusBadRow;
+    if (c >= a.max_pages) return nullptr;
+    if (c < have) return a.block_table + (int64_t)b * a.max_pages + c;
+    const int64_t f = (int64_t)fresh[b] + (c - have);
+    return f < a.num_free ? a.free_pages + f : nullptr;
+  }
+
+  // Rows of cached positions pos .. pos+3 of request b: one table entry where they share a page.
+  __device__ __forceinline__ int4 rows4(int b, int pos, uint32_t& status) const {
+    const int32_t* table = a.block_table + (int64_t)b * a.max_pages;
+    int32_t r[kPerThread], page0 = -1;
+    int c0 = -1;
+#pragma unroll
+    for (int k = 0; k < kPerThread; ++k) {
+      const int c = a.page_shift >= 0 ? (pos + k) >> a.page_shift : (int)((uint32_t)(pos + k) / (uint32_t)a.page_size);
+      int32_t page = page0;
+      if (c != c0) {
+        page = c < a.max_pages ? table[c] : -1;
+        if (k == 0) {
+          c0 = c;
+          page0 = page;
+        }
+      }
+      if (c < a.max_pages) {
+        r[k] = row_on(page, c, pos + k, status);
       } else {
+        r[k] = -1;
         status |= kStatusNoPage;
       }
     }
-    if (page < 0) return -1;
-    const int64_t r = page * a.page_size + (pos - c * a.page_size);
-    if (r >= a.pool_rows) {
-      status |= kStatusBadRow;
-      return -1;
-    }
-    return (int32_t)r;
+    return make_int4(r[0], r[1], r[2], r[3]);
   }
 };
 
-// Exclusive scan of value(b), b < batch, into out[0 .. batch], by the block;
-// sums saturate at 2^31 - 1.
-template <typename F>
-__device__ __forceinline__ void block_scan(int batch, int32_t* out, uint32_t* warp_sum, F value) {
+__device__ __forceinline__ uint32_t add_sat(uint32_t x, uint32_t y) {  // both at most 2^31 - 1
+  const uint32_t s = x + y;
+  return s > 0x7FFFFFFFu ? 0x7FFFFFFFu : s;
+}
+
+// The three exclusive scans, by the block: kThreads requests at a time, all
+// three sums together (one pair of barriers); sums stop at 2^31 - 1.
+__device__ __forceinline__ void scan_requests(const SlotsDev& d) {
+  __shared__ uint32_t warp_sum[3][kThreads / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  auto add = [](uint32_t x, uint32_t y) {
-    const uint32_t s = x + y;  // both at most 2^31 - 1
-    return s > 0x7FFFFFFFu ? 0x7FFFFFFFu : s;
-  };
-  uint32_t carry = 0;
-  for (int base = 0; base < batch; base += kThreads) {
+  int32_t* const out[3] = {d.kv, d.qo, d.fresh};
+  uint32_t carry[3] = {0, 0, 0};
+#pragma unroll 1
+  for (int base = 0; base < d.a.batch; base += kThreads) {
     const int b = base + threadIdx.x;
-    const uint32_t v = b < batch ? (uint32_t)value(b) : 0u;
-    uint32_t x = v;
+    uint32_t x[3] = {0, 0, 0};
+    if (b < d.a.batch) {
+      const int P = d.seq_len(b), T = d.new_len(b);
+      x[0] = (uint32_t)P;
+      x[1] = (uint32_t)T;
+      x[2] = (uint32_t)(d.pages((int64_t)P + T) - d.pages(P));
+    }
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-      const uint32_t y = __shfl_up_sync(0xffffffffu, x, off);
-      if (lane >= off) x = add(x, y);
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, x[k], off);
+        if (lane >= off) x[k] = add_sat(x[k], y);
+      }
     }
-    if (lane == 31) warp_sum[warp] = x;
+    if (lane == 31) {
+#pragma unroll
+      for (int k = 0; k < 3; ++k) warp_sum[k][warp] = x[k];
+    }
     __syncthreads();
-    uint32_t before = carry;
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w)
-      if (w < warp) before = add(before, warp_sum[w]);
-    if (b < batch) out[b + 1] = (int32_t)add(before, x);
+    for (int k = 0; k < 3; ++k) {
+      uint32_t before = carry[k];
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) carry = add(carry, warp_sum[w]);
+      for (int w = 0; w < kThreads / 32; ++w) {
+        const uint32_t s = warp_sum[k][w];
+        if (w < warp) before = add_sat(before, s);
+        carry[k] = add_sat(carry[k], s);
+      }
+      if (b < d.a.batch) out[k][b + 1] = (int32_t)add_sat(before, x[k]);
+    }
     __syncthreads();
   }
-  if (threadIdx.x == 0) out[0] = 0;
+  if (threadIdx.x < 3) out[threadIdx.x][0] = 0;
+  __syncthreads();
 }
 
 __global__ void __launch_bounds__(kThreads) slots_kernel(SlotsArgs args) {
   extern __shared__ int32_t scans[];
-  __shared__ uint32_t warp_sum[kThreads / 32];
   const int n1 = args.batch + 1;
   const SlotsDev d{args, scans, scans + n1, scans + 2 * n1};
   const SlotsArgs& a = d.a;
-  block_scan(a.batch, d.kv, warp_sum, [&](int b) { return d.seq_len(b); });
-  block_scan(a.batch, d.qo, warp_sum, [&](int b) { return d.new_len(b); });
-  block_scan(a.batch, d.fresh, warp_sum, [&](int b) {
-    const int64_t P = d.seq_len(b);
-    return (int32_t)(d.pages(P + d.new_len(b)) - d.pages(P));
-  });
-  __syncthreads();
+  scan_requests(d);
 
   uint32_t status = 0;
   const int64_t K = d.kv[a.batch], N = d.qo[a.batch], F = d.fresh[a.batch];
@@ -152,26 +182,50 @@ __global__ void __launch_bounds__(kThreads) slots_kernel(SlotsArgs args) {
   const int lane = threadIdx.x & 31;
   // One pass over both maps: chunks of 128 entries, the prefixes' first.
   const int64_t c_kv = (n_kv + 127) / 128, c_loc = (n_loc + 127) / 128;
+  const bool wide = (reinterpret_cast<uintptr_t>(a.kv_indices) & 15) == 0;
   for (int64_t c = warp0; c < c_kv + c_loc; c += warps) {
     const bool pre = c < c_kv;
     const int32_t* scan = pre ? d.kv : d.qo;
     int32_t* out = pre ? a.kv_indices : a.out_cache_loc;
     const int64_t n = pre ? n_kv : n_loc;
-    const int64_t x0 = (pre ? c : c - c_kv) * 128 + lane;
-    int32_t r[kPerThread];
+    const int64_t first = (pre ? c : c - c_kv) * 128;
+    const int64_t x0 = first + kPerThread * lane;
+    // The chunk's first entry finds its request for the warp; only a chunk that
+    // crosses into other requests searches again.
+    const int b0 = d.owner(scan, first);
+    if (pre && first + 128 <= n && first + 128 <= scan[b0 + 1]) {
+      const int4 r = d.rows4(b0, (int)(x0 - scan[b0]), status);
+      if (wide) {
+        *reinterpret_cast<int4*>(out + x0) = r;
+      } else {
+        out[x0] = r.x;
+        out[x0 + 1] = r.y;
+        out[x0 + 2] = r.z;
+        out[x0 + 3] = r.w;
+      }
+      continue;
+    }
+    const int32_t* at[kPerThread];
+    int64_t pos[kPerThread], page_no[kPerThread];
 #pragma unroll
     for (int k = 0; k < kPerThread; ++k) {
-      const int64_t x = x0 + 32 * k;
-      r[k] = -1;
+      const int64_t x = first + lane + 32 * k;
+      at[k] = nullptr;
       if (x < n) {
         const int b = d.owner(scan, x);
-        const int64_t pos = x - scan[b] + (pre ? 0 : d.kv[b + 1] - d.kv[b]);
-        r[k] = d.row(b, pos, status);
+        pos[k] = x - scan[b] + (pre ? 0 : d.kv[b + 1] - d.kv[b]);
+        at[k] = d.page_at(b, pos[k], page_no[k]);
+        if (!at[k]) status |= kStatusNoPage;
       }
     }
+    int32_t page[kPerThread];
 #pragma unroll
-    for (int k = 0; k < kPerThread; ++k)
-      if (x0 + 32 * k < n) out[x0 + 32 * k] = r[k];
+    for (int k = 0; k < kPerThread; ++k) page[k] = at[k] ? *at[k] : -1;
+#pragma unroll
+    for (int k = 0; k < kPerThread; ++k) {
+      const int64_t x = first + lane + 32 * k;
+      if (x < n) out[x] = at[k] ? d.row_on(page[k], page_no[k], pos[k], status) : -1;
+    }
   }
   // The fresh pages' table entries.
   for (int64_t f = (int64_t)blockIdx.x * kThreads + threadIdx.x; f < F; f += (int64_t)gridDim.x * kThreads) {

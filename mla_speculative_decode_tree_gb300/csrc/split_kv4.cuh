@@ -612,10 +612,10 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
     const int key0 = 8 * w + (lane >> 2);
     const uint32_t off0 = key0 * 128 + (((2 * q) ^ (key0 & 7)) << 4);
     const uint32_t off1 = key0 * 128 + (((2 * q + 1) ^ (key0 & 7)) << 4);
-    const uint8_t* row[2];
-    int32_t id[2];
+    int32_t row[2], id[2];  // pool rows of the tile being loaded, and of the one after
     uint4 code[2][kKv4Blocks], scale[2];
     bool ok = true, more = true;
+    auto at = [&](int h, int byte) { return a.kv4_pool + 16 * q + byte + (uint64_t)(uint32_t)row[h] * kKv4RowBytes; };
     // Pool rows of the own keys of tile t, if there is one.  (A key without a
     // row reads row 0: its weight is 0, and a 4-bit value is finite whatever the
     // bytes.)
@@ -632,11 +632,11 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
     if (more) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        row[h] = a.kv4_pool + (int64_t)id[h] * kKv4RowBytes + 16 * q;
-        scale[h] = kv4::ldg_stream(row[h] + kKv4ScaleOff);
+        row[h] = id[h];
+        scale[h] = kv4::ldg_stream(at(h, kKv4ScaleOff));
 #pragma unroll
         for (int u = 0; u < kKv4Blocks; ++u)
-          code[h][kv4::block_of(u)] = kv4::ldg_stream(row[h] + 64 * kv4::block_of(u));
+          code[h][kv4::block_of(u)] = kv4::ldg_stream(at(h, 64 * kv4::block_of(u)));
       }
     }
     bool have = more;
@@ -649,8 +649,8 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         kv4::make_valid(scale[h]);
-        row[h] = a.kv4_pool + (int64_t)id[h] * kKv4RowBytes + 16 * q;
-        next_scale[h] = kv4::ldg_stream(row[h] + kKv4ScaleOff);
+        row[h] = id[h];
+        next_scale[h] = kv4::ldg_stream(at(h, kKv4ScaleOff));
       }
 #pragma unroll
       for (int u = 0; u < kKv4Blocks; ++u) {
@@ -677,8 +677,8 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
           }
           __syncwarp();
           if (lane == 0 && !(a.test_stall && t + u == 0)) mbar_arrive(&ctl.full[sl]);
-          code[0][m] = kv4::ldg_stream(row[0] + 64 * m);
-          code[1][m] = kv4::ldg_stream(row[1] + 64 * m);
+          code[0][m] = kv4::ldg_stream(at(0, 64 * m));
+          code[1][m] = kv4::ldg_stream(at(1, 64 * m));
         }
       }
       have = more;
@@ -919,9 +919,7 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
     for (int k = 0;; ++k) {
       // (every warp is done with the last segment's tables)
       if (!meet(wait_warp(&ctl.seg_full[k & 1], (k >> 1) & 1))) break;
-      const Kv4Segment sg = ctl.seg[k & 1];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl.seg_empty[k & 1]);
+      const Kv4Segment& sg = ctl.seg[k & 1];
       if (sg.nt == 0) break;
       const int nrows = sg.nrows;
       const int64_t grow0 = sg.q0 * a.H + sg.r0;  // global row of the group's first row
@@ -1209,6 +1207,8 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
         }
       }
       tc::fence_before_sync();  // O^T may be overwritten once P^T of the next tile is written
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl.seg_empty[k & 1]);
     }
   }
 
