@@ -184,11 +184,15 @@ def mla_verify_plan_describe(plan: Plan) -> MlaVerifyPlanInfo:
 def mla_verify_run_varlen(plan: Plan, q_nope_absorbed, q_rope, kv_pool, kv_indptr, kv_indices, qo_indptr,
                           out_cache_loc, custom_mask, mask_indptr, batch: int, sm_scale: float, nsplit: int,
                           workspace, o, lse, stream=None, workspace_bytes: Optional[int] = None):
+    args = (q_nope_absorbed, q_rope, kv_pool, kv_indptr, kv_indices, qo_indptr, out_cache_loc, custom_mask, mask_indptr,
+            workspace, o, lse)
+    try:  # all tensors, as a rule
+        qn, qr, kv, kp, ki, qo, loc, cm, mp, ws, po, pl = [t.data_ptr() for t in args]
+    except AttributeError:
+        qn, qr, kv, kp, ki, qo, loc, cm, mp, ws, po, pl = map(_ptr, args)
     rc = (_lib or load()).mla_verify_run_varlen(
-        plan.handle, _ptr(q_nope_absorbed), _ptr(q_rope), _ptr(kv_pool), _ptr(kv_indptr), _ptr(kv_indices),
-        _ptr(qo_indptr), _ptr(out_cache_loc), _ptr(custom_mask), _ptr(mask_indptr), int(batch), float(sm_scale),
-        int(nsplit), _ptr(workspace), plan.workspace_bytes if workspace_bytes is None else int(workspace_bytes),
-        _ptr(o), _ptr(lse), _stream(stream))
+        plan.handle, qn, qr, kv, kp, ki, qo, loc, cm, mp, int(batch), float(sm_scale), int(nsplit), ws,
+        plan.workspace_bytes if workspace_bytes is None else int(workspace_bytes), po, pl, _stream(stream))
     if rc:
         _check(rc, "mla_verify_run_varlen")
 

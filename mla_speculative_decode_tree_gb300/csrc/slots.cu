@@ -21,9 +21,12 @@
 namespace mlav {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
 constexpr int kPerThread = 4;  // consecutive outputs per thread: a warp's pass covers 128
 
+// kPow2: pages of 2^page_shift rows.
+template <bool kPow2>
 struct SlotsDev {
   SlotsArgs a;
   int32_t* kv;     // shared: exclusive scans, [batch + 1] each
@@ -39,7 +42,7 @@ struct SlotsDev {
     return v > 0 ? v : 0;
   }
   __device__ __forceinline__ int64_t page_of(int64_t pos) const {
-    if (a.page_shift >= 0) return pos >> a.page_shift;
+    if (kPow2) return pos >> a.page_shift;
     if ((pos >> 32) == 0) return (uint32_t)pos / (uint32_t)a.page_size;
     return (int64_t)((uint64_t)pos / (uint32_t)a.page_size);
   }
@@ -83,7 +86,7 @@ struct SlotsDev {
     int c0 = -1;
 #pragma unroll
     for (int k = 0; k < kPerThread; ++k) {
-      const int c = a.page_shift >= 0 ? (pos + k) >> a.page_shift : (int)((uint32_t)(pos + k) / (uint32_t)a.page_size);
+      const int c = kPow2 ? (pos + k) >> a.page_shift : (int)((uint32_t)(pos + k) / (uint32_t)a.page_size);
       int32_t page = page0;
       if (c != c0) {
         page = c < a.max_pages ? table[c] : -1;
@@ -108,10 +111,23 @@ __device__ __forceinline__ uint32_t add_sat(uint32_t x, uint32_t y) {  // both a
   return s > 0x7FFFFFFFu ? 0x7FFFFFFFu : s;
 }
 
+// Inclusive scans of three values over the warp.
+__device__ __forceinline__ void scan3(uint32_t (&x)[3], int lane) {
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, x[k], off);
+      if (lane >= off) x[k] = add_sat(x[k], y);
+    }
+  }
+}
+
 // The three exclusive scans, by the block: kThreads requests at a time, all
-// three sums together (one pair of barriers); sums stop at 2^31 - 1.
-__device__ __forceinline__ void scan_requests(const SlotsDev& d) {
-  __shared__ uint32_t warp_sum[3][kThreads / 32];
+// three sums together; sums stop at 2^31 - 1.
+template <bool kPow2>
+__device__ __forceinline__ void scan_requests(const SlotsDev<kPow2>& d) {
+  __shared__ uint32_t warp_sum[3][kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int32_t* const out[3] = {d.kv, d.qo, d.fresh};
   uint32_t carry[3] = {0, 0, 0};
@@ -125,29 +141,21 @@ __device__ __forceinline__ void scan_requests(const SlotsDev& d) {
       x[1] = (uint32_t)T;
       x[2] = (uint32_t)(d.pages((int64_t)P + T) - d.pages(P));
     }
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-#pragma unroll
-      for (int k = 0; k < 3; ++k) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, x[k], off);
-        if (lane >= off) x[k] = add_sat(x[k], y);
-      }
-    }
+    scan3(x, lane);
     if (lane == 31) {
 #pragma unroll
       for (int k = 0; k < 3; ++k) warp_sum[k][warp] = x[k];
     }
     __syncthreads();
+    uint32_t sum[3];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) sum[k] = lane < kWarps ? warp_sum[k][lane] : 0u;
+    scan3(sum, lane);
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
-      uint32_t before = carry[k];
-#pragma unroll
-      for (int w = 0; w < kThreads / 32; ++w) {
-        const uint32_t s = warp_sum[k][w];
-        if (w < warp) before = add_sat(before, s);
-        carry[k] = add_sat(carry[k], s);
-      }
-      if (b < d.a.batch) out[k][b + 1] = (int32_t)add_sat(before, x[k]);
+      const uint32_t before = __shfl_sync(0xffffffffu, sum[k], warp > 0 ? warp - 1 : 0);
+      if (b < d.a.batch) out[k][b + 1] = (int32_t)add_sat(add_sat(carry[k], warp > 0 ? before : 0u), x[k]);
+      carry[k] = add_sat(carry[k], __shfl_sync(0xffffffffu, sum[k], 31));
     }
     __syncthreads();
   }
@@ -155,10 +163,11 @@ __device__ __forceinline__ void scan_requests(const SlotsDev& d) {
   __syncthreads();
 }
 
+template <bool kPow2>
 __global__ void __launch_bounds__(kThreads) slots_kernel(SlotsArgs args) {
   extern __shared__ int32_t scans[];
   const int n1 = args.batch + 1;
-  const SlotsDev d{args, scans, scans + n1, scans + 2 * n1};
+  const SlotsDev<kPow2> d{args, scans, scans + n1, scans + 2 * n1};
   const SlotsArgs& a = d.a;
   scan_requests(d);
 
@@ -243,16 +252,17 @@ cudaError_t launch_slots(const SlotsArgs& a, cudaStream_t stream) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
+  auto kernel = a.page_shift >= 0 ? slots_kernel<true> : slots_kernel<false>;
   const int smem = 3 * (a.batch + 1) * (int)sizeof(int32_t);
-  if (smem > 48 * 1024) {
-    e = cudaFuncSetAttribute(slots_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (smem > 47 * 1024) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }
   // The totals are on the device; the arrays' capacities bound them.
   const int64_t want = (a.kv_capacity + a.loc_capacity + kThreads * kPerThread - 1) / (kThreads * kPerThread);
-  const int64_t cap = (int64_t)sms * 4;
+  const int64_t cap = (int64_t)sms * 2;
   const int grid = (int)(want < 1 ? 1 : want < cap ? want : cap);
-  slots_kernel<<<grid, kThreads, smem, stream>>>(a);
+  kernel<<<grid, kThreads, smem, stream>>>(a);
   return cudaGetLastError();
 }
 
