@@ -119,20 +119,28 @@ struct Kv4Segment {
   int32_t nt;          // tiles
   int32_t tile0;       // the first one
   int32_t rot;         // tile t of the segment is tile0 + (t + rot) % nt
-  int32_t batch;       // request
   int32_t n_tokens;    // its query tokens
   int32_t i0, ntok;    // tokens the row group spans
   int32_t r0, nrows;   // its rows within the request
   int32_t keys;        // L: keys of the request
+  int32_t prefix;      // P
+  int32_t kv0;         // its place in kv_indices
+  int32_t mask0;       // its place in the mask (bits)
   int64_t q0;          // first token row of the request
   int64_t prow;        // row of the partial outputs
+};
+struct Kv4Request {
+  int32_t n, keys, prefix, kv0, mask0, groups;
+  int64_t q0;
 };
 // Where the hand-out of segments stands (kv4::next_segment).
 struct Kv4Cursor {
   int64_t x, x_end, piece;  // own piece of the axis
   int64_t carry;            // axis before request `base`
-  int32_t base;
+  int32_t base;             // the 32 requests in `req` and `end`
   int32_t done;
+  Kv4Request req[32];
+  int64_t end[32];          // inclusive scan of their lengths on the axis, from `carry`
 };
 constexpr uint32_t kTileFirst = 1, kTileEnd = 2;  // first tile of a segment; no tile, the end of all
 
@@ -412,24 +420,19 @@ __device__ __forceinline__ void columns_to_smem(const float (&x)[HC], float* dst
 // first tile) + b * groups_max + g on, by CTA, which no two segments share.
 // Otherwise: one chunk of one row group per CTA (the grid), or none.
 struct Schedule {
-  // Query tokens and keys of request b, and its length on the axis.
-  struct Req {
-    int64_t q0;
-    int n, keys, tiles, groups;
-    int64_t cost;
-  };
-  static __device__ __forceinline__ Req request(const SplitArgs& a, int nq, int b) {
-    Req r = {};
-    if (b < a.batch) {
-      const RequestTokens rq = request_tokens(a, b);
-      r.q0 = rq.q0;
-      r.n = rq.n;
-      r.keys = a.kv_indptr[b + 1] - a.kv_indptr[b] + rq.n;
-      r.tiles = (r.keys + kKeysPerTile - 1) / kKeysPerTile;
-      r.groups = (rq.n * a.H + nq - 1) / nq;
-      r.cost = (int64_t)r.groups * (r.tiles + a.seg_cost);
-    }
-    return r;
+  // Request b and its length on the axis (none past the batch).
+  static __device__ __forceinline__ int64_t request(const SplitArgs& a, int nq, int b, Kv4Request& r) {
+    r = {};
+    if (b >= a.batch) return 0;
+    const RequestTokens rq = request_tokens(a, b);
+    r.kv0 = a.kv_indptr[b];
+    r.prefix = a.kv_indptr[b + 1] - r.kv0;
+    r.mask0 = a.mask_indptr[b];
+    r.q0 = rq.q0;
+    r.n = rq.n;
+    r.keys = r.prefix + rq.n;
+    r.groups = (rq.n * a.H + nq - 1) / nq;
+    return (int64_t)r.groups * ((r.keys + kKeysPerTile - 1) / kKeysPerTile + a.seg_cost);
   }
   static __device__ __forceinline__ int64_t scan(int64_t v, int lane) {  // inclusive, over the warp
 #pragma unroll 1
@@ -439,107 +442,130 @@ struct Schedule {
     }
     return v;
   }
+  // (numbers below 2^31, as a rule: a tenth of the 64-bit division's time)
+  static __device__ __forceinline__ int64_t divide(int64_t x, int64_t y) {
+    return ((x | y) >> 32) == 0 ? (int64_t)((uint32_t)x / (uint32_t)y) : x / y;
+  }
+  // Requests base .. base+31 into the cursor; returns the axis after them.
+  static __device__ __forceinline__ int64_t fetch(const SplitArgs& a, int nq, int lane, int base, int64_t carry,
+                                                  Kv4Cursor& c) {
+    Kv4Request r;
+    const int64_t incl = carry + scan(request(a, nq, base + lane, r), lane);
+    c.req[lane] = r;
+    c.end[lane] = incl;
+    if (lane == 0) {
+      c.base = base;
+      c.carry = carry;
+    }
+    __syncwarp();
+    return __shfl_sync(0xffffffffu, incl, 31);
+  }
 
   static __device__ __forceinline__ void start(const SplitArgs& a, int nq, int lane, Kv4Cursor& c) {
     int64_t total = 0, piece = 1;
     if (a.seg_table) {
 #pragma unroll 1
-      for (int b = 0; b < a.batch; b += 32)
-        total += __shfl_sync(0xffffffffu, scan(request(a, nq, b + lane).cost, lane), 31);
-      piece = (total + gridDim.x - 1) / gridDim.x;
+      for (int b = 0; b < a.batch; b += 32) total = fetch(a, nq, lane, b, total, c);
+      piece = divide(total + gridDim.x - 1, gridDim.x);
       piece = piece < 1 ? 1 : piece;
+      if (a.batch > 32) fetch(a, nq, lane, 0, 0, c);
+    } else {
+      fetch(a, nq, lane, blockIdx.z, 0, c);  // (only its own request counts)
     }
     if (lane == 0) {
       const int64_t x = blockIdx.x * piece;
-      c = {x, x + piece < total ? x + piece : total, piece, 0, 0, 0};
+      c.x = x;
+      c.x_end = x + piece < total ? x + piece : total;
+      c.piece = piece;
+      c.done = 0;
     }
     __syncwarp();
   }
 
-  static __device__ __forceinline__ void rows(const SplitArgs& a, int nq, int g, Kv4Segment& s) {
+  static __device__ __forceinline__ void rows(const SplitArgs& a, int nq, int g, const Kv4Request& r, Kv4Segment& s) {
+    s.q0 = r.q0;
+    s.n_tokens = r.n;
+    s.keys = r.keys;
+    s.prefix = r.prefix;
+    s.kv0 = r.kv0;
+    s.mask0 = r.mask0;
     s.r0 = g * nq;
-    s.nrows = s.n_tokens * a.H - s.r0 < nq ? s.n_tokens * a.H - s.r0 : nq;
+    s.nrows = r.n * a.H - s.r0 < nq ? r.n * a.H - s.r0 : nq;
     s.i0 = s.r0 / a.H;
     s.ntok = (s.r0 + s.nrows - 1) / a.H - s.i0 + 1;
   }
 
-  // The next segment, or one of no tiles, in s (a register copy in every lane).
+  // The next segment, or one of no tiles (the whole warp calls it, lane 0 writes s).
   static __device__ __forceinline__ void next(const SplitArgs& a, int nq, int lane, Kv4Cursor& c, Kv4Segment& s) {
-    s.nt = 0;
     if (!a.seg_table) {
-      const int b = blockIdx.z, g = blockIdx.x;
-      const bool done = c.done != 0;
+      const Kv4Request& r = c.req[0];
+      const int g = blockIdx.x;
+      const bool none = c.done || g >= r.groups;
       __syncwarp();
-      if (done || b >= a.batch) return;
-      if (lane == 0) c.done = 1;
-      const Req r = request(a, nq, b);
-      if (g >= r.groups) return;
-      s.batch = b;
-      s.q0 = r.q0;
-      s.n_tokens = r.n;
-      s.keys = r.keys;
-      rows(a, nq, g, s);
-      s.prow = (int64_t)blockIdx.y * a.rows_max + r.q0 * a.H + s.r0;
+      if (lane == 0) {
+        c.done = 1;
+        s.nt = 0;
+      }
+      if (none) return;
       // chunk_len, in tiles
+      const int tiles = (r.keys + kKeysPerTile - 1) / kKeysPerTile;
       const int per = (int)(((uint32_t)r.keys + (uint32_t)a.nsplit - 1u) / (uint32_t)a.nsplit);
       int chunk = (per + kKeysPerTile - 1) / kKeysPerTile;
       chunk = chunk < a.min_chunk / kKeysPerTile ? a.min_chunk / kKeysPerTile : chunk;
       const int64_t t0 = (int64_t)blockIdx.y * chunk;
-      if (t0 >= r.tiles) {  // an empty chunk
-        for (int n = lane; n < s.nrows; n += 32) a.part_lse[s.prow + n] = -INFINITY;
+      const int64_t prow = (int64_t)blockIdx.y * a.rows_max + r.q0 * a.H + g * nq;
+      if (t0 >= tiles) {  // an empty chunk
+        const int nrows = r.n * a.H - g * nq;
+        for (int n = lane; n < nrows && n < nq; n += 32) a.part_lse[prow + n] = -INFINITY;
         return;
       }
-      s.tile0 = (int)t0;
-      s.nt = r.tiles - s.tile0 < chunk ? r.tiles - s.tile0 : chunk;
-      // The row groups of a chunk read the same keys; staggered they read them
-      // from L2 one after the other.
-      s.rot = g % s.nt;
+      if (lane == 0) {
+        rows(a, nq, g, r, s);
+        s.prow = prow;
+        s.tile0 = (int)t0;
+        s.nt = tiles - s.tile0 < chunk ? tiles - s.tile0 : chunk;
+        // The row groups of a chunk read the same keys; staggered they read them
+        // from L2 one after the other.
+        s.rot = g % s.nt;
+      }
       return;
     }
-    int64_t x = c.x, carry = c.carry;
-    int base = c.base;
+    int64_t x = c.x;
     const int64_t x_end = c.x_end;
     __syncwarp();
 #pragma unroll 1
     while (x < x_end) {
-      const Req r = request(a, nq, base + lane);
-      const int64_t incl = carry + scan(r.cost, lane);
-      const uint32_t past = __ballot_sync(0xffffffffu, incl > x);
+      const uint32_t past = __ballot_sync(0xffffffffu, c.end[lane] > x);
       if (!past) {
-        carry = __shfl_sync(0xffffffffu, incl, 31);
-        base += 32;
+        fetch(a, nq, lane, c.base + 32, c.end[31], c);
         continue;
       }
       const int l = __ffs(past) - 1;
-      s.batch = base + l;
-      s.q0 = __shfl_sync(0xffffffffu, r.q0, l);
-      s.n_tokens = __shfl_sync(0xffffffffu, r.n, l);
-      s.keys = __shfl_sync(0xffffffffu, r.keys, l);
-      const int tiles = __shfl_sync(0xffffffffu, r.tiles, l);
-      const int64_t from = __shfl_sync(0xffffffffu, incl - r.cost, l);  // the request's place on the axis
-      const int g = (int)((x - from) / (tiles + a.seg_cost));
+      const Kv4Request& r = c.req[l];
+      const int tiles = (r.keys + kKeysPerTile - 1) / kKeysPerTile;
+      const int64_t from = l ? c.end[l - 1] : c.carry;  // the request's place on the axis
+      const int g = (int)divide(x - from, tiles + a.seg_cost);
       const int64_t first = from + (int64_t)g * (tiles + a.seg_cost) + a.seg_cost;  // the group's first tile
       const int64_t end = first + tiles;
       const int64_t t0 = x > first ? x - first : 0;
       x = x_end < end ? x_end : end;
       if (x - first <= t0) continue;  // only of the group's start
-      rows(a, nq, g, s);
-      const int slot = s.batch * a.groups_max + g;
-      s.prow = (int64_t)(blockIdx.x + slot) * nq;
-      s.tile0 = (int)t0;
-      s.nt = (int)(x - first - t0);
-      s.rot = 0;
       if (lane == 0) {
+        const int slot = (c.base + l) * a.groups_max + g;
+        rows(a, nq, g, r, s);
+        s.prow = (int64_t)(blockIdx.x + slot) * nq;
+        s.tile0 = (int)t0;
+        s.nt = (int)(x - first - t0);
+        s.rot = 0;
         // where the merge finds the group's partials, and how many
         if (t0 == 0)
-          a.seg_table[slot] = make_int2(blockIdx.x + slot, (int)((end - 1) / c.piece) - (int)blockIdx.x + 1);
+          a.seg_table[slot] = make_int2(blockIdx.x + slot, (int)divide(end - 1, c.piece) - (int)blockIdx.x + 1);
         c.x = x;
-        c.carry = carry;
-        c.base = base;
       }
       __syncwarp();
       return;
     }
+    if (lane == 0) s.nt = 0;
   }
 };
 
@@ -806,18 +832,14 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
 #pragma unroll 1
       for (int k = 0; ok; ++k) {
         if (iw == 0) {
-          Kv4Segment sg;
-          kv4::Schedule::next(a, NQ, lane, ctl.cursor, sg);
           if (!(ok = wait_warp(&ctl.seg_empty[k & 1], ((k >> 1) & 1) ^ 1))) break;
-          if (lane == 0) {
-            ctl.seg[k & 1] = sg;
-            mbar_arrive(&ctl.seg_full[k & 1]);
-          }
+          kv4::Schedule::next(a, NQ, lane, ctl.cursor, ctl.seg[k & 1]);
           __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl.seg_full[k & 1]);
         }
         if (!(ok = wait_warp(&ctl.seg_full[k & 1], (k >> 1) & 1))) break;
         const Kv4Segment& sg = ctl.seg[k & 1];
-        const int nt = sg.nt, b = sg.batch;
+        const int nt = sg.nt;
         if (nt == 0) {
           // the end, as one more tile
           const int r = t_seg % Cfg::kIndexRing;
@@ -829,14 +851,12 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
           break;
         }
         const int tile0 = sg.tile0, rot = sg.rot, i0 = sg.i0, ntok = sg.ntok, L = sg.keys, n_tok = sg.n_tokens;
-        const int64_t q0 = sg.q0;
+        const int P = sg.prefix;
+        const int32_t* pre_ids = a.kv_indices + sg.kv0;
+        const int32_t* new_ids = a.out_cache_loc + sg.q0 - P;
+        const int64_t block0 = sg.mask0;
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl.seg_empty[k & 1]);
-        const int64_t kv_base = a.kv_indptr[b];
-        const int P = (int)(a.kv_indptr[b + 1] - kv_base);
-        const int32_t* pre_ids = a.kv_indices + kv_base;
-        const int32_t* new_ids = a.out_cache_loc + q0 - P;
-        const int64_t block0 = (int64_t)a.mask_indptr[b];
         const uint8_t* mask_lo = a.mask + (block0 >> 3);  // the request's mask block, in whole bytes
         const uint8_t* mask_hi = a.mask + ((block0 + (int64_t)n_tok * L + 7) >> 3);
 #pragma unroll 1
@@ -844,38 +864,49 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
           const int t = t_seg + i;
           const int r = t % Cfg::kIndexRing;
           const int key0 = (tile0 + (i + rot < nt ? i + rot : i + rot - nt)) * kKeys;
-          if (!(ok = wait_warp(&ctl.idx_empty[r], ((t / Cfg::kIndexRing) & 1) ^ 1))) break;
-          uint32_t valid[4];
+          // all the tile's loads first: one latency
+          int32_t id[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int key = key0 + 32 * j + lane;
-            const int32_t id = key < P ? __ldg(pre_ids + key) : key < L ? __ldg(new_ids + key) : -1;
-            const bool in = id >= 0 && id < a.pool_rows;
-            if (!in && key < L) bad = 1;  // left out, and reported
-            valid[j] = __ballot_sync(0xffffffffu, in);
-            ctl.row_id[r][32 * j + lane] = in ? id : 0;
+            const int32_t* p = key < P ? pre_ids + key : new_ids + key;
+            id[j] = key < L ? __ldg(p) : -1;
           }
-          uint32_t blind = 0;  // bit j: some token does not see all of the j-th 32 keys
-#pragma unroll 1
-          for (int tok = lane; tok - lane < ntok; tok += 32) {
+          uint32_t w[5], valid[4], blind = 0;  // blind: bit j, some token does not see all of the j-th 32 keys
+          int shift;
+          auto load_mask = [&](int tok) {
             const int64_t bit = block0 + (int64_t)(i0 + tok) * L + key0;
             const uintptr_t byte = reinterpret_cast<uintptr_t>(a.mask + (bit >> 3));
             const uint8_t* p = reinterpret_cast<const uint8_t*>(byte & ~(uintptr_t)3);
-            const int shift = 8 * (int)(byte & 3) + (int)(bit & 7);
-            uint32_t w[5] = {0, 0, 0, 0, 0};
-            if (tok < ntok) {
-              if (p >= mask_lo && p + 20 <= mask_hi) {
+            shift = 8 * (int)(byte & 3) + (int)(bit & 7);
+            w[0] = w[1] = w[2] = w[3] = w[4] = 0;
+            if (tok >= ntok) return;
+            if (p >= mask_lo && p + 20 <= mask_hi) {
 #pragma unroll
-                for (int j = 0; j < 5; ++j) w[j] = __ldg(reinterpret_cast<const uint32_t*>(p) + j);
-              } else {  // at an end of the mask block: only its own bytes are read
+              for (int j = 0; j < 5; ++j) w[j] = __ldg(reinterpret_cast<const uint32_t*>(p) + j);
+            } else {  // at an end of the mask block: only its own bytes are read
 #pragma unroll 1
-                for (int n = 0; n < 20; ++n) {
-                  const uint32_t v = p + n >= mask_lo && p + n < mask_hi ? __ldg(p + n) : 0u;
+              for (int n = 0; n < 20; ++n) {
+                const uint32_t v = p + n >= mask_lo && p + n < mask_hi ? __ldg(p + n) : 0u;
 #pragma unroll
-                  for (int j = 0; j < 4; ++j) w[j] = __funnelshift_r(w[j], w[j + 1], 8);
-                  w[4] = (w[4] >> 8) | (v << 24);
-                }
+                for (int j = 0; j < 4; ++j) w[j] = __funnelshift_r(w[j], w[j + 1], 8);
+                w[4] = (w[4] >> 8) | (v << 24);
               }
+            }
+          };
+          int tok = lane;
+          load_mask(tok);
+          if (!(ok = wait_warp(&ctl.idx_empty[r], ((t / Cfg::kIndexRing) & 1) ^ 1))) break;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const bool in = id[j] >= 0 && id[j] < a.pool_rows;
+            if (!in && key0 + 32 * j + lane < L) bad = 1;  // left out, and reported
+            valid[j] = __ballot_sync(0xffffffffu, in);
+            ctl.row_id[r][32 * j + lane] = in ? id[j] : 0;
+          }
+#pragma unroll 1
+          for (;; load_mask(tok)) {
+            if (tok < ntok) {
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
                 const uint32_t v = __funnelshift_r(w[j], w[j + 1], shift) & valid[j];
@@ -883,6 +914,8 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
                 if (v != 0xffffffffu) blind |= 1u << j;
               }
             }
+            tok += 32;
+            if (tok - lane >= ntok) break;
           }
           blind = __reduce_or_sync(0xffffffffu, blind);
           if (lane < 4) ctl.see_all[r][lane] = !((blind >> lane) & 1);
@@ -1059,21 +1092,22 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
             for (int c = 0; c < HC; ++c) x[c] = ((vis >> c) & 1u) ? x[c] : -INFINITY;
           }
         };
-        bool need = false;
-        if (!my_abort) {
+        const bool first = t == t_first;  // there is no maximum yet
+        bool need = first;
+        if (!my_abort && !first) {
           load_scores(true);
           float top = fmaxf(x[0], x[1]);
 #pragma unroll
           for (int c = 2; c < HC; c += 2) top = kv4::max3(top, x[c], x[c + 1]);
           need = top > kKv4Limit;
-        } else {
+        } else if (my_abort) {
 #pragma unroll
           for (int c = 0; c < HC; ++c) x[c] = -INFINITY;
         }
         bool rescale = false;
         if (kv4::bar_any(bar_id, 128, need || my_abort || ctl.abort)) {
-          // Rare: a score passed the running max by too much, a column
-          // saw its first key, or a wait gave up.
+          // Rare but for a segment's first tile: a score passed the running max
+          // by too much, a column saw its first key, or a wait gave up.
           const bool ab = __any_sync(0xffffffffu, my_abort) || ctl.abort;
           if (lane == 0) ctl.flag[warp] = ab ? 1 : 0;
           if (!my_abort) load_scores(false);
