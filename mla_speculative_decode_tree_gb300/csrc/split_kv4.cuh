@@ -79,15 +79,18 @@ struct Kv4Cfg {
   static constexpr int kIndexWarps = 2;
   static constexpr int kIndexRing = 4;                     // tiles of row ids and mask words in flight
   static constexpr int kExpandWarp = kSoftmaxWarps + 4;
-  static constexpr int kExpandWarps = 8;
+  static constexpr int kOwnKeys = kCG <= 2 ? 1 : 2;              // keys of a tile per expansion thread
+  static constexpr int kExpandWarps = 16 / kOwnKeys;
   static constexpr int kThreads = 32 * (kExpandWarp + kExpandWarps);
-  // Registers per thread by role.  A block starts with 65536 / kThreads rounded down to what its warps can all
-  // have (128, 96, 80 or 72); the shares together are at most the start's, or the last warps would wait for ever.
-  static constexpr int kRegsStart = kCG == 1 ? 128 : kCG == 2 ? 96 : kCG == 3 ? 80 : 72;
+  // Registers per thread by role.  A block starts with 65536 / kThreads rounded down to what all its warps can
+  // have; the shares together are at most the start's, or the last warps would wait for ever.
+  static constexpr int kWarpgroups = kThreads / 128;
+  static constexpr int kRegsStart = 65536 / kThreads / 8 * 8 > 128 ? 128 : 65536 / kThreads / 8 * 8;
   static constexpr int kRegsMma = 48;
-  static constexpr int kRegsSoftmax = kCG == 1 ? 128 : kCG == 2 ? 96 : kCG == 3 ? 80 : 72;
-  static constexpr int kRegsExpand = kCG == 1 ? 128 : kCG == 2 ? 120 : kCG == 3 ? 96 : 80;
-  static_assert(kCG * kRegsSoftmax + kRegsMma + 2 * kRegsExpand <= (kCG + 3) * kRegsStart, "register shares");
+  static constexpr int kRegsSoftmax = kCG == 1 ? 96 : kCG == 2 ? 88 : kCG == 3 ? 80 : 72;
+  static constexpr int kRegsExpand = kCG == 1 ? 80 : kCG == 2 ? 64 : kCG == 3 ? 96 : 80;
+  static_assert(kCG * kRegsSoftmax + kRegsMma + (kExpandWarps / 4) * kRegsExpand <= kWarpgroups * kRegsStart,
+                "register shares");
   static constexpr int kQBlock = 2 * NQ * 128;  // one 128-channel block of q_hi rows, then q_lo rows
   static constexpr int kQRope = 2 * NQ * 64;    // RoPE channels, once: the residual codes meet the same bytes
   static constexpr int kQBytes = 4 * kQBlock + kQRope;
@@ -295,9 +298,9 @@ __device__ __forceinline__ void regs_to() {
   if constexpr (kTo < kFrom) regs_dec<kTo>();
 }
 
-__device__ __forceinline__ uint4 ldg_stream(const void* p) {
+__device__ __forceinline__ uint4 ldg128(const void* p) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+  asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
   return v;
@@ -379,9 +382,7 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
   return false;
 }
 
-// Max (or sum) of v[0..15] over the warp, index by index: lane l returns that
-// of index l / 2.
-template <bool kMax>
+// Sum of v[0..15] over the warp, index by index: lane l returns that of index l / 2.
 __device__ __forceinline__ float reduce16(float (&v)[16], int lane) {
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) {
@@ -390,23 +391,35 @@ __device__ __forceinline__ float reduce16(float (&v)[16], int lane) {
     for (int m = 0; m < o; ++m) {
       const float send = upper ? v[m] : v[m + o];
       const float keep = upper ? v[m + o] : v[m];
-      const float got = __shfl_xor_sync(0xffffffffu, send, 2 * o);
-      v[m] = kMax ? fmaxf(keep, got) : keep + got;
+      v[m] = keep + __shfl_xor_sync(0xffffffffu, send, 2 * o);
     }
   }
-  const float got = __shfl_xor_sync(0xffffffffu, v[0], 1);
-  return kMax ? fmaxf(v[0], got) : v[0] + got;
+  return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
 }
 
-template <int HC, bool kMax>
-__device__ __forceinline__ void columns_to_smem(const float (&x)[HC], float* dst, int lane) {
+__device__ __forceinline__ float warp_max(float x) {
+  float d;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(d) : "f"(x));
+  return d;
+}
+
+// Max (or sum) of each of the 16 columns over the warp, to dst.
+template <bool kMax>
+__device__ __forceinline__ void columns_to_smem(const float (&x)[16], float* dst, int lane) {
+  if constexpr (kMax) {
+    float r = 0.f;
 #pragma unroll
-  for (int g = 0; g < HC / 16; ++g) {
+    for (int k = 0; k < 16; ++k) {
+      const float m = warp_max(x[k]);
+      r = lane == k ? m : r;
+    }
+    if (lane < 16) dst[lane] = r;
+  } else {
     float v[16];
 #pragma unroll
-    for (int k = 0; k < 16; ++k) v[k] = x[16 * g + k];
-    const float r = reduce16<kMax>(v, lane);
-    if ((lane & 1) == 0) dst[16 * g + (lane >> 1)] = r;
+    for (int k = 0; k < 16; ++k) v[k] = x[k];
+    const float r = reduce16(v, lane);
+    if ((lane & 1) == 0) dst[lane >> 1] = r;
   }
 }
 
@@ -628,8 +641,8 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
 
   if (warp >= Cfg::kExpandWarp) {
     // =========================== expansion ===================================
-    // Thread (warp w, lane) owns codes 32q..32q+31 of each block of keys
-    // 8w + lane/4 and 64 + 8w + lane/4, q = lane % 4: a warp's load of one
+    // Thread (warp w, lane) owns codes 32q..32q+31 of each block of key 8w +
+    // lane/4 (and of 64 + that, with 8 warps), q = lane % 4: a warp's load of one
     // block covers 8 rows x 64 contiguous bytes, and its 16-byte stores reach
     // all 32 banks (8 lanes = 2 keys x 4 chunks of opposite parity).
     kv4::regs_to<Cfg::kRegsStart, Cfg::kRegsExpand>();
@@ -638,8 +651,9 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
     const int key0 = 8 * w + (lane >> 2);
     const uint32_t off0 = key0 * 128 + (((2 * q) ^ (key0 & 7)) << 4);
     const uint32_t off1 = key0 * 128 + (((2 * q + 1) ^ (key0 & 7)) << 4);
-    int32_t row[2], id[2];  // pool rows of the tile being loaded, and of the one after
-    uint4 code[2][kKv4Blocks], scale[2];
+    constexpr int K = Cfg::kOwnKeys;
+    int32_t row[K], id[K];  // pool rows of the tile being loaded, and of the one after
+    uint4 code[K][kKv4Blocks], scale[K];
     bool ok = true, more = true;
     auto at = [&](int h, int byte) { return a.kv4_pool + 16 * q + byte + (uint64_t)(uint32_t)row[h] * kKv4RowBytes; };
     // Pool rows of the own keys of tile t, if there is one.  (A key without a
@@ -650,19 +664,19 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
       ok = wait_warp(&ctl.idx_full[r], (t / Cfg::kIndexRing) & 1);
       more = ok && !(ctl.tile[r] & kTileEnd);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) id[h] = more ? ctl.row_id[r][key0 + 64 * h] : 0;
+      for (int h = 0; h < K; ++h) id[h] = more ? ctl.row_id[r][key0 + 64 * h] : 0;
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl.idx_empty[r]);
     };
     read_ids(0);
     if (more) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < K; ++h) {
         row[h] = id[h];
-        scale[h] = kv4::ldg_stream(at(h, kKv4ScaleOff));
+        scale[h] = kv4::ldg128(at(h, kKv4ScaleOff));
 #pragma unroll
         for (int u = 0; u < kKv4Blocks; ++u)
-          code[h][kv4::block_of(u)] = kv4::ldg_stream(at(h, 64 * kv4::block_of(u)));
+          code[h][kv4::block_of(u)] = kv4::ldg128(at(h, 64 * kv4::block_of(u)));
       }
     }
     bool have = more;
@@ -671,12 +685,12 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
     for (int t = 0; have && ok; ++t) {
       // Loads of tile t+1 follow the use of their registers in tile t; after the
       // last tile they read row 0.
-      uint4 next_scale[2];
+      uint4 next_scale[K];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < K; ++h) {
         kv4::make_valid(scale[h]);
         row[h] = id[h];
-        next_scale[h] = kv4::ldg_stream(at(h, kKv4ScaleOff));
+        next_scale[h] = kv4::ldg128(at(h, kKv4ScaleOff));
       }
 #pragma unroll
       for (int u = 0; u < kKv4Blocks; ++u) {
@@ -686,10 +700,10 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
           // (one copy of the code for both keys: the roles' loops share the
           // instruction cache)
 #pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
-            const uint4 c = h ? code[1][m] : code[0][m];
-            const uint32_t sw = h ? (m < 2 ? scale[1].x : m < 4 ? scale[1].y : scale[1].z)
-                                  : (m < 2 ? scale[0].x : m < 4 ? scale[0].y : scale[0].z);
+          for (int h = 0; h < K; ++h) {
+            const uint4 c = h ? code[K - 1][m] : code[0][m];
+            const uint4 sc = h ? scale[K - 1] : scale[0];
+            const uint32_t sw = m < 2 ? sc.x : m < 4 ? sc.y : sc.z;
             uint32_t lo[2], hi[2], o[8];
             kv4::scale_table((sw >> (16 * (m & 1))) & 0xFFu, lo[0], hi[0]);
             kv4::scale_table((sw >> (16 * (m & 1) + 8)) & 0xFFu, lo[1], hi[1]);
@@ -703,14 +717,14 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
           }
           __syncwarp();
           if (lane == 0 && !(a.test_stall && t + u == 0)) mbar_arrive(&ctl.full[sl]);
-          code[0][m] = kv4::ldg_stream(at(0, 64 * m));
-          code[1][m] = kv4::ldg_stream(at(1, 64 * m));
+#pragma unroll
+          for (int h = 0; h < K; ++h) code[h][m] = kv4::ldg128(at(h, 64 * m));
         }
       }
       have = more;
       if (ok && more) read_ids(t + 2);
-      scale[0] = next_scale[0];
-      scale[1] = next_scale[1];
+#pragma unroll
+      for (int h = 0; h < K; ++h) scale[h] = next_scale[h];
     }
   } else if (warp >= Cfg::kMmaWarp) {
     // ============================ MMA issue ==================================
@@ -1093,7 +1107,7 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
           }
         };
         const bool first = t == t_first;  // there is no maximum yet
-        bool need = first;
+        bool need = false;
         if (!my_abort && !first) {
           load_scores(true);
           float top = fmaxf(x[0], x[1]);
@@ -1105,13 +1119,13 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
           for (int c = 0; c < HC; ++c) x[c] = -INFINITY;
         }
         bool rescale = false;
-        if (kv4::bar_any(bar_id, 128, need || my_abort || ctl.abort)) {
+        if (first || kv4::bar_any(bar_id, 128, need || my_abort || ctl.abort)) {
           // Rare but for a segment's first tile: a score passed the running max
           // by too much, a column saw its first key, or a wait gave up.
           const bool ab = __any_sync(0xffffffffu, my_abort) || ctl.abort;
           if (lane == 0) ctl.flag[warp] = ab ? 1 : 0;
           if (!my_abort) load_scores(false);
-          kv4::columns_to_smem<HC, true>(x, &ctl.red[quad][c0], lane);
+          kv4::columns_to_smem<true>(x, &ctl.red[quad][c0], lane);
           named_bar_sync(bar_id, 128);
           my_abort =
               (ctl.flag[4 * half] | ctl.flag[4 * half + 1] | ctl.flag[4 * half + 2] | ctl.flag[4 * half + 3]) != 0;
@@ -1202,7 +1216,7 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
 
       // ---- the segment's end: l, LSE, O = O^T / l -----------------------------
       named_bar_sync(bar_id, 128);  // (a raise of the last tile has read red)
-      kv4::columns_to_smem<HC, false>(acc, &ctl.red[quad][c0], lane);
+      kv4::columns_to_smem<false>(acc, &ctl.red[quad][c0], lane);
       if (!my_abort) my_abort = !kv4::wait(&ctl.pv_done[(t_end - 1) & 1], ((t_end - 1) >> 1) & 1, &ctl.abort);
       tc::fence_after_sync();
       if (kv4::bar_any(bar_id, 128, my_abort || ctl.abort)) {
