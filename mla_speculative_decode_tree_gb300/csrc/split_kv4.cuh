@@ -98,6 +98,14 @@ struct Kv4Cfg {
   static constexpr int kPBytes = 2 * NQ * kKeys;
   static constexpr int kPBufs = NQ >= 48 ? 1 : 2;
   static constexpr int kSlotBytes = kKeys * 128;
+  // With one key per expansion thread a block is short work beside its wait, signal and loads: the value blocks then go
+  // two at a time (GB300, 16-row groups, 16 decode requests: 44.2 -> 43.1 us per call; 32-row groups, 16 ragged
+  // requests: 478 -> 446).  With two keys single blocks are better (48 rows, 185k keys: 78.9 against 84.1 us; 64 rows,
+  // 64k keys: 110.8 against 113.3): S^T starts sooner.
+  static constexpr bool kPairs = kOwnKeys == 1;
+  // Blocks are handed on in runs that end at last(u), the u-th block's run.
+  __host__ __device__ static constexpr int last(int u) { return kPairs && u > 0 ? (u + 1) / 2 * 2 : u; }
+  __host__ __device__ static constexpr bool opens_run(int u) { return u == 0 || last(u - 1) != last(u); }
   static constexpr bool kRopeSlot = NQ <= 48;
   static constexpr int kSlots = kRopeSlot ? 9 : 8;
   // Slot of the u-th block of tile t, and the parity of its fill there.
@@ -628,6 +636,8 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
     tc::tmem_alloc(&ctl.tmem_base, 512);
     tc::tmem_relinquish();
   }
+  // (its loads' latency passes beside the rest of the set-up)
+  if (warp == Cfg::kIndexWarp) kv4::Schedule::start(a, NQ, lane, ctl.cursor);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -695,7 +705,12 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
 #pragma unroll
       for (int u = 0; u < kKv4Blocks; ++u) {
         const int m = kv4::block_of(u), sl = Cfg::slot(t, u);
-        ok = ok && wait_warp(&ctl.empty[sl], Cfg::fill(t, u) ^ 1);
+        // (O^T frees the value blocks' slots in the order 0, 1, 2, 3: the wait for
+        // the run's highest block covers the other)
+        if (Cfg::opens_run(u)) {
+          const int z = Cfg::last(u) == kKv4Blocks - 1 ? u : Cfg::last(u);
+          ok = ok && wait_warp(&ctl.empty[Cfg::slot(t, z)], Cfg::fill(t, z) ^ 1);
+        }
         if (ok) {
           // (one copy of the code for both keys: the roles' loops share the
           // instruction cache)
@@ -715,10 +730,16 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
             kv4::sts128(dst + off0, o[0], o[1], o[2], o[3]);
             kv4::sts128(dst + off1, o[4], o[5], o[6], o[7]);
           }
-          __syncwarp();
-          if (lane == 0 && !(a.test_stall && t + u == 0)) mbar_arrive(&ctl.full[sl]);
+          if (u == Cfg::last(u)) {
+            __syncwarp();
+            if (lane == 0 && !(a.test_stall && t + u == 0)) mbar_arrive(&ctl.full[sl]);
 #pragma unroll
-          for (int h = 0; h < K; ++h) code[h][m] = kv4::ldg128(at(h, 64 * m));
+            for (int b = 0; b < kKv4Blocks; ++b) {
+              if (Cfg::last(b) != u) continue;
+#pragma unroll
+              for (int h = 0; h < K; ++h) code[h][kv4::block_of(b)] = kv4::ldg128(at(h, 64 * kv4::block_of(b)));
+            }
+          }
         }
       }
       have = more;
@@ -774,7 +795,10 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
 #pragma unroll 1
           for (int u = 0; u < kKv4Blocks; ++u) {
             const int slot = Cfg::slot(t, u);
-            if (!(ok = wait_mma(&ctl.full[slot], Cfg::fill(t, u)))) break;
+            if (Cfg::opens_run(u)) {
+              const int z = Cfg::last(u);
+              if (!(ok = wait_mma(&ctl.full[Cfg::slot(t, z)], Cfg::fill(t, z)))) break;
+            }
             const uint64_t ad = desc_k + (uint32_t)(slot * (Cfg::kSlotBytes >> 4));
             if (leader && u == 0) {
 #pragma unroll
@@ -839,7 +863,6 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
       // the pool rows of the tile's keys, and per 32 keys and token the mask's
       // bits, less keys that have no row.
       const int iw = warp - Cfg::kIndexWarp;
-      if (iw == 0) kv4::Schedule::start(a, NQ, lane, ctl.cursor);
       uint32_t bad = 0;
       int t_seg = 0;  // first tile of the segment in the count of all
       bool ok = true;
