@@ -735,6 +735,7 @@ int mla_verify_build_slots(mla_verify_plan_t pl, const int32_t* seq_lens, const 
   for (int s = 0; s < 31; ++s)
     if (page_size == (1 << s)) a.page_shift = s;
   a.max_pages = max_pages;
+  a.whole_pages = (uint32_t)(pl->p.pool_rows / page_size);
   a.num_free = num_free;
   cudaError_t e = launch_slots(a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MLA_VERIFY_OK : cuda_fail(e);

@@ -283,6 +283,7 @@ struct SlotsArgs {
   uint32_t* status;           // workspace header word 0
   int64_t pool_rows, kv_capacity, loc_capacity;
   int32_t batch, q_len, page_size, page_shift, max_pages, num_free;  // page_shift: log2, or -1
+  uint32_t whole_pages;       // pages that lie wholly in the pool
 };
 constexpr int kMaxSlotsBatch = 4096;  // requests of one slot-map build
 cudaError_t launch_slots(const SlotsArgs& a, cudaStream_t stream);

@@ -21,9 +21,9 @@
 namespace mlav {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 1024;  // one block per SM: the scans are done once there
 constexpr int kWarps = kThreads / 32;
-constexpr int kPerThread = 4;  // consecutive outputs per thread: a warp's pass covers 128
+constexpr int kPerThread = 4;  // consecutive outputs per thread: a warp's chunk is 128
 
 // kPow2: pages of 2^page_shift rows.
 template <bool kPow2>
@@ -46,17 +46,32 @@ struct SlotsDev {
     if ((pos >> 32) == 0) return (uint32_t)pos / (uint32_t)a.page_size;
     return (int64_t)((uint64_t)pos / (uint32_t)a.page_size);
   }
+  __device__ __forceinline__ int page_of_entry(int pos) const {
+    return kPow2 ? pos >> a.page_shift : (int)((uint32_t)pos / (uint32_t)a.page_size);
+  }
   __device__ __forceinline__ int64_t pages(int64_t tokens) const { return page_of(tokens + a.page_size - 1); }
 
-  // The last b with scan[b] <= x (requests without entries are skipped).
-  __device__ __forceinline__ int owner(const int32_t* scan, int64_t x) const {
-    int lo = 0, hi = a.batch - 1;
+  // The last b of lo..hi with scan[b] <= x (requests without entries are skipped).
+  __device__ __forceinline__ int owner(const int32_t* scan, int32_t x, int lo, int hi) const {
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if (scan[mid] <= x)
         lo = mid;
       else
         hi = mid - 1;
+    }
+    return lo;
+  }
+
+  // The same for the warp's common x: 32 probes at a time.
+  __device__ __forceinline__ int owner_warp(const int32_t* scan, int32_t x, int lane) const {
+    int lo = 0, n = a.batch;
+    while (n > 1) {
+      const int step = (n + 31) >> 5, i = lane * step;
+      const uint32_t below = __ballot_sync(0xffffffffu, i < n && (i == 0 || scan[lo + i] <= x));
+      const int last = (31 - __clz(below)) * step;
+      lo += last;
+      n = n - last < step ? n - last : step;
     }
     return lo;
   }
@@ -79,28 +94,30 @@ struct SlotsDev {
     return f < a.num_free ? a.free_pages + f : nullptr;
   }
 
-  // Rows of cached positions pos .. pos+3 of request b: one table entry where they share a page.
+  // Rows of cached positions pos .. pos+3 of request b.
   __device__ __forceinline__ int4 rows4(int b, int pos, uint32_t& status) const {
     const int32_t* table = a.block_table + (int64_t)b * a.max_pages;
-    int32_t r[kPerThread], page0 = -1;
-    int c0 = -1;
-#pragma unroll
-    for (int k = 0; k < kPerThread; ++k) {
-      const int c = kPow2 ? (pos + k) >> a.page_shift : (int)((uint32_t)(pos + k) / (uint32_t)a.page_size);
-      int32_t page = page0;
-      if (c != c0) {
-        page = c < a.max_pages ? table[c] : -1;
-        if (k == 0) {
-          c0 = c;
-          page0 = page;
+    if (a.page_size >= kPerThread) {
+      // they lie on two pages at most, both whole in the pool as a rule
+      const int c0 = page_of_entry(pos), c1 = page_of_entry(pos + 3);
+      if (c1 < a.max_pages) {
+        const uint32_t p0 = (uint32_t)table[c0], p1 = (uint32_t)table[c1];
+        if (p0 < a.whole_pages && p1 < a.whole_pages) {
+          const int x = (int)(p0 - c0) * a.page_size + pos, y = (int)(p1 - c1) * a.page_size + pos;
+          const int next = c1 * a.page_size - pos;  // from here on the second page
+          return make_int4(0 < next ? x : y, (1 < next ? x : y) + 1, (2 < next ? x : y) + 2, (3 < next ? x : y) + 3);
         }
       }
-      if (c < a.max_pages) {
-        r[k] = row_on(page, c, pos + k, status);
-      } else {
-        r[k] = -1;
+    }
+    int32_t r[kPerThread];
+#pragma unroll
+    for (int k = 0; k < kPerThread; ++k) {
+      const int c = page_of_entry(pos + k);
+      r[k] = -1;
+      if (c < a.max_pages)
+        r[k] = row_on(table[c], c, pos + k, status);
+      else
         status |= kStatusNoPage;
-      }
     }
     return make_int4(r[0], r[1], r[2], r[3]);
   }
@@ -129,7 +146,6 @@ template <bool kPow2>
 __device__ __forceinline__ void scan_requests(const SlotsDev<kPow2>& d) {
   __shared__ uint32_t warp_sum[3][kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int32_t* const out[3] = {d.kv, d.qo, d.fresh};
   uint32_t carry[3] = {0, 0, 0};
 #pragma unroll 1
   for (int base = 0; base < d.a.batch; base += kThreads) {
@@ -141,7 +157,7 @@ __device__ __forceinline__ void scan_requests(const SlotsDev<kPow2>& d) {
       x[1] = (uint32_t)T;
       x[2] = (uint32_t)(d.pages((int64_t)P + T) - d.pages(P));
     }
-    scan3(x, lane);
+    if (base + 32 * warp < d.a.batch) scan3(x, lane);
     if (lane == 31) {
 #pragma unroll
       for (int k = 0; k < 3; ++k) warp_sum[k][warp] = x[k];
@@ -149,17 +165,18 @@ __device__ __forceinline__ void scan_requests(const SlotsDev<kPow2>& d) {
     __syncthreads();
     uint32_t sum[3];
 #pragma unroll
-    for (int k = 0; k < 3; ++k) sum[k] = lane < kWarps ? warp_sum[k][lane] : 0u;
+    for (int k = 0; k < 3; ++k) sum[k] = warp_sum[k][lane];
     scan3(sum, lane);
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
       const uint32_t before = __shfl_sync(0xffffffffu, sum[k], warp > 0 ? warp - 1 : 0);
-      if (b < d.a.batch) out[k][b + 1] = (int32_t)add_sat(add_sat(carry[k], warp > 0 ? before : 0u), x[k]);
+      int32_t* const out = k == 0 ? d.kv : k == 1 ? d.qo : d.fresh;
+      if (b < d.a.batch) out[b + 1] = (int32_t)add_sat(add_sat(carry[k], warp > 0 ? before : 0u), x[k]);
       carry[k] = add_sat(carry[k], __shfl_sync(0xffffffffu, sum[k], 31));
     }
     __syncthreads();
   }
-  if (threadIdx.x < 3) out[threadIdx.x][0] = 0;
+  if (threadIdx.x == 0) d.kv[0] = d.qo[0] = d.fresh[0] = 0;
   __syncthreads();
 }
 
@@ -184,26 +201,27 @@ __global__ void __launch_bounds__(kThreads) slots_kernel(SlotsArgs args) {
       if (K > a.kv_capacity || N > a.loc_capacity) status |= kStatusCapacity;
     }
   }
-  const int64_t n_kv = K < a.kv_capacity ? K : a.kv_capacity;
-  const int64_t n_loc = N < a.loc_capacity ? N : a.loc_capacity;
-  const int64_t warp0 = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5;
-  const int64_t warps = ((int64_t)gridDim.x * kThreads) >> 5;
+  // (the scans stop at 2^31 - 1: 32 bits count the entries)
+  const int n_kv = (int)(K < a.kv_capacity ? K : a.kv_capacity);
+  const int n_loc = (int)(N < a.loc_capacity ? N : a.loc_capacity);
+  const int warps = gridDim.x * kWarps;
   const int lane = threadIdx.x & 31;
   // One pass over both maps: chunks of 128 entries, the prefixes' first.
-  const int64_t c_kv = (n_kv + 127) / 128, c_loc = (n_loc + 127) / 128;
+  const int c_kv = (int)(((uint32_t)n_kv + 127) / 128), c_all = c_kv + (int)(((uint32_t)n_loc + 127) / 128);
   const bool wide = (reinterpret_cast<uintptr_t>(a.kv_indices) & 15) == 0;
-  for (int64_t c = warp0; c < c_kv + c_loc; c += warps) {
+  for (int c = (threadIdx.x >> 5) * gridDim.x + blockIdx.x; c < c_all; c += warps) {  // few chunks go to all SMs
     const bool pre = c < c_kv;
     const int32_t* scan = pre ? d.kv : d.qo;
     int32_t* out = pre ? a.kv_indices : a.out_cache_loc;
-    const int64_t n = pre ? n_kv : n_loc;
-    const int64_t first = (pre ? c : c - c_kv) * 128;
-    const int64_t x0 = first + kPerThread * lane;
-    // The chunk's first entry finds its request for the warp; only a chunk that
-    // crosses into other requests searches again.
-    const int b0 = d.owner(scan, first);
-    if (pre && first + 128 <= n && first + 128 <= scan[b0 + 1]) {
-      const int4 r = d.rows4(b0, (int)(x0 - scan[b0]), status);
+    const int n = pre ? n_kv : n_loc;
+    const int first = (pre ? c : c - c_kv) * 128;
+    // The chunk's first entry finds its request for the warp, in a chunk of
+    // several requests the last one too.
+    const int left = n - first;
+    const int b0 = d.owner_warp(scan, first, lane);
+    if (pre && left >= 128 && scan[b0 + 1] - first >= 128) {
+      const int x0 = first + kPerThread * lane;
+      const int4 r = d.rows4(b0, x0 - scan[b0], status);
       if (wide) {
         *reinterpret_cast<int4*>(out + x0) = r;
       } else {
@@ -214,15 +232,16 @@ __global__ void __launch_bounds__(kThreads) slots_kernel(SlotsArgs args) {
       }
       continue;
     }
+    const int b1 = d.owner_warp(scan, first + (left < 128 ? left : 128) - 1, lane);
     const int32_t* at[kPerThread];
     int64_t pos[kPerThread], page_no[kPerThread];
 #pragma unroll
     for (int k = 0; k < kPerThread; ++k) {
-      const int64_t x = first + lane + 32 * k;
       at[k] = nullptr;
-      if (x < n) {
-        const int b = d.owner(scan, x);
-        pos[k] = x - scan[b] + (pre ? 0 : d.kv[b + 1] - d.kv[b]);
+      if (lane + 32 * k < left) {
+        const int x = first + lane + 32 * k;
+        const int b = d.owner(scan, x, b0, b1);
+        pos[k] = (int64_t)(x - scan[b]) + (pre ? 0 : d.kv[b + 1] - d.kv[b]);
         at[k] = d.page_at(b, pos[k], page_no[k]);
         if (!at[k]) status |= kStatusNoPage;
       }
@@ -232,13 +251,14 @@ __global__ void __launch_bounds__(kThreads) slots_kernel(SlotsArgs args) {
     for (int k = 0; k < kPerThread; ++k) page[k] = at[k] ? *at[k] : -1;
 #pragma unroll
     for (int k = 0; k < kPerThread; ++k) {
-      const int64_t x = first + lane + 32 * k;
-      if (x < n) out[x] = at[k] ? d.row_on(page[k], page_no[k], pos[k], status) : -1;
+      if (lane + 32 * k < left)
+        out[first + lane + 32 * k] = at[k] ? d.row_on(page[k], page_no[k], pos[k], status) : -1;
     }
   }
-  // The fresh pages' table entries.
-  for (int64_t f = (int64_t)blockIdx.x * kThreads + threadIdx.x; f < F; f += (int64_t)gridDim.x * kThreads) {
-    const int b = d.owner(d.fresh, f);
+  // The fresh pages' table entries (the last warps have the fewest chunks).
+  for (int64_t f = (int64_t)(kThreads - 1 - threadIdx.x) * gridDim.x + blockIdx.x; f < F;
+       f += (int64_t)gridDim.x * kThreads) {
+    const int b = d.owner(d.fresh, f, 0, a.batch - 1);
     const int64_t c = d.pages(d.kv[b + 1] - d.kv[b]) + (f - d.fresh[b]);
     if (c < a.max_pages) a.block_table[(int64_t)b * a.max_pages + c] = f < a.num_free ? a.free_pages[f] : -1;
   }
@@ -259,8 +279,8 @@ cudaError_t launch_slots(const SlotsArgs& a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
   }
   // The totals are on the device; the arrays' capacities bound them.
-  const int64_t want = (a.kv_capacity + a.loc_capacity + kThreads * kPerThread - 1) / (kThreads * kPerThread);
-  const int64_t cap = (int64_t)sms * 2;
+  const int64_t want = (a.kv_capacity + a.loc_capacity + 511) / 512;  // at least four chunks for a block
+  const int64_t cap = (int64_t)sms;
   const int grid = (int)(want < 1 ? 1 : want < cap ? want : cap);
   kernel<<<grid, kThreads, smem, stream>>>(a);
   return cudaGetLastError();
