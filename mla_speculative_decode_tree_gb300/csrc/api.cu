@@ -33,6 +33,7 @@ struct mla_verify_plan_s {
   bool kv4;  // the pool holds 4-bit rows (MLA_VERIFY_KV4)
   int pieces;  // > 0: the 4-bit kernel's CTAs, which take the work in equal pieces (nsplit = 0)
   int seg_cost;  // its start and end of a row group, in tiles
+  int merge_rows;  // rows per merge block then
 };
 
 namespace {
@@ -420,8 +421,8 @@ int mla_verify_plan(const mla_verify_params* params, size_t* workspace_bytes, ml
     pl->off_lse = round_up(kWsHeader + sizeof(int2) * spans, 256);
     pl->off_o = round_up(pl->off_lse + sizeof(float) * rows, 256);
     pl->ws_bytes = pl->off_o + sizeof(float) * rows * kDLatent;
-    const int per_block = pl->merge_quarter ? 2 : 4;
-    pl->merge_blocks = (int)((rows_b + per_block - 1) / per_block) * p.max_batch;
+    pl->merge_rows = merge_pieces_rows(rows_max, device_sm_count());
+    pl->merge_blocks = (int)((rows_b + pl->merge_rows - 1) / pl->merge_rows) * p.max_batch;
   }
   *workspace_bytes = pl->ws_bytes;
   *out = pl;
@@ -550,6 +551,7 @@ int merge_impl(mla_verify_plan_t pl, int32_t batch, int32_t nsplit, const int32_
     m.nq = pl->nq;
     m.groups_max = pl->groups;
     m.T = pl->p.q_len;
+    m.rows_per_block = pl->merge_rows;
   }
   cudaError_t e = pl->pieces ? launch_merge_pieces(m, static_cast<cudaStream_t>(stream))
                              : launch_merge(m, static_cast<cudaStream_t>(stream));

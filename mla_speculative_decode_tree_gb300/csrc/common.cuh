@@ -77,7 +77,7 @@ struct MergeArgs {
   float* lse;        // [rows]
   uint32_t* status;  // header words 0 (accumulated) and 1 (last call)
   const int2* seg_table;  // work in equal pieces: see SplitArgs; T tokens per request or qo_indptr
-  int32_t nq, groups_max, T;
+  int32_t nq, groups_max, T, rows_per_block;
   int32_t quarter;      // four warps per row (few rows) instead of two
   int32_t speculative;  // quarter layout: load the first 16 splits' partials before their LSEs
 };
@@ -288,6 +288,7 @@ struct SlotsArgs {
 constexpr int kMaxSlotsBatch = 4096;  // requests of one slot-map build
 cudaError_t launch_slots(const SlotsArgs& a, cudaStream_t stream);
 int merge_blocks(int rows, bool quarter);
+int merge_pieces_rows(int64_t rows, int sms);
 bool merge_quarter_fits(int64_t rows, int sms);
 
 constexpr int kSimtRowsPerCta = 8;  // one warp per query row
