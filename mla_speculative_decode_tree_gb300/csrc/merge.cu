@@ -92,7 +92,7 @@ __device__ __forceinline__ void merge_weights(const float* lse, int n, int64_t s
 // step, ... below n.  kAtOnce partials are read at a time, the first ones before
 // the LSEs are known; what has weight 0 was never written and is dropped.
 __device__ __forceinline__ void merge_partials(const float* lse, const float* part, int first, int step, int n,
-                                               int64_t stride, int lane, float& M, float& W, float (&acc)[4 * kV]) {
+                                               int64_t stride, int lane, float& M, float& W, float (&acc)[16]) {
   float w[kAtOnce];
   float4 v[kAtOnce][4];
   auto load = [&](int s0) {
