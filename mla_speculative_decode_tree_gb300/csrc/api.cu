@@ -181,9 +181,14 @@ cudaError_t kv4_launch(int nq, const SplitArgs& a, dim3 grid, cudaStream_t st) {
   }
 }
 
-// Times of the 4-bit kernel on GB300 (clocks near 1.95 GHz): a tile, and what a
-// row group's start and end (queries in, outputs out) add, in tiles.
-double kv4_tile_us(int nq) { return nq >= 64 ? 3.1 : nq >= 48 ? 2.7 : nq >= 32 ? 2.4 : 2.2; }
+// Times of the 4-bit kernel on GB300 (clocks near 2 GHz): a tile, and what a
+// row group's start and end (queries in, outputs out) add, in tiles.  Larger
+// groups expand a tile's keys for more rows, smaller ones waste fewer columns
+// and spread finer.  Whole calls by group size 16 / 32 / 48 / 64: 576 rows over
+// 4k keys 32.1 / 26.0 / 24.1 / 26.7 us, over 64k 255 / 154 / 117 / 110 us; 72
+// rows over 185k 113 / 90 / 75 / 84 us; 16 ragged requests 720 / 430 / 330 /
+// 289 us.  The model takes the least of each.
+double kv4_tile_us(int nq) { return nq >= 64 ? 3.05 : nq >= 48 ? 2.6 : nq >= 32 ? 2.3 : 1.95; }
 constexpr int kKv4SegCost = 2;
 
 // Row-group size: the least modelled time of a CTA's equal piece of the work

@@ -9,7 +9,9 @@
 // maximum needs no shuffle.  The RoPE channels are only four groups, so with
 // many rows a warp takes four rows and codes their RoPE parts together, a group
 // per lane; with few it takes one, and more SMs share the work (see many()).
-// 65,536 rows: store 24.3 us (4.15 TB/s), load 18.4 us (5.5 TB/s).
+// 65,536 rows (GB300): store 23.2 us (4.35 TB/s), load 17.9 us (5.6 TB/s); a
+// plain copy of as many bytes takes 15.  What the store has beside its traffic
+// is coding: its ALU pipe is 68 % busy.
 //
 // Coding a group: the largest magnitude by 16-bit integer maxima (bf16
 // magnitudes order as integers), the exponent from its bits, then the
@@ -22,7 +24,9 @@
 namespace mlav {
 namespace {
 
-constexpr int kThreads = 256;
+// Warps need no company: small blocks leave a finer tail (32,768 rows stored and read back at 256 / 128 / 64 / 32 threads: store
+// 22.0 / 21.3 / 20.9 / 20.9 us).
+constexpr int kThreads = 64;
 constexpr int kManyRows = 4;  // rows per warp when there are enough
 
 struct Vec32 {

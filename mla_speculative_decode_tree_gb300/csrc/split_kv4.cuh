@@ -1,13 +1,12 @@
 // Tensor-core (tcgen05) split kernel over a 4-bit latent cache (kv4.cuh).
 //
-// The split kernel's job and orientation are those of split_tc.cuh: one CTA
-// takes one request, one chunk of its keys and one group of NQ query rows;
-// 128 keys per tile lie on the MMA's M, the query rows on N; it leaves a
-// normalised partial O and an LSE per row for the merge kernel.  What differs
-// is the operand type.  A 4-bit value with a power-of-two scale is an exact
-// e5m2 float, so a tile is expanded to 8 bits, not 16: 80 KB for 128 keys,
-// half the shared memory, half the stores, and K = 32 per MMA.  The bf16
-// queries and the fp32 weights P become pairs of e4m3 floats:
+// The split kernel's job and orientation are those of split_tc.cuh: a group of
+// NQ query rows of one request lies on the MMA's N, 128 keys per tile on its M;
+// a partial is a normalised O and an LSE per row, for the merge kernel.  What
+// differs is the operand type.  A 4-bit value with a power-of-two scale is an
+// exact e5m2 float, so a tile is expanded to 8 bits, not 16: 80 KB for 128
+// keys, half the stores, and K = 32 per MMA.  The bf16 queries and the fp32
+// weights P become pairs of 8-bit floats:
 //
 //   q * 2^x = q_hi + q_lo / 32     (x per row: the row's largest |q| in [128, 256))
 //   S^T     = K . [q_hi | q_lo]^T  one MMA chain with N = 2 NQ; s = (S_hi + S_lo / 32) * c,
@@ -18,37 +17,59 @@
 // q_lo the other four exactly (down to 2^-15 of the row's largest value, below
 // which the error is under 2^-23 of it): scores are as exact as with bf16
 // operands.  p_hi + p_lo keeps 8 to 9 bits, as much as a bf16 P would, down
-// to 2^-18 of the row's largest weight.  The products and sums are fp32.
+// to 2^-18 of the row's largest weight.  The products and sums are fp32.  A
+// single e4m3 P instead of the pair would take a quarter off the MMAs and 3 % off
+// the call (64k keys, NQ = 64), for four significant bits in place of eight.
 //
-// The RoPE residual codes are 64 more K columns against a second copy of
-// q_rope, so a key is 640 codes: five blocks of 128, 20 k-steps of 32.
+// The RoPE residual codes are 64 more K columns against the same q_rope, so a
+// key is 640 codes: five blocks of 128, 20 k-steps of 32.
 //
-// NQ <= 48: p_hi and 16 * p_lo sit side by side on N as well and O^T keeps
-// both halves in tensor memory (4 x 2 NQ columns), added in the epilogue.  An
-// M = 128 MMA costs ~64 cycles up to N = 96 -- it is bound by reading its 4 KB
-// A operand from shared memory -- so the second half is nearly free.  NQ = 64:
-// both halves accumulate into one O^T (tensor memory holds 512 columns).
+// p_lo.  NQ <= 32: p_hi and 16 * p_lo (both e4m3) sit side by side on N and O^T
+// keeps both halves in tensor memory (4 x 2 NQ columns), added at the end.  An
+// M = 128 MMA costs 32 + N/4 cycles, most of it for reading its 4 KB A operand
+// from shared memory, so the second half is nearly free.  NQ = 48 and 64: p_lo
+// is e5m2 and accumulates into the same O^T, a second MMA (tensor memory holds
+// 512 columns).
 //
-// Warp roles:
-//   warps 0..4CG-1      softmax (CG column groups of HC query columns).  They
-//                       first turn the CTA's queries into q_hi, q_lo.
-//   warp 4CG            tensor memory, and the MMAs
-//   8 warps after it    expansion.  A thread owns quarter q (32 codes) of each
-//                       block of two keys.  It loads the next tile's codes
-//                       into registers as it finishes this tile's blocks, so
-//                       every global load has a whole tile's time to land and
-//                       no packed staging passes through shared memory.
+// Work.  With nsplit = 0 the grid is one CTA per SM.  All row groups' tiles,
+// each group with kKv4SegCost tiles more for its start and end, form one axis
+// that is cut into equal pieces; a CTA works through the segments of its piece
+// (kv4::Schedule).  Lengths are read on the device, so a captured graph follows
+// them.  With nsplit >= 1 a CTA takes one chunk of one row group.
 //
-// Slots.  A ring of 16 KB slots (128 keys x 128 channels, 8 bits, in the
-// 128-byte-swizzle atom of 8 keys x 128 bytes) takes the blocks of the tiles in
-// order.  The same bytes are the K-major A operand of S^T and the MN-major A
-// operand of O^T.  A tile's RoPE block is free after S^T, its value block m
-// after O^T block m.  MMA order: S^T(t+1) as far as the ring reaches past tile
-// t, then O^T(t), then the rest of S^T(t+1) -- so the softmax of tile t runs
-// beside S^T(t+1), and the expansion of t+1 beside O^T(t).
+// Warp roles (CG = NQ / 16 column groups; registers are dealt out by role):
+//   4 CG warps     softmax: a thread owns one key and 16 columns.  They also
+//                  turn a segment's queries into q_hi, q_lo, and write O out.
+//   1 + 1 warps    MMAs of S^T and of O^T, and the tensor memory
+//   2 warps        segments, row ids, mask words, a ring of 4 tiles ahead
+//   8 or 16 warps  expansion.  A thread owns quarter q (32 codes) of each block
+//                  of one key (NQ <= 32) or two.  It loads the next tile's
+//                  codes into registers as it finishes this tile's blocks, so a
+//                  load has a whole tile's time to land and no packed staging
+//                  passes through shared memory.
+//
+// Slots.  Two sets of four 16 KB slots (128 keys x 128 channels, 8 bits, in the
+// 128-byte-swizzle atom of 8 keys x 128 bytes), by tile parity, take the value
+// blocks; the RoPE block has its own slot (NQ <= 48), or goes through block 0's
+// slot first (NQ = 64; shared memory is full).  The same bytes are the K-major
+// A operand of S^T and the MN-major A operand of O^T.  The RoPE block is free
+// after S^T, value block m after O^T block m.
 //
 // P^T is written MN-major (a thread owns one key, its columns are contiguous:
 // 16-byte stores), in the unswizzled layout of 16 columns x 8 keys cores.
+//
+// What bounds it (GB300).  576 rows over 64k keys, NQ = 64: 110 us per call, 0.74
+// PFLOP/s of the bf16-equivalent work; the tensor pipe is 49 % busy, the ALUs 51 %,
+// shared memory 85 % (45 % loads and stores, 40 % MMA operands).  No unit is
+// the limit alone: a tile takes ~5500 cycles, its expansion ~4700 of them, and
+// a slot set's round -- expand, S^T, softmax, O^T -- twice that.  Timed without
+// the exponentials and conversions it takes 107 us, without the softmax's
+// meeting 104, with half the expansion 109.7, with all of these cut 100.
+// Decode (16 requests, NQ = 16): 43 us, 2.1 TB/s; ~8 us are start-up (three
+// dependent reads: lengths, row ids, rows) and 4 the merge.  Neither polling in
+// place of suspended waits, nor a first pass over the expansion's code while it
+// waits for row ids, nor asking for the next slot a block ahead gained
+// anything (64k keys: 113, 115 and 118 us against 111).
 //
 // Waits are bounded as in split_tc.cuh.
 #pragma once
@@ -662,7 +683,7 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
     const uint32_t off0 = key0 * 128 + (((2 * q) ^ (key0 & 7)) << 4);
     const uint32_t off1 = key0 * 128 + (((2 * q + 1) ^ (key0 & 7)) << 4);
     constexpr int K = Cfg::kOwnKeys;
-    int32_t row[K], id[K];  // pool rows of the tile being loaded, and of the one after
+    int32_t row[K] = {}, id[K] = {};  // pool rows of the tile being loaded, and of the one after
     uint4 code[K][kKv4Blocks], scale[K];
     bool ok = true, more = true;
     auto at = [&](int h, int byte) { return a.kv4_pool + 16 * q + byte + (uint64_t)(uint32_t)row[h] * kKv4RowBytes; };
