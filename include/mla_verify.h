@@ -112,7 +112,9 @@ extern "C" {
  * bf16, the scores, softmax and sums fp32, and the values enter the products
  * exactly.  A row that a call references must have been stored (or be masked:
  * unlike a bf16 row, a masked 4-bit row may hold any bytes).  Each query value
- * must be finite.  A 4-bit row takes a third of a bf16 row's memory.
+ * must be finite (the tensor-core kernel with nsplit = 0 returns NaN for a row
+ * that has an infinity or a NaN).  A 4-bit row takes a third of a bf16 row's
+ * memory.
  * With MLA_VERIFY_FUSED_MERGE or MLA_VERIFY_REFETCH_VALUES: EINVAL. */
 #define MLA_VERIFY_KV4 0x10
 #define MLA_VERIFY_KV4_ROW_BYTES 384
@@ -137,7 +139,9 @@ typedef struct {
                        *       and its other chunks are empty;
                        * 0: the plan picks the number of chunks (describe().grid_y) and the
                        *    row-group size for this GPU from max_batch and max_kv_len; runs then
-                       *    pass nsplit = 0 as well */
+                       *    pass nsplit = 0 as well.  With MLA_VERIFY_KV4 on the tensor-core
+                       *    kernel there are no chunks: one CTA per SM takes an equal piece of
+                       *    all the requests' work, measured on the device at each call */
   int32_t d_latent;   /* must be 512 */
   int32_t d_rope;     /* must be 64 */
   int32_t flags;      /* OR of MLA_VERIFY_FORCE_SIMT, MLA_VERIFY_FUSED_MERGE, MLA_VERIFY_REFETCH_VALUES,
@@ -149,7 +153,8 @@ typedef struct {
   int32_t kernel;        /* 1 = tcgen05 tensor-core split kernel, 0 = CUDA-core split kernel */
   int32_t rows_per_cta;  /* query rows (token x head pairs) one split CTA covers */
   int32_t keys_per_tile; /* keys per pipeline tile (128) */
-  int32_t grid_x, grid_y, grid_z; /* split grid: row groups x KV chunks per request x max_batch */
+  int32_t grid_x, grid_y, grid_z; /* split grid: row groups x KV chunks per request x max_batch;
+                                   * SMs x 1 x 1 for MLA_VERIFY_KV4 with nsplit = 0 */
   int32_t merge_blocks;  /* merge grid size; 0 when the split kernel merges (MLA_VERIFY_FUSED_MERGE) */
   int32_t smem_bytes;    /* dynamic shared memory of the split kernel */
   size_t workspace_bytes;
@@ -165,7 +170,10 @@ typedef struct {
  * device workspace every run with this plan needs (fp32 partial O and LSE
  * for grid_y x max_batch*q_len*num_heads rows -- grid_y = nsplit, or the
  * plan's count when nsplit = 0 -- plus a 256-byte header, and
- * for MLA_VERIFY_FUSED_MERGE one 32-bit counter per request and row group).
+ * for MLA_VERIFY_FUSED_MERGE one 32-bit counter per request and row group;
+ * for MLA_VERIFY_KV4 with nsplit = 0 on the tensor-core kernel, O and LSE of
+ * rows_per_cta rows per SM and per request and row group, the header, and 8
+ * bytes per request and row group).
  * The workspace must be 256-byte aligned and zero-filled once before its
  * first use (e.g. torch.zeros, or mla_verify_workspace_init); the library
  * keeps the header and the counters consistent afterwards (after a call that

@@ -103,3 +103,20 @@ def test_bits_do_not_depend_on_a_neighbours_contents():
     o2, l2 = v.run(d, 3, wl["sm_scale"])
     assert torch.equal(o[:2], o2[:2]) and torch.equal(o[4:6], o2[4:6]) and torch.equal(lse[4:6], l2[4:6])
     assert not torch.equal(o[2:4], o2[2:4])
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("heads,keys", [(5, 40), (8, 3000), (64, 20000)])
+def test_a_query_that_is_not_finite_makes_its_row_nan(bad, heads, keys):
+    """... and no other row of its group."""
+    wl = U.workload(2, heads, [2, 1], [keys, 100], keys + 200, seed=heads)
+    d, v = U.device(wl), U.verifier(wl)
+    o, lse = (x[:3].clone() for x in v.run(d, 2, wl["sm_scale"]))
+    d["q_nope"][0, 1, 17] = bad
+    d["q_rope"][2, heads - 1, 3] = bad
+    o2, l2 = (x[:3] for x in v.run(d, 2, wl["sm_scale"]))
+    assert v.status() == 0
+    hit = torch.zeros((3, heads), dtype=torch.bool, device="cuda")
+    hit[0, 1] = hit[2, heads - 1] = True
+    assert bool(o2[hit].isnan().all()) and bool(l2[hit].isnan().all())
+    assert torch.equal(o2[~hit], o[~hit]) and torch.equal(l2[~hit], lse[~hit])
