@@ -81,15 +81,6 @@ __device__ __forceinline__ int kv4_exponent_of(float a) {
   return e > kKv4EMax ? kKv4EMax : e;
 }
 
-// Nearest magnitude of y = |x| / 2^e, ties to the even one, at most 6; a NaN
-// compares false everywhere and becomes 0.
-__device__ __forceinline__ uint32_t kv4_magnitude(float y) {
-  return (y > 0.25f) + (y >= 0.75f) + (y > 1.25f) + (y >= 1.75f) + (y > 2.5f) + (y >= 3.5f) + (y > 5.0f);
-}
-
-// Position of the sign of channel i in its word.
-__device__ __forceinline__ int kv4_sign_bit(int i) { return i < 4 ? 8 * i + 7 : 8 * (i - 4) + 3; }
-
 #endif  // __CUDACC__
 
 cudaError_t launch_store_kv4(const void* latent, int64_t latent_stride, const void* rope, int64_t rope_stride,
