@@ -189,6 +189,9 @@ cudaError_t kv4_launch(int nq, const SplitArgs& a, dim3 grid, cudaStream_t st) {
 // rows over 185k 113 / 90 / 75 / 84 us; 16 ragged requests 720 / 430 / 330 /
 // 289 us.  The model takes the least of each.
 double kv4_tile_us(int nq) { return nq >= 64 ? 3.05 : nq >= 48 ? 2.6 : nq >= 32 ? 2.3 : 1.95; }
+// With 1 / 2 / 3 tiles: 576 rows over 4k keys 29.2 / 24.2 / 24.1 us, over 64k
+// 112.9 / 110.4 / 108.6; 16 ragged requests 294.7 / 288.8 / 292.0; 16 decode
+// requests 43.2 / 42.9 / 43.5.
 constexpr int kKv4SegCost = 2;
 
 // Row-group size: the least modelled time of a CTA's equal piece of the work
