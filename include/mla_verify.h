@@ -109,12 +109,14 @@ extern "C" {
  *
  * A key's RoPE value is the sum of its code's and its residual's.  Attention
  * over a 4-bit pool is the operation above on these values: the queries stay
- * bf16, the scores, softmax and sums fp32, and the values enter the products
- * exactly.  A row that a call references must have been stored (or be masked:
- * unlike a bf16 row, a masked 4-bit row may hold any bytes).  Each query value
- * must be finite (the tensor-core kernel with nsplit = 0 returns NaN for a row
- * that has an infinity or a NaN).  A 4-bit row takes a third of a bf16 row's
- * memory.
+ * bf16, the scores, softmax, LSE and sums fp32, and the values enter the
+ * products exactly.  In the tensor-core kernel a weight enters the value product
+ * with an error of at most 2^-8 + 2^-11 of itself, and small ones, however many
+ * there are, lose at most 2^-8 of the row's total together.  A row that a call
+ * references must have been stored (or be masked: unlike a bf16 row, a masked
+ * 4-bit row may hold any bytes).  Each query value must be finite (the
+ * tensor-core kernel with nsplit = 0 returns NaN for a row that has an infinity
+ * or a NaN).  A 4-bit row takes a third of a bf16 row's memory.
  * With MLA_VERIFY_FUSED_MERGE or MLA_VERIFY_REFETCH_VALUES: EINVAL. */
 #define MLA_VERIFY_KV4 0x10
 #define MLA_VERIFY_KV4_ROW_BYTES 384

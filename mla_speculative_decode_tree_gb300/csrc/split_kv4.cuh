@@ -16,15 +16,37 @@
 // e4m3 carries 4 significant bits, so q_hi takes a bf16 value's upper four and
 // q_lo the other four exactly (down to 2^-15 of the row's largest value, below
 // which the error is under 2^-23 of it): scores are as exact as with bf16
-// operands.  p_hi + p_lo keeps 8 to 9 bits, as much as a bf16 P would, down
-// to 2^-18 of the row's largest weight.  The products and sums are fp32.  A
-// single e4m3 P instead of the pair would take a quarter off the MMAs and 3 % off
-// the call (64k keys, NQ = 64), for four significant bits in place of eight.
+// operands.  The products and sums are fp32.  A single e4m3 P instead of the
+// pair would take a quarter off the MMAs and 3 % off the call (64k keys, NQ = 64),
+// for four significant bits in place of seven or eight.
+//
+// What P keeps.  In a column's scale a weight p >= 2^-6 is off by at most 2^-8 of
+// itself (2^-9 for NQ <= 32) and 2^-11 from its way through a half; a smaller one
+// by at most 2^-14 (2^-15), however small it is: 8-bit floats end there, a bf16 P
+// would not.  Many small weights below one large one -- a sink above a long tail,
+// as language models have it -- would so lose what they are together, which l,
+// summed from p itself, still counts.  So the scale follows them: now and then a
+// column's mean weight so far is looked at, and where it is below 2^-5 the scale
+// is raised until the tile's maximum maps to 2^6, O^T and l with it (fp32 has room
+// for 2^80).  What all the small ones lose is then at most 2^-8 of l (2^-9):
+// n keys lose n * 2^-14.  They are weighed a tile after they were looked at, so
+// where a mean of 2^-5 was found after k tiles, the next verdict is a tile after
+// the next look, and the sum is at least 8, the first maximum, by then:
+//   k        1              3                5                9 ...
+//   verdict  512 / 2^14     768 / 2^14       1280 / 2^14      1792 / 2^14
+//   of       8              12               20               36
+// each 2^-8 or less.  A maximum just mapped to 2^6 faces six tiles at most:
+// 2^-10.4.  A sink 11 above a tail of 32,767 equal keys: 0.1 % off in O; with a
+// scale from the maximum alone (2^2 to 2^8) up to 31 % (NQ <= 32) and 5 %.  It costs 2 to 4 % of the call (64k keys 111.0 -> 114.9 us,
+// 185k 75.2 -> 77.8, 16 ragged requests 291 -> 297, decode 43.2 -> 44.2), nearly all
+// of it in the rescales that the smaller headroom brings.  Maxima at 2^4 and 2^6
+// would cost 7 % at 64k keys; 2^2 and 2^4 with a mean of 2^-6 1.5 %, for a
+// bound of 2^-6.
 //
 // The RoPE residual codes are 64 more K columns against the same q_rope, so a
 // key is 640 codes: five blocks of 128, 20 k-steps of 32.
 //
-// p_lo.  NQ <= 32: p_hi and 16 * p_lo (both e4m3) sit side by side on N and O^T
+// p_lo.  NQ <= 32: p_hi and 32 * p_lo (both e4m3) sit side by side on N and O^T
 // keeps both halves in tensor memory (4 x 2 NQ columns), added at the end.  An
 // M = 128 MMA costs 32 + N/4 cycles, most of it for reading its 4 KB A operand
 // from shared memory, so the second half is nearly free.  NQ = 48 and 64: p_lo
@@ -79,12 +101,20 @@
 
 namespace mlav {
 
-// Base 2.  The running max of a column maps to p = 2^kKv4Top, the first one it
-// sees to 2^kKv4First (scores usually grow for a while), and it is raised when
-// a score would pass 2^kKv4Limit (e4m3 ends at 448).
-constexpr float kKv4First = 2.0f, kKv4Top = 4.0f, kKv4Limit = 8.0f;
+// Base 2.  A column's scale of p: the first maximum it sees maps to 2^kKv4First
+// (scores usually grow for a while), one that would pass 2^kKv4Limit (e4m3 ends
+// at 448) lowers the scale until it maps to 2^kKv4Top, and a mean weight below
+// kKv4MeanP raises it until the tile's maximum does (What P keeps, above).
+constexpr float kKv4First = 3.0f, kKv4Top = 6.0f, kKv4Limit = 8.0f;
+constexpr float kKv4MeanP = 0.03125f;
+constexpr float kKv4MaxSum = 1.2e24f;  // 2^80: a sum that the raised scale may not pass
+// Whether the mean is looked at after so many tiles of a segment: 1, 3, 5, 9, 13, ...  (Not after two in a row: the
+// sums of one look are read in the tile in which the next ones would be written.)
+__device__ __forceinline__ bool kv4_looks_at_mean(int done) {
+  return (done & 3) == 1 || done == 3;
+}
 constexpr float kQLoScale = 32.f;
-constexpr float kPLoScale = 16.f;  // concatenated halves only
+constexpr float kPLoScale = 32.f;  // concatenated halves only
 
 template <int NQ>
 struct Kv4Cfg {
@@ -162,8 +192,7 @@ struct Kv4Segment {
   int64_t prow;        // row of the partial outputs
 };
 struct Kv4Request {
-  int32_t n, keys, prefix, kv0, mask0, groups;
-  int64_t q0;
+  int32_t n, keys, kv0, mask0, groups, q0;
 };
 // Where the hand-out of segments stands (kv4::next_segment).
 struct Kv4Cursor {
@@ -192,7 +221,8 @@ struct Kv4Ctl {
   alignas(16) float nmu[NQ];     // what turns a score into log2 p; +inf before any visible key
   alignas(16) float alpha[NQ];   // rescale factor of the tile; 1/l in the epilogue
   alignas(16) float red[4][NQ];
-  uint32_t colmask[kMaxQLen][Kv4Cfg<NQ>::kCG];  // per token: which of a column group's columns are its
+  alignas(16) float sum[4][NQ];  // sums of p where the mean is looked at
+  uint16_t colmask[kMaxQLen][Kv4Cfg<NQ>::kCG];  // per token: which of a column group's columns are its
   Kv4Segment seg[2];
   Kv4Cursor cursor;
   uint32_t tile[Kv4Cfg<NQ>::kIndexRing];                     // kTile* bits
@@ -468,11 +498,10 @@ struct Schedule {
     if (b >= a.batch) return 0;
     const RequestTokens rq = request_tokens(a, b);
     r.kv0 = a.kv_indptr[b];
-    r.prefix = a.kv_indptr[b + 1] - r.kv0;
     r.mask0 = a.mask_indptr[b];
-    r.q0 = rq.q0;
+    r.q0 = (int)rq.q0;
     r.n = rq.n;
-    r.keys = r.prefix + rq.n;
+    r.keys = a.kv_indptr[b + 1] - r.kv0 + rq.n;
     r.groups = (rq.n * a.H + nq - 1) / nq;
     return (int64_t)r.groups * ((r.keys + kKeysPerTile - 1) / kKeysPerTile + a.seg_cost);
   }
@@ -528,7 +557,7 @@ struct Schedule {
     s.q0 = r.q0;
     s.n_tokens = r.n;
     s.keys = r.keys;
-    s.prefix = r.prefix;
+    s.prefix = r.keys - r.n;
     s.kv0 = r.kv0;
     s.mask0 = r.mask0;
     s.r0 = g * nq;
@@ -555,7 +584,7 @@ struct Schedule {
       int chunk = (per + kKeysPerTile - 1) / kKeysPerTile;
       chunk = chunk < a.min_chunk / kKeysPerTile ? a.min_chunk / kKeysPerTile : chunk;
       const int64_t t0 = (int64_t)blockIdx.y * chunk;
-      const int64_t prow = (int64_t)blockIdx.y * a.rows_max + r.q0 * a.H + g * nq;
+      const int64_t prow = (int64_t)blockIdx.y * a.rows_max + (int64_t)r.q0 * a.H + g * nq;
       if (t0 >= tiles) {  // an empty chunk
         const int nrows = r.n * a.H - g * nq;
         for (int n = lane; n < nrows && n < nq; n += 32) a.part_lse[prow + n] = -INFINITY;
@@ -1024,7 +1053,7 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
         const int lo = first < 0 ? 0 : first;
         int hi = first + a.H < HC ? first + a.H : HC;
         hi = nrows - h * HC < hi ? nrows - h * HC : hi;
-        ctl.colmask[tok][h] = hi > lo ? (0xFFFFFFFFu >> (32 - (hi - lo))) << lo : 0u;
+        ctl.colmask[tok][h] = (uint16_t)(hi > lo ? (0xFFFFu >> (HC - (hi - lo))) << lo : 0u);
       }
       // Queries: warp w turns rows w, w + warps, ... into q_hi and q_lo, two at
       // a time so that their loads overlap.  Lane l holds channels 8l..8l+7 and
@@ -1152,12 +1181,25 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
         };
         const bool first = t == t_first;  // there is no maximum yet
         bool need = false;
+        const int done = t - t_first;
+        // The sums so far: written in one tile, weighed up in the next, with its
+        // meeting in between.  Lane c of each warp weighs column c0 + c; one that has
+        // seen no key, or is no row, asks for nothing.
+        if (kv4_looks_at_mean(done)) kv4::columns_to_smem<false>(acc, &ctl.sum[quad][c0], lane);
+        float l = 0.f;
+        bool small = false;
+        if (kv4_looks_at_mean(done - 1) && lane < HC) {
+          const int n = c0 + lane;
+          l = (ctl.sum[0][n] + ctl.sum[1][n]) + (ctl.sum[2][n] + ctl.sum[3][n]);
+          small = l > 0.f && l < (float)(done - 1) * (kKeys * kKv4MeanP) && n < nrows;
+          need = small;
+        }
         if (!my_abort && !first) {
           load_scores(true);
           float top = fmaxf(x[0], x[1]);
 #pragma unroll
           for (int c = 2; c < HC; c += 2) top = kv4::max3(top, x[c], x[c + 1]);
-          need = top > kKv4Limit;
+          need = need || top > kKv4Limit;
         } else if (my_abort) {
 #pragma unroll
           for (int c = 0; c < HC; ++c) x[c] = -INFINITY;
@@ -1165,7 +1207,8 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
         bool rescale = false;
         if (first || kv4::bar_any(bar_id, 128, need || my_abort || ctl.abort)) {
           // Rare but for a segment's first tile: a score passed the running max
-          // by too much, a column saw its first key, or a wait gave up.
+          // by too much, a column saw its first key, its weights have become
+          // small, or a wait gave up.
           const bool ab = __any_sync(0xffffffffu, my_abort) || ctl.abort;
           if (lane == 0) ctl.flag[warp] = ab ? 1 : 0;
           if (!my_abort) load_scores(false);
@@ -1180,6 +1223,14 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
             const float cm = fmaxf(fmaxf(ctl.red[0][n], ctl.red[1][n]), fmaxf(ctl.red[2][n], ctl.red[3][n]));
             const float old = ctl.nmu[n];
             float al = 1.f;
+            if (small && cm + old < kKv4Top) {
+              const float up = ex2_approx(kKv4Top - cm - old);  // (cm = -inf: +inf)
+              if (l * up < kKv4MaxSum) {
+                al = up;
+                ctl.nmu[n] = kKv4Top - cm;
+                raised = true;
+              }
+            }
             if (cm + old > kKv4Limit) {  // old = +inf: the first visible key (cm = -inf gives NaN, no)
               const float nm = (old == INFINITY ? kKv4First : kKv4Top) - cm;
               al = old == INFINITY ? 0.f : ex2_approx(nm - old);
@@ -1243,8 +1294,8 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
             uint32_t r23 = kv4::sub_f16x2(h23, kv4::cvt_f16x2_e4m3x2(u23));
             hi[k4] = u01 | (u23 << 16);
             if constexpr (Cfg::kConcat) {
-              r01 = kv4::mul_f16x2(r01, 0x4C004C00u);  // 16: kPLoScale
-              r23 = kv4::mul_f16x2(r23, 0x4C004C00u);
+              r01 = kv4::mul_f16x2(r01, 0x50005000u);  // 32: kPLoScale
+              r23 = kv4::mul_f16x2(r23, 0x50005000u);
               lo[k4] = kv4::cvt_e4m3x2_f16x2(r01) | (kv4::cvt_e4m3x2_f16x2(r23) << 16);
             } else {
               lo[k4] = kv4::cvt_e5m2x2_f16x2(r01) | (kv4::cvt_e5m2x2_f16x2(r23) << 16);
