@@ -560,6 +560,7 @@ int merge_impl(mla_verify_plan_t pl, int32_t batch, int32_t nsplit, const int32_
     m.groups_max = pl->groups;
     m.T = pl->p.q_len;
     m.rows_per_block = pl->merge_rows;
+    m.partials = pl->p.max_batch * pl->groups + pl->pieces;
   }
   cudaError_t e = pl->pieces ? launch_merge_pieces(m, static_cast<cudaStream_t>(stream))
                              : launch_merge(m, static_cast<cudaStream_t>(stream));

@@ -78,6 +78,7 @@ struct MergeArgs {
   uint32_t* status;  // header words 0 (accumulated) and 1 (last call)
   const int2* seg_table;  // work in equal pieces: see SplitArgs; T tokens per request or qo_indptr
   int32_t nq, groups_max, T, rows_per_block;
+  int32_t partials;     // of nq rows that the workspace has room for
   int32_t quarter;      // four warps per row (few rows) instead of two
   int32_t speculative;  // quarter layout: load the first 16 splits' partials before their LSEs
 };

@@ -155,8 +155,16 @@ __global__ void __launch_bounds__(32 * kPieceWarps, 5) merge_pieces_kernel(Merge
   const int64_t stride = a.nq;  // rows from one partial of a group to the next
   const int2* table = a.seg_table + b * a.groups_max;
   const int g0 = r0 / a.nq;  // the rows lie in two groups at most
-  const int2 seg0 = table[g0];
-  const int2 seg1 = (r0 + rows - 1) / a.nq != g0 ? table[g0 + 1] : seg0;
+  // A split CTA that gave up has not written the entries of its later row groups:
+  // they hold what stood there, and one that points out of the workspace counts
+  // as no partials.
+  auto entry = [&](int g) -> int2 {
+    const int2 s = table[g];
+    const bool in = s.x >= 0 && s.y >= 0 && s.y <= a.partials && s.x <= a.partials - s.y;
+    return in ? s : make_int2(0, 0);
+  };
+  const int2 seg0 = entry(g0);
+  const int2 seg1 = (r0 + rows - 1) / a.nq != g0 ? entry(g0 + 1) : seg0;
   auto place = [&](int r, int& n) -> int64_t {  // first partial's row of row r0 + r, and how many
     const int2 seg = (r0 + r) / a.nq == g0 ? seg0 : seg1;
     n = seg.y;
