@@ -115,8 +115,8 @@ extern "C" {
  * there are, lose at most 2^-8 of the row's total together.  A row that a call
  * references must have been stored (or be masked: unlike a bf16 row, a masked
  * 4-bit row may hold any bytes).  Each query value must be finite (the
- * tensor-core kernel with nsplit = 0 returns NaN for a row that has an infinity
- * or a NaN).  A 4-bit row takes a third of a bf16 row's memory.
+ * tensor-core kernel returns NaN for a row that has an infinity or a NaN and
+ * sees a key).  A 4-bit row takes a third of a bf16 row's memory.
  * With MLA_VERIFY_FUSED_MERGE or MLA_VERIFY_REFETCH_VALUES: EINVAL. */
 #define MLA_VERIFY_KV4 0x10
 #define MLA_VERIFY_KV4_ROW_BYTES 384

@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(128 * kQuarterRowsPerBlock, 2) merge_quarter_k
 // rows_per_block rows of a request, at most 4: a warp per row where the row
 // groups have few partials, else one row after the other with the partials
 // dealt out to the warps.  Lane l owns columns 128 k + 4 l .. + 3.  Sums run in
-// a fixed order.  A NaN LSE makes the row NaN.
+// a fixed order.  An LSE of +inf makes the row NaN.
 //
 // What bounds it is the chain of reads: lengths, table, LSEs and partials.  A
 // warp per quarter or half row, as in the merges above, left a single long
@@ -72,15 +72,9 @@ constexpr int kAtOnce = 3;
 // Largest LSE of a row's n partials, `stride` apart, and the sum of their weights.
 __device__ __forceinline__ void merge_weights(const float* lse, int n, int64_t stride, int lane, float& M, float& W) {
   M = -INFINITY;
-  bool nan = false;
-  for (int s = lane; s < n; s += 32) {
-    const float x = lse[s * stride];
-    nan |= x != x;
-    M = fmaxf(M, x);
-  }
+  for (int s = lane; s < n; s += 32) M = fmaxf(M, lse[s * stride]);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-  if (__any_sync(0xffffffffu, nan)) M = NAN;
   W = 0.f;
   if (M == -INFINITY) return;
   for (int s = lane; s < n; s += 32) W += expf(lse[s * stride] - M);  // (-inf gives 0)

@@ -1322,8 +1322,13 @@ __global__ void __launch_bounds__(Kv4Cfg<NQ>::kThreads, 1) split_kv4_kernel(cons
         const int n = c0 + j;
         const float l = (ctl.red[0][n] + ctl.red[1][n]) + (ctl.red[2][n] + ctl.red[3][n]);
         ctl.alpha[n] = l == 0.f ? 0.f : 1.f / l;
+        // A row that is not a number gets +inf: the largest of its LSEs in any merge,
+        // where its weight exp(inf - inf) makes the row NaN.  (A NaN would be passed
+        // over by their maxima, and the row would read as one that sees nothing.)
         if (n < nrows)
-          a.part_lse[sg.prow + n] = l == 0.f ? -INFINITY : (__log2f(l) - ctl.nmu[n]) * 0.69314718055994530942f;
+          a.part_lse[sg.prow + n] = l == 0.f ? -INFINITY
+                                    : l != l ? INFINITY
+                                             : (__log2f(l) - ctl.nmu[n]) * 0.69314718055994530942f;
       }
       named_bar_sync(bar_id, 128);
       // Thread (quad, lane) holds latent column 128m + j of rows c0..c0+HC: a
