@@ -522,6 +522,7 @@ struct Schedule {
                                                   Kv4Cursor& c) {
     Kv4Request r;
     const int64_t incl = carry + scan(request(a, nq, base + lane, r), lane);
+    __syncwarp();  // every lane has read what is replaced (shuffles order no memory)
     c.req[lane] = r;
     c.end[lane] = incl;
     if (lane == 0) {
