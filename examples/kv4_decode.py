@@ -3,12 +3,13 @@
 One step is four calls in one CUDA graph: block tables and slot maps from the
 requests' lengths, the drafts' keys stored into the 4-bit pool, the drafts' tree
 masks, the verify attention.  Lengths change from step to step; the captured
-graph reads them on the device.  Between steps the host hands back the pages
-that only rejected drafts used.
+graph reads them on the device.  Between steps the rows of the accepted path
+move to the front of the new ones, and the host hands back the pages that only
+rejected drafts used.
 
     python examples/kv4_decode.py            # random weights; prints the step time and an error
 
-Synthetic: tokens and queries are random, and so is the number of accepted drafts.
+Synthetic: tokens and queries are random, and so are the draft trees and the path through each that is accepted.
 """
 
 import argparse
@@ -84,13 +85,18 @@ class Kv4Decoder:
         self.graph.replay()
         return self.out
 
-    def accept(self, accepted):
-        """accepted[b] of request b's new tokens stay: the first of them, moved there where the tree's path is not a
-        prefix.  Pages that hold none of them are free again."""
+    def accept(self, paths):
+        """Of request b's new tokens those on paths[b] stay: a path of its draft tree, node numbers from a root on (empty:
+        none).  Their rows move to the first of the new rows; pages past them are free again."""
         status = self.v.status()  # (waits for the step)
         if status:
             raise RuntimeError("verify step reported status 0x%x" % status)
-        old, new, k = self.seq_lens.tolist(), self.new_lens.tolist(), 0
+        old, new, at, k = self.seq_lens.tolist(), self.new_lens.tolist(), self.qo_indptr.tolist(), 0
+        src = [at[b] + i for b, path in enumerate(paths) for i in path]
+        dst = [at[b] + i for b, path in enumerate(paths) for i in range(len(path))]
+        if src != dst:
+            src, dst = (self.slots[torch.tensor(x, device=self.slots.device)].long() for x in (src, dst))
+            self.pool[dst] = self.pool[src]  # (all read before any is written: a row may be both)
         taken = self.free_host[::-1][:int(self.used)]
         del self.free_host[len(self.free_host) - len(taken):]
         for b in range(self.batch):
@@ -98,10 +104,10 @@ class Kv4Decoder:
             fresh = -(-(old[b] + new[b]) // self.page) - have
             pages = self.table_host[b] + taken[k:k + fresh]
             k += fresh
-            keep = -(-(old[b] + accepted[b]) // self.page)
+            keep = -(-(old[b] + len(paths[b])) // self.page)
             self.table_host[b], back = pages[:keep], pages[keep:]
             self.free_host.extend(back)
-        self.seq_lens += torch.tensor(accepted, dtype=torch.int32, device=self.seq_lens.device)
+        self.seq_lens += torch.tensor([len(path) for path in paths], dtype=torch.int32, device=self.seq_lens.device)
 
 
 def exact(dec, b, t0, t1):
@@ -120,6 +126,15 @@ def exact(dec, b, t0, t1):
     s = torch.einsum("nhd,kd->nhk", q, kv.double()) * dec.scale
     p = torch.softmax(s.masked_fill(~see[:, None, :], float("-inf")), -1)
     return torch.einsum("nhk,kd->nhd", p, kv[:, :512].double())
+
+
+def random_path(parents, rng):
+    """Node numbers from a root to a random node of a draft tree, or none."""
+    path, i = [], int(rng.integers(-1, len(parents)))
+    while i >= 0:
+        path.append(i)
+        i = int(parents[i])
+    return path[::-1]
 
 
 def main(batch=8, heads=16, drafts=6, prompt=2000, steps=6, page=64, seed=0):
@@ -156,7 +171,7 @@ def main(batch=8, heads=16, drafts=6, prompt=2000, steps=6, page=64, seed=0):
             if at[b + 1] > at[b]:
                 ref = exact(dec, b, at[b], at[b + 1])
                 worst = max(worst, float((o[at[b]:at[b + 1]].double() - ref).norm() / ref.norm()))
-        dec.accept([int(rng.integers(0, t + 1)) for t in new])
+        dec.accept([random_path(parents[at[b]:at[b + 1]], rng) for b in range(batch)])
     return worst, float(np.median(times)), dec
 
 
