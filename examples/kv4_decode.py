@@ -62,11 +62,15 @@ class Kv4Decoder:
                           custom_mask=self.mask, mask_indptr=self.mask_indptr), self.batch, self.scale)
 
     def prefill(self, b, latent, rope):
-        """Store a prompt of request b: latent bf16 [n, 512], rope bf16 [n, 64]."""
+        """Store a prompt as request b's, in place of what it held: latent bf16 [n, 512], rope bf16 [n, 64]."""
         n = latent.shape[0]
-        pages = [self.free_host.pop() for _ in range(-(-n // self.page))]
+        need = -(-n // self.page)
+        if need > len(self.free_host) + len(self.table_host[b]) or need > self.table.shape[1]:
+            raise ValueError("no room for a prompt of %d tokens" % n)
+        self.free_host.extend(self.table_host[b])
+        pages = [self.free_host.pop() for _ in range(need)]
         self.table_host[b] = pages
-        row = np.concatenate([np.arange(p * self.page, (p + 1) * self.page) for p in pages])[:n].astype(np.int32)
+        row = (np.array(pages, np.int32)[:, None] * self.page + np.arange(self.page, dtype=np.int32)).reshape(-1)[:n]
         B.mla_verify_store_kv4(self.v.plan, latent, rope, torch.from_numpy(row).to(latent.device), self.pool,
                                self.v.workspace)
         self.seq_lens[b] = n
