@@ -14,7 +14,7 @@
 // Every block scans the lengths of all requests itself (at most 4096: 32 KB
 // from L2), so no block waits on another and one launch does everything; a
 // row in a fresh page reads the free list, not the table entry another block
-// writes.  The three exclusive scans stay in shared memory.  A warp takes 128
+// writes.  The three exclusive scans and P_b stay in shared memory.  A warp takes 128
 // output entries; their request is found by a warp-wide search there, and a
 // chunk inside one request's prefix -- nearly all -- then needs two table
 // entries per thread and one 16-byte store.
@@ -41,6 +41,7 @@ struct SlotsDev {
   int32_t* kv;     // shared: exclusive scans, [batch + 1] each
   int32_t* qo;
   int32_t* fresh;
+  int32_t* cached;  // P_b (the scan's sums stop at 2^31 - 1, so its differences are not it)
 
   __device__ __forceinline__ int seq_len(int b) const {
     const int v = a.seq_lens[b];
@@ -96,7 +97,7 @@ struct SlotsDev {
   // Where the page of position pos of request b is written, its c-th page; null where there is none.
   __device__ __forceinline__ const int32_t* page_at(int b, int64_t pos, int64_t& c) const {
     c = page_of(pos);
-    const int64_t have = pages(kv[b + 1] - kv[b]);
+    const int64_t have = pages(cached[b]);
     if (c >= a.max_pages) return nullptr;
     if (c < have) return a.block_table + (int64_t)b * a.max_pages + c;
     const int64_t f = (int64_t)fresh[b] + (c - have);
@@ -162,6 +163,7 @@ __device__ __forceinline__ void scan_requests(const SlotsDev<kPow2>& d) {
     uint32_t x[3] = {0, 0, 0};
     if (b < d.a.batch) {
       const int P = d.seq_len(b), T = d.new_len(b);
+      d.cached[b] = P;
       x[0] = (uint32_t)P;
       x[1] = (uint32_t)T;
       x[2] = (uint32_t)(d.pages((int64_t)P + T) - d.pages(P));
@@ -193,7 +195,7 @@ template <bool kPow2>
 __global__ void __launch_bounds__(kThreads) slots_kernel(SlotsArgs args) {
   extern __shared__ int32_t scans[];
   const int n1 = args.batch + 1;
-  const SlotsDev<kPow2> d{args, scans, scans + n1, scans + 2 * n1};
+  const SlotsDev<kPow2> d{args, scans, scans + n1, scans + 2 * n1, scans + 3 * n1};
   const SlotsArgs& a = d.a;
   scan_requests(d);
 
@@ -250,7 +252,7 @@ __global__ void __launch_bounds__(kThreads) slots_kernel(SlotsArgs args) {
       if (lane + 32 * k < left) {
         const int x = first + lane + 32 * k;
         const int b = d.owner(scan, x, b0, b1);
-        pos[k] = (int64_t)(x - scan[b]) + (pre ? 0 : d.kv[b + 1] - d.kv[b]);
+        pos[k] = (int64_t)(x - scan[b]) + (pre ? 0 : d.cached[b]);
         at[k] = d.page_at(b, pos[k], page_no[k]);
         if (!at[k]) status |= kStatusNoPage;
       }
@@ -268,7 +270,7 @@ __global__ void __launch_bounds__(kThreads) slots_kernel(SlotsArgs args) {
   for (int64_t f = (int64_t)(kThreads - 1 - threadIdx.x) * gridDim.x + blockIdx.x; f < F;
        f += (int64_t)gridDim.x * kThreads) {
     const int b = d.owner(d.fresh, f, 0, a.batch - 1);
-    const int64_t c = d.pages(d.kv[b + 1] - d.kv[b]) + (f - d.fresh[b]);
+    const int64_t c = d.pages(d.cached[b]) + (f - d.fresh[b]);
     if (c < a.max_pages) a.block_table[(int64_t)b * a.max_pages + c] = f < a.num_free ? a.free_pages[f] : -1;
   }
   if (status) atomicOr(a.status, status);
@@ -282,7 +284,7 @@ cudaError_t launch_slots(const SlotsArgs& a, cudaStream_t stream) {
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   auto kernel = a.page_shift >= 0 ? slots_kernel<true> : slots_kernel<false>;
-  const int smem = 3 * (a.batch + 1) * (int)sizeof(int32_t);
+  const int smem = (4 * a.batch + 3) * (int)sizeof(int32_t);
   if (smem > 47 * 1024) {
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
