@@ -185,13 +185,14 @@ cudaError_t kv4_launch(int nq, const SplitArgs& a, dim3 grid, cudaStream_t st) {
 // row group's start and end (queries in, outputs out) add, in tiles.  Larger
 // groups expand a tile's keys for more rows, smaller ones waste fewer columns
 // and spread finer.  Whole calls by group size 16 / 32 / 48 / 64: 576 rows over
-// 4k keys 32.1 / 26.0 / 24.1 / 26.7 us, over 64k 255 / 154 / 117 / 110 us; 72
-// rows over 185k 113 / 90 / 75 / 84 us; 16 ragged requests 720 / 430 / 330 /
-// 289 us.  The model takes the least of each.
+// 4k keys 33.2 / 26.8 / 24.2 / 26.9 us, over 64k 263 / 160 / 124 / 115 us; 72
+// rows over 185k 116 / 93 / 77 / 88 us; 16 ragged requests 738 / 439 / 343 /
+// 297 us; 16 decode requests 44.0 / 51.9 / 55.3 / 60.8 us.  The model takes the
+// least of each.
 double kv4_tile_us(int nq) { return nq >= 64 ? 3.05 : nq >= 48 ? 2.6 : nq >= 32 ? 2.3 : 1.95; }
-// With 1 / 2 / 3 tiles: 576 rows over 4k keys 29.2 / 24.2 / 24.1 us, over 64k
-// 112.9 / 110.4 / 108.6; 16 ragged requests 294.7 / 288.8 / 292.0; 16 decode
-// requests 43.2 / 42.9 / 43.5.
+// With 1 / 2 / 3 tiles: 576 rows over 4k keys 29.6 / 24.2 / 24.2 us, over 64k
+// 117.9 / 115.1 / 113.5; 16 ragged requests 305.8 / 297.1 / 297.6; 16 decode
+// requests 44.3 / 44.0 / 45.4.
 constexpr int kKv4SegCost = 2;
 
 // Row-group size: the least modelled time of a CTA's equal piece of the work

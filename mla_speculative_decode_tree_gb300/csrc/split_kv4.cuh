@@ -14,9 +14,8 @@
 //   p       = p_hi + p_lo          O^T += V^T . p_hi, V^T . p_lo
 //
 // e4m3 carries 4 significant bits, so q_hi takes a bf16 value's upper four and
-// q_lo the other four exactly (down to 2^-15 of the row's largest value, below
-// which the error is under 2^-23 of it): scores are as exact as with bf16
-// operands.  The products and sums are fp32.  A single e4m3 P instead of the
+// q_lo the other four exactly, down to 2^-14 of the row's largest value; smaller
+// ones are off by at most 2^-22 of it.  The products and sums are fp32.  A single e4m3 P instead of the
 // pair would take a quarter off the MMAs and 3 % off the call (64k keys, NQ = 64),
 // for four significant bits in place of seven or eight.
 //
@@ -80,18 +79,19 @@
 // P^T is written MN-major (a thread owns one key, its columns are contiguous:
 // 16-byte stores), in the unswizzled layout of 16 columns x 8 keys cores.
 //
-// What bounds it (GB300).  576 rows over 64k keys, NQ = 64: 110 us per call, 0.74
-// PFLOP/s of the bf16-equivalent work; the tensor pipe is 49 % busy, the ALUs 51 %,
-// shared memory 85 % (45 % loads and stores, 40 % MMA operands).  No unit is
-// the limit alone: a tile takes ~5500 cycles, its expansion ~4700 of them, and
-// a slot set's round -- expand, S^T, softmax, O^T -- twice that.  Timed without
-// the exponentials and conversions it takes 107 us, without the softmax's
-// meeting 104, with half the expansion 109.7, with all of these cut 100.
-// Decode (16 requests, NQ = 16): 43 us, 2.1 TB/s; ~8 us are start-up (three
-// dependent reads: lengths, row ids, rows) and 4 the merge.  Neither polling in
-// place of suspended waits, nor a first pass over the expansion's code while it
-// waits for row ids, nor asking for the next slot a block ahead gained
-// anything (64k keys: 113, 115 and 118 us against 111).
+// What bounds it (GB300).  576 rows over 64k keys, NQ = 64: 115 us per call, 0.72
+// PFLOP/s of the bf16-equivalent work; the tensor pipe is 47 % busy, the ALUs 54 %,
+// shared memory 84 % (46 % loads and stores, 38 % MMA operands).  No unit is
+// the limit alone.  Measured when the scale of P came from the maximum alone (110
+// us): a tile takes ~5500 cycles, its expansion ~4700 of them, and a slot set's
+// round -- expand, S^T, softmax, O^T -- twice that.  Timed without the
+// exponentials and conversions it took 107 us, without the softmax's meeting
+// 104, with half the expansion 109.7, with all of these cut 100.  Neither polling
+// in place of suspended waits, nor a first pass over the expansion's code while it
+// waits for row ids, nor asking for the next slot a block ahead gained anything
+// (113, 115 and 118 us against 111).
+// Decode (16 requests, NQ = 16): 44 us, 2.0 TB/s; ~8 us are start-up (three
+// dependent reads: lengths, row ids, rows) and 4 the merge.
 //
 // Waits are bounded as in split_tc.cuh.
 #pragma once
