@@ -16,7 +16,7 @@ Verification is defined in whole numbers, so that no order of summation changes 
 round(p * 2^38), random numbers as k = floor(u * 2^24).  The walk starts at node 0 of a request's tree with r = p(node)
 and Z = 2^38.  The children of the node that the walk is at are tried in ascending order: with s = q(node) * Z >> 38
 (without draft probabilities: Z at the child's token, else 0) child c with token x is accepted when k[c] * s(x) <
-r(x) * 2^24.  Then the walk goes on from c, else Z -= sum(min(r, s)) and r = max(r - s, 0).  The next token is the first
+r(x) * 2^24.  Then the walk goes on from c, else Z = max(Z - sum(min(r, s)), 0) and r = max(r - s, 0).  The next token is the first
 one at which the running sum of r exceeds floor(k * sum(r) / 2^24).
 """
 
@@ -393,7 +393,7 @@ def _plain_accept(s):
             sc = torch.zeros((B, V), dtype=torch.long, device=dev).scatter_(1, x, Z)
         takes = tries & (k[at] * sc.gather(1, x)[:, 0] < r.gather(1, x)[:, 0] << 24)
         fails = (tries & ~takes)[:, None]
-        Z = torch.where(fails, Z - torch.minimum(r, sc).sum(1, keepdim=True), Z)
+        Z = torch.where(fails, (Z - torch.minimum(r, sc).sum(1, keepdim=True)).clamp(min=0), Z)
         r = torch.where(fails, (r - sc).clamp(min=0), r)
         cur = torch.where(takes, torch.full_like(cur, c), cur)
         Z = torch.where(takes[:, None], torch.full_like(Z, 1 << ONE), Z)
