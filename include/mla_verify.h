@@ -120,6 +120,11 @@ extern "C" {
  * With MLA_VERIFY_FUSED_MERGE or MLA_VERIFY_REFETCH_VALUES: EINVAL. */
 #define MLA_VERIFY_KV4 0x10
 #define MLA_VERIFY_KV4_ROW_BYTES 384
+/* Requests in groups, each group with one prefix that all its requests see:
+ * the plan of mla_verify_run_shared (and of no other run).  nsplit must be 0,
+ * max_batch at most 1024; max_kv_len bounds a request's own keys.  Only
+ * MLA_VERIFY_FORCE_SIMT and MLA_VERIFY_TEST_STALL_GATHER may be given with it. */
+#define MLA_VERIFY_SHARED 0x20
 /* Test only: the tensor-core split kernel's gather never signals its first
  * block, so every CTA's bounded pipeline waits run out (about 2 s), the CTAs
  * drain and return, and the call reports MLA_VERIFY_DEV_TIMEOUT; its outputs
@@ -463,6 +468,184 @@ int mla_verify_build_slots(mla_verify_plan_t plan, const int32_t* seq_lens, cons
                            int32_t num_free, int32_t* pages_used, int32_t* kv_indptr, int32_t* kv_indices,
                            int64_t kv_capacity, int32_t* qo_indptr, int32_t* out_cache_loc, int64_t loc_capacity,
                            void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * One verify call for requests that share prefixes: system prompts, documents,
+ * samples of one prompt.  Requests group_indptr[g] .. group_indptr[g+1]-1 all see
+ * the shared_indptr[g+1] - shared_indptr[g] keys of group g's prefix, each before
+ * keys of its own:
+ *
+ *   row(j)   = shared_indices[shared_indptr[g] + j]      for j <  S_g
+ *            = kv_indices[kv_indptr[b] + j - S_g]        for j <  S_g + P_b
+ *            = out_cache_loc[qo_indptr[b] + j - S_g - P_b]   behind them
+ *   vis(i,j) = true                                      for j <  S_g
+ *            = bit (mask_indptr[b] + i*(P_b + T_b) + j - S_g) of custom_mask
+ *
+ * O and LSE are those of mla_verify_run_varlen with these rows and visibilities
+ * (up to rounding), but a prefix is read once for 128 query rows of its group
+ * -- token, head pairs of all its requests -- in place of once per request.
+ * The mask holds the own keys only; its blocks and mask_indptr are what
+ * mla_verify_build_tree_mask_varlen writes from kv_indptr and qo_indptr.
+ *
+ *  plan             with MLA_VERIFY_SHARED
+ *  group_indptr     int32 [num_groups+1], group_indptr[0] = 0, non-decreasing,
+ *                   group_indptr[num_groups] = batch: every request is in a group
+ *                   (of one request, or with an empty prefix, where it shares none)
+ *  shared_indptr    int32 [num_groups+1], non-decreasing
+ *  shared_indices   int32 pool rows of the prefixes (NULL when all are empty)
+ *  kv_indptr, kv_indices   the requests' own prefixes behind the shared ones
+ *  qo_indptr        int32 [batch+1], or NULL: q_len tokens each
+ *  num_groups       1 .. max_batch
+ *  everything else as mla_verify_run_varlen
+ *
+ * Two launches.  The work of all groups and requests is cut into equal pieces,
+ * one per pair of SMs, from the lengths on the device, so a captured call follows
+ * new lengths.  A key whose row is outside the pool is left out for every token
+ * and raises MLA_VERIFY_DEV_BAD_ROW.  Errors: EINVAL (also a plan without
+ * MLA_VERIFY_SHARED), EWORKSPACE, EUNSUPPORTED, ECUDA.
+ */
+int mla_verify_run_shared(mla_verify_plan_t plan, const void* q_nope_absorbed, const void* q_rope, const void* kv_pool,
+                          const int32_t* group_indptr, const int32_t* shared_indptr, const int32_t* shared_indices,
+                          const int32_t* kv_indptr, const int32_t* kv_indices, const int32_t* qo_indptr,
+                          const int32_t* out_cache_loc, const uint8_t* custom_mask, const int32_t* mask_indptr,
+                          int32_t batch, int32_t num_groups, float sm_scale, void* workspace, size_t workspace_bytes,
+                          void* o, float* lse, void* stream);
+
+/*
+ * Verify each request's draft tree against the target's probabilities and draw
+ * the token behind the accepted path, from given random numbers: the tokens are
+ * then distributed as if drawn from the target one by one.  One kernel on
+ * `stream`, no allocation, no host synchronisation.
+ *
+ *  target_probs   fp32 rows of `vocab` probabilities, target_stride elements apart:
+ *                 row qo_indptr[b] + i is the target's distribution of the token
+ *                 after node i of request b's tree (softmax of the model's logits,
+ *                 with whatever temperature and cut-offs)
+ *  draft_probs    the same rows of the draft model: the distribution that the
+ *                 children of node i were drawn from, independently of each other;
+ *                 or NULL: the children were not drawn but proposed (a greedy or
+ *                 top-k draft, an n-gram), in the order of their numbers
+ *  vocab          1 .. 2^30; strides at least vocab
+ *  draft_tokens   int32 [tokens]: the token of each node
+ *  parents        int32 [tokens], as mla_verify_build_tree_mask_varlen; node 0 is the
+ *                 token that the last step left, which is accepted as it is (its
+ *                 entry is not read), and a node that no path joins to it is never
+ *                 reached
+ *  qo_indptr      int32 [batch+1], or NULL: the plan's q_len nodes each
+ *  uniform        fp32 [tokens] in [0, 1): the test of each node
+ *  uniform_next   fp32 [batch] in [0, 1): the draw of the next token
+ *  accepted       int32 [batch, q_len] output: node numbers of the accepted path, 0
+ *                 first, ascending; -1 behind them
+ *  num_accepted   int32 [batch] output: how many (0 for a request without nodes)
+ *  next_tokens    int32 [batch] output: the token drawn behind the path; -1 for a
+ *                 request without nodes or with a target row of zeros
+ *  workspace      the plan's workspace
+ *
+ * The arithmetic is in whole numbers, so the tokens do not depend on the order of
+ * any sum: a probability is w(p) = round(p * 2^38), ties to even (outside [0, 1]
+ * clamped, NaN 0), a random number k(u) = floor(u * 2^24).  At a node r = w(target
+ * row) and Z = 2^38.  For each child c with token x, in ascending order: s =
+ * floor(w(draft row) * Z / 2^38) -- without draft_probs Z at x and 0 elsewhere --
+ * and the walk goes on from c if k(uniform of c) * s(x) < r(x) * 2^24; otherwise
+ * Z = max(Z - sum(min(r, s)), 0) and r = max(r - s, 0).  Where no child is left the
+ * next token is the least t with sum_{i<=t} r(i) > floor(k(uniform_next) * sum(r) /
+ * 2^24); where nothing is left of r (only roundings do that), with r = w(target
+ * row).  A child whose token is outside [0, vocab) is passed over.  Errors:
+ * EINVAL, EWORKSPACE, EUNSUPPORTED, ECUDA.
+ */
+int mla_verify_accept_drafts(mla_verify_plan_t plan, const float* target_probs, int64_t target_stride,
+                             const float* draft_probs, int64_t draft_stride, int32_t vocab, const int32_t* draft_tokens,
+                             const int32_t* parents, const int32_t* qo_indptr, const float* uniform,
+                             const float* uniform_next, int32_t batch, int32_t* accepted, int32_t* num_accepted,
+                             int32_t* next_tokens, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Keep a step's accepted tokens: the cache rows of the accepted path move to the
+ * front of the request's new rows, in every layer's pool, the request grows by
+ * their number, and the pages that they fill are counted.  One kernel on `stream`,
+ * no allocation, no host synchronisation.
+ *
+ *  kv_pool        num_layers pools of the plan's row format and pool_rows rows,
+ *                 layer_stride bytes apart (a multiple of 16); 16-byte aligned
+ *  qo_indptr      int32 [batch+1], or NULL: the plan's q_len tokens each
+ *  out_cache_loc  int32 [tokens]: pool row of each new token (mla_verify_build_slots)
+ *  accepted       int32 [batch, q_len], num_accepted int32 [batch]: the path, as
+ *                 mla_verify_accept_drafts writes it: node numbers, ascending
+ *  seq_lens       int32 [batch]: cached tokens before the step
+ *  new_seq_lens   int32 [batch] output: seq_lens + the path's length (may be seq_lens)
+ *  page_size, block_table, max_pages   as mla_verify_build_slots
+ *  page_refs      int32 [num_pages]: requests that hold each page.  The pages of
+ *                 block_table that the step took and the path reaches get 1; those
+ *                 that only rejected drafts used keep 0 and are free again.
+ *                 block_table and page_refs are both NULL where pages are not counted
+ *  workspace      the plan's workspace (only its status word is used)
+ *
+ * For each j below the path's length, row out_cache_loc[first + path[j]] is copied
+ * whole to row out_cache_loc[first + j].  The rows of a call must be distinct.  A
+ * path ends before an entry that is not above the one before it or outside the
+ * tree, and a copy from or to a row outside the pool is left out; each raises
+ * MLA_VERIFY_DEV_BAD_ROW.  batch at most 65535.  Errors: EINVAL, EWORKSPACE,
+ * EUNSUPPORTED, ECUDA.
+ */
+int mla_verify_commit_drafts(mla_verify_plan_t plan, void* kv_pool, int32_t num_layers, int64_t layer_stride,
+                             const int32_t* qo_indptr, const int32_t* out_cache_loc, const int32_t* accepted,
+                             const int32_t* num_accepted, int32_t batch, const int32_t* seq_lens,
+                             int32_t* new_seq_lens, int32_t page_size, const int32_t* block_table, int32_t max_pages,
+                             int32_t* page_refs, int32_t num_pages, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+/*
+ * The free pages, from the reference counts: free_pages (int32 [num_pages]) gets
+ * the numbers of the pages with page_refs = 0 in ascending order and -1 behind
+ * them, num_free (int32 [1]) how many they are.  One kernel on `stream`.  The list
+ * is what mla_verify_build_slots and mla_verify_fork take pages from (their
+ * num_free may be num_pages: an entry of -1 is no page).  Errors: EINVAL,
+ * EUNSUPPORTED, ECUDA.
+ */
+int mla_verify_list_free_pages(mla_verify_plan_t plan, const int32_t* page_refs, int32_t num_pages, int32_t* free_pages,
+                               int32_t* num_free, void* stream);
+
+/*
+ * Fork requests: dst[i] becomes a copy of src[i] that shares its full pages; a
+ * last page that is not full is copied to a fresh one, in every layer's pool.  One
+ * kernel on `stream`, no allocation, no host synchronisation.
+ *
+ *  kv_pool, num_layers, layer_stride   as mla_verify_commit_drafts
+ *  src, dst       int32 [n]: requests.  dst[i] must hold nothing; a request may be
+ *                 forked any number of times
+ *  n              0 .. 4096 (0 enqueues nothing)
+ *  block_table    int32 [num_requests, max_pages]; dst's entries are written
+ *  seq_lens       int32 [num_requests]; dst's are written
+ *  page_refs      int32 [num_pages]: one more for a shared page, 1 for a fresh one
+ *  free_pages     int32 [num_free]: fresh pages, taken from the front in the
+ *                 forks' order
+ *  pages_used     int32 [1] output: how many were taken
+ *  workspace      the plan's workspace (only its status word is used)
+ *
+ * A fork from or to a request outside [0, num_requests), or into a request that
+ * is a source of the call or the destination of an earlier fork, is left out and
+ * raises MLA_VERIFY_DEV_BAD_ROW (as do table entries outside [0, num_pages)).
+ * Without a free page for its last one a fork holds the full pages only and the
+ * call raises MLA_VERIFY_DEV_NO_PAGE.  Errors: EINVAL, EWORKSPACE, EUNSUPPORTED,
+ * ECUDA.
+ */
+int mla_verify_fork(mla_verify_plan_t plan, void* kv_pool, int32_t num_layers, int64_t layer_stride, const int32_t* src,
+                    const int32_t* dst, int32_t n, int32_t page_size, int32_t* block_table, int32_t num_requests,
+                    int32_t max_pages, int32_t* seq_lens, int32_t* page_refs, int32_t num_pages,
+                    const int32_t* free_pages, int32_t num_free, int32_t* pages_used, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
+/*
+ * Release requests: each page of requests[i] (int32 [n], n at most 4096) is held
+ * by one less, and its length becomes 0.  Table entries stay as they are.  An entry
+ * outside [0, num_requests) is passed over and raises MLA_VERIFY_DEV_BAD_ROW, as
+ * does a page without a reference or outside [0, num_pages); one that repeats an
+ * earlier entry has no effect.  One kernel on `stream`.  Other arguments and
+ * errors as mla_verify_fork.
+ */
+int mla_verify_release(mla_verify_plan_t plan, const int32_t* requests, int32_t n, int32_t page_size,
+                       const int32_t* block_table, int32_t num_requests, int32_t max_pages, int32_t* seq_lens,
+                       int32_t* page_refs, int32_t num_pages, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Free the plan (NULL is accepted).  Returns MLA_VERIFY_OK. */
 int mla_verify_destroy(mla_verify_plan_t plan);

@@ -29,13 +29,16 @@ MLA_VERIFY_FUSED_MERGE = 0x2
 MLA_VERIFY_REFETCH_VALUES = 0x4
 MLA_VERIFY_KV4 = 0x10
 MLA_VERIFY_KV4_ROW_BYTES = 384
+MLA_VERIFY_SHARED = 0x20
 MLA_VERIFY_TEST_STALL_GATHER = 0x100
 
 EXPORTED = ("mla_verify_plan", "mla_verify_plan_describe", "mla_verify_run", "mla_verify_split",
             "mla_verify_merge", "mla_verify_workspace_init", "mla_verify_read_status", "mla_verify_destroy",
             "mla_verify_strerror", "mla_verify_run_noalloc", "mla_verify_build_tree_mask",
             "mla_verify_run_varlen", "mla_verify_relocate_kv", "mla_verify_build_tree_mask_varlen",
-            "mla_verify_store_kv4", "mla_verify_load_kv4", "mla_verify_build_slots")
+            "mla_verify_store_kv4", "mla_verify_load_kv4", "mla_verify_build_slots", "mla_verify_run_shared",
+            "mla_verify_accept_drafts", "mla_verify_commit_drafts", "mla_verify_list_free_pages", "mla_verify_fork",
+            "mla_verify_release")
 
 
 class MlaVerifyParams(ctypes.Structure):
@@ -86,6 +89,12 @@ def load(path: str = LIB_PATH):
     lib.mla_verify_store_kv4.argtypes = [P, P, i64, P, i64, P, i64, P, P, sz, P]
     lib.mla_verify_load_kv4.argtypes = [P, P, P, i64, P, i64, P, i64, P, sz, P]
     lib.mla_verify_build_slots.argtypes = [P, P, P, i32, i32, P, i32, P, i32, P, P, P, i64, P, P, i64, P, sz, P]
+    lib.mla_verify_run_shared.argtypes = [P] * 13 + [i32, i32, f32, P, sz, P, P, P]
+    lib.mla_verify_accept_drafts.argtypes = [P, P, i64, P, i64, i32, P, P, P, P, P, i32, P, P, P, P, sz, P]
+    lib.mla_verify_commit_drafts.argtypes = [P, P, i32, i64, P, P, P, P, i32, P, P, i32, P, i32, P, i32, P, sz, P]
+    lib.mla_verify_list_free_pages.argtypes = [P, P, i32, P, P, P]
+    lib.mla_verify_fork.argtypes = [P, P, i32, i64, P, P, i32, i32, P, i32, i32, P, P, i32, P, i32, P, P, sz, P]
+    lib.mla_verify_release.argtypes = [P, P, i32, i32, P, i32, i32, P, P, i32, P, sz, P]
     lib.mla_verify_read_status.argtypes = [P, P, P, ctypes.POINTER(ctypes.c_uint32)]
     lib.mla_verify_destroy.argtypes = [P]
     lib.mla_verify_strerror.argtypes = [ctypes.c_int]
@@ -328,6 +337,166 @@ def mla_verify_build_slots(plan: Plan, seq_lens, new_lens, batch: int, page_size
         out_cache_loc.numel(), workspace.data_ptr(), workspace.nbytes, _stream(stream))
     if rc:
         _check(rc, "mla_verify_build_slots")
+
+
+def mla_verify_run_shared(plan: Plan, q_nope_absorbed, q_rope, kv_pool, group_indptr, shared_indptr, shared_indices,
+                          kv_indptr, kv_indices, qo_indptr, out_cache_loc, custom_mask, mask_indptr, batch: int,
+                          num_groups: int, sm_scale: float, workspace, o, lse, stream=None,
+                          workspace_bytes: Optional[int] = None):
+    """Verify attention for requests in groups with shared prefixes (qo_indptr None: the plan's q_len tokens each)."""
+    args = (q_nope_absorbed, q_rope, kv_pool, group_indptr, shared_indptr, shared_indices, kv_indptr, kv_indices,
+            qo_indptr, out_cache_loc, custom_mask, mask_indptr, workspace, o, lse)
+    qn, qr, kv, gp, sp, si, kp, ki, qo, loc, cm, mp, ws, po, pl = map(_ptr, args)
+    rc = (_lib or load()).mla_verify_run_shared(
+        plan.handle, qn, qr, kv, gp, sp, si, kp, ki, qo, loc, cm, mp, int(batch), int(num_groups), float(sm_scale), ws,
+        plan.workspace_bytes if workspace_bytes is None else int(workspace_bytes), po, pl, _stream(stream))
+    if rc:
+        _check(rc, "mla_verify_run_shared")
+
+
+def _int32s(**tensors):
+    for what, x in tensors.items():
+        _int32(x, what)
+
+
+def _at_least(n: int, **tensors):
+    for what, x in tensors.items():
+        if x.numel() < n:
+            raise ValueError("%s is too short: %d entries, %d needed" % (what, x.numel(), n))
+
+
+def _prob_rows(x, vocab: int, what: str) -> int:
+    """Row stride of fp32 [rows, vocab] probabilities with contiguous rows."""
+    if x.dtype is not (_torch or _load_torch()).float32 or x.dim() != 2 or x.shape[1] != vocab or (
+            vocab > 1 and x.stride(1) != 1):
+        raise ValueError("%s: fp32 [rows, %d] with contiguous rows expected, got %s %s strides %s"
+                         % (what, vocab, x.dtype, tuple(x.shape), x.stride()))
+    return x.stride(0) if x.shape[0] > 1 else max(vocab, x.stride(0))
+
+
+def mla_verify_accept_drafts(plan: Plan, target_probs, draft_probs, draft_tokens, parents, qo_indptr, uniform,
+                             uniform_next, batch: int, accepted, num_accepted, next_tokens, workspace, stream=None):
+    """Draft trees against the target's probabilities (draft_probs None: proposed, not drawn; qo_indptr None: q_len nodes
+    each): accepted int32 [batch, q_len], num_accepted and next_tokens int32 [batch] are written."""
+    torch = _torch or _load_torch()
+    vocab = target_probs.shape[-1]
+    _int32s(draft_tokens=draft_tokens, parents=parents, accepted=accepted, num_accepted=num_accepted,
+            next_tokens=next_tokens)
+    for what, x in (("uniform", uniform), ("uniform_next", uniform_next)):
+        if x.dtype is not torch.float32 or not x.is_contiguous():
+            raise ValueError("%s: a contiguous fp32 tensor expected" % what)
+    _at_least(batch, num_accepted=num_accepted, next_tokens=next_tokens, uniform_next=uniform_next)
+    _at_least(batch * plan.params.q_len, accepted=accepted)
+    if qo_indptr is not None:
+        _int32(qo_indptr, "qo_indptr")
+        _at_least(batch + 1, qo_indptr=qo_indptr)
+    else:
+        _at_least(batch * plan.params.q_len, draft_tokens=draft_tokens, parents=parents, uniform=uniform)
+        if target_probs.shape[0] < batch * plan.params.q_len:
+            raise ValueError("target_probs has too few rows")
+    if draft_probs is not None and draft_probs.shape[0] < target_probs.shape[0]:
+        raise ValueError("draft_probs has fewer rows than target_probs")
+    rc = (_lib or load()).mla_verify_accept_drafts(
+        plan.handle, target_probs.data_ptr(), _prob_rows(target_probs, vocab, "target_probs"), _ptr(draft_probs),
+        0 if draft_probs is None else _prob_rows(draft_probs, vocab, "draft_probs"), vocab, draft_tokens.data_ptr(),
+        parents.data_ptr(), _ptr(qo_indptr), uniform.data_ptr(), uniform_next.data_ptr(), int(batch),
+        accepted.data_ptr(), num_accepted.data_ptr(), next_tokens.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+        _stream(stream))
+    if rc:
+        _check(rc, "mla_verify_accept_drafts")
+
+
+def _layers_of(plan: Plan, kv_pool):
+    """(layers, bytes from one to the next) of a pool [rows, row] or [layers, rows, row] of whole rows."""
+    kv4 = plan.params.flags & MLA_VERIFY_KV4
+    torch = _torch or _load_torch()
+    row, dtype = (MLA_VERIFY_KV4_ROW_BYTES, torch.uint8) if kv4 else (576, torch.bfloat16)
+    if kv_pool.dtype is not dtype or kv_pool.dim() not in (2, 3) or kv_pool.shape[-2:] != (plan.params.pool_rows, row) or (
+            kv_pool.stride(-1) != 1 or (kv_pool.stride(-2) != row and kv_pool.shape[-2] > 1)):
+        raise ValueError("kv_pool: %s [layers, %d, %d] expected, got %s %s strides %s"
+                         % (dtype, plan.params.pool_rows, row, kv_pool.dtype, tuple(kv_pool.shape), kv_pool.stride()))
+    if kv_pool.dim() == 2 or kv_pool.shape[0] == 1:
+        return 1, 0
+    return kv_pool.shape[0], kv_pool.stride(0) * kv_pool.element_size()
+
+
+def mla_verify_commit_drafts(plan: Plan, kv_pool, qo_indptr, out_cache_loc, accepted, num_accepted, batch: int, seq_lens,
+                             new_seq_lens, page_size: int, block_table, page_refs, workspace, stream=None):
+    """The accepted paths' rows to the front of the new rows of kv_pool ([rows, row] or [layers, rows, row]), lengths and
+    page counts (block_table int32 [>= batch, max_pages] and page_refs None: no pages)."""
+    _int32s(out_cache_loc=out_cache_loc, accepted=accepted, num_accepted=num_accepted, seq_lens=seq_lens,
+            new_seq_lens=new_seq_lens)
+    _at_least(batch, num_accepted=num_accepted, seq_lens=seq_lens, new_seq_lens=new_seq_lens)
+    _at_least(batch * plan.params.q_len, accepted=accepted)
+    if qo_indptr is not None:
+        _int32(qo_indptr, "qo_indptr")
+        _at_least(batch + 1, qo_indptr=qo_indptr)
+    else:
+        _at_least(batch * plan.params.q_len, out_cache_loc=out_cache_loc)
+    max_pages = num_pages = 0
+    if (block_table is None) != (page_refs is None):
+        raise ValueError("block_table and page_refs go together")
+    if block_table is not None:
+        _int32s(block_table=block_table, page_refs=page_refs)
+        if block_table.shape[0] < batch:
+            raise ValueError("block_table has too few rows")
+        max_pages, num_pages = block_table.shape[1], page_refs.numel()
+    layers, stride = _layers_of(plan, kv_pool)
+    rc = (_lib or load()).mla_verify_commit_drafts(
+        plan.handle, kv_pool.data_ptr(), layers, stride, _ptr(qo_indptr), out_cache_loc.data_ptr(), accepted.data_ptr(),
+        num_accepted.data_ptr(), int(batch), seq_lens.data_ptr(), new_seq_lens.data_ptr(), int(page_size),
+        _ptr(block_table), max_pages, _ptr(page_refs), num_pages, workspace.data_ptr(), workspace.nbytes,
+        _stream(stream))
+    if rc:
+        _check(rc, "mla_verify_commit_drafts")
+
+
+def mla_verify_list_free_pages(plan: Plan, page_refs, free_pages, num_free, stream=None):
+    """Pages without a reference, ascending, into free_pages (-1 behind them), and their number."""
+    _int32s(page_refs=page_refs, free_pages=free_pages, num_free=num_free)
+    _at_least(page_refs.numel(), free_pages=free_pages)
+    _at_least(1, num_free=num_free)
+    rc = (_lib or load()).mla_verify_list_free_pages(plan.handle, page_refs.data_ptr(), page_refs.numel(),
+                                                     free_pages.data_ptr(), num_free.data_ptr(), _stream(stream))
+    if rc:
+        _check(rc, "mla_verify_list_free_pages")
+
+
+def _page_arrays(block_table, seq_lens, page_refs):
+    _int32s(block_table=block_table, seq_lens=seq_lens, page_refs=page_refs)
+    requests, max_pages = block_table.shape
+    _at_least(requests, seq_lens=seq_lens)
+    return requests, max_pages
+
+
+def mla_verify_fork(plan: Plan, kv_pool, src, dst, page_size: int, block_table, seq_lens, page_refs, free_pages,
+                    pages_used, workspace, stream=None):
+    """Requests dst become copies of requests src: full pages shared, the last one copied (all layers of kv_pool)."""
+    requests, max_pages = _page_arrays(block_table, seq_lens, page_refs)
+    _int32s(src=src, dst=dst, free_pages=free_pages, pages_used=pages_used)
+    n = src.numel()
+    _at_least(n, dst=dst)
+    _at_least(1, pages_used=pages_used)
+    layers, stride = _layers_of(plan, kv_pool)
+    rc = (_lib or load()).mla_verify_fork(
+        plan.handle, kv_pool.data_ptr(), layers, stride, src.data_ptr(), dst.data_ptr(), n, int(page_size),
+        block_table.data_ptr(), requests, max_pages, seq_lens.data_ptr(), page_refs.data_ptr(), page_refs.numel(),
+        free_pages.data_ptr(), free_pages.numel(), pages_used.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+        _stream(stream))
+    if rc:
+        _check(rc, "mla_verify_fork")
+
+
+def mla_verify_release(plan: Plan, requests, page_size: int, block_table, seq_lens, page_refs, workspace, stream=None):
+    """Requests let go of their pages; their lengths become 0."""
+    rows, max_pages = _page_arrays(block_table, seq_lens, page_refs)
+    _int32(requests, "requests")
+    rc = (_lib or load()).mla_verify_release(
+        plan.handle, requests.data_ptr(), requests.numel(), int(page_size), block_table.data_ptr(), rows, max_pages,
+        seq_lens.data_ptr(), page_refs.data_ptr(), page_refs.numel(), workspace.data_ptr(), workspace.nbytes,
+        _stream(stream))
+    if rc:
+        _check(rc, "mla_verify_release")
 
 
 def mla_verify_workspace_init(plan: Plan, workspace, stream=None):

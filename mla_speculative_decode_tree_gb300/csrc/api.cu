@@ -11,30 +11,9 @@
 #include <new>
 
 #include "../../include/mla_verify.h"
-#include "kv4.cuh"
+#include "plan.cuh"
 
 using namespace mlav;
-
-struct mla_verify_plan_s {
-  mla_verify_params p;
-  int kernel;  // 1 = tcgen05, 0 = CUDA cores
-  int nq;      // query rows per split CTA
-  bool resident;  // tensor-core kernel in resident-tile mode (each key lands once per CTA)
-  int groups;  // row groups per request
-  int64_t rows_max;
-  bool fused;  // the split kernel merges (MLA_VERIFY_FUSED_MERGE on the tensor-core kernel)
-  int splits;  // KV chunks per request = grid dimension = partials per row (nsplit, or the plan's count)
-  int min_chunk;  // shortest chunk of any request (keys)
-  int chunk_granule;  // chunk lengths are multiples of it (keys)
-  size_t off_cnt, off_lse, off_o, ws_bytes;  // [0, off_lse) must be zero between calls
-  int merge_blocks;
-  bool merge_quarter;  // merge with four warps per row (at most one wave of rows)
-  int smem;
-  bool kv4;  // the pool holds 4-bit rows (MLA_VERIFY_KV4)
-  int pieces;  // > 0: the 4-bit kernel's CTAs, which take the work in equal pieces (nsplit = 0)
-  int seg_cost;  // its start and end of a row group, in tiles
-  int merge_rows;  // rows per merge block then
-};
 
 namespace {
 
@@ -270,6 +249,10 @@ int encode_bf16_2d(EncodeTiledFn enc, CUtensorMap* map, const void* base, uint64
 std::mutex g_dev_mu;
 int g_dev_state[64];  // 0 unknown, 1 ok, 2 unsupported
 
+}  // namespace
+
+namespace mlav {
+
 int check_device() {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -286,8 +269,6 @@ int check_device() {
   return g_dev_state[dev] == 1 ? MLA_VERIFY_OK : MLA_VERIFY_EUNSUPPORTED;
 }
 
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
 // The input arrays of a split launch (everything but the workspace).
 int check_inputs(const void* q_nope_absorbed, const void* q_rope, const void* kv_pool, const int32_t* kv_indptr,
                  const int32_t* kv_indices, const int32_t* out_cache_loc, const uint8_t* custom_mask,
@@ -303,9 +284,17 @@ int check_inputs(const void* q_nope_absorbed, const void* q_rope, const void* kv
   return MLA_VERIFY_OK;
 }
 
+int check_workspace(const mla_verify_plan_s* pl, const void* workspace, size_t workspace_bytes) {
+  if (!workspace || workspace_bytes < pl->ws_bytes) return MLA_VERIFY_EWORKSPACE;
+  return aligned(workspace, 256) ? MLA_VERIFY_OK : MLA_VERIFY_EINVAL;
+}
+
+}  // namespace mlav
+
+namespace {
 
 int check_common(const mla_verify_plan_s* pl, int32_t batch, int32_t nsplit, void* ws, size_t ws_bytes) {
-  if (!pl) return MLA_VERIFY_EINVAL;
+  if (!pl || pl->shared) return MLA_VERIFY_EINVAL;  // (a shared plan has its own run)
   if (batch < 0 || batch > pl->p.max_batch) return MLA_VERIFY_EINVAL;
   if (nsplit != pl->p.nsplit) return MLA_VERIFY_EINVAL;
   if (batch == 0) return MLA_VERIFY_OK;
@@ -331,7 +320,7 @@ int check_run_args(const mla_verify_plan_s* pl, const void* q_nope_absorbed, con
                    const void* kv_pool, const int32_t* kv_indptr, const int32_t* kv_indices,
                    const int32_t* out_cache_loc, const uint8_t* custom_mask, const int32_t* mask_indptr,
                    int32_t batch, float sm_scale, int32_t nsplit, const void* o, const float* lse) {
-  if (!pl) return MLA_VERIFY_EINVAL;
+  if (!pl || pl->shared) return MLA_VERIFY_EINVAL;
   if (batch < 0 || batch > pl->p.max_batch || nsplit != pl->p.nsplit) return MLA_VERIFY_EINVAL;
   if (batch == 0) return MLA_VERIFY_OK;
   if (!o || !lse || !aligned(o, 16) || !aligned(lse, 4)) return MLA_VERIFY_EINVAL;
@@ -352,7 +341,11 @@ int mla_verify_plan(const mla_verify_params* params, size_t* workspace_bytes, ml
     return MLA_VERIFY_EINVAL;
   if (p.d_latent != kDLatent || p.d_rope != kDRope) return MLA_VERIFY_EUNSUPPORTED;
   if ((p.flags & ~(MLA_VERIFY_FORCE_SIMT | MLA_VERIFY_FUSED_MERGE | MLA_VERIFY_REFETCH_VALUES | MLA_VERIFY_KV4 |
-                   MLA_VERIFY_TEST_STALL_GATHER)) != 0)
+                   MLA_VERIFY_SHARED | MLA_VERIFY_TEST_STALL_GATHER)) != 0)
+    return MLA_VERIFY_EINVAL;
+  if ((p.flags & MLA_VERIFY_SHARED) &&
+      (p.nsplit != 0 || p.max_batch > kMaxSharedBatch ||
+       (p.flags & (MLA_VERIFY_FUSED_MERGE | MLA_VERIFY_REFETCH_VALUES | MLA_VERIFY_KV4))))
     return MLA_VERIFY_EINVAL;
   if ((p.flags & MLA_VERIFY_KV4) && (p.flags & (MLA_VERIFY_FUSED_MERGE | MLA_VERIFY_REFETCH_VALUES)))
     return MLA_VERIFY_EINVAL;
@@ -433,6 +426,8 @@ int mla_verify_plan(const mla_verify_params* params, size_t* workspace_bytes, ml
     pl->merge_rows = merge_pieces_rows(rows_max, device_sm_count());
     pl->merge_blocks = (int)((rows_b + pl->merge_rows - 1) / pl->merge_rows) * p.max_batch;
   }
+  pl->shared = (p.flags & MLA_VERIFY_SHARED) != 0;
+  if (pl->shared) plan_shared(pl, device_sm_count());
   *workspace_bytes = pl->ws_bytes;
   *out = pl;
   return MLA_VERIFY_OK;
@@ -443,7 +438,7 @@ int mla_verify_plan_describe(mla_verify_plan_t pl, mla_verify_plan_info* info) {
   info->kernel = pl->kernel;
   info->rows_per_cta = pl->nq;
   info->resident_tile = pl->resident ? 1 : 0;
-  info->keys_per_tile = kKeysPerTile;
+  info->keys_per_tile = pl->shared && pl->kernel ? kSharedKeys : kKeysPerTile;
   info->grid_x = pl->pieces ? pl->pieces : pl->groups;
   info->grid_y = pl->splits;
   info->grid_z = pl->pieces ? 1 : pl->p.max_batch;

@@ -57,7 +57,100 @@ struct SplitArgs {
   int2* seg_table;
   int32_t seg_cost;              // start and end of a row group, in tiles
   int32_t groups_max;            // row groups of a request of T tokens
+  // CUDA-core kernel only: "request" b is requests group_indptr[b] ..
+  // group_indptr[b+1]-1 of `requests` (the last one's end is `requests`) over a
+  // prefix of theirs, which all their tokens see (no mask, no drafts).
+  const int32_t* group_indptr;
+  int32_t requests;
 };
+
+// Requests in groups, each group with a shared prefix (split_shared.cu).
+struct SharedArgs {
+  const __nv_bfloat16* q_nope;    // [B*T, H, 512]
+  const __nv_bfloat16* q_rope;    // [B*T, H, 64]
+  const __nv_bfloat16* kv_pool;   // [pool_rows, 576]
+  const int32_t* group_indptr;    // [groups+1] requests of each group
+  const int32_t* shared_indptr;   // [groups+1]
+  const int32_t* shared_indices;  // rows of the shared prefixes
+  const int32_t* kv_indptr;       // [B+1]
+  const int32_t* kv_indices;      // rows of the requests' own prefixes
+  const int32_t* out_cache_loc;   // [B*T]
+  const uint8_t* mask;            // own keys only, packed bits LSB-first
+  const int32_t* mask_indptr;     // [B] bit offsets
+  const int32_t* qo_indptr;       // [B+1], or null: T tokens each
+  int32_t batch, groups, H, T;
+  int32_t clusters;               // CTA pairs
+  int32_t test_stall;
+  int64_t pool_rows;
+  int64_t rows_max;               // max_batch*T*H
+  float scale_log2;
+  int2* table;                    // [2*rows_max]: a row group's first row -> first pair that has a partial of it, how many
+  float* part_lse;                // [2*rows_max + 128*clusters]
+  float* part_o;                  // the same rows x 512
+  uint32_t* status;
+  __nv_bfloat16* o;               // [B*T*H, 512]
+  float* lse;
+};
+constexpr int kSharedRows = 128;       // query rows per CTA pair
+constexpr int kSharedKeys = 64;        // keys per tile
+constexpr int kMaxSharedBatch = 1024;  // requests of one call
+
+// Pool layers that a cache operator moves rows in.
+struct PoolLayers {
+  uint8_t* base;
+  int64_t layer_stride;  // bytes
+  int32_t layers, row_bytes;
+  int64_t rows;
+};
+struct AcceptArgs {
+  const float* target;  // [*, vocab], row strides in elements
+  const float* draft;   // or null
+  int64_t target_stride, draft_stride;
+  const int32_t* tokens;
+  const int32_t* parents;
+  const int32_t* qo_indptr;  // or null: T each
+  const float* u;
+  const float* u_next;
+  int32_t batch, T, vocab;
+  int32_t* accepted;  // [batch, T]
+  int32_t* num_accepted;
+  int32_t* next_tokens;
+};
+struct CommitArgs {
+  PoolLayers pool;
+  const int32_t* qo_indptr;  // or null: T each
+  const int32_t* out_cache_loc;
+  const int32_t* accepted;  // [batch, T]
+  const int32_t* num_accepted;
+  int32_t batch, T, page_size, max_pages;
+  const int32_t* seq_lens;
+  int32_t* new_seq_lens;
+  const int32_t* block_table;  // [batch, max_pages], or null: no pages
+  int32_t* page_refs;          // [num_pages]
+  int32_t num_pages;
+  uint32_t* status;
+};
+struct ForkArgs {
+  PoolLayers pool;
+  const int32_t* src;
+  const int32_t* dst;
+  int32_t n, page_size, max_pages, requests, num_pages, num_free;
+  int32_t* block_table;
+  int32_t* seq_lens;
+  int32_t* page_refs;
+  const int32_t* free_pages;
+  int32_t* pages_used;
+  uint32_t* status;
+};
+struct ReleaseArgs {
+  const int32_t* which;
+  int32_t n, page_size, max_pages, requests, num_pages;
+  const int32_t* block_table;
+  int32_t* seq_lens;
+  int32_t* page_refs;
+  uint32_t* status;
+};
+constexpr int kMaxForks = 4096;  // entries of one fork or release call
 
 // TMA descriptors of one call: the pool for row gathers (box 64 columns x 1
 // row, 128-byte swizzle) and the two query tensors (box 64 columns x NQ rows).
@@ -288,6 +381,15 @@ struct SlotsArgs {
 };
 constexpr int kMaxSlotsBatch = 4096;  // requests of one slot-map build
 cudaError_t launch_slots(const SlotsArgs& a, cudaStream_t stream);
+cudaError_t launch_split_shared(const SharedArgs& a, cudaStream_t stream);
+cudaError_t launch_merge_shared(const SharedArgs& a, cudaStream_t stream);
+int split_shared_smem();
+cudaError_t launch_accept(const AcceptArgs& a, cudaStream_t stream);
+cudaError_t launch_commit(const CommitArgs& a, cudaStream_t stream);
+cudaError_t launch_list_free(const int32_t* page_refs, int num_pages, int32_t* free_pages, int32_t* num_free,
+                             cudaStream_t stream);
+cudaError_t launch_fork(const ForkArgs& a, cudaStream_t stream);
+cudaError_t launch_release(const ReleaseArgs& a, cudaStream_t stream);
 int merge_blocks(int rows, bool quarter);
 int merge_pieces_rows(int64_t rows, int sms);
 bool merge_quarter_fits(int64_t rows, int sms);

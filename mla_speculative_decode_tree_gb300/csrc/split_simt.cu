@@ -11,6 +11,9 @@
 // §"Vectorized Loads: The Final Push"; Custom sm_120 Verify Kernel, §"The
 // Float4 Vectorization"].
 //
+// kGroups: the shared part of requests in groups (MLA_VERIFY_SHARED): the rows
+// of all tokens of a group against its prefix.
+//
 // kKv4: the rows of a 4-bit pool (kv4.cuh).  The lanes own the same columns:
 // the words of 8 codes l and l+32 of the latent, and, lanes 0-7, word l of the
 // RoPE codes and of their residuals.
@@ -82,7 +85,19 @@ struct LaneRow<true> {
   }
 };
 
-template <bool kKv4>
+// Tokens of request b, or of the requests of group b.
+template <bool kGroups>
+__device__ __forceinline__ RequestTokens tokens_of(const SplitArgs& a, int b) {
+  if (!kGroups) return request_tokens(a, b);
+  auto clip = [&](int r) { return r < 0 ? 0 : r > a.requests ? a.requests : r; };
+  const int r0 = b == 0 ? 0 : clip(a.group_indptr[b]);
+  const int r1 = b == a.batch - 1 ? a.requests : clip(a.group_indptr[b + 1]);
+  if (!a.qo_indptr) return {(int64_t)r0 * a.T, r1 > r0 ? (r1 - r0) * a.T : 0};
+  const int64_t q0 = a.qo_indptr[r0], n = a.qo_indptr[r1 > r0 ? r1 : r0] - q0, most = (int64_t)(r1 - r0) * a.T;
+  return {q0, (int)(n < most ? n : most)};
+}
+
+template <bool kKv4, bool kGroups>
 __global__ void __launch_bounds__(32 * kSimtRowsPerCta) split_simt_kernel(SplitArgs a) {
   const int b = blockIdx.z;
   if (b >= a.batch) return;
@@ -91,8 +106,8 @@ __global__ void __launch_bounds__(32 * kSimtRowsPerCta) split_simt_kernel(SplitA
   const int s = blockIdx.y;
   const int64_t kv_base = a.kv_indptr[b];
   const int64_t P = (int64_t)a.kv_indptr[b + 1] - kv_base;
-  const RequestTokens rq = request_tokens(a, b);
-  const int64_t L = P + rq.n;
+  const RequestTokens rq = tokens_of<kGroups>(a, b);
+  const int64_t L = kGroups ? P : P + rq.n;
   const int64_t chunk = chunk_len(L, a.nsplit, a.min_chunk, a.chunk_granule);
   const int64_t j0 = (int64_t)s * chunk;
   const int64_t j1 = (j0 + chunk < L) ? j0 + chunk : L;
@@ -118,7 +133,7 @@ __global__ void __launch_bounds__(32 * kSimtRowsPerCta) split_simt_kernel(SplitA
     bf16x8_to_f32(lane < 8 ? __ldg(qp + lane) : z, qr);
   }
 
-  const int64_t mask_row = (int64_t)a.mask_indptr[b] + (int64_t)i * L;
+  const int64_t mask_row = kGroups ? 0 : (int64_t)a.mask_indptr[b] + (int64_t)i * L;
   float m = -INFINITY, lsum = 0.f;
   float acc_a[8], acc_b[8];
 #pragma unroll
@@ -130,7 +145,7 @@ __global__ void __launch_bounds__(32 * kSimtRowsPerCta) split_simt_kernel(SplitA
 #pragma unroll
     for (int u = 0; u < kKeysPerStep; ++u) {
       const int64_t j = jb + u;
-      vis[u] = (j < j1) && mask_bit(a.mask, mask_row + j);
+      vis[u] = (j < j1) && (kGroups || mask_bit(a.mask, mask_row + j));
       key[u].clear();
       if (vis[u]) {
         const int64_t row = resolve_row(a, rq.q0, P, kv_base, j);
@@ -199,10 +214,12 @@ __global__ void __launch_bounds__(32 * kSimtRowsPerCta) split_simt_kernel(SplitA
 }  // namespace
 
 cudaError_t launch_split_simt(const SplitArgs& a, dim3 grid, cudaStream_t stream) {
-  if (a.kv4_pool)
-    split_simt_kernel<true><<<grid, 32 * kSimtRowsPerCta, 0, stream>>>(a);
+  if (a.group_indptr)
+    split_simt_kernel<false, true><<<grid, 32 * kSimtRowsPerCta, 0, stream>>>(a);
+  else if (a.kv4_pool)
+    split_simt_kernel<true, false><<<grid, 32 * kSimtRowsPerCta, 0, stream>>>(a);
   else
-    split_simt_kernel<false><<<grid, 32 * kSimtRowsPerCta, 0, stream>>>(a);
+    split_simt_kernel<false, false><<<grid, 32 * kSimtRowsPerCta, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
