@@ -16,9 +16,15 @@ void plan_shared(mla_verify_plan_s* pl, int sms) {
   auto round_up = [](size_t x, size_t a) { return (x + a - 1) / a * a; };
   size_t rows;
   pl->fused = false;
-  pl->kernel = 0;
-  pl->pieces = 0;
-  {
+  pl->resident = pl->kernel == 1;
+  if (pl->kernel) {
+    pl->nq = kSharedRows;
+    pl->pieces = sms / 2 > 1 ? sms / 2 : 1;
+    pl->splits = 1;
+    pl->smem = split_shared_smem();
+    rows = 2 * (size_t)pl->rows_max + (size_t)kSharedRows * pl->pieces;
+    pl->off_lse = round_up(kWsHeader + sizeof(int2) * 2 * (size_t)pl->rows_max, 256);
+  } else {
     pl->shared_splits = 8;
     pl->own_splits = 4;
     pl->splits = pl->shared_splits + pl->own_splits;
@@ -162,7 +168,9 @@ int mla_verify_run_shared(mla_verify_plan_t pl, const void* q_nope_absorbed, con
   a.o = static_cast<__nv_bfloat16*>(o);
   a.lse = lse;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return done(run_shared_simt(pl, a, st));
+  if (!pl->kernel) return done(run_shared_simt(pl, a, st));
+  const cudaError_t e = launch_split_shared(a, st);
+  return e != cudaSuccess ? done(e) : done(launch_merge_shared(a, st));
 }
 
 int mla_verify_accept_drafts(mla_verify_plan_t pl, const float* target_probs, int64_t target_stride,

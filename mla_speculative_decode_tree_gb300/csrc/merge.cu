@@ -207,7 +207,119 @@ __global__ void __launch_bounds__(32 * kPieceWarps, 5) merge_pieces_kernel(Merge
   }
 }
 
+// Partials of requests in groups (split_shared.cu): a row's entry in the table
+// names the CTA pairs that have a partial of its shared part, rows_max further on
+// those of its own part; pair w's stands 128 * w rows behind the row's place.
+// kWarps warps take a row's partials in turn, kAtOnce at a time; the sums run in a
+// fixed order.
+template <int kWarps>
+__global__ void __launch_bounds__(128, 5) merge_shared_kernel(SharedArgs a) {
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    const uint32_t st = a.status[0];
+    if (st) atomicOr(a.status + 1, st);
+    a.status[0] = 0u;
+  }
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t row = kWarps == 1 ? (int64_t)blockIdx.x * 4 + warp : blockIdx.x;
+  const int64_t rows = (a.qo_indptr ? (int64_t)a.qo_indptr[a.batch] : (int64_t)a.batch * a.T) * a.H;
+  if (row >= rows || row >= (int64_t)a.batch * a.T * a.H) return;
+  // (an entry that was not written -- a CTA that gave up -- points nowhere else)
+  auto entry = [&](int2 e) -> int2 {
+    const bool in = e.x >= 0 && e.y >= 0 && e.x <= a.clusters && e.y <= a.clusters - e.x;
+    return in ? e : make_int2(0, 0);
+  };
+  const int2 sh = entry(a.table[row]), ow = entry(a.table[a.rows_max + row]);
+  const int n = sh.y + ow.y;
+  auto place = [&](int s) -> int64_t {
+    return s < sh.y ? row + (int64_t)kSharedRows * (sh.x + s) : a.rows_max + row + (int64_t)kSharedRows * (ow.x + s - sh.y);
+  };
+  float w[kAtOnce];
+  float4 v[kAtOnce][4];
+  auto load = [&](int s0) {
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int s = s0 + u * kWarps;
+      w[u] = -INFINITY;
+      if (s < n) {
+        const int64_t at = place(s);
+        w[u] = a.part_lse[at];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          v[u][k] = *reinterpret_cast<const float4*>(a.part_o + at * kDLatent + 128 * k + 4 * lane);
+      }
+    }
+  };
+  const int first = kWarps == 1 ? 0 : warp;
+  load(first);  // (before the LSEs are known: what has weight 0 was never written and is dropped)
+  float M = -INFINITY, W = 0.f;
+  for (int s = lane; s < n; s += 32) M = fmaxf(M, a.part_lse[place(s)]);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+  if (M != -INFINITY) {
+    for (int s = lane; s < n; s += 32) W += expf(a.part_lse[place(s)] - M);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) W += __shfl_xor_sync(0xffffffffu, W, off);
+  }
+  float acc[16];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) acc[k] = 0.f;
+#pragma unroll 1
+  for (int s0 = first; s0 < n;) {
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      if (w[u] == -INFINITY) continue;
+      const float x = expf(w[u] - M);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        acc[4 * k + 0] = fmaf(x, v[u][k].x, acc[4 * k + 0]);
+        acc[4 * k + 1] = fmaf(x, v[u][k].y, acc[4 * k + 1]);
+        acc[4 * k + 2] = fmaf(x, v[u][k].z, acc[4 * k + 2]);
+        acc[4 * k + 3] = fmaf(x, v[u][k].w, acc[4 * k + 3]);
+      }
+    }
+    s0 += kAtOnce * kWarps;
+    load(s0);
+  }
+  const float inv = W == 0.f ? 0.f : 1.f / W;
+  if constexpr (kWarps == 1) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      *reinterpret_cast<uint2*>(a.o + row * kDLatent + 128 * k + 4 * lane) =
+          make_uint2(pack_bf16(acc[4 * k] * inv, acc[4 * k + 1] * inv),
+                     pack_bf16(acc[4 * k + 2] * inv, acc[4 * k + 3] * inv));
+    if (lane == 0) a.lse[row] = M + logf(W);  // (nothing visible: -inf)
+  } else {
+    __shared__ float4 sums[kWarps][kDLatent / 4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      sums[warp][32 * k + lane] = make_float4(acc[4 * k], acc[4 * k + 1], acc[4 * k + 2], acc[4 * k + 3]);
+    __syncthreads();
+    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float4 y = sums[k][threadIdx.x];
+      t.x += y.x;
+      t.y += y.y;
+      t.z += y.z;
+      t.w += y.w;
+    }
+    reinterpret_cast<uint2*>(a.o + row * kDLatent)[threadIdx.x] =
+        make_uint2(pack_bf16(t.x * inv, t.y * inv), pack_bf16(t.z * inv, t.w * inv));
+    if (threadIdx.x == 0) a.lse[row] = M + logf(W);
+  }
+}
+
 }  // namespace
+
+cudaError_t launch_merge_shared(const SharedArgs& a, cudaStream_t stream) {
+  // Few rows have many partials each: four warps a row, while the blocks fit two waves.
+  const int64_t rows = (int64_t)a.batch * a.T * a.H;
+  if (rows <= 152 * 5 * 2)
+    merge_shared_kernel<4><<<(unsigned)rows, 128, 0, stream>>>(a);
+  else
+    merge_shared_kernel<1><<<(unsigned)((rows + 3) / 4), 128, 0, stream>>>(a);
+  return cudaGetLastError();
+}
 
 // Rows per block: up to 4 while that still leaves four blocks per SM.
 int merge_pieces_rows(int64_t rows, int sms) {
