@@ -27,7 +27,7 @@
 //
 // Warps: 0-7 softmax (thread = a query row and 32 of the tile's keys; it also
 // brings its row's Q into tensor memory and takes O out of it), 8 issues the MMAs,
-// 9-12 gather rows with 16-byte cp.async.  In the steady state the issuing thread
+// 12-15 gather rows with 16-byte cp.async.  In the steady state the issuing thread
 // runs QK(t+1), PV(t), QK(t+2), ...: S is read out of tensor memory at once, so
 // one S buffer is enough for the tensor pipe to have QK(t+1) to do while the
 // softmax of tile t runs.
@@ -53,27 +53,32 @@ namespace cg = cooperative_groups;
 
 constexpr int kRows = kSharedRows, kKeys = kSharedKeys;
 constexpr int kHalfLatent = kDLatent / 2, kHalfRope = kDRope / 2;
-constexpr int kStages = 3;
-constexpr int kBlockBytes = kKeys * 128;        // 64 columns of a tile
-constexpr int kStageBytes = 5 * kBlockBytes;
+constexpr int kStages = 4;
+constexpr int kBlockBytes = kKeys * 128;        // 64 latent columns of a tile
+constexpr int kRopeOff = 4 * kBlockBytes;       // 32 RoPE columns: 64 keys x 64 bytes
+constexpr int kStageBytes = kRopeOff + kKeys * 64;
+constexpr uint64_t kSwizzle64B = 4;
 constexpr int kXBytes = kRows * kKeys * 4;      // the other CTA's S
 constexpr int kSoftmaxWarps = 8;
 constexpr int kMmaWarp = kSoftmaxWarps;
-constexpr int kGatherWarp = kMmaWarp + 1, kGatherWarps = 4;
+constexpr int kGatherWarp = kMmaWarp + 4, kGatherWarps = 4;  // (a warpgroup each: registers go by warpgroup)
 constexpr int kThreads = 32 * (kGatherWarp + kGatherWarps);
+// Registers per thread by warpgroup; together at most the 4 x 128 of the launch.
+constexpr int kRegsSoftmax = 184, kRegsMma = 56, kRegsGather = 80;
+static_assert(kThreads == 512 && 2 * kRegsSoftmax + kRegsMma + kRegsGather <= 512, "register shares");
 constexpr int kKeysPerWarp = kKeys / kGatherWarps;  // gathered by a warp
 constexpr int kColO = 0, kColQ = 256, kColS = 400, kColP = 464;
 constexpr float kHeadroom = 8.0f;  // base 2, before the running maximum is raised
 // Start and end of a row group, in tiles.
 constexpr int kSegCost = 5;
 constexpr int kMaxSpans = 2 * kMaxSharedBatch;
+constexpr int64_t kAxisEnd = 0xFFFFFFFF;  // (2^32 tiles would take half a day)
 
 struct Ctl {
   uint64_t full[kStages], empty[kStages];
   uint64_t q_full, s_full, s_free, p_full, pv_done, x_full[2], mma_idle;
   uint32_t tmem_base;
   int abort;
-  int64_t total;
   uint16_t valid[kStages][kGatherWarps];  // keys of a tile that exist, 16 bits per gather warp
   int failed[2][4];                       // softmax warps that gave up, by half of the keys and quarter of the rows
   float red[2][kRows];                    // per half of the keys: row maxima, sums
@@ -84,7 +89,7 @@ struct Ctl {
 constexpr int kOffX = kStages * kStageBytes;
 constexpr int kOffCtl = kOffX + 2 * kXBytes;
 constexpr int kOffEnds = (kOffCtl + (int)sizeof(Ctl) + 15) / 16 * 16;
-constexpr int kSmem = kOffEnds + 1024;  // + the axis (8 bytes per group and request) + alignment slack
+constexpr int kSmem = kOffEnds + 1024;  // + the axis (4 bytes per group and request) + alignment slack
 
 // ---- wider TMEM accesses ------------------------------------------------------
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
@@ -123,6 +128,19 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
       : "memory");
 }
 
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+// mbar_wait_spin by a whole warp, with no look at the clock for the first polls.
+__device__ __forceinline__ bool wait_spin(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* status) {
+#pragma unroll 1
+  for (int it = 0; it < 64; ++it)
+    if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, mbar_wait_spin(bar, parity, abort, status));
+}
+
 // ---- the other CTA of the pair -------------------------------------------------
 __device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
   uint32_t r;
@@ -136,32 +154,6 @@ __device__ __forceinline__ void send16(uint32_t dst, uint32_t bar, float a, floa
       "r"(__float_as_uint(a)), "r"(__float_as_uint(b)), "r"(__float_as_uint(c)), "r"(__float_as_uint(d)), "r"(bar)
       : "memory");
 }
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
-      : "memory");
-  return ok != 0;
-}
-// mbar_wait for bytes from the other CTA.
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* status) {
-  if (mbar_try_wait_cluster(bar, parity)) return true;
-  const uint64_t t0 = global_timer_ns();
-  for (uint32_t it = 1; it < (1u << 30); ++it) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
-    if ((it & 63u) == 0) {
-      if (*abort) return false;
-      if (global_timer_ns() - t0 > kWaitLimitNs) break;
-    }
-  }
-  *abort = 1;
-  atomicOr(status, kStatusTimeout);
-  return false;
-}
 __device__ __forceinline__ bool or_sync(int id, bool p) {  // over the 64 threads that share rows
   uint32_t r;
   asm volatile(
@@ -170,6 +162,35 @@ __device__ __forceinline__ bool or_sync(int id, bool p) {  // over the 64 thread
       : "r"(p ? 1u : 0u), "r"(id)
       : "memory");
   return r != 0;
+}
+
+// ---- pairs of fp32 values in one instruction ---------------------------------------
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+template <int kRegs>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
 // ---- the axis --------------------------------------------------------------------
@@ -232,7 +253,7 @@ __device__ __forceinline__ int64_t tiles_of(const Span& s) { return (s.keys + kK
 
 // Where a pair is on the axis; every role of its CTAs walks it by itself.
 struct Cursor {
-  const int64_t* ends;  // shared memory: end of each span on the axis
+  const uint32_t* ends;  // shared memory: end of each span on the axis
   int spans, e;
   int64_t x, x_end, piece;
   int pair;
@@ -285,7 +306,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint8_t* smem = smem_raw + pad;
   const uint32_t sbase = raw_addr + pad;
   Ctl& ctl = *reinterpret_cast<Ctl*>(smem + kOffCtl);
-  int64_t* ends = reinterpret_cast<int64_t*>(smem + kOffEnds);
+  uint32_t* ends = reinterpret_cast<uint32_t*>(smem + kOffEnds);
   cg::cluster_group cluster = cg::this_cluster();
   const uint32_t rank = cluster.block_rank();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -297,7 +318,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(&ctl.empty[k], 1);
     }
     mbar_init(&ctl.q_full, kSoftmaxWarps);
-    mbar_init(&ctl.s_full, 1);
+    mbar_init(&ctl.s_full, 2);  // the product, and the issuing lane (which has seen the tile's valid bits)
     mbar_init(&ctl.s_free, kSoftmaxWarps);
     mbar_init(&ctl.p_full, kSoftmaxWarps);
     mbar_init(&ctl.pv_done, 1);
@@ -332,10 +353,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       __syncthreads();
       int64_t before = carry;
       for (int w = 0; w < warp; ++w) before += ctl.warp_sum[w];
-      if (e < cur.spans) ends[e] = before + v;
+      if (e < cur.spans) ends[e] = (uint32_t)(before + v < kAxisEnd ? before + v : kAxisEnd);
       for (int w = 0; w < kThreads / 32; ++w) carry += ctl.warp_sum[w];
       __syncthreads();
     }
+    carry = carry < kAxisEnd ? carry : kAxisEnd;
     const int64_t pairs = a.clusters;
     cur.piece = (carry + pairs - 1) / pairs;
     cur.piece = cur.piece < 1 ? 1 : cur.piece;
@@ -358,131 +380,173 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t tmem = ctl.tmem_base;
 
   if (warp >= kGatherWarp) {
+    fewer_registers<kRegsGather>();
     // ============================ gather ================================================
     // Warp gw fills keys 16 gw .. 16 gw + 15 of each tile: per key one instruction of 32 lanes x 16 bytes for this
-    // CTA's 512 latent bytes, and one for the 64 RoPE bytes of eight keys.
+    // CTA's 512 latent bytes, and one for the 64 RoPE bytes of eight keys.  A tile's rows are asked into L2 two tiles
+    // ahead: what a row costs beside that -- DRAM, the page's translation -- is then off the path.
     const int gw = warp - kGatherWarp;
     uint32_t bad = 0;
-    int64_t tt = 0;  // tiles so far
+    uint32_t tt = 0, stage = 0, phase = 1;
     bool stop = false;
     Segment g;
+    const int blk = lane >> 3, chunk = lane & 7;
+    const __nv_bfloat16* const latent = a.kv_pool + rank * kHalfLatent + lane * 8;
+    const __nv_bfloat16* const rope = a.kv_pool + kDLatent + rank * kHalfRope + (lane & 3) * 8;
     while (!stop && next_segment(a, cur, g)) {
       const int32_t* index = g.s.own ? a.kv_indices : a.shared_indices;
-      auto load_id = [&](int t) -> int32_t {  // of this lane's key of tile t (lanes 0..15)
-        const int64_t j = (g.tile0 + t) * kKeys + gw * kKeysPerWarp + (lane & 15);
+      const int64_t key0 = g.tile0 * kKeys + gw * kKeysPerWarp + (lane & 15);
+      auto load_id = [&](int t) -> int32_t {  // of this lane's key of tile t (both halves of the warp hold all 16)
+        const int64_t j = key0 + (int64_t)t * kKeys;
         if (t >= g.nt || j >= g.s.keys) return -1;  // no such key
         return j < g.s.prefix ? __ldg(index + g.s.kv0 + j) : __ldg(a.out_cache_loc + g.s.q0 + (j - g.s.prefix));
       };
-      int32_t id0 = load_id(0), id1 = load_id(1);
+      auto ask = [&](int32_t id) {  // this CTA's lines of the rows: four of the latent, one with the RoPE columns
+        if (id < 0 || id >= a.pool_rows) return;
+        const char* row = reinterpret_cast<const char*>(a.kv_pool + (int64_t)id * kDRow);
+        const int line = 2 * (lane >> 4);
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(row + rank * 512 + line * 128));
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(row + rank * 512 + line * 128 + 128));
+        if (lane >= 16) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + 1024 + rank * 64));
+      };
+      int32_t id0 = load_id(0), id1 = load_id(1), id2 = load_id(2);
+      ask(id1);
 #pragma unroll 1
       for (int t = 0; t < g.nt; ++t, ++tt) {
         int32_t row = id0;
         id0 = id1;
-        id1 = load_id(t + 2);
+        id1 = id2;
+        id2 = load_id(t + 3);
+        ask(id1);
         const bool ok = row >= 0 && row < a.pool_rows;
-        if (!ok && (g.tile0 + t) * kKeys + gw * kKeysPerWarp + (lane & 15) < g.s.keys) bad = 1;
+        if (!ok && key0 + (int64_t)t * kKeys < g.s.keys) bad = 1;
         row = ok ? row : -1;
         const uint32_t valid = __ballot_sync(0xffffffffu, ok) & 0xFFFFu;
-        const int stage = (int)(tt % kStages);
-        const bool got = mbar_wait(&ctl.empty[stage], ((uint32_t)(tt / kStages) & 1u) ^ 1u, &ctl.abort, a.status);
+        const bool got = mbar_wait(&ctl.empty[stage], phase, &ctl.abort, a.status);
         if (!__all_sync(0xffffffffu, got)) {
           stop = true;
           break;
         }
-        if (a.test_stall && tt == 0) continue;  // test only: the first tile never lands
-        if (lane == 0) ctl.valid[stage][gw] = (uint16_t)valid;
-        const uint32_t dst = sbase + stage * kStageBytes;
-        const int blk = lane >> 3, chunk = lane & 7;
-        const __nv_bfloat16* src = a.kv_pool + rank * kHalfLatent + lane * 8;
+        if (!(a.test_stall && tt == 0)) {  // test only: the first tile never lands
+          if (lane == 0) ctl.valid[stage][gw] = (uint16_t)valid;
+          const uint32_t dst = sbase + stage * kStageBytes;
 #pragma unroll
-        for (int k = 0; k < kKeysPerWarp; ++k) {
-          const int key = gw * kKeysPerWarp + k;
-          const int32_t r = __shfl_sync(0xffffffffu, row, k);
-          cp_async16(dst + blk * kBlockBytes + key * 128 + ((chunk ^ (key & 7)) << 4),
-                     src + (int64_t)(r < 0 ? 0 : r) * kDRow, r < 0 ? 0u : 16u);
-        }
+          for (int k = 0; k < kKeysPerWarp; ++k) {
+            const int key = gw * kKeysPerWarp + k;
+            const int32_t r = __shfl_sync(0xffffffffu, row, k);
+            cp_async16(dst + blk * kBlockBytes + key * 128 + ((chunk ^ (key & 7)) << 4),
+                       latent + (int64_t)(r < 0 ? 0 : r) * kDRow, r < 0 ? 0u : 16u);
+          }
 #pragma unroll
-        for (int k = 0; k < kKeysPerWarp; k += 8) {
-          const int key = gw * kKeysPerWarp + k + (lane >> 2);
-          const int32_t r = __shfl_sync(0xffffffffu, row, k + (lane >> 2));
-          cp_async16(dst + 4 * kBlockBytes + key * 128 + (((lane & 3) ^ (key & 7)) << 4),
-                     a.kv_pool + (int64_t)(r < 0 ? 0 : r) * kDRow + kDLatent + rank * kHalfRope + (lane & 3) * 8,
-                     r < 0 ? 0u : 16u);
+          for (int k = 0; k < kKeysPerWarp; k += 8) {
+            const int key = gw * kKeysPerWarp + k + (lane >> 2);
+            const int32_t r = __shfl_sync(0xffffffffu, row, k + (lane >> 2));
+            cp_async16(dst + kRopeOff + key * 64 + (((lane & 3) ^ ((key >> 1) & 3)) << 4),
+                       rope + (int64_t)(r < 0 ? 0 : r) * kDRow, r < 0 ? 0u : 16u);
+          }
+          cp_async_arrive(&ctl.full[stage]);
+          if (lane == 0) mbar_arrive(&ctl.full[stage]);
         }
-        cp_async_arrive(&ctl.full[stage]);
-        if (lane == 0) mbar_arrive(&ctl.full[stage]);
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
     }
     cp_async_wait_all();
     if (bad) atomicOr(a.status, kStatusBadRow);
-  } else if (warp == kMmaWarp) {
-    // ============================ MMA issue ==============================================
-    if (lane == 0) {
+  } else if (warp >= kMmaWarp) {
+    fewer_registers<kRegsMma>();
+    if (warp == kMmaWarp) {
+      // ============================ MMA issue ==============================================
+      // The whole warp walks the loop and one elected lane issues, so that what an MMA
+      // takes its descriptors from stays warp-uniform.
+      const bool leader = elect_one();
       constexpr uint32_t idesc_qk = tc::idesc_bf16_f32(kRows, kKeys, false, false);
       constexpr uint32_t idesc_pv = tc::idesc_bf16_f32(kRows, kHalfLatent, false, true);
+      const uint64_t desc_k = tc::smem_desc(sbase, 16, 1024, tc::kSwizzle128B);
+      const uint64_t desc_r = tc::smem_desc(sbase + kRopeOff, 16, 512, kSwizzle64B);
+      const uint64_t desc_v = tc::smem_desc(sbase, kBlockBytes, 1024, tc::kSwizzle128B);
       bool ok = true;
-      int64_t tt = 0;  // tiles whose scores have been issued
+      uint32_t tt = 0, stage = 0, phase = 0;  // tiles whose scores have been issued; the next one's place
+      uint32_t ps = 0;                        // the stage of the next value product
       uint32_t seg = 0;
       Segment g;
-      auto qk = [&]() {  // scores of tile tt
-        const int stage = (int)(tt % kStages);
-        ok = mbar_wait_spin(&ctl.full[stage], (uint32_t)(tt / kStages) & 1u, &ctl.abort, a.status);
-        if (ok && tt > 0) ok = mbar_wait_spin(&ctl.s_free, (uint32_t)(tt - 1) & 1u, &ctl.abort, a.status);
+      auto qk = [&]() {  // scores of the next tile
+        ok = wait_spin(&ctl.full[stage], phase, &ctl.abort, a.status);
+        if (ok && tt > 0) ok = wait_spin(&ctl.s_free, (tt - 1) & 1u, &ctl.abort, a.status);
         if (!ok) return;
         fence_proxy_async_smem();
         tc::fence_after_sync();
-        const uint32_t base = sbase + stage * kStageBytes;
+        const uint32_t at = stage * (kStageBytes >> 4);
+        const uint64_t d = desc_k + at, dr = desc_r + at;
+        if (leader) {
 #pragma unroll
-        for (int k = 0; k < 18; ++k)
-          mma_bf16_ts(tmem + kColS, tmem + kColQ + 8 * k,
-                      tc::smem_desc(base + (k >> 2) * kBlockBytes + (k & 3) * 32, 16, 1024, tc::kSwizzle128B), idesc_qk,
-                      k > 0);
-        tc::mma_commit(&ctl.s_full);
+          for (int k = 0; k < 16; ++k)
+            mma_bf16_ts(tmem + kColS, tmem + kColQ + 8 * k, d + (uint32_t)(((k >> 2) * kBlockBytes + (k & 3) * 32) >> 4),
+                        idesc_qk, k > 0);
+          mma_bf16_ts(tmem + kColS, tmem + kColQ + 128, dr, idesc_qk, 1u);
+          mma_bf16_ts(tmem + kColS, tmem + kColQ + 136, dr + 2, idesc_qk, 1u);
+          tc::mma_commit(&ctl.s_full);
+          mbar_arrive(&ctl.s_full);
+        }
         ++tt;
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
       };
-      auto pv = [&](int64_t u, bool first) {  // O += P V of tile u
-        ok = mbar_wait_spin(&ctl.p_full, (uint32_t)u & 1u, &ctl.abort, a.status);
+      auto pv = [&](uint32_t u, bool first) {  // O += P V of tile u
+        ok = wait_spin(&ctl.p_full, u & 1u, &ctl.abort, a.status);
         if (!ok) return;
         tc::fence_after_sync();
-        const int stage = (int)(u % kStages);
-        const uint32_t base = sbase + stage * kStageBytes;
+        const uint64_t d = desc_v + (uint32_t)(ps * (kStageBytes >> 4));
+        if (leader) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          mma_bf16_ts(tmem + kColO, tmem + kColP + 8 * k,
-                      tc::smem_desc(base + k * 2048, kBlockBytes, 1024, tc::kSwizzle128B), idesc_pv, !(first && k == 0));
-        tc::mma_commit(&ctl.empty[stage]);
-        tc::mma_commit(&ctl.pv_done);
+          for (int k = 0; k < 4; ++k)
+            mma_bf16_ts(tmem + kColO, tmem + kColP + 8 * k, d + (uint32_t)(k * 2048 >> 4), idesc_pv, !(first && k == 0));
+          tc::mma_commit(&ctl.empty[ps]);
+          tc::mma_commit(&ctl.pv_done);
+        }
+        if (++ps == kStages) ps = 0;
       };
       while (ok && next_segment(a, cur, g)) {
         if (g.nt == 0) continue;
-        ok = mbar_wait_spin(&ctl.q_full, seg & 1u, &ctl.abort, a.status);
+        ok = wait_spin(&ctl.q_full, seg & 1u, &ctl.abort, a.status);
         tc::fence_after_sync();
         ++seg;
+        const uint32_t first = tt;
+        // The scores run two tiles ahead of the values.
         if (ok) qk();
+        if (ok && g.nt > 1) qk();
 #pragma unroll 1
         for (int t = 0; t < g.nt && ok; ++t) {
-          if (t + 1 < g.nt) qk();
-          if (ok) pv(t + 1 < g.nt ? tt - 2 : tt - 1, t == 0);
+          if (t + 2 < g.nt) qk();
+          if (ok) pv(first + t, t == 0);
         }
       }
-      // Drain: every MMA this thread issued has completed before tensor memory is freed.
-      tc::mma_commit(&ctl.mma_idle);
+      // Drain: every MMA of this warp has completed before tensor memory is freed.
+      if (leader) tc::mma_commit(&ctl.mma_idle);
       const uint64_t t0 = global_timer_ns();
       for (uint32_t it = 0; it < (1u << 30); ++it)
         if (mbar_try_wait(&ctl.mma_idle, 0) || ((it & 63u) == 63u && global_timer_ns() - t0 > kWaitLimitNs)) break;
+      __syncwarp();
     }
-    __syncwarp();
   } else {
+    more_registers<kRegsSoftmax>();
     // ============================ softmax ================================================
     const int quad = warp & 3, half = warp >> 2;
     const int r = 32 * quad + lane;  // query row in the group = TMEM lane
     const uint32_t t_lane = tmem + ((uint32_t)(32 * quad) << 16);
-    const float scale = a.scale_log2;
+    // Scores are kept unscaled, as S or, for a negative scale, -S; a scale of 0 becomes one that no difference survives.
+    const float scale = fmaxf(fabsf(a.scale_log2), 1e-30f);
+    const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
+    const uint64_t scale2 = pair(scale, scale);
     const uint32_t other = rank ^ 1u;
     const uint32_t x_own = sbase + kOffX + half * 8 * kRows * 16 + r * 16;
     const uint32_t x_peer = peer_addr(x_own, other);
     const uint32_t bar_peer[2] = {peer_addr(smem_u32(&ctl.x_full[0]), other), peer_addr(smem_u32(&ctl.x_full[1]), other)};
-    int64_t tt = 0;
+    uint32_t tt = 0, stage = 0;
     bool stop = false, fail = false;
     Segment g;
     while (!stop && next_segment(a, cur, g)) {
@@ -501,6 +565,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int k = 0; k < 16; ++k) v[k] = __ldg(reinterpret_cast<const uint4*>(qn) + k);
         v[16] = __ldg(reinterpret_cast<const uint4*>(qr));
         v[17] = __ldg(reinterpret_cast<const uint4*>(qr) + 1);
+        if (flip) {
+#pragma unroll
+          for (int k = 0; k < 18; ++k) v[k] = make_uint4(v[k].x ^ flip, v[k].y ^ flip, v[k].z ^ flip, v[k].w ^ flip);
+        }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const uint32_t w[16] = {v[4 * k].x,     v[4 * k].y,     v[4 * k].z,     v[4 * k].w,
@@ -519,23 +587,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
       const int token = row_in ? (g.r0 + r) / a.H : 0;
       const int64_t mask_row = g.s.mask0 + (int64_t)token * g.s.keys;
-      float m = -INFINITY;              // running maximum, base 2
-      float l_round = 0.f, l_full = 0.f;  // of this thread's keys: sums of the weights as P has them, and before rounding
+      float m = -INFINITY;                // running maximum, base 2
+      // of this thread's keys: sums of the weights as P has them, and before rounding (even and odd keys)
+      uint64_t l_round = 0, l_full = 0;
+      // This CTA's part of the next tile's scores: read out of tensor memory and sent to the other CTA while the tile
+      // before it is at its softmax.
+      float n[32];
+      auto take = [&](uint32_t u) {  // tile u's part into n
+        if (tid == 0) tma::arrive_expect_tx(&ctl.x_full[u & 1], (uint32_t)quads * 2u * 32u * 128u);
+        const bool got = mbar_wait(&ctl.s_full, u & 1u, &ctl.abort, a.status);
+        fail |= !__all_sync(0xffffffffu, got);
+        tc::fence_after_sync();
+        if (active) {
+          tmem_ld32(t_lane + kColS + 32 * half, n);
+          tc::tmem_wait_ld();
+        }
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl.s_free);
+      };
+      auto send = [&](uint32_t u, int c) {  // keys 4c .. 4c+3 of it
+        send16(x_peer + (u & 1) * kXBytes + c * kRows * 16, bar_peer[u & 1], n[4 * c], n[4 * c + 1], n[4 * c + 2],
+               n[4 * c + 3]);
+      };
+      take(tt);
+      if (active) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) send(tt, c);
+      }
 #pragma unroll 1
       for (int t = 0; t < g.nt; ++t, ++tt) {
-        const int stage = (int)(tt % kStages);
         const int buf = (int)(tt & 1);
-        if (tid == 0) tma::arrive_expect_tx(&ctl.x_full[buf], (uint32_t)quads * 2u * 32u * 128u);
+        const bool more = t + 1 < g.nt;
         // which of the 32 keys this row sees
-        const int64_t key0 = (g.tile0 + t) * kKeys + 32 * half;
         uint32_t sees = 0xFFFFFFFFu;
         if (g.s.own) {
           sees = 0;
-          const int64_t n = g.s.keys - key0 < 32 ? g.s.keys - key0 : 32;
-          if (row_in && n > 0) {
+          const int64_t key0 = (g.tile0 + t) * kKeys + 32 * half;
+          const int64_t left = g.s.keys - key0 < 32 ? g.s.keys - key0 : 32;
+          if (row_in && left > 0) {
             const int64_t bit = mask_row + key0;
             const uint8_t* p = a.mask + (bit >> 3);
-            const int shift = (int)(bit & 7), bytes = (int)((shift + n + 7) >> 3);
+            const int shift = (int)(bit & 7), bytes = (int)((shift + left + 7) >> 3);
             uint64_t w = 0;
 #pragma unroll
             for (int i = 0; i < 5; ++i)
@@ -543,47 +636,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             sees = (uint32_t)(w >> shift);
           }
         }
-        bool got = mbar_wait(&ctl.full[stage], (uint32_t)(tt / kStages) & 1u, &ctl.abort, a.status);
         sees &= (uint32_t)ctl.valid[stage][2 * half] | ((uint32_t)ctl.valid[stage][2 * half + 1] << 16);
-        got = got && mbar_wait(&ctl.s_full, (uint32_t)tt & 1u, &ctl.abort, a.status);
-        fail |= !__all_sync(0xffffffffu, got);
-        tc::fence_after_sync();
-        float s[32];
+        if (++stage == kStages) stage = 0;
+        uint64_t s[16];
         if (active) {
-          tmem_ld32(t_lane + kColS + 32 * half, s);
-          tc::tmem_wait_ld();
-        }
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl.s_free);
-        if (active) {
-          const uint32_t off = buf * kXBytes;
-#pragma unroll
-          for (int c = 0; c < 8; ++c)
-            send16(x_peer + off + c * kRows * 16, bar_peer[buf], s[4 * c], s[4 * c + 1], s[4 * c + 2], s[4 * c + 3]);
-        }
-        got = mbar_wait_cluster(&ctl.x_full[buf], (uint32_t)(tt >> 1) & 1u, &ctl.abort, a.status);
-        fail |= !__all_sync(0xffffffffu, got);
-        bool raise = false;
-        float top = -INFINITY;
-        if (active) {
+          const bool got = mbar_wait(&ctl.x_full[buf], (tt >> 1) & 1u, &ctl.abort, a.status);
+          fail |= !__all_sync(0xffffffffu, got);
           const uint32_t off = buf * kXBytes;
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
-            float x[4];
-            asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
-                         : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3])
+            uint64_t x0, x1;
+            asm volatile("ld.shared.v2.b64 {%0,%1}, [%2];"
+                         : "=l"(x0), "=l"(x1)
                          : "r"(x_own + off + c * kRows * 16)
                          : "memory");
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[4 * c + i] = (s[4 * c + i] + x[i]) * scale;
+            s[2 * c] = add2(pair(n[4 * c], n[4 * c + 1]), x0);
+            s[2 * c + 1] = add2(pair(n[4 * c + 2], n[4 * c + 3]), x1);
           }
+        }
+        if (more) take(tt + 1);
+        bool raise = false;
+        float top = -INFINITY, alpha = 1.f;
+        if (active) {
           if (sees != 0xFFFFFFFFu) {
 #pragma unroll
-            for (int k = 0; k < 32; ++k) s[k] = (sees >> k) & 1u ? s[k] : -INFINITY;
+            for (int k = 0; k < 16; ++k) {
+              float x, y;
+              unpair(s[k], x, y);
+              s[k] = pair((sees >> (2 * k)) & 1u ? x : -INFINITY, (sees >> (2 * k + 1)) & 1u ? y : -INFINITY);
+            }
           }
 #pragma unroll
-          for (int k = 0; k < 32; ++k) top = fmaxf(top, s[k]);
+          for (int k = 0; k < 16; ++k) {
+            float x, y;
+            unpair(s[k], x, y);
+            top = fmaxf(top, fmaxf(x, y));
+          }
+          top *= scale;
           raise = top > m + kHeadroom;  // (m = -inf: any key that is seen)
           // The two warps of a quarter stay together: they leave the loop in the same place.
           raise = or_sync(1 + quad, raise || fail);
@@ -594,48 +683,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             top = fmaxf(top, ctl.red[half ^ 1][r]);
             fail |= ctl.failed[half ^ 1][quad] != 0;
             named_bar_sync(1 + quad, 64);  // (read before the next raise writes)
+            if (top > m + kHeadroom) {
+              alpha = m == -INFINITY ? 0.f : ex2_approx(m - top);
+              m = top;
+            }
+            const uint64_t alpha2 = pair(alpha, alpha);
+            l_round = fma2(l_round, alpha2, 0);
+            l_full = fma2(l_full, alpha2, 0);
           }
         }
         if (fail) {
           stop = true;
           break;
         }
+        uint32_t w[16];
+        if (active) {
+          const float mu = m == -INFINITY ? 0.f : -m;
+          const uint64_t mu2 = pair(mu, mu);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            float p0, p1;
+            unpair(fma2(s[k], scale2, mu2), p0, p1);
+            p0 = ex2_approx(p0);
+            p1 = ex2_approx(p1);
+            const __nv_bfloat162 h = __floats2bfloat162_rn(p0, p1);
+            w[k] = *reinterpret_cast<const uint32_t*>(&h);
+            l_full = add2(l_full, pair(p0, p1));
+            l_round = add2(l_round, pair(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u)));
+            if (more && (k & 1)) send(tt + 1, k >> 1);  // (the way to the other CTA is narrow: spread over the exponentials)
+          }
+        }
         // P(t) overwrites what PV(t-1) reads, and a rescaled O needs it complete.
         if (t > 0) {
-          got = mbar_wait(&ctl.pv_done, (uint32_t)(tt - 1) & 1u, &ctl.abort, a.status);
+          const bool got = mbar_wait(&ctl.pv_done, (tt - 1) & 1u, &ctl.abort, a.status);
           fail |= !__all_sync(0xffffffffu, got);  // (left at the next meeting)
         }
         tc::fence_after_sync();
         if (active) {
-          if (raise) {
-            float alpha = 1.f;
-            if (top > m + kHeadroom) {
-              alpha = m == -INFINITY ? 0.f : ex2_approx(m - top);
-              m = top;
-            }
-            l_round *= alpha;
-            l_full *= alpha;
-            if (t > 0) {
+          if (raise && t > 0) {
 #pragma unroll 1
-              for (int c = 0; c < 16; ++c) {
-                float v[8];
-                tc::tmem_ld8(t_lane + kColO + half * 128 + 8 * c, v);
-                tc::tmem_wait_ld();
+            for (int c = 0; c < 16; ++c) {
+              float v[8];
+              tc::tmem_ld8(t_lane + kColO + half * 128 + 8 * c, v);
+              tc::tmem_wait_ld();
 #pragma unroll
-                for (int k = 0; k < 8; ++k) v[k] *= alpha;
-                tc::tmem_st8(t_lane + kColO + half * 128 + 8 * c, v);
-              }
+              for (int k = 0; k < 8; ++k) v[k] *= alpha;
+              tc::tmem_st8(t_lane + kColO + half * 128 + 8 * c, v);
             }
-          }
-          const float mu = m == -INFINITY ? 0.f : m;
-          uint32_t w[16];
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const float p0 = ex2_approx(s[2 * k] - mu), p1 = ex2_approx(s[2 * k + 1] - mu);
-            const __nv_bfloat162 h = __floats2bfloat162_rn(p0, p1);
-            w[k] = *reinterpret_cast<const uint32_t*>(&h);
-            l_full += p0 + p1;
-            l_round += __uint_as_float(w[k] << 16) + __uint_as_float(w[k] & 0xFFFF0000u);
           }
           tmem_st16(t_lane + kColP + 16 * half, w);
           tc::tmem_wait_st();
@@ -646,14 +740,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       if (stop) break;
       // ---- the row group's partial -----------------------------------------------------
-      const bool got = mbar_wait(&ctl.pv_done, (uint32_t)(tt - 1) & 1u, &ctl.abort, a.status);
+      const bool got = mbar_wait(&ctl.pv_done, (tt - 1) & 1u, &ctl.abort, a.status);
       fail |= !__all_sync(0xffffffffu, got);
       stop = active ? or_sync(1 + quad, fail) : fail;
       if (stop) break;
       tc::fence_after_sync();
       if (active) {
-        ctl.red[half][r] = l_round;
-        ctl.red2[half][r] = l_full;
+        float even, odd;
+        unpair(l_round, even, odd);
+        ctl.red[half][r] = even + odd;
+        unpair(l_full, even, odd);
+        ctl.red2[half][r] = even + odd;
         named_bar_sync(1 + quad, 64);
         const float lr = ctl.red[0][r] + ctl.red[1][r], lf = ctl.red2[0][r] + ctl.red2[1][r];
         named_bar_sync(1 + quad, 64);
@@ -698,11 +795,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 }  // namespace
 
-int split_shared_smem() { return kSmem + (int)sizeof(int64_t) * kMaxSpans; }
+int split_shared_smem() { return kSmem + (int)sizeof(uint32_t) * kMaxSpans; }
 
 cudaError_t launch_split_shared(const SharedArgs& a, cudaStream_t stream) {
-  const int smem = kSmem + (int)sizeof(int64_t) * (a.groups + a.batch);
-  static_assert(kSmem + sizeof(int64_t) * kMaxSpans <= 232448, "shared memory budget exceeded");
+  const int smem = kSmem + (int)sizeof(uint32_t) * (a.groups + a.batch);
+  static_assert(kSmem + sizeof(uint32_t) * kMaxSpans <= 232448, "shared memory budget exceeded");
   cudaError_t e = cudaFuncSetAttribute(split_shared_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        split_shared_smem());
   if (e != cudaSuccess) return e;
