@@ -5,32 +5,36 @@
 // requests of a group, or of one request) -- and a run of 64-key tiles, and
 // leaves the group's partial softmax statistics for the merge.  Query rows sit on
 // the MMA's M = 128, so an fp32 O of 512 latent columns would fill tensor memory
-// (128 lanes x 512 columns).  The pair splits the latent columns instead: CTA c
-// owns latent columns 256c .. 256c+255 and RoPE columns 32c .. 32c+31, of the keys
-// as of the queries, and
-//   S_c[128 x 64]   = Q_c[128 x 288] . K_c^T        (18 MMAs, K = 16, N = 64)
-//   S               = S_0 + S_1                      (each half sent to the other CTA)
-//   O_c[128 x 256] += P[128 x 64] . V_c[64 x 256]    (4 MMAs, K = 16, N = 256)
-// so each key lands once per pair and each CTA gathers half of its row.  Both
-// CTAs hold the same S bit for bit (the sum of two commutes) and do the same
-// softmax; 64 exponentials per row and tile are cheaper than another exchange.
+// (128 lanes x 512 columns).  The pair shares the work of a tile: CTA c takes the
+// scores and the softmax of 32 of its keys, and half of O's columns,
+//   S_c[128 x 32]   = Q[128 x 576] . K_c^T            (36 MMAs, K = 16, N = 32)
+//   O_c[128 x 256] += P[128 x 64] . V[64 x 256 of 512] (4 MMAs, K = 16, N = 256)
+// and sends its half of P to the other CTA: 64 bytes per row and tile.  (Splitting
+// the latent columns in both products was built first.  It gathers a quarter less
+// and its MMAs are 1.3 times shorter, but it sends scores, 256 bytes per row and
+// tile: between two CTAs pass about 19 bytes per clock, and stores on their way
+// there hold up every other shared-memory access.  128k keys x 2048 rows took
+// 859 us so.)
 //
-// Q_c (as 144 columns of bf16 pairs) and P (32 columns) are A operands in tensor
-// memory, so shared memory feeds the B operands only, 64 bytes per clock at full
-// rate: with A there too the score product would take 1.5 times as long.
-// Tensor memory: O 0..255, Q 256..399, S 400..463, P 464..495.
+// Each CTA keeps, per row, a reference for its own weights, p = 2^(s - m), and
+// one for its half of O, M; both are whole numbers, so the weights change from one
+// to the other exactly, and neither CTA waits for the other's maximum.
 //
-// Shared memory: kStages tiles of K_c in five blocks of 64 keys x 128 bytes (four
-// latent blocks and one of which the first half is used), 128-byte swizzled: that
-// atom is the K-major layout of the score product's B and the MN-major layout of
-// the value product's; and two buffers for the other CTA's S (32 KB each).
+// A operands in tensor memory spare shared memory: with A there an MMA with N = 32
+// takes 16 cycles, with A in shared memory 40.  What fits is Q's first 384
+// channels (192 columns of bf16 pairs) and P (32 columns); the other 192 channels
+// are in shared memory.  Tensor memory: O 0..255, Q 256..447, S 448..479, P 480..511.
 //
-// Warps: 0-7 softmax (thread = a query row and 32 of the tile's keys; it also
-// brings its row's Q into tensor memory and takes O out of it), 8 issues the MMAs,
-// 12-15 gather rows with 16-byte cp.async.  In the steady state the issuing thread
-// runs QK(t+1), PV(t), QK(t+2), ...: S is read out of tensor memory at once, so
-// one S buffer is enough for the tensor pipe to have QK(t+1) to do while the
-// softmax of tile t runs.
+// Shared memory, all in blocks of 64 columns (128 bytes) of keys or query rows,
+// 128-byte swizzled -- the K-major layout of the score product and the MN-major
+// one of the value product's B: Q's three blocks; a ring of what only the scores
+// read (of this CTA's 32 keys the other CTA's half of the latent, and the RoPE
+// columns); a ring of values (the 64 keys, this CTA's half); the other CTA's P.
+//
+// Warps: 0-7 softmax (thread = a query row and 16 of the CTA's keys; it also
+// brings its row's Q in and takes O out of tensor memory), 8 issues the MMAs, 12-15
+// gather rows with 16-byte cp.async.  The issuing warp runs QK(t+1), PV(t),
+// QK(t+2), ...: the tensor pipe has QK(t+1) to do while the softmax of tile t runs.
 //
 // Work in equal pieces: the row groups of all groups' shared parts, then of all
 // requests' own parts, each as long as its tiles and kSegCost more, form an axis;
@@ -52,13 +56,14 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kRows = kSharedRows, kKeys = kSharedKeys;
-constexpr int kHalfLatent = kDLatent / 2, kHalfRope = kDRope / 2;
-constexpr int kStages = 4;
-constexpr int kBlockBytes = kKeys * 128;        // 64 latent columns of a tile
-constexpr int kRopeOff = 4 * kBlockBytes;       // 32 RoPE columns: 64 keys x 64 bytes
-constexpr int kStageBytes = kRopeOff + kKeys * 64;
-constexpr uint64_t kSwizzle64B = 4;
-constexpr int kXBytes = kRows * kKeys * 4;      // the other CTA's S
+constexpr int kOwnKeys = kKeys / 2;             // a CTA's keys of a tile
+constexpr int kHalfLatent = kDLatent / 2;
+constexpr int kBlockBytes = kOwnKeys * 128;     // 64 columns of 32 keys
+constexpr int kQBlock = kRows * 128;            // 64 columns of Q
+constexpr int kQSteps = 24;                     // k-steps of 16 channels with Q in tensor memory (6 blocks)
+constexpr int kScoreStages = 2, kScoreBytes = 5 * kBlockBytes;  // the other half of the latent, RoPE
+constexpr int kValueStages = 3, kValueBytes = 8 * kBlockBytes;  // own half: own keys, then the other CTA's
+constexpr int kPBytes = kRows * kOwnKeys * 2;   // the other CTA's P
 constexpr int kSoftmaxWarps = 8;
 constexpr int kMmaWarp = kSoftmaxWarps;
 constexpr int kGatherWarp = kMmaWarp + 4, kGatherWarps = 4;  // (a warpgroup each: registers go by warpgroup)
@@ -66,28 +71,34 @@ constexpr int kThreads = 32 * (kGatherWarp + kGatherWarps);
 // Registers per thread by warpgroup; together at most the 4 x 128 of the launch.
 constexpr int kRegsSoftmax = 184, kRegsMma = 56, kRegsGather = 80;
 static_assert(kThreads == 512 && 2 * kRegsSoftmax + kRegsMma + kRegsGather <= 512, "register shares");
-constexpr int kKeysPerWarp = kKeys / kGatherWarps;  // gathered by a warp
-constexpr int kColO = 0, kColQ = 256, kColS = 400, kColP = 464;
-constexpr float kHeadroom = 8.0f;  // base 2, before the running maximum is raised
+constexpr int kKeysPerWarp = kOwnKeys / kGatherWarps;  // of either half, gathered by a warp
+constexpr int kColO = 0, kColQ = 256, kColS = 448, kColP = 480;
+// Base 2, before a reference is raised.  Weights and O are floating numbers, so a
+// reference far below the maximum costs no precision; what it must not do is overflow.
+constexpr float kRowHeadroom = 16.0f, kOutHeadroom = 32.0f;
 // Start and end of a row group, in tiles.
 constexpr int kSegCost = 5;
 constexpr int kMaxSpans = 2 * kMaxSharedBatch;
 constexpr int64_t kAxisEnd = 0xFFFFFFFF;  // (2^32 tiles would take half a day)
 
 struct Ctl {
-  uint64_t full[kStages], empty[kStages];
-  uint64_t q_full, s_full, s_free, p_full, pv_done, x_full[2], mma_idle;
+  uint64_t full[kValueStages], empty_score[kScoreStages], empty_value[kValueStages];
+  uint64_t q_full, s_full, s_free, p_full, pv_done, x_full[2], l_full, mma_idle;
   uint32_t tmem_base;
   int abort;
-  uint16_t valid[kStages][kGatherWarps];  // keys of a tile that exist, 16 bits per gather warp
-  int failed[2][4];                       // softmax warps that gave up, by half of the keys and quarter of the rows
-  float red[2][kRows];                    // per half of the keys: row maxima, sums
+  alignas(4) uint8_t valid[kValueStages][kGatherWarps];  // own keys of a tile that exist, 8 bits per gather warp
+  int failed[2][4];     // softmax warps that gave up, by half of the keys and quarter of the rows
+  float red[2][kRows];  // per half of the keys: row maxima, sums
   float red2[2][kRows];
+  float x_ref[2][kRows];         // the other CTA's references, with its P
+  alignas(16) float4 x_sum[2][kRows];  // at the end of a row group: its reference and sums, per half of its keys
   int64_t warp_sum[kThreads / 32];
 };
 
-constexpr int kOffX = kStages * kStageBytes;
-constexpr int kOffCtl = kOffX + 2 * kXBytes;
+constexpr int kOffScore = 3 * kQBlock;
+constexpr int kOffValue = kOffScore + kScoreStages * kScoreBytes;
+constexpr int kOffX = kOffValue + kValueStages * kValueBytes;
+constexpr int kOffCtl = kOffX + 2 * kPBytes;
 constexpr int kOffEnds = (kOffCtl + (int)sizeof(Ctl) + 15) / 16 * 16;
 constexpr int kSmem = kOffEnds + 1024;  // + the axis (4 bytes per group and request) + alignment slack
 
@@ -104,6 +115,16 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
       : "r"(taddr));
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -148,11 +169,27 @@ __device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
   return r;
 }
 // 16 bytes into the other CTA's shared memory, counted by its barrier.
-__device__ __forceinline__ void send16(uint32_t dst, uint32_t bar, float a, float b, float c, float d) {
+__device__ __forceinline__ void send16(uint32_t dst, uint32_t bar, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile(
-      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1,%2,%3,%4}, [%5];" ::"r"(dst),
-      "r"(__float_as_uint(a)), "r"(__float_as_uint(b)), "r"(__float_as_uint(c)), "r"(__float_as_uint(d)), "r"(bar)
+      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1,%2,%3,%4}, [%5];" ::"r"(dst), "r"(a), "r"(b),
+      "r"(c), "r"(d), "r"(bar)
       : "memory");
+}
+__device__ __forceinline__ void send4(uint32_t dst, uint32_t bar, float a) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(dst),
+               "r"(__float_as_uint(a)), "r"(bar)
+               : "memory");
+}
+// 2^(a - b) of whole numbers (a = -inf: 0).
+__device__ __forceinline__ float ratio(float a, float b) {
+  const float d = a - b;
+  return d >= -126.f ? __int_as_float(((int)fminf(d, 127.f) + 127) << 23) : 0.f;
+}
+// Weights from one reference to another (an exact product).
+__device__ __forceinline__ uint32_t scale_bf16x2(uint32_t w, uint32_t f) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(w), "r"(f));
+  return r;
 }
 __device__ __forceinline__ bool or_sync(int id, bool p) {  // over the 64 threads that share rows
   uint32_t r;
@@ -313,10 +350,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   // ---- set-up: barriers, tensor memory, the axis ------------------------------------
   if (tid == 0) {
-    for (int k = 0; k < kStages; ++k) {
+    for (int k = 0; k < kValueStages; ++k) {
       mbar_init(&ctl.full[k], kGatherWarps * 33);  // every lane's copies and, per warp, its valid bits
-      mbar_init(&ctl.empty[k], 1);
+      mbar_init(&ctl.empty_value[k], 1);
     }
+    for (int k = 0; k < kScoreStages; ++k) mbar_init(&ctl.empty_score[k], 1);
     mbar_init(&ctl.q_full, kSoftmaxWarps);
     mbar_init(&ctl.s_full, 2);  // the product, and the issuing lane (which has seen the tile's valid bits)
     mbar_init(&ctl.s_free, kSoftmaxWarps);
@@ -324,6 +362,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(&ctl.pv_done, 1);
     mbar_init(&ctl.x_full[0], 1);
     mbar_init(&ctl.x_full[1], 1);
+    mbar_init(&ctl.l_full, 1);
     mbar_init(&ctl.mma_idle, 1);
     ctl.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -382,32 +421,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp >= kGatherWarp) {
     fewer_registers<kRegsGather>();
     // ============================ gather ================================================
-    // Warp gw fills keys 16 gw .. 16 gw + 15 of each tile: per key one instruction of 32 lanes x 16 bytes for this
-    // CTA's 512 latent bytes, and one for the 64 RoPE bytes of eight keys.  A tile's rows are asked into L2 two tiles
-    // ahead: what a row costs beside that -- DRAM, the page's translation -- is then off the path.
+    // Warp gw fills eight keys of each half of a tile: of this CTA's half whole rows (two instructions of 32 lanes x 16
+    // bytes per key for the latent, one for the RoPE bytes of four keys), of the other's this CTA's half of the latent.
+    // A tile's rows are asked into L2 two tiles ahead: what a row costs beside that -- DRAM, the page's translation --
+    // is then off the path.
     const int gw = warp - kGatherWarp;
     uint32_t bad = 0;
-    uint32_t tt = 0, stage = 0, phase = 1;
+    uint32_t tt = 0, sa = 0, pa = 1, sv = 0, pvp = 1;  // tiles so far; places in the two rings and their parities
     bool stop = false;
     Segment g;
     const int blk = lane >> 3, chunk = lane & 7;
-    const __nv_bfloat16* const latent = a.kv_pool + rank * kHalfLatent + lane * 8;
-    const __nv_bfloat16* const rope = a.kv_pool + kDLatent + rank * kHalfRope + (lane & 3) * 8;
+    const int theirs = (lane >> 3) & 1;  // lanes 0..7 hold the rows of own keys, 8..15 of the other CTA's (16..31 again)
+    const int key_in = kOwnKeys * (theirs ? 1 - (int)rank : (int)rank) + gw * kKeysPerWarp + (lane & 7);
+    const __nv_bfloat16* const latent = a.kv_pool + lane * 8;
     while (!stop && next_segment(a, cur, g)) {
       const int32_t* index = g.s.own ? a.kv_indices : a.shared_indices;
-      const int64_t key0 = g.tile0 * kKeys + gw * kKeysPerWarp + (lane & 15);
-      auto load_id = [&](int t) -> int32_t {  // of this lane's key of tile t (both halves of the warp hold all 16)
+      const int64_t key0 = g.tile0 * kKeys + key_in;
+      auto load_id = [&](int t) -> int32_t {  // of this lane's key of tile t
         const int64_t j = key0 + (int64_t)t * kKeys;
         if (t >= g.nt || j >= g.s.keys) return -1;  // no such key
         return j < g.s.prefix ? __ldg(index + g.s.kv0 + j) : __ldg(a.out_cache_loc + g.s.q0 + (j - g.s.prefix));
       };
-      auto ask = [&](int32_t id) {  // this CTA's lines of the rows: four of the latent, one with the RoPE columns
-        if (id < 0 || id >= a.pool_rows) return;
-        const char* row = reinterpret_cast<const char*>(a.kv_pool + (int64_t)id * kDRow);
-        const int line = 2 * (lane >> 4);
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(row + rank * 512 + line * 128));
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(row + rank * 512 + line * 128 + 128));
-        if (lane >= 16) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + 1024 + rank * 64));
+      auto ask = [&](int32_t id) {  // nine lines of an own key's row, four of another's
+        const int32_t mine = __shfl_sync(0xffffffffu, id, lane & 7), other = __shfl_sync(0xffffffffu, id, 8 + (lane & 7));
+        if (mine >= 0 && mine < a.pool_rows) {
+          const char* row = reinterpret_cast<const char*>(a.kv_pool + (int64_t)mine * kDRow);
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(row + blk * 128));
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(row + blk * 128 + 512));
+          if (blk == 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + 1024));
+        }
+        if (other >= 0 && other < a.pool_rows)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char*>(a.kv_pool + (int64_t)other * kDRow) +
+                                                        rank * 512 + blk * 128));
       };
       int32_t id0 = load_id(0), id1 = load_id(1), id2 = load_id(2);
       ask(id1);
@@ -421,35 +466,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const bool ok = row >= 0 && row < a.pool_rows;
         if (!ok && key0 + (int64_t)t * kKeys < g.s.keys) bad = 1;
         row = ok ? row : -1;
-        const uint32_t valid = __ballot_sync(0xffffffffu, ok) & 0xFFFFu;
-        const bool got = mbar_wait(&ctl.empty[stage], phase, &ctl.abort, a.status);
+        const uint32_t valid = __ballot_sync(0xffffffffu, ok) & 0xFFu;
+        bool got = mbar_wait(&ctl.empty_score[sa], pa, &ctl.abort, a.status);
+        got = got && mbar_wait(&ctl.empty_value[sv], pvp, &ctl.abort, a.status);
         if (!__all_sync(0xffffffffu, got)) {
           stop = true;
           break;
         }
         if (!(a.test_stall && tt == 0)) {  // test only: the first tile never lands
-          if (lane == 0) ctl.valid[stage][gw] = (uint16_t)valid;
-          const uint32_t dst = sbase + stage * kStageBytes;
+          if (lane == 0) ctl.valid[sv][gw] = (uint8_t)valid;
+          const uint32_t score = sbase + kOffScore + sa * kScoreBytes, value = sbase + kOffValue + sv * kValueBytes;
+          const uint32_t half0 = rank == 0 ? value : score, half1 = rank == 0 ? score : value;
 #pragma unroll
           for (int k = 0; k < kKeysPerWarp; ++k) {
             const int key = gw * kKeysPerWarp + k;
             const int32_t r = __shfl_sync(0xffffffffu, row, k);
-            cp_async16(dst + blk * kBlockBytes + key * 128 + ((chunk ^ (key & 7)) << 4),
-                       latent + (int64_t)(r < 0 ? 0 : r) * kDRow, r < 0 ? 0u : 16u);
+            const uint32_t at = blk * kBlockBytes + key * 128 + ((chunk ^ (key & 7)) << 4), n = r < 0 ? 0u : 16u;
+            const __nv_bfloat16* src = latent + (int64_t)(r < 0 ? 0 : r) * kDRow;
+            cp_async16(half0 + at, src, n);
+            cp_async16(half1 + at, src + kHalfLatent, n);
           }
 #pragma unroll
-          for (int k = 0; k < kKeysPerWarp; k += 8) {
-            const int key = gw * kKeysPerWarp + k + (lane >> 2);
-            const int32_t r = __shfl_sync(0xffffffffu, row, k + (lane >> 2));
-            cp_async16(dst + kRopeOff + key * 64 + (((lane & 3) ^ ((key >> 1) & 3)) << 4),
-                       rope + (int64_t)(r < 0 ? 0 : r) * kDRow, r < 0 ? 0u : 16u);
+          for (int k = 0; k < kKeysPerWarp; k += 4) {
+            const int key = gw * kKeysPerWarp + k + blk;
+            const int32_t r = __shfl_sync(0xffffffffu, row, k + blk);
+            cp_async16(score + 4 * kBlockBytes + key * 128 + ((chunk ^ (key & 7)) << 4),
+                       a.kv_pool + (int64_t)(r < 0 ? 0 : r) * kDRow + kDLatent + chunk * 8, r < 0 ? 0u : 16u);
           }
-          cp_async_arrive(&ctl.full[stage]);
-          if (lane == 0) mbar_arrive(&ctl.full[stage]);
+#pragma unroll
+          for (int k = 0; k < kKeysPerWarp; ++k) {
+            const int key = gw * kKeysPerWarp + k;
+            const int32_t r = __shfl_sync(0xffffffffu, row, 8 + k);
+            cp_async16(value + 4 * kBlockBytes + blk * kBlockBytes + key * 128 + ((chunk ^ (key & 7)) << 4),
+                       latent + (int64_t)(r < 0 ? 0 : r) * kDRow + rank * kHalfLatent, r < 0 ? 0u : 16u);
+          }
+          cp_async_arrive(&ctl.full[sv]);
+          if (lane == 0) mbar_arrive(&ctl.full[sv]);
         }
-        if (++stage == kStages) {
-          stage = 0;
-          phase ^= 1u;
+        if (++sa == kScoreStages) {
+          sa = 0;
+          pa ^= 1u;
+        }
+        if (++sv == kValueStages) {
+          sv = 0;
+          pvp ^= 1u;
         }
       }
     }
@@ -462,37 +522,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // The whole warp walks the loop and one elected lane issues, so that what an MMA
       // takes its descriptors from stays warp-uniform.
       const bool leader = elect_one();
-      constexpr uint32_t idesc_qk = tc::idesc_bf16_f32(kRows, kKeys, false, false);
+      constexpr uint32_t idesc_qk = tc::idesc_bf16_f32(kRows, kOwnKeys, false, false);
       constexpr uint32_t idesc_pv = tc::idesc_bf16_f32(kRows, kHalfLatent, false, true);
-      const uint64_t desc_k = tc::smem_desc(sbase, 16, 1024, tc::kSwizzle128B);
-      const uint64_t desc_r = tc::smem_desc(sbase + kRopeOff, 16, 512, kSwizzle64B);
-      const uint64_t desc_v = tc::smem_desc(sbase, kBlockBytes, 1024, tc::kSwizzle128B);
+      const uint64_t desc_q = tc::smem_desc(sbase, 16, 1024, tc::kSwizzle128B);
+      const uint64_t desc_s = tc::smem_desc(sbase + kOffScore, 16, 1024, tc::kSwizzle128B);
+      const uint64_t desc_k = tc::smem_desc(sbase + kOffValue, 16, 1024, tc::kSwizzle128B);
+      const uint64_t desc_v = tc::smem_desc(sbase + kOffValue, kBlockBytes, 1024, tc::kSwizzle128B);
       bool ok = true;
-      uint32_t tt = 0, stage = 0, phase = 0;  // tiles whose scores have been issued; the next one's place
-      uint32_t ps = 0;                        // the stage of the next value product
+      uint32_t tt = 0, sa = 0, sv = 0, phase = 0;  // tiles whose scores have been issued; the next one's places
+      uint32_t ps = 0;                             // the place of the next value product
       uint32_t seg = 0;
       Segment g;
       auto qk = [&]() {  // scores of the next tile
-        ok = wait_spin(&ctl.full[stage], phase, &ctl.abort, a.status);
+        ok = wait_spin(&ctl.full[sv], phase, &ctl.abort, a.status);
         if (ok && tt > 0) ok = wait_spin(&ctl.s_free, (tt - 1) & 1u, &ctl.abort, a.status);
         if (!ok) return;
         fence_proxy_async_smem();
         tc::fence_after_sync();
-        const uint32_t at = stage * (kStageBytes >> 4);
-        const uint64_t d = desc_k + at, dr = desc_r + at;
+        const uint64_t ds = desc_s + (uint32_t)(sa * (kScoreBytes >> 4)), dv = desc_k + (uint32_t)(sv * (kValueBytes >> 4));
+        const uint64_t half0 = rank == 0 ? dv : ds, half1 = rank == 0 ? ds : dv;  // latent channels 0..255, 256..511
         if (leader) {
 #pragma unroll
-          for (int k = 0; k < 16; ++k)
-            mma_bf16_ts(tmem + kColS, tmem + kColQ + 8 * k, d + (uint32_t)(((k >> 2) * kBlockBytes + (k & 3) * 32) >> 4),
-                        idesc_qk, k > 0);
-          mma_bf16_ts(tmem + kColS, tmem + kColQ + 128, dr, idesc_qk, 1u);
-          mma_bf16_ts(tmem + kColS, tmem + kColQ + 136, dr + 2, idesc_qk, 1u);
+          for (int k = 0; k < 32; ++k) {
+            const uint64_t d = (k < 16 ? half0 : half1) + (uint32_t)((((k >> 2) & 3) * kBlockBytes + (k & 3) * 32) >> 4);
+            if (k < kQSteps)
+              mma_bf16_ts(tmem + kColS, tmem + kColQ + 8 * k, d, idesc_qk, k > 0);
+            else
+              tc::mma_bf16_ss(tmem + kColS, desc_q + (uint32_t)((((k - kQSteps) >> 2) * kQBlock + (k & 3) * 32) >> 4), d,
+                              idesc_qk, 1u);
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            tc::mma_bf16_ss(tmem + kColS, desc_q + (uint32_t)((2 * kQBlock + k * 32) >> 4),
+                            ds + (uint32_t)((4 * kBlockBytes + k * 32) >> 4), idesc_qk, 1u);
+          tc::mma_commit(&ctl.empty_score[sa]);
           tc::mma_commit(&ctl.s_full);
           mbar_arrive(&ctl.s_full);
         }
         ++tt;
-        if (++stage == kStages) {
-          stage = 0;
+        if (++sa == kScoreStages) sa = 0;
+        if (++sv == kValueStages) {
+          sv = 0;
           phase ^= 1u;
         }
       };
@@ -500,15 +570,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ok = wait_spin(&ctl.p_full, u & 1u, &ctl.abort, a.status);
         if (!ok) return;
         tc::fence_after_sync();
-        const uint64_t d = desc_v + (uint32_t)(ps * (kStageBytes >> 4));
+        const uint64_t d = desc_v + (uint32_t)(ps * (kValueBytes >> 4));
         if (leader) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_bf16_ts(tmem + kColO, tmem + kColP + 8 * k, d + (uint32_t)(k * 2048 >> 4), idesc_pv, !(first && k == 0));
-          tc::mma_commit(&ctl.empty[ps]);
+          for (int k = 0; k < 4; ++k)  // own keys, then the other CTA's
+            mma_bf16_ts(tmem + kColO, tmem + kColP + 8 * k,
+                        d + (uint32_t)(((k >> 1) * 4 * kBlockBytes + (k & 1) * 2048) >> 4), idesc_pv, !(first && k == 0));
+          tc::mma_commit(&ctl.empty_value[ps]);
           tc::mma_commit(&ctl.pv_done);
         }
-        if (++ps == kStages) ps = 0;
+        if (++ps == kValueStages) ps = 0;
       };
       while (ok && next_segment(a, cur, g)) {
         if (g.nt == 0) continue;
@@ -516,12 +587,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tc::fence_after_sync();
         ++seg;
         const uint32_t first = tt;
-        // The scores run two tiles ahead of the values.
         if (ok) qk();
-        if (ok && g.nt > 1) qk();
 #pragma unroll 1
         for (int t = 0; t < g.nt && ok; ++t) {
-          if (t + 2 < g.nt) qk();
+          if (t + 1 < g.nt) qk();
           if (ok) pv(first + t, t == 0);
         }
       }
@@ -543,42 +612,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
     const uint64_t scale2 = pair(scale, scale);
     const uint32_t other = rank ^ 1u;
-    const uint32_t x_own = sbase + kOffX + half * 8 * kRows * 16 + r * 16;
-    const uint32_t x_peer = peer_addr(x_own, other);
-    const uint32_t bar_peer[2] = {peer_addr(smem_u32(&ctl.x_full[0]), other), peer_addr(smem_u32(&ctl.x_full[1]), other)};
-    uint32_t tt = 0, stage = 0;
+    const uint32_t x_own = sbase + kOffX + (2 * half * kRows + r) * 16, x_peer = peer_addr(x_own, other);
+    const uint32_t ref_peer = peer_addr(smem_u32(&ctl.x_ref[0][r]), other);
+    const uint32_t sum_peer = peer_addr(smem_u32(&ctl.x_sum[half][r]), other);
+    const uint32_t bar_peer = peer_addr(smem_u32(&ctl.x_full[0]), other);
+    const uint32_t l_bar_peer = peer_addr(smem_u32(&ctl.l_full), other);
+    uint32_t tt = 0, stage = 0, seg = 0;
     bool stop = false, fail = false;
     Segment g;
     while (!stop && next_segment(a, cur, g)) {
       const bool row_in = r < g.nrows;
-      if (rank == 0 && half == 0 && row_in && (g.tile0 == 0))
-        a.table[g.place + r] = make_int2((int)g.first_pair, g.pairs);
+      if (rank == 0 && half == 0 && row_in && g.tile0 == 0) a.table[g.place + r] = make_int2((int)g.first_pair, g.pairs);
       if (g.nt == 0) continue;
       const bool active = 32 * quad < g.nrows;  // this warp's quarter has rows at all
-      const int quads = (g.nrows + 31) / 32;
-      // ---- Q: this thread's half of the row's slice --------------------------------------
+      const uint32_t quads = (g.nrows + 31) / 32;
+      // ---- Q: channels 0..383 into tensor memory, the others into shared memory, half of each by this thread -------
       if (active) {
-        const __nv_bfloat16* qn = a.q_nope + (g.row0 + (row_in ? r : 0)) * kDLatent + rank * kHalfLatent + half * 128;
-        const __nv_bfloat16* qr = a.q_rope + (g.row0 + (row_in ? r : 0)) * kDRope + rank * kHalfRope + half * 16;
-        uint4 v[18];
+        const uint4* qn = reinterpret_cast<const uint4*>(a.q_nope + (g.row0 + (row_in ? r : 0)) * kDLatent);
+        const uint4* qr = reinterpret_cast<const uint4*>(a.q_rope + (g.row0 + (row_in ? r : 0)) * kDRope);
+        auto load = [&](const uint4* p) {
+          const uint4 x = __ldg(p);
+          return make_uint4(x.x ^ flip, x.y ^ flip, x.z ^ flip, x.w ^ flip);
+        };
+        uint4 v[24], y[12];
 #pragma unroll
-        for (int k = 0; k < 16; ++k) v[k] = __ldg(reinterpret_cast<const uint4*>(qn) + k);
-        v[16] = __ldg(reinterpret_cast<const uint4*>(qr));
-        v[17] = __ldg(reinterpret_cast<const uint4*>(qr) + 1);
-        if (flip) {
+        for (int k = 0; k < 24; ++k) v[k] = load(qn + 24 * half + k);
 #pragma unroll
-          for (int k = 0; k < 18; ++k) v[k] = make_uint4(v[k].x ^ flip, v[k].y ^ flip, v[k].z ^ flip, v[k].w ^ flip);
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < 6; ++k) {
           const uint32_t w[16] = {v[4 * k].x,     v[4 * k].y,     v[4 * k].z,     v[4 * k].w,
                                   v[4 * k + 1].x, v[4 * k + 1].y, v[4 * k + 1].z, v[4 * k + 1].w,
                                   v[4 * k + 2].x, v[4 * k + 2].y, v[4 * k + 2].z, v[4 * k + 2].w,
                                   v[4 * k + 3].x, v[4 * k + 3].y, v[4 * k + 3].z, v[4 * k + 3].w};
-          tmem_st16(t_lane + kColQ + half * 64 + 16 * k, w);
+          tmem_st16(t_lane + kColQ + 96 * half + 16 * k, w);
         }
-        const uint32_t w[8] = {v[16].x, v[16].y, v[16].z, v[16].w, v[17].x, v[17].y, v[17].z, v[17].w};
-        tmem_st8u(t_lane + kColQ + 128 + half * 8, w);
+#pragma unroll
+        for (int k = 0; k < 12; ++k) {
+          const int c = 12 * half + k;  // 16-byte piece of the 192 channels
+          y[k] = load(c < 16 ? qn + 48 + c : qr + c - 16);
+        }
+#pragma unroll
+        for (int k = 0; k < 12; ++k) {
+          const int c = 12 * half + k;
+          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(sbase + (c >> 3) * kQBlock + r * 128 +
+                                                                     (((c & 7) ^ (r & 7)) << 4)),
+                       "r"(y[k].x), "r"(y[k].y), "r"(y[k].z), "r"(y[k].w)
+                       : "memory");
+        }
+        fence_proxy_async_smem();
         tc::tmem_wait_st();
       }
       tc::fence_before_sync();
@@ -587,93 +667,55 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
       const int token = row_in ? (g.r0 + r) / a.H : 0;
       const int64_t mask_row = g.s.mask0 + (int64_t)token * g.s.keys;
-      float m = -INFINITY;                // running maximum, base 2
+      float m = -INFINITY, M = -INFINITY;  // the row's references: of this CTA's weights, of its half of O
       // of this thread's keys: sums of the weights as P has them, and before rounding (even and odd keys)
       uint64_t l_round = 0, l_full = 0;
-      // This CTA's part of the next tile's scores: read out of tensor memory and sent to the other CTA while the tile
-      // before it is at its softmax.
-      float n[32];
-      auto take = [&](uint32_t u) {  // tile u's part into n
-        if (tid == 0) tma::arrive_expect_tx(&ctl.x_full[u & 1], (uint32_t)quads * 2u * 32u * 128u);
-        const bool got = mbar_wait(&ctl.s_full, u & 1u, &ctl.abort, a.status);
+#pragma unroll 1
+      for (int t = 0; t < g.nt; ++t, ++tt) {
+        const uint32_t buf = tt & 1u;
+        if (tid == 0) tma::arrive_expect_tx(&ctl.x_full[buf], quads * (2 * 32 * 32 + 32 * 4));
+        // which of the 16 keys this row sees
+        uint32_t sees = 0xFFFFu;
+        if (g.s.own) {
+          sees = 0;
+          const int64_t key0 = (g.tile0 + t) * kKeys + kOwnKeys * rank + 16 * half;
+          const int64_t left = g.s.keys - key0 < 16 ? g.s.keys - key0 : 16;
+          if (row_in && left > 0) {
+            const int64_t bit = mask_row + key0;
+            const uint8_t* p = a.mask + (bit >> 3);
+            const int shift = (int)(bit & 7), bytes = (int)((shift + left + 7) >> 3);
+            uint32_t w = 0;
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+              if (i < bytes) w |= (uint32_t)__ldg(p + i) << (8 * i);
+            sees = (w >> shift) & 0xFFFFu;
+          }
+        }
+        // ---- this CTA's half of the scores, and their weights -----------------------------
+        bool got = mbar_wait(&ctl.s_full, buf, &ctl.abort, a.status);
         fail |= !__all_sync(0xffffffffu, got);
         tc::fence_after_sync();
+        float n[16];
         if (active) {
-          tmem_ld32(t_lane + kColS + 32 * half, n);
+          tmem_ld16(t_lane + kColS + 16 * half, n);
           tc::tmem_wait_ld();
         }
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl.s_free);
-      };
-      auto send = [&](uint32_t u, int c) {  // keys 4c .. 4c+3 of it
-        send16(x_peer + (u & 1) * kXBytes + c * kRows * 16, bar_peer[u & 1], n[4 * c], n[4 * c + 1], n[4 * c + 2],
-               n[4 * c + 3]);
-      };
-      take(tt);
-      if (active) {
-#pragma unroll
-        for (int c = 0; c < 8; ++c) send(tt, c);
-      }
-#pragma unroll 1
-      for (int t = 0; t < g.nt; ++t, ++tt) {
-        const int buf = (int)(tt & 1);
-        const bool more = t + 1 < g.nt;
-        // which of the 32 keys this row sees
-        uint32_t sees = 0xFFFFFFFFu;
-        if (g.s.own) {
-          sees = 0;
-          const int64_t key0 = (g.tile0 + t) * kKeys + 32 * half;
-          const int64_t left = g.s.keys - key0 < 32 ? g.s.keys - key0 : 32;
-          if (row_in && left > 0) {
-            const int64_t bit = mask_row + key0;
-            const uint8_t* p = a.mask + (bit >> 3);
-            const int shift = (int)(bit & 7), bytes = (int)((shift + left + 7) >> 3);
-            uint64_t w = 0;
-#pragma unroll
-            for (int i = 0; i < 5; ++i)
-              if (i < bytes) w |= (uint64_t)__ldg(p + i) << (8 * i);
-            sees = (uint32_t)(w >> shift);
-          }
-        }
-        sees &= (uint32_t)ctl.valid[stage][2 * half] | ((uint32_t)ctl.valid[stage][2 * half + 1] << 16);
-        if (++stage == kStages) stage = 0;
-        uint64_t s[16];
-        if (active) {
-          const bool got = mbar_wait(&ctl.x_full[buf], (tt >> 1) & 1u, &ctl.abort, a.status);
-          fail |= !__all_sync(0xffffffffu, got);
-          const uint32_t off = buf * kXBytes;
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            uint64_t x0, x1;
-            asm volatile("ld.shared.v2.b64 {%0,%1}, [%2];"
-                         : "=l"(x0), "=l"(x1)
-                         : "r"(x_own + off + c * kRows * 16)
-                         : "memory");
-            s[2 * c] = add2(pair(n[4 * c], n[4 * c + 1]), x0);
-            s[2 * c + 1] = add2(pair(n[4 * c + 2], n[4 * c + 3]), x1);
-          }
-        }
-        if (more) take(tt + 1);
+        sees &= *reinterpret_cast<const uint16_t*>(&ctl.valid[stage][2 * half]);
+        if (++stage == kValueStages) stage = 0;
         bool raise = false;
-        float top = -INFINITY, alpha = 1.f;
         if (active) {
-          if (sees != 0xFFFFFFFFu) {
+          if (sees != 0xFFFFu) {
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              float x, y;
-              unpair(s[k], x, y);
-              s[k] = pair((sees >> (2 * k)) & 1u ? x : -INFINITY, (sees >> (2 * k + 1)) & 1u ? y : -INFINITY);
-            }
+            for (int k = 0; k < 16; ++k) n[k] = (sees >> k) & 1u ? n[k] : -INFINITY;
           }
+          float top = n[0];
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            float x, y;
-            unpair(s[k], x, y);
-            top = fmaxf(top, fmaxf(x, y));
-          }
+          for (int k = 1; k < 16; ++k) top = fmaxf(top, n[k]);
           top *= scale;
-          raise = top > m + kHeadroom;  // (m = -inf: any key that is seen)
+          raise = top > m + kRowHeadroom;  // (m = -inf: any key that is seen)
           // The two warps of a quarter stay together: they leave the loop in the same place.
           raise = or_sync(1 + quad, raise || fail);
           if (raise) {
@@ -683,44 +725,62 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             top = fmaxf(top, ctl.red[half ^ 1][r]);
             fail |= ctl.failed[half ^ 1][quad] != 0;
             named_bar_sync(1 + quad, 64);  // (read before the next raise writes)
-            if (top > m + kHeadroom) {
-              alpha = m == -INFINITY ? 0.f : ex2_approx(m - top);
-              m = top;
+            if (top > m + kRowHeadroom) {
+              const float up = ceilf(top), alpha = ratio(m, up);
+              const uint64_t alpha2 = pair(alpha, alpha);
+              l_round = fma2(l_round, alpha2, 0);
+              l_full = fma2(l_full, alpha2, 0);
+              m = up;
             }
-            const uint64_t alpha2 = pair(alpha, alpha);
-            l_round = fma2(l_round, alpha2, 0);
-            l_full = fma2(l_full, alpha2, 0);
           }
         }
         if (fail) {
           stop = true;
           break;
         }
-        uint32_t w[16];
+        uint32_t w[8];
         if (active) {
           const float mu = m == -INFINITY ? 0.f : -m;
           const uint64_t mu2 = pair(mu, mu);
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
+          for (int k = 0; k < 8; ++k) {
             float p0, p1;
-            unpair(fma2(s[k], scale2, mu2), p0, p1);
+            unpair(fma2(pair(n[2 * k], n[2 * k + 1]), scale2, mu2), p0, p1);
             p0 = ex2_approx(p0);
             p1 = ex2_approx(p1);
             const __nv_bfloat162 h = __floats2bfloat162_rn(p0, p1);
             w[k] = *reinterpret_cast<const uint32_t*>(&h);
             l_full = add2(l_full, pair(p0, p1));
             l_round = add2(l_round, pair(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u)));
-            if (more && (k & 1)) send(tt + 1, k >> 1);  // (the way to the other CTA is narrow: spread over the exponentials)
           }
+          const uint32_t off = buf * kPBytes, bar = bar_peer + buf * 8;
+          send16(x_peer + off, bar, w[0], w[1], w[2], w[3]);
+          send16(x_peer + off + kRows * 16, bar, w[4], w[5], w[6], w[7]);
+          if (half == 0) send4(ref_peer + buf * kRows * 4, bar, m);
         }
-        // P(t) overwrites what PV(t-1) reads, and a rescaled O needs it complete.
+        // ---- both halves into P, which PV(t-1) reads until it is complete ------------------
         if (t > 0) {
-          const bool got = mbar_wait(&ctl.pv_done, (tt - 1) & 1u, &ctl.abort, a.status);
+          got = mbar_wait(&ctl.pv_done, (tt - 1) & 1u, &ctl.abort, a.status);
           fail |= !__all_sync(0xffffffffu, got);  // (left at the next meeting)
+          tc::fence_after_sync();
         }
-        tc::fence_after_sync();
         if (active) {
-          if (raise && t > 0) {
+          got = mbar_wait(&ctl.x_full[buf], (tt >> 1) & 1u, &ctl.abort, a.status);
+          fail |= !__all_sync(0xffffffffu, got);
+          uint32_t x[8];
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(x[4 * c]), "=r"(x[4 * c + 1]), "=r"(x[4 * c + 2]), "=r"(x[4 * c + 3])
+                         : "r"(x_own + buf * kPBytes + c * kRows * 16)
+                         : "memory");
+          const float mx = *reinterpret_cast<volatile float*>(&ctl.x_ref[buf][r]);
+          const float high = fmaxf(m, mx);
+          const bool lift = high > M + kOutHeadroom;  // (M = -inf: the first key that either CTA sees)
+          const float old = M;
+          if (lift) M = high;
+          if (t > 0 && __any_sync(0xffffffffu, lift && old != -INFINITY)) {
+            const float alpha = lift ? ratio(old, M) : 1.f;
 #pragma unroll 1
             for (int c = 0; c < 16; ++c) {
               float v[8];
@@ -731,7 +791,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               tc::tmem_st8(t_lane + kColO + half * 128 + 8 * c, v);
             }
           }
-          tmem_st16(t_lane + kColP + 16 * half, w);
+          if (__any_sync(0xffffffffu, m != M || mx != M)) {
+            const uint32_t f = __float_as_uint(ratio(m, M)) >> 16, fx = __float_as_uint(ratio(mx, M)) >> 16;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              w[k] = scale_bf16x2(w[k], f | f << 16);
+              x[k] = scale_bf16x2(x[k], fx | fx << 16);
+            }
+          }
+          tmem_st8u(t_lane + kColP + 8 * half, w);
+          tmem_st8u(t_lane + kColP + 16 + 8 * half, x);
           tc::tmem_wait_st();
         }
         tc::fence_before_sync();
@@ -740,31 +809,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       if (stop) break;
       // ---- the row group's partial -----------------------------------------------------
-      const bool got = mbar_wait(&ctl.pv_done, (tt - 1) & 1u, &ctl.abort, a.status);
+      if (tid == 0) tma::arrive_expect_tx(&ctl.l_full, quads * 2 * 32 * 16);
+      float lr = 0.f, lf = 0.f;
+      if (active) {
+        float even, odd;
+        unpair(l_round, even, odd);
+        lr = even + odd;
+        unpair(l_full, even, odd);
+        lf = even + odd;
+        send16(sum_peer, l_bar_peer, __float_as_uint(m), __float_as_uint(lr), __float_as_uint(lf), 0u);
+        ctl.red[half][r] = lr;
+        ctl.red2[half][r] = lf;
+      }
+      bool got = mbar_wait(&ctl.pv_done, (tt - 1) & 1u, &ctl.abort, a.status);
+      if (active) got = got && mbar_wait(&ctl.l_full, seg & 1u, &ctl.abort, a.status);
+      ++seg;
       fail |= !__all_sync(0xffffffffu, got);
       stop = active ? or_sync(1 + quad, fail) : fail;
       if (stop) break;
       tc::fence_after_sync();
       if (active) {
-        float even, odd;
-        unpair(l_round, even, odd);
-        ctl.red[half][r] = even + odd;
-        unpair(l_full, even, odd);
-        ctl.red2[half][r] = even + odd;
-        named_bar_sync(1 + quad, 64);
-        const float lr = ctl.red[0][r] + ctl.red[1][r], lf = ctl.red2[0][r] + ctl.red2[1][r];
+        const float4 x0 = ctl.x_sum[0][r], x1 = ctl.x_sum[1][r];
+        const float f = ratio(m, M), fx = ratio(x0.x, M);
+        lr = (ctl.red[0][r] + ctl.red[1][r]) * f + (x0.y + x1.y) * fx;
+        lf = (ctl.red2[0][r] + ctl.red2[1][r]) * f + (x0.z + x1.z) * fx;
         named_bar_sync(1 + quad, 64);
         const int64_t at = g.place + (int64_t)kRows * cur.pair + r;
-        const float inv = lr > 0.f ? 1.f / lr : 0.f;
+        const bool seen = !(lr <= 0.f);  // (a NaN is passed on)
+        const float inv = 1.f / lr;
         if (rank == 0 && half == 0 && row_in)
-          a.part_lse[at] = lr > 0.f ? (m + __log2f(lf)) * 0.69314718055994530942f : -INFINITY;
+          a.part_lse[at] = seen ? (M + __log2f(lf)) * 0.69314718055994530942f : -INFINITY;
         float* out = a.part_o + at * kDLatent + rank * kHalfLatent + half * 128;
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           float v[32];
           tmem_ld32(t_lane + kColO + half * 128 + 32 * c, v);
           tc::tmem_wait_ld();
-          if (row_in && lr > 0.f) {
+          if (row_in && seen) {
 #pragma unroll
             for (int k = 0; k < 32; k += 8)
               asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(out + 32 * c + k),
