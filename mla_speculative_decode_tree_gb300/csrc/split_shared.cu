@@ -421,19 +421,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp >= kGatherWarp) {
     fewer_registers<kRegsGather>();
     // ============================ gather ================================================
-    // Warp gw fills eight keys of each half of a tile: of this CTA's half whole rows (two instructions of 32 lanes x 16
-    // bytes per key for the latent, one for the RoPE bytes of four keys), of the other's this CTA's half of the latent.
-    // A tile's rows are asked into L2 two tiles ahead: what a row costs beside that -- DRAM, the page's translation --
-    // is then off the path.
+    // Warp gw fills eight keys of each half of a tile: of this CTA's half whole rows, of the other's this CTA's half of
+    // the latent.  An instruction copies 128 bytes of four keys, a lane 16 bytes of key lane/8 or lane/8 + 4; a row's
+    // pieces then differ by constants.
     const int gw = warp - kGatherWarp;
     uint32_t bad = 0;
     uint32_t tt = 0, sa = 0, pa = 1, sv = 0, pvp = 1;  // tiles so far; places in the two rings and their parities
     bool stop = false;
     Segment g;
-    const int blk = lane >> 3, chunk = lane & 7;
-    const int theirs = (lane >> 3) & 1;  // lanes 0..7 hold the rows of own keys, 8..15 of the other CTA's (16..31 again)
-    const int key_in = kOwnKeys * (theirs ? 1 - (int)rank : (int)rank) + gw * kKeysPerWarp + (lane & 7);
-    const __nv_bfloat16* const latent = a.kv_pool + lane * 8;
+    const int sub = lane >> 3, chunk = lane & 7;
+    const int theirs = sub & 1;  // lanes 0..7 hold the rows of own keys, 8..15 of the other CTA's (16..31 again)
+    const int key_in = kOwnKeys * (theirs ? 1 - (int)rank : (int)rank) + gw * kKeysPerWarp + chunk;
+    // (keys sub and sub + 4 of the warp's eight: rows 128 bytes, the swizzle takes the key's last three bits)
+    const uint32_t to = (gw * kKeysPerWarp + sub) * 128, to_a = to + ((chunk ^ sub) << 4),
+                   to_b = to + 512 + ((chunk ^ (sub + 4)) << 4);
     while (!stop && next_segment(a, cur, g)) {
       const int32_t* index = g.s.own ? a.kv_indices : a.shared_indices;
       const int64_t key0 = g.tile0 * kKeys + key_in;
@@ -442,31 +443,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (t >= g.nt || j >= g.s.keys) return -1;  // no such key
         return j < g.s.prefix ? __ldg(index + g.s.kv0 + j) : __ldg(a.out_cache_loc + g.s.q0 + (j - g.s.prefix));
       };
-      auto ask = [&](int32_t id) {  // nine lines of an own key's row, four of another's
-        const int32_t mine = __shfl_sync(0xffffffffu, id, lane & 7), other = __shfl_sync(0xffffffffu, id, 8 + (lane & 7));
-        if (mine >= 0 && mine < a.pool_rows) {
-          const char* row = reinterpret_cast<const char*>(a.kv_pool + (int64_t)mine * kDRow);
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(row + blk * 128));
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(row + blk * 128 + 512));
-          if (blk == 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + 1024));
-        }
-        if (other >= 0 && other < a.pool_rows)
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char*>(a.kv_pool + (int64_t)other * kDRow) +
-                                                        rank * 512 + blk * 128));
-      };
-      int32_t id0 = load_id(0), id1 = load_id(1), id2 = load_id(2);
-      ask(id1);
+      int32_t id0 = load_id(0), id1 = load_id(1);
 #pragma unroll 1
       for (int t = 0; t < g.nt; ++t, ++tt) {
         int32_t row = id0;
         id0 = id1;
-        id1 = id2;
-        id2 = load_id(t + 3);
-        ask(id1);
+        id1 = load_id(t + 2);
         const bool ok = row >= 0 && row < a.pool_rows;
         if (!ok && key0 + (int64_t)t * kKeys < g.s.keys) bad = 1;
         row = ok ? row : -1;
         const uint32_t valid = __ballot_sync(0xffffffffu, ok) & 0xFFu;
+        const __nv_bfloat16* src[4];  // own keys sub, sub + 4; the other CTA's
+        uint32_t n[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int32_t r = __shfl_sync(0xffffffffu, row, 4 * k + sub);
+          n[k] = r < 0 ? 0u : 16u;
+          src[k] = a.kv_pool + (int64_t)(r < 0 ? 0 : r) * kDRow + chunk * 8 + (k >= 2 ? rank * kHalfLatent : 0);
+        }
         bool got = mbar_wait(&ctl.empty_score[sa], pa, &ctl.abort, a.status);
         got = got && mbar_wait(&ctl.empty_value[sv], pvp, &ctl.abort, a.status);
         if (!__all_sync(0xffffffffu, got)) {
@@ -476,29 +470,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (!(a.test_stall && tt == 0)) {  // test only: the first tile never lands
           if (lane == 0) ctl.valid[sv][gw] = (uint8_t)valid;
           const uint32_t score = sbase + kOffScore + sa * kScoreBytes, value = sbase + kOffValue + sv * kValueBytes;
-          const uint32_t half0 = rank == 0 ? value : score, half1 = rank == 0 ? score : value;
+          const uint32_t half[2] = {rank == 0 ? value : score, rank == 0 ? score : value};
 #pragma unroll
-          for (int k = 0; k < kKeysPerWarp; ++k) {
-            const int key = gw * kKeysPerWarp + k;
-            const int32_t r = __shfl_sync(0xffffffffu, row, k);
-            const uint32_t at = blk * kBlockBytes + key * 128 + ((chunk ^ (key & 7)) << 4), n = r < 0 ? 0u : 16u;
-            const __nv_bfloat16* src = latent + (int64_t)(r < 0 ? 0 : r) * kDRow;
-            cp_async16(half0 + at, src, n);
-            cp_async16(half1 + at, src + kHalfLatent, n);
+          for (int blk = 0; blk < 8; ++blk) {
+            const uint32_t dst = half[blk >> 2] + (blk & 3) * kBlockBytes;
+            cp_async16(dst + to_a, src[0] + 64 * blk, n[0]);
+            cp_async16(dst + to_b, src[1] + 64 * blk, n[1]);
           }
+          cp_async16(score + 4 * kBlockBytes + to_a, src[0] + kDLatent, n[0]);
+          cp_async16(score + 4 * kBlockBytes + to_b, src[1] + kDLatent, n[1]);
 #pragma unroll
-          for (int k = 0; k < kKeysPerWarp; k += 4) {
-            const int key = gw * kKeysPerWarp + k + blk;
-            const int32_t r = __shfl_sync(0xffffffffu, row, k + blk);
-            cp_async16(score + 4 * kBlockBytes + key * 128 + ((chunk ^ (key & 7)) << 4),
-                       a.kv_pool + (int64_t)(r < 0 ? 0 : r) * kDRow + kDLatent + chunk * 8, r < 0 ? 0u : 16u);
-          }
-#pragma unroll
-          for (int k = 0; k < kKeysPerWarp; ++k) {
-            const int key = gw * kKeysPerWarp + k;
-            const int32_t r = __shfl_sync(0xffffffffu, row, 8 + k);
-            cp_async16(value + 4 * kBlockBytes + blk * kBlockBytes + key * 128 + ((chunk ^ (key & 7)) << 4),
-                       latent + (int64_t)(r < 0 ? 0 : r) * kDRow + rank * kHalfLatent, r < 0 ? 0u : 16u);
+          for (int blk = 0; blk < 4; ++blk) {
+            const uint32_t dst = value + (4 + blk) * kBlockBytes;
+            cp_async16(dst + to_a, src[2] + 64 * blk, n[2]);
+            cp_async16(dst + to_b, src[3] + 64 * blk, n[3]);
           }
           cp_async_arrive(&ctl.full[sv]);
           if (lane == 0) mbar_arrive(&ctl.full[sv]);
