@@ -61,17 +61,20 @@ constexpr int kHalfLatent = kDLatent / 2;
 constexpr int kBlockBytes = kOwnKeys * 128;     // 64 columns of 32 keys
 constexpr int kQBlock = kRows * 128;            // 64 columns of Q
 constexpr int kQSteps = 24;                     // k-steps of 16 channels with Q in tensor memory (6 blocks)
-constexpr int kScoreStages = 2, kScoreBytes = 5 * kBlockBytes;  // the other half of the latent, RoPE
-constexpr int kValueStages = 3, kValueBytes = 8 * kBlockBytes;  // own half: own keys, then the other CTA's
+// Rings.  Of this CTA's keys: the half of the latent that only the scores read, with the RoPE columns, and the half
+// that the values need too; of the other CTA's keys the latter half.
+constexpr int kScoreStages = 2, kScoreBytes = 5 * kBlockBytes;
+constexpr int kOwnStages = 4, kOtherStages = 2, kValueBytes = 4 * kBlockBytes;
 constexpr int kPBytes = kRows * kOwnKeys * 2;   // the other CTA's P
 constexpr int kSoftmaxWarps = 8;
 constexpr int kMmaWarp = kSoftmaxWarps;
-constexpr int kGatherWarp = kMmaWarp + 4, kGatherWarps = 4;  // (a warpgroup each: registers go by warpgroup)
+constexpr int kOtherWarp = kMmaWarp + 1, kOtherWarps = 2;    // gather the other CTA's keys
+constexpr int kGatherWarp = kMmaWarp + 4, kGatherWarps = 4;  // gather own keys (a warpgroup of their own: registers)
 constexpr int kThreads = 32 * (kGatherWarp + kGatherWarps);
 // Registers per thread by warpgroup; together at most the 4 x 128 of the launch.
 constexpr int kRegsSoftmax = 184, kRegsMma = 56, kRegsGather = 80;
 static_assert(kThreads == 512 && 2 * kRegsSoftmax + kRegsMma + kRegsGather <= 512, "register shares");
-constexpr int kKeysPerWarp = kOwnKeys / kGatherWarps;  // of either half, gathered by a warp
+constexpr int kKeysPerWarp = kOwnKeys / kGatherWarps;  // own keys gathered by a warp
 constexpr int kColO = 0, kColQ = 256, kColS = 448, kColP = 480;
 // Base 2, before a reference is raised.  Weights and O are floating numbers, so a
 // reference far below the maximum costs no precision; what it must not do is overflow.
@@ -82,11 +85,12 @@ constexpr int kMaxSpans = 2 * kMaxSharedBatch;
 constexpr int64_t kAxisEnd = 0xFFFFFFFF;  // (2^32 tiles would take half a day)
 
 struct Ctl {
-  uint64_t full[kValueStages], empty_score[kScoreStages], empty_value[kValueStages];
+  uint64_t full[kOwnStages], empty_own[kOwnStages], empty_score[kScoreStages];
+  uint64_t full_other[kOtherStages], empty_other[kOtherStages];
   uint64_t q_full, s_full, s_free, p_full, pv_done, x_full[2], l_full, mma_idle;
   uint32_t tmem_base;
   int abort;
-  alignas(4) uint8_t valid[kValueStages][kGatherWarps];  // own keys of a tile that exist, 8 bits per gather warp
+  alignas(4) uint8_t valid[kOwnStages][kGatherWarps];  // own keys of a tile that exist, 8 bits per gather warp
   int failed[2][4];     // softmax warps that gave up, by half of the keys and quarter of the rows
   float red[2][kRows];  // per half of the keys: row maxima, sums
   float red2[2][kRows];
@@ -96,8 +100,9 @@ struct Ctl {
 };
 
 constexpr int kOffScore = 3 * kQBlock;
-constexpr int kOffValue = kOffScore + kScoreStages * kScoreBytes;
-constexpr int kOffX = kOffValue + kValueStages * kValueBytes;
+constexpr int kOffOwn = kOffScore + kScoreStages * kScoreBytes;
+constexpr int kOffOther = kOffOwn + kOwnStages * kValueBytes;
+constexpr int kOffX = kOffOther + kOtherStages * kValueBytes;
 constexpr int kOffCtl = kOffX + 2 * kPBytes;
 constexpr int kOffEnds = (kOffCtl + (int)sizeof(Ctl) + 15) / 16 * 16;
 constexpr int kSmem = kOffEnds + 1024;  // + the axis (4 bytes per group and request) + alignment slack
@@ -160,6 +165,12 @@ __device__ __forceinline__ bool wait_spin(uint64_t* bar, uint32_t parity, volati
   for (int it = 0; it < 64; ++it)
     if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
   return __all_sync(0xffffffffu, mbar_wait_spin(bar, parity, abort, status));
+}
+
+// mbar_wait by a whole warp: one test where the phase is over already, as it mostly is.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* status) {
+  if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status));
 }
 
 // ---- the other CTA of the pair -------------------------------------------------
@@ -307,6 +318,14 @@ struct Segment {
   int pairs;  // that have a partial of it
 };
 
+// Row id of key `key` + tiles of the segment; -1 where there is no such key.
+__device__ __forceinline__ int32_t load_id(const SharedArgs& a, const Segment& g, int64_t key, int t) {
+  const int64_t j = key + (int64_t)t * kKeys;
+  if (t >= g.nt || j >= g.s.keys) return -1;
+  return j < g.s.prefix ? __ldg((g.s.own ? a.kv_indices : a.shared_indices) + g.s.kv0 + j)
+                        : __ldg(a.out_cache_loc + g.s.q0 + (j - g.s.prefix));
+}
+
 // The next row group and run of tiles of the pair; false at the end of its piece.
 __device__ __forceinline__ bool next_segment(const SharedArgs& a, Cursor& c, Segment& g) {
   while (c.x < c.x_end) {
@@ -350,9 +369,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   // ---- set-up: barriers, tensor memory, the axis ------------------------------------
   if (tid == 0) {
-    for (int k = 0; k < kValueStages; ++k) {
+    for (int k = 0; k < kOwnStages; ++k) {
       mbar_init(&ctl.full[k], kGatherWarps * 33);  // every lane's copies and, per warp, its valid bits
-      mbar_init(&ctl.empty_value[k], 1);
+      mbar_init(&ctl.empty_own[k], 1);
+    }
+    for (int k = 0; k < kOtherStages; ++k) {
+      mbar_init(&ctl.full_other[k], kOtherWarps * 32);
+      mbar_init(&ctl.empty_other[k], 1);
     }
     for (int k = 0; k < kScoreStages; ++k) mbar_init(&ctl.empty_score[k], 1);
     mbar_init(&ctl.q_full, kSoftmaxWarps);
@@ -421,55 +444,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp >= kGatherWarp) {
     fewer_registers<kRegsGather>();
     // ============================ gather ================================================
-    // Warp gw fills eight keys of each half of a tile: of this CTA's half whole rows, of the other's this CTA's half of
-    // the latent.  An instruction copies 128 bytes of four keys, a lane 16 bytes of key lane/8 or lane/8 + 4; a row's
-    // pieces then differ by constants.
+    // Own keys: warp gw fills eight of the 32.  An instruction copies 128 bytes of four keys, a lane 16 bytes of key
+    // lane/8 or lane/8 + 4; a row's pieces then differ by constants.
     const int gw = warp - kGatherWarp;
     uint32_t bad = 0;
-    uint32_t tt = 0, sa = 0, pa = 1, sv = 0, pvp = 1;  // tiles so far; places in the two rings and their parities
+    uint32_t tt = 0, sa = 0, pa = 1, so = 0, po = 1;  // tiles so far; places in the two rings and their parities
     bool stop = false;
     Segment g;
     const int sub = lane >> 3, chunk = lane & 7;
-    const int theirs = sub & 1;  // lanes 0..7 hold the rows of own keys, 8..15 of the other CTA's (16..31 again)
-    const int key_in = kOwnKeys * (theirs ? 1 - (int)rank : (int)rank) + gw * kKeysPerWarp + chunk;
-    // (keys sub and sub + 4 of the warp's eight: rows 128 bytes, the swizzle takes the key's last three bits)
+    // (the swizzle takes the key's last three bits: those of keys sub and sub + 4 of the eight)
     const uint32_t to = (gw * kKeysPerWarp + sub) * 128, to_a = to + ((chunk ^ sub) << 4),
                    to_b = to + 512 + ((chunk ^ (sub + 4)) << 4);
     while (!stop && next_segment(a, cur, g)) {
-      const int32_t* index = g.s.own ? a.kv_indices : a.shared_indices;
-      const int64_t key0 = g.tile0 * kKeys + key_in;
-      auto load_id = [&](int t) -> int32_t {  // of this lane's key of tile t
-        const int64_t j = key0 + (int64_t)t * kKeys;
-        if (t >= g.nt || j >= g.s.keys) return -1;  // no such key
-        return j < g.s.prefix ? __ldg(index + g.s.kv0 + j) : __ldg(a.out_cache_loc + g.s.q0 + (j - g.s.prefix));
-      };
-      int32_t id0 = load_id(0), id1 = load_id(1);
+      const int64_t key0 = g.tile0 * kKeys + kOwnKeys * rank + gw * kKeysPerWarp + chunk;  // (the lanes hold them four times)
+      int32_t id0 = load_id(a, g, key0, 0), id1 = load_id(a, g, key0, 1);
 #pragma unroll 1
       for (int t = 0; t < g.nt; ++t, ++tt) {
         int32_t row = id0;
         id0 = id1;
-        id1 = load_id(t + 2);
+        id1 = load_id(a, g, key0, t + 2);
         const bool ok = row >= 0 && row < a.pool_rows;
         if (!ok && key0 + (int64_t)t * kKeys < g.s.keys) bad = 1;
         row = ok ? row : -1;
         const uint32_t valid = __ballot_sync(0xffffffffu, ok) & 0xFFu;
-        const __nv_bfloat16* src[4];  // own keys sub, sub + 4; the other CTA's
-        uint32_t n[4];
+        const __nv_bfloat16* src[2];
+        uint32_t n[2];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < 2; ++k) {
           const int32_t r = __shfl_sync(0xffffffffu, row, 4 * k + sub);
           n[k] = r < 0 ? 0u : 16u;
-          src[k] = a.kv_pool + (int64_t)(r < 0 ? 0 : r) * kDRow + chunk * 8 + (k >= 2 ? rank * kHalfLatent : 0);
+          src[k] = a.kv_pool + (int64_t)(r < 0 ? 0 : r) * kDRow + chunk * 8;
         }
-        bool got = mbar_wait(&ctl.empty_score[sa], pa, &ctl.abort, a.status);
-        got = got && mbar_wait(&ctl.empty_value[sv], pvp, &ctl.abort, a.status);
-        if (!__all_sync(0xffffffffu, got)) {
+        if (!wait_warp(&ctl.empty_score[sa], pa, &ctl.abort, a.status) ||
+            !wait_warp(&ctl.empty_own[so], po, &ctl.abort, a.status)) {
           stop = true;
           break;
         }
         if (!(a.test_stall && tt == 0)) {  // test only: the first tile never lands
-          if (lane == 0) ctl.valid[sv][gw] = (uint8_t)valid;
-          const uint32_t score = sbase + kOffScore + sa * kScoreBytes, value = sbase + kOffValue + sv * kValueBytes;
+          if (lane == 0) ctl.valid[so][gw] = (uint8_t)valid;
+          const uint32_t score = sbase + kOffScore + sa * kScoreBytes, value = sbase + kOffOwn + so * kValueBytes;
           const uint32_t half[2] = {rank == 0 ? value : score, rank == 0 ? score : value};
 #pragma unroll
           for (int blk = 0; blk < 8; ++blk) {
@@ -479,22 +492,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           cp_async16(score + 4 * kBlockBytes + to_a, src[0] + kDLatent, n[0]);
           cp_async16(score + 4 * kBlockBytes + to_b, src[1] + kDLatent, n[1]);
-#pragma unroll
-          for (int blk = 0; blk < 4; ++blk) {
-            const uint32_t dst = value + (4 + blk) * kBlockBytes;
-            cp_async16(dst + to_a, src[2] + 64 * blk, n[2]);
-            cp_async16(dst + to_b, src[3] + 64 * blk, n[3]);
-          }
-          cp_async_arrive(&ctl.full[sv]);
-          if (lane == 0) mbar_arrive(&ctl.full[sv]);
+          cp_async_arrive(&ctl.full[so]);
+          if (lane == 0) mbar_arrive(&ctl.full[so]);
         }
         if (++sa == kScoreStages) {
           sa = 0;
           pa ^= 1u;
         }
-        if (++sv == kValueStages) {
-          sv = 0;
-          pvp ^= 1u;
+        if (++so == kOwnStages) {
+          so = 0;
+          po ^= 1u;
         }
       }
     }
@@ -511,20 +518,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       constexpr uint32_t idesc_pv = tc::idesc_bf16_f32(kRows, kHalfLatent, false, true);
       const uint64_t desc_q = tc::smem_desc(sbase, 16, 1024, tc::kSwizzle128B);
       const uint64_t desc_s = tc::smem_desc(sbase + kOffScore, 16, 1024, tc::kSwizzle128B);
-      const uint64_t desc_k = tc::smem_desc(sbase + kOffValue, 16, 1024, tc::kSwizzle128B);
-      const uint64_t desc_v = tc::smem_desc(sbase + kOffValue, kBlockBytes, 1024, tc::kSwizzle128B);
+      const uint64_t desc_k = tc::smem_desc(sbase + kOffOwn, 16, 1024, tc::kSwizzle128B);
+      const uint64_t desc_v = tc::smem_desc(sbase + kOffOwn, kBlockBytes, 1024, tc::kSwizzle128B);
+      const uint64_t desc_x = tc::smem_desc(sbase + kOffOther, kBlockBytes, 1024, tc::kSwizzle128B);
       bool ok = true;
-      uint32_t tt = 0, sa = 0, sv = 0, phase = 0;  // tiles whose scores have been issued; the next one's places
-      uint32_t ps = 0;                             // the place of the next value product
+      uint32_t nq = 0, np = 0;  // tiles whose scores, whose values have been issued
       uint32_t seg = 0;
       Segment g;
-      auto qk = [&]() {  // scores of the next tile
-        ok = wait_spin(&ctl.full[sv], phase, &ctl.abort, a.status);
-        if (ok && tt > 0) ok = wait_spin(&ctl.s_free, (tt - 1) & 1u, &ctl.abort, a.status);
-        if (!ok) return;
+      auto qk = [&]() {  // scores of tile nq, which has landed
         fence_proxy_async_smem();
         tc::fence_after_sync();
-        const uint64_t ds = desc_s + (uint32_t)(sa * (kScoreBytes >> 4)), dv = desc_k + (uint32_t)(sv * (kValueBytes >> 4));
+        const uint64_t ds = desc_s + (nq % kScoreStages) * (uint32_t)(kScoreBytes >> 4),
+                       dv = desc_k + (nq % kOwnStages) * (uint32_t)(kValueBytes >> 4);
         const uint64_t half0 = rank == 0 ? dv : ds, half1 = rank == 0 ? ds : dv;  // latent channels 0..255, 256..511
         if (leader) {
 #pragma unroll
@@ -540,43 +545,58 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int k = 0; k < 4; ++k)
             tc::mma_bf16_ss(tmem + kColS, desc_q + (uint32_t)((2 * kQBlock + k * 32) >> 4),
                             ds + (uint32_t)((4 * kBlockBytes + k * 32) >> 4), idesc_qk, 1u);
-          tc::mma_commit(&ctl.empty_score[sa]);
+          tc::mma_commit(&ctl.empty_score[nq % kScoreStages]);
           tc::mma_commit(&ctl.s_full);
           mbar_arrive(&ctl.s_full);
         }
-        ++tt;
-        if (++sa == kScoreStages) sa = 0;
-        if (++sv == kValueStages) {
-          sv = 0;
-          phase ^= 1u;
-        }
+        ++nq;
       };
-      auto pv = [&](uint32_t u, bool first) {  // O += P V of tile u
-        ok = wait_spin(&ctl.p_full, u & 1u, &ctl.abort, a.status);
-        if (!ok) return;
+      auto pv = [&](bool first) {  // O += P V of tile np
+        fence_proxy_async_smem();
         tc::fence_after_sync();
-        const uint64_t d = desc_v + (uint32_t)(ps * (kValueBytes >> 4));
+        const uint64_t dv = desc_v + (np % kOwnStages) * (uint32_t)(kValueBytes >> 4),
+                       dx = desc_x + (np % kOtherStages) * (uint32_t)(kValueBytes >> 4);
         if (leader) {
 #pragma unroll
           for (int k = 0; k < 4; ++k)  // own keys, then the other CTA's
-            mma_bf16_ts(tmem + kColO, tmem + kColP + 8 * k,
-                        d + (uint32_t)(((k >> 1) * 4 * kBlockBytes + (k & 1) * 2048) >> 4), idesc_pv, !(first && k == 0));
-          tc::mma_commit(&ctl.empty_value[ps]);
+            mma_bf16_ts(tmem + kColO, tmem + kColP + 8 * k, (k < 2 ? dv : dx) + (uint32_t)((k & 1) * 2048 >> 4), idesc_pv,
+                        !(first && k == 0));
+          tc::mma_commit(&ctl.empty_own[np % kOwnStages]);
+          tc::mma_commit(&ctl.empty_other[np % kOtherStages]);
           tc::mma_commit(&ctl.pv_done);
         }
-        if (++ps == kValueStages) ps = 0;
+        ++np;
       };
       while (ok && next_segment(a, cur, g)) {
         if (g.nt == 0) continue;
         ok = wait_spin(&ctl.q_full, seg & 1u, &ctl.abort, a.status);
         tc::fence_after_sync();
         ++seg;
-        const uint32_t first = tt;
-        if (ok) qk();
-#pragma unroll 1
-        for (int t = 0; t < g.nt && ok; ++t) {
-          if (t + 1 < g.nt) qk();
-          if (ok) pv(first + t, t == 0);
+        const uint32_t first = np, end = np + g.nt;
+        // What is ready goes first: a tile's values, or the scores of one of the next.
+        uint64_t since = 0;
+        for (uint32_t idle = 0; ok && np != end;) {
+          if (np != nq &&
+              __all_sync(0xffffffffu, mbar_test_wait(&ctl.p_full, np & 1u) &&
+                                          mbar_test_wait(&ctl.full_other[np % kOtherStages], np / kOtherStages & 1u))) {
+            pv(np == first);
+            idle = 0;
+          } else if (nq != end && __all_sync(0xffffffffu, mbar_test_wait(&ctl.full[nq % kOwnStages], nq / kOwnStages & 1u) &&
+                                                              (nq == 0 || mbar_test_wait(&ctl.s_free, (nq - 1) & 1u)))) {
+            qk();
+            idle = 0;
+          } else if ((++idle & 255u) == 0) {
+            const uint64_t now = __shfl_sync(0xffffffffu, global_timer_ns(), 0);
+            if (idle == 256) since = now;
+            if (now - since > kWaitLimitNs || idle > (1u << 30)) {
+              if (leader) {
+                ctl.abort = 1;
+                atomicOr(a.status, kStatusTimeout);
+              }
+              ok = false;
+            }
+            if (__any_sync(0xffffffffu, *(volatile int*)&ctl.abort)) ok = false;
+          }
         }
       }
       // Drain: every MMA of this warp has completed before tensor memory is freed.
@@ -585,6 +605,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (uint32_t it = 0; it < (1u << 30); ++it)
         if (mbar_try_wait(&ctl.mma_idle, 0) || ((it & 63u) == 63u && global_timer_ns() - t0 > kWaitLimitNs)) break;
       __syncwarp();
+    } else if (warp < kOtherWarp + kOtherWarps) {
+      // ==================== gather: the other CTA's keys, this CTA's half of the latent ====================
+      // A warp fills 16 keys: 128 bytes of four per instruction.
+      const int gw = warp - kOtherWarp, sub = lane >> 3, chunk = lane & 7;
+      uint32_t so = 0, po = 1;
+      bool stop = false;
+      Segment g;
+      const uint32_t to = (16 * gw + sub) * 128, to_a = to + ((chunk ^ sub) << 4), to_b = to + ((chunk ^ (sub + 4)) << 4);
+      while (!stop && next_segment(a, cur, g)) {
+        const int64_t key0 = g.tile0 * kKeys + kOwnKeys * (rank ^ 1u) + 16 * gw + (lane & 15);
+        int32_t id0 = load_id(a, g, key0, 0), id1 = load_id(a, g, key0, 1);
+#pragma unroll 1
+        for (int t = 0; t < g.nt; ++t) {
+          const int32_t row = id0 >= 0 && id0 < a.pool_rows ? id0 : -1;  // (the CTA that they belong to reports bad ones)
+          id0 = id1;
+          id1 = load_id(a, g, key0, t + 2);
+          if (!wait_warp(&ctl.empty_other[so], po, &ctl.abort, a.status)) {
+            stop = true;
+            break;
+          }
+          const uint32_t value = sbase + kOffOther + so * kValueBytes;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int32_t r = __shfl_sync(0xffffffffu, row, 4 * k + sub);
+            const __nv_bfloat16* src = a.kv_pool + (int64_t)(r < 0 ? 0 : r) * kDRow + rank * kHalfLatent + chunk * 8;
+#pragma unroll
+            for (int blk = 0; blk < 4; ++blk)
+              cp_async16(value + blk * kBlockBytes + 512 * k + (k & 1 ? to_b : to_a), src + 64 * blk, r < 0 ? 0u : 16u);
+          }
+          cp_async_arrive(&ctl.full_other[so]);
+          if (++so == kOtherStages) {
+            so = 0;
+            po ^= 1u;
+          }
+        }
+      }
+      cp_async_wait_all();
     }
   } else {
     more_registers<kRegsSoftmax>();
@@ -677,8 +734,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
         // ---- this CTA's half of the scores, and their weights -----------------------------
-        bool got = mbar_wait(&ctl.s_full, buf, &ctl.abort, a.status);
-        fail |= !__all_sync(0xffffffffu, got);
+        fail |= !wait_warp(&ctl.s_full, buf, &ctl.abort, a.status);
         tc::fence_after_sync();
         float n[16];
         if (active) {
@@ -689,7 +745,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl.s_free);
         sees &= *reinterpret_cast<const uint16_t*>(&ctl.valid[stage][2 * half]);
-        if (++stage == kValueStages) stage = 0;
+        if (++stage == kOwnStages) stage = 0;
         bool raise = false;
         if (active) {
           if (sees != 0xFFFFu) {
@@ -745,13 +801,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         // ---- both halves into P, which PV(t-1) reads until it is complete ------------------
         if (t > 0) {
-          got = mbar_wait(&ctl.pv_done, (tt - 1) & 1u, &ctl.abort, a.status);
-          fail |= !__all_sync(0xffffffffu, got);  // (left at the next meeting)
+          fail |= !wait_warp(&ctl.pv_done, (tt - 1) & 1u, &ctl.abort, a.status);  // (left at the next meeting)
           tc::fence_after_sync();
         }
         if (active) {
-          got = mbar_wait(&ctl.x_full[buf], (tt >> 1) & 1u, &ctl.abort, a.status);
-          fail |= !__all_sync(0xffffffffu, got);
+          fail |= !wait_warp(&ctl.x_full[buf], (tt >> 1) & 1u, &ctl.abort, a.status);
           uint32_t x[8];
 #pragma unroll
           for (int c = 0; c < 2; ++c)
@@ -806,10 +860,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ctl.red[half][r] = lr;
         ctl.red2[half][r] = lf;
       }
-      bool got = mbar_wait(&ctl.pv_done, (tt - 1) & 1u, &ctl.abort, a.status);
-      if (active) got = got && mbar_wait(&ctl.l_full, seg & 1u, &ctl.abort, a.status);
+      fail |= !wait_warp(&ctl.pv_done, (tt - 1) & 1u, &ctl.abort, a.status);
+      if (active) fail |= !wait_warp(&ctl.l_full, seg & 1u, &ctl.abort, a.status);
       ++seg;
-      fail |= !__all_sync(0xffffffffu, got);
       stop = active ? or_sync(1 + quad, fail) : fail;
       if (stop) break;
       tc::fence_after_sync();
