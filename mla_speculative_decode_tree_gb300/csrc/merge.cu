@@ -255,11 +255,10 @@ __global__ void __launch_bounds__(128, 5) merge_shared_kernel(SharedArgs a) {
   for (int s = lane; s < n; s += 32) M = fmaxf(M, a.part_lse[place(s)]);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-  if (M != -INFINITY) {
-    for (int s = lane; s < n; s += 32) W += expf(a.part_lse[place(s)] - M);
+  if (M == -INFINITY) M = 0.f;  // no partial's weights count, or (a query that is not finite) they are NaN and W is
+  for (int s = lane; s < n; s += 32) W += expf(a.part_lse[place(s)] - M);
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) W += __shfl_xor_sync(0xffffffffu, W, off);
-  }
+  for (int off = 16; off > 0; off >>= 1) W += __shfl_xor_sync(0xffffffffu, W, off);
   float acc[16];
 #pragma unroll
   for (int k = 0; k < 16; ++k) acc[k] = 0.f;
