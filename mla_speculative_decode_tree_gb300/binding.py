@@ -556,9 +556,15 @@ class Verifier:
         self.rows_max = rows
 
     def run(self, d: dict, batch: int, sm_scale: float, stream=None):
-        """One call; with d["qo_indptr"] present, the varlen entry point.  Returns the
-        output buffers' first batch*q_len token rows (varlen: the call's rows come first)."""
-        if "qo_indptr" in d:
+        """One call; with d["qo_indptr"] present, the varlen entry point, with d["group_indptr"] present (a plan with
+        MLA_VERIFY_SHARED) the one for shared prefixes.  Returns the output buffers' first batch*q_len token rows (with
+        qo_indptr the call's rows come first)."""
+        if "group_indptr" in d:
+            mla_verify_run_shared(self.plan, d["q_nope"], d["q_rope"], d["kv_pool"], d["group_indptr"],
+                                  d["shared_indptr"], d["shared_indices"], d["kv_indptr"], d["kv_indices"],
+                                  d.get("qo_indptr"), d["out_cache_loc"], d["custom_mask"], d["mask_indptr"], batch,
+                                  d["group_indptr"].numel() - 1, sm_scale, self.workspace, self.o, self.lse, stream=stream)
+        elif "qo_indptr" in d:
             mla_verify_run_varlen(self.plan, d["q_nope"], d["q_rope"], d["kv_pool"], d["kv_indptr"],
                                   d["kv_indices"], d["qo_indptr"], d["out_cache_loc"], d["custom_mask"],
                                   d["mask_indptr"], batch, sm_scale, self.plan.nsplit, self.workspace, self.o,
