@@ -65,20 +65,24 @@ constexpr int kQSteps = 24;                     // k-steps of 16 channels with Q
 // that the values need too; of the other CTA's keys the latter half.
 constexpr int kScoreStages = 2, kScoreBytes = 5 * kBlockBytes;
 constexpr int kOwnStages = 4, kOtherStages = 2, kValueBytes = 4 * kBlockBytes;
-constexpr int kPBytes = kRows * kOwnKeys * 2;   // the other CTA's P
+constexpr int kPPiece = kRows * 16;               // eight keys' weights of all rows
+constexpr int kPBytes = 2 * (kOwnKeys / 8) * kPPiece;  // a CTA's weights of two tiles
 constexpr int kSoftmaxWarps = 8;
-constexpr int kMmaWarp = kSoftmaxWarps;
+constexpr int kMmaWarp = kSoftmaxWarps;  // issues the score products,
 constexpr int kOtherWarp = kMmaWarp + 1, kOtherWarps = 2;    // gather the other CTA's keys
+constexpr int kValueWarp = kMmaWarp + 3;                     // issues the value products
 constexpr int kGatherWarp = kMmaWarp + 4, kGatherWarps = 4;  // gather own keys (a warpgroup of their own: registers)
 constexpr int kThreads = 32 * (kGatherWarp + kGatherWarps);
 // Registers per thread by warpgroup; together at most the 4 x 128 of the launch.
-constexpr int kRegsSoftmax = 184, kRegsMma = 56, kRegsGather = 80;
+constexpr int kRegsSoftmax = 144, kRegsMma = 112, kRegsGather = 112;
 static_assert(kThreads == 512 && 2 * kRegsSoftmax + kRegsMma + kRegsGather <= 512, "register shares");
 constexpr int kKeysPerWarp = kOwnKeys / kGatherWarps;  // own keys gathered by a warp
-constexpr int kColO = 0, kColQ = 256, kColS = 448, kColP = 480;
+constexpr int kColO = 0, kColQ = 256, kColS = 448;  // (S: 32 columns for a step's first tile, 32 for its second)
 // Base 2, before a reference is raised.  Weights and O are floating numbers, so a
 // reference far below the maximum costs no precision; what it must not do is overflow.
 constexpr float kRowHeadroom = 16.0f, kOutHeadroom = 32.0f;
+// References are 16 + a multiple of 32: those of both CTAs, and of O, are mostly the same one.
+constexpr float kRefStep = 32.0f, kRefOffset = 16.0f;
 // Start and end of a row group, in tiles.
 constexpr int kSegCost = 5;
 constexpr int kMaxSpans = 2 * kMaxSharedBatch;
@@ -87,25 +91,28 @@ constexpr int64_t kAxisEnd = 0xFFFFFFFF;  // (2^32 tiles would take half a day)
 struct Ctl {
   uint64_t full[kOwnStages], empty_own[kOwnStages], empty_score[kScoreStages];
   uint64_t full_other[kOtherStages], empty_other[kOtherStages];
-  uint64_t q_full, s_full, s_free, p_full, pv_done, x_full[2], l_full, mma_idle;
+  uint64_t q_full, s_full[2], s_free[2], p_full[2], pv_done[2], x_full[2], l_full, mma_idle;  // [2]: even, odd tiles
+  uint64_t m_set[2][4];  // by quarter of the rows: a tile's M stands in m_row
   uint32_t tmem_base;
   int abort;
   alignas(4) uint8_t valid[kOwnStages][kGatherWarps];  // own keys of a tile that exist, 8 bits per gather warp
-  int failed[2][4];     // softmax warps that gave up, by half of the keys and quarter of the rows
-  float red[2][kRows];  // per half of the keys: row maxima, sums
-  float red2[2][kRows];
-  float x_ref[2][kRows];         // the other CTA's references, with its P
-  alignas(16) float4 x_sum[2][kRows];  // at the end of a row group: its reference and sums, per half of its keys
+  float m_row[kRows];                  // reference of O
+  float x_ref[2][kRows];               // the other CTA's references, with its weights
+  float sum[2][3][kRows];              // at the end of a row group: references and sums of even and odd tiles,
+  alignas(16) float4 x_sum[2][kRows];  // and the other CTA's
+  uint32_t some[kMaxSpans / 32];  // which spans of the axis have a length
   int64_t warp_sum[kThreads / 32];
 };
 
 constexpr int kOffScore = 3 * kQBlock;
 constexpr int kOffOwn = kOffScore + kScoreStages * kScoreBytes;
 constexpr int kOffOther = kOffOwn + kOwnStages * kValueBytes;
-constexpr int kOffX = kOffOther + kOtherStages * kValueBytes;
-constexpr int kOffCtl = kOffX + 2 * kPBytes;
-constexpr int kOffEnds = (kOffCtl + (int)sizeof(Ctl) + 15) / 16 * 16;
-constexpr int kSmem = kOffEnds + 1024;  // + the axis (4 bytes per group and request) + alignment slack
+constexpr int kOffP = kOffOther + kOtherStages * kValueBytes;
+constexpr int kOffX = kOffP + kPBytes;
+constexpr int kOffCtl = kOffX + kPBytes;
+constexpr int kOffEnds = kOffScore;  // the axis, while it is set up
+constexpr int kSmem = kOffCtl + (int)sizeof(Ctl) + 1024;  // (alignment slack)
+static_assert(kMaxSpans * 4 <= kOffP - kOffEnds && kGatherWarps == 4, "places in shared memory");
 
 // ---- wider TMEM accesses ------------------------------------------------------
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
@@ -174,6 +181,13 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volati
 }
 
 // ---- the other CTA of the pair -------------------------------------------------
+// Arrive once on `bar` of the other CTA when every MMA issued before by this thread completes.
+__device__ __forceinline__ void commit_to(uint64_t* bar, uint32_t rank) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
+      "h"((uint16_t)(1u << rank))
+      : "memory");
+}
 __device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
   uint32_t r;
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
@@ -202,16 +216,24 @@ __device__ __forceinline__ uint32_t scale_bf16x2(uint32_t w, uint32_t f) {
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(w), "r"(f));
   return r;
 }
-__device__ __forceinline__ bool or_sync(int id, bool p) {  // over the 64 threads that share rows
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred a, b;\n\tsetp.ne.u32 a, %1, 0;\n\tbarrier.cta.red.or.pred b, %2, 64, a;\n\tselp.u32 %0, 1, 0, b;\n\t}"
-      : "=r"(r)
-      : "r"(p ? 1u : 0u), "r"(id)
-      : "memory");
-  return r != 0;
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
-
+// A row's 32 weights in shared memory, by a power of two.
+__device__ __forceinline__ void scale_weights(uint32_t at, float by) {
+  const uint32_t f = __float_as_uint(by) >> 16, f2 = f | f << 16;
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    uint32_t x[4];
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                 : "r"(at + c * kPPiece)
+                 : "memory");
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[k] = scale_bf16x2(x[k], f2);
+    sts128(at + c * kPPiece, x[0], x[1], x[2], x[3]);
+  }
+}
 // ---- pairs of fp32 values in one instruction ---------------------------------------
 __device__ __forceinline__ uint64_t pair(float lo, float hi) {
   uint64_t r;
@@ -301,8 +323,9 @@ __device__ __forceinline__ int64_t tiles_of(const Span& s) { return (s.keys + kK
 
 // Where a pair is on the axis; every role of its CTAs walks it by itself.
 struct Cursor {
-  const uint32_t* ends;  // shared memory: end of each span on the axis
+  const uint32_t* some;  // bit e: span e has a length
   int spans, e;
+  int64_t start;  // of span e
   int64_t x, x_end, piece;
   int pair;
 };
@@ -326,15 +349,28 @@ __device__ __forceinline__ int32_t load_id(const SharedArgs& a, const Segment& g
                         : __ldg(a.out_cache_loc + g.s.q0 + (j - g.s.prefix));
 }
 
+// First span with a length from span e on.
+__device__ __forceinline__ int next_span(const Cursor& c, int e) {
+  while (e < c.spans) {
+    const uint32_t w = c.some[e >> 5] >> (e & 31);
+    if (w) return e + __ffs(w) - 1;
+    e = (e | 31) + 1;
+  }
+  return c.spans;
+}
+
 // The next row group and run of tiles of the pair; false at the end of its piece.
 __device__ __forceinline__ bool next_segment(const SharedArgs& a, Cursor& c, Segment& g) {
   while (c.x < c.x_end) {
-    while (c.e < c.spans && c.ends[c.e] <= c.x) ++c.e;
     if (c.e >= c.spans) return false;
     g.s = span_of(a, c.e);
-    const int64_t start = c.e ? c.ends[c.e - 1] : 0;
-    const int64_t tiles = tiles_of(g.s), len = tiles + kSegCost;
-    const int64_t i = (c.x - start) / len, e0 = start + i * len, e1 = e0 + len;
+    const int64_t tiles = tiles_of(g.s), len = tiles + kSegCost, all = groups_of(a, g.s) * len;
+    if (c.start + all <= c.x) {
+      c.start += all;
+      c.e = next_span(c, c.e + 1);
+      continue;
+    }
+    const int64_t i = (c.x - c.start) / len, e0 = c.start + i * len, e1 = e0 + len;
     g.r0 = (int)(i * kRows);
     const int64_t left = (int64_t)g.s.ntok * a.H - g.r0;
     g.nrows = left < kRows ? (int)left : kRows;
@@ -379,14 +415,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     for (int k = 0; k < kScoreStages; ++k) mbar_init(&ctl.empty_score[k], 1);
     mbar_init(&ctl.q_full, kSoftmaxWarps);
-    mbar_init(&ctl.s_full, 2);  // the product, and the issuing lane (which has seen the tile's valid bits)
-    mbar_init(&ctl.s_free, kSoftmaxWarps);
-    mbar_init(&ctl.p_full, kSoftmaxWarps);
-    mbar_init(&ctl.pv_done, 1);
-    mbar_init(&ctl.x_full[0], 1);
-    mbar_init(&ctl.x_full[1], 1);
-    mbar_init(&ctl.l_full, 1);
-    mbar_init(&ctl.mma_idle, 1);
+    for (int k = 0; k < 2; ++k) {
+      mbar_init(&ctl.s_full[k], 2);  // the product, and the issuing lane (which has seen the tile's valid bits)
+      mbar_init(&ctl.s_free[k], kSoftmaxWarps / 2);
+    }
+    for (int k = 0; k < 2; ++k) {
+      mbar_init(&ctl.p_full[k], kSoftmaxWarps / 2);
+      mbar_init(&ctl.pv_done[k], 2);  // of both CTAs
+      mbar_init(&ctl.x_full[k], 1);
+      for (int q = 0; q < 4; ++q) mbar_init(&ctl.m_set[k][q], 1);
+    }
+    mbar_init(&ctl.l_full, 1 + kSoftmaxWarps);
+    mbar_init(&ctl.mma_idle, 2);
     ctl.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -395,7 +435,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc::tmem_relinquish();
   }
   Cursor cur;
-  cur.ends = ends;
+  cur.some = ctl.some;
   cur.spans = a.groups + a.batch;
   {
     int64_t carry = 0;
@@ -406,12 +446,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const Span s = span_of(a, e);
         v = groups_of(a, s) * (tiles_of(s) + kSegCost);
       }
+      const int64_t len = v;
 #pragma unroll 1
       for (int o = 1; o < 32; o <<= 1) {
         const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
         if (lane >= o) v += y;
       }
       if (lane == 31) ctl.warp_sum[warp] = v;
+      const uint32_t some = __ballot_sync(0xffffffffu, len > 0);
+      if (lane == 0 && e < kMaxSpans) ctl.some[e >> 5] = some;
       __syncthreads();
       int64_t before = carry;
       for (int w = 0; w < warp; ++w) before += ctl.warp_sum[w];
@@ -435,6 +478,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         hi = mid;
     }
     cur.e = lo;
+    cur.start = lo ? ends[lo - 1] : 0;
   }
   tc::fence_before_sync();
   cluster.sync();
@@ -509,97 +553,90 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (bad) atomicOr(a.status, kStatusBadRow);
   } else if (warp >= kMmaWarp) {
     fewer_registers<kRegsMma>();
-    if (warp == kMmaWarp) {
+    if (warp == kMmaWarp || warp == kValueWarp) {
       // ============================ MMA issue ==============================================
-      // The whole warp walks the loop and one elected lane issues, so that what an MMA
-      // takes its descriptors from stays warp-uniform.
+      // One warp issues the score products, one the value products: each product waits for its own operands, and
+      // the tensor pipe has the other one's to do meanwhile.  A whole warp walks the loop and one elected lane issues,
+      // so that what an MMA takes its descriptors from stays warp-uniform.
       const bool leader = elect_one();
-      constexpr uint32_t idesc_qk = tc::idesc_bf16_f32(kRows, kOwnKeys, false, false);
-      constexpr uint32_t idesc_pv = tc::idesc_bf16_f32(kRows, kHalfLatent, false, true);
-      const uint64_t desc_q = tc::smem_desc(sbase, 16, 1024, tc::kSwizzle128B);
-      const uint64_t desc_s = tc::smem_desc(sbase + kOffScore, 16, 1024, tc::kSwizzle128B);
-      const uint64_t desc_k = tc::smem_desc(sbase + kOffOwn, 16, 1024, tc::kSwizzle128B);
-      const uint64_t desc_v = tc::smem_desc(sbase + kOffOwn, kBlockBytes, 1024, tc::kSwizzle128B);
-      const uint64_t desc_x = tc::smem_desc(sbase + kOffOther, kBlockBytes, 1024, tc::kSwizzle128B);
       bool ok = true;
-      uint32_t nq = 0, np = 0;  // tiles whose scores, whose values have been issued
-      uint32_t seg = 0;
       Segment g;
-      auto qk = [&]() {  // scores of tile nq, which has landed
-        fence_proxy_async_smem();
-        tc::fence_after_sync();
-        const uint64_t ds = desc_s + (nq % kScoreStages) * (uint32_t)(kScoreBytes >> 4),
-                       dv = desc_k + (nq % kOwnStages) * (uint32_t)(kValueBytes >> 4);
-        const uint64_t half0 = rank == 0 ? dv : ds, half1 = rank == 0 ? ds : dv;  // latent channels 0..255, 256..511
-        if (leader) {
+      if (warp == kMmaWarp) {
+        constexpr uint32_t idesc = tc::idesc_bf16_f32(kRows, kOwnKeys, false, false);
+        const uint64_t desc_q = tc::smem_desc(sbase, 16, 1024, tc::kSwizzle128B);
+        const uint64_t desc_s = tc::smem_desc(sbase + kOffScore, 16, 1024, tc::kSwizzle128B);
+        const uint64_t desc_k = tc::smem_desc(sbase + kOffOwn, 16, 1024, tc::kSwizzle128B);
+        uint32_t tile = 0, seg = 0;
+        uint32_t used = 0;  // places for scores that have been used, and (bits 2, 3) the parity of their last use
+        while (ok && next_segment(a, cur, g)) {
+          if (g.nt == 0) continue;
+          ok = wait_spin(&ctl.q_full, seg & 1u, &ctl.abort, a.status);
+          ++seg;
+          for (int t = 0; ok && t < g.nt; ++t, ++tile) {
+            const uint32_t h = t & 1;
+            if (used >> h & 1u) ok = wait_spin(&ctl.s_free[h], used >> (2 + h) & 1u, &ctl.abort, a.status);
+            ok = ok && wait_spin(&ctl.full[tile % kOwnStages], tile / kOwnStages & 1u, &ctl.abort, a.status);
+            if (!ok) break;
+            used = used >> h & 1u ? used ^ 4u << h : used | 1u << h;
+            fence_proxy_async_smem();
+            tc::fence_after_sync();
+            const uint64_t ds = desc_s + (tile % kScoreStages) * (uint32_t)(kScoreBytes >> 4),
+                           dv = desc_k + (tile % kOwnStages) * (uint32_t)(kValueBytes >> 4);
+            const uint64_t half0 = rank == 0 ? dv : ds, half1 = rank == 0 ? ds : dv;  // latent channels 0..255, 256..511
+            const uint32_t d_s = tmem + kColS + 32 * h;
+            if (leader) {
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            const uint64_t d = (k < 16 ? half0 : half1) + (uint32_t)((((k >> 2) & 3) * kBlockBytes + (k & 3) * 32) >> 4);
-            if (k < kQSteps)
-              mma_bf16_ts(tmem + kColS, tmem + kColQ + 8 * k, d, idesc_qk, k > 0);
-            else
-              tc::mma_bf16_ss(tmem + kColS, desc_q + (uint32_t)((((k - kQSteps) >> 2) * kQBlock + (k & 3) * 32) >> 4), d,
-                              idesc_qk, 1u);
-          }
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            tc::mma_bf16_ss(tmem + kColS, desc_q + (uint32_t)((2 * kQBlock + k * 32) >> 4),
-                            ds + (uint32_t)((4 * kBlockBytes + k * 32) >> 4), idesc_qk, 1u);
-          tc::mma_commit(&ctl.empty_score[nq % kScoreStages]);
-          tc::mma_commit(&ctl.s_full);
-          mbar_arrive(&ctl.s_full);
-        }
-        ++nq;
-      };
-      auto pv = [&](bool first) {  // O += P V of tile np
-        fence_proxy_async_smem();
-        tc::fence_after_sync();
-        const uint64_t dv = desc_v + (np % kOwnStages) * (uint32_t)(kValueBytes >> 4),
-                       dx = desc_x + (np % kOtherStages) * (uint32_t)(kValueBytes >> 4);
-        if (leader) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k)  // own keys, then the other CTA's
-            mma_bf16_ts(tmem + kColO, tmem + kColP + 8 * k, (k < 2 ? dv : dx) + (uint32_t)((k & 1) * 2048 >> 4), idesc_pv,
-                        !(first && k == 0));
-          tc::mma_commit(&ctl.empty_own[np % kOwnStages]);
-          tc::mma_commit(&ctl.empty_other[np % kOtherStages]);
-          tc::mma_commit(&ctl.pv_done);
-        }
-        ++np;
-      };
-      while (ok && next_segment(a, cur, g)) {
-        if (g.nt == 0) continue;
-        ok = wait_spin(&ctl.q_full, seg & 1u, &ctl.abort, a.status);
-        tc::fence_after_sync();
-        ++seg;
-        const uint32_t first = np, end = np + g.nt;
-        // What is ready goes first: a tile's values, or the scores of one of the next.
-        uint64_t since = 0;
-        for (uint32_t idle = 0; ok && np != end;) {
-          if (np != nq &&
-              __all_sync(0xffffffffu, mbar_test_wait(&ctl.p_full, np & 1u) &&
-                                          mbar_test_wait(&ctl.full_other[np % kOtherStages], np / kOtherStages & 1u))) {
-            pv(np == first);
-            idle = 0;
-          } else if (nq != end && __all_sync(0xffffffffu, mbar_test_wait(&ctl.full[nq % kOwnStages], nq / kOwnStages & 1u) &&
-                                                              (nq == 0 || mbar_test_wait(&ctl.s_free, (nq - 1) & 1u)))) {
-            qk();
-            idle = 0;
-          } else if ((++idle & 255u) == 0) {
-            const uint64_t now = __shfl_sync(0xffffffffu, global_timer_ns(), 0);
-            if (idle == 256) since = now;
-            if (now - since > kWaitLimitNs || idle > (1u << 30)) {
-              if (leader) {
-                ctl.abort = 1;
-                atomicOr(a.status, kStatusTimeout);
+              for (int k = 0; k < 32; ++k) {
+                const uint64_t d = (k < 16 ? half0 : half1) + (uint32_t)((((k >> 2) & 3) * kBlockBytes + (k & 3) * 32) >> 4);
+                if (k < kQSteps)
+                  mma_bf16_ts(d_s, tmem + kColQ + 8 * k, d, idesc, k > 0);
+                else
+                  tc::mma_bf16_ss(d_s, desc_q + (uint32_t)((((k - kQSteps) >> 2) * kQBlock + (k & 3) * 32) >> 4), d, idesc, 1u);
               }
-              ok = false;
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                tc::mma_bf16_ss(d_s, desc_q + (uint32_t)((2 * kQBlock + k * 32) >> 4),
+                                ds + (uint32_t)((4 * kBlockBytes + k * 32) >> 4), idesc, 1u);
+              tc::mma_commit(&ctl.s_full[h]);
+              tc::mma_commit(&ctl.empty_score[tile % kScoreStages]);
+              mbar_arrive(&ctl.s_full[h]);
             }
-            if (__any_sync(0xffffffffu, *(volatile int*)&ctl.abort)) ok = false;
+          }
+        }
+      } else {
+        constexpr uint32_t idesc = tc::idesc_bf16_f32(kRows, kHalfLatent, false, true);
+        const uint64_t desc_v = tc::smem_desc(sbase + kOffOwn, kBlockBytes, 1024, tc::kSwizzle128B);
+        const uint64_t desc_o = tc::smem_desc(sbase + kOffOther, kBlockBytes, 1024, tc::kSwizzle128B);
+        // (weights, not swizzled: eight keys of eight rows in 128 bytes, the rows' next eight behind them)
+        const uint64_t desc_p = tc::smem_desc(sbase + kOffP, kPPiece, 128, 0);
+        const uint64_t desc_x = tc::smem_desc(sbase + kOffX, kPPiece, 128, 0);
+        uint32_t tile = 0, uses0 = 0, uses1 = 0;
+        while (ok && next_segment(a, cur, g)) {
+          for (int t = 0; ok && t < g.nt; ++t, ++tile) {
+            const uint32_t h = t & 1;
+            ok = wait_spin(&ctl.full_other[tile % kOtherStages], tile / kOtherStages & 1u, &ctl.abort, a.status) &&
+                 wait_spin(&ctl.p_full[h], (h ? uses1 : uses0) & 1u, &ctl.abort, a.status);
+            if (!ok) break;
+            uses0 += h ^ 1u;
+            uses1 += h;
+            fence_proxy_async_smem();
+            tc::fence_after_sync();
+            const uint64_t dv = desc_v + (tile % kOwnStages) * (uint32_t)(kValueBytes >> 4),
+                           dx = desc_o + (tile % kOtherStages) * (uint32_t)(kValueBytes >> 4);
+            if (leader) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)  // own keys, then the other CTA's
+                tc::mma_bf16_ss(tmem + kColO, (k < 2 ? desc_p : desc_x) + (4 * h + 2 * (k & 1)) * (uint32_t)(kPPiece >> 4),
+                                (k < 2 ? dv : dx) + (uint32_t)((k & 1) * 2048 >> 4), idesc, t > 0 || k > 0);
+              tc::mma_commit(&ctl.pv_done[h]);
+              commit_to(&ctl.pv_done[h], rank ^ 1u);
+              tc::mma_commit(&ctl.empty_own[tile % kOwnStages]);
+              tc::mma_commit(&ctl.empty_other[tile % kOtherStages]);
+            }
           }
         }
       }
-      // Drain: every MMA of this warp has completed before tensor memory is freed.
+      // Drain: every MMA of both warps has completed before tensor memory is freed.
       if (leader) tc::mma_commit(&ctl.mma_idle);
       const uint64_t t0 = global_timer_ns();
       for (uint32_t it = 0; it < (1u << 30); ++it)
@@ -654,13 +691,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
     const uint64_t scale2 = pair(scale, scale);
     const uint32_t other = rank ^ 1u;
-    const uint32_t x_own = sbase + kOffX + (2 * half * kRows + r) * 16, x_peer = peer_addr(x_own, other);
-    const uint32_t ref_peer = peer_addr(smem_u32(&ctl.x_ref[0][r]), other);
+    const uint32_t p_own = sbase + kOffP + 4 * half * kPPiece + r * 16, x_own = p_own + (kOffX - kOffP);
+    const uint32_t x_peer = peer_addr(x_own, other);
+    const uint32_t ref_peer = peer_addr(smem_u32(&ctl.x_ref[half][r]), other);
     const uint32_t sum_peer = peer_addr(smem_u32(&ctl.x_sum[half][r]), other);
-    const uint32_t bar_peer = peer_addr(smem_u32(&ctl.x_full[0]), other);
+    const uint32_t bar_peer = peer_addr(smem_u32(&ctl.x_full[half]), other);
     const uint32_t l_bar_peer = peer_addr(smem_u32(&ctl.l_full), other);
-    uint32_t tt = 0, stage = 0, seg = 0;
-    bool stop = false, fail = false;
+    uint32_t uses = 0, uses_other = 0, tile = 0, seg = 0;  // tiles of this warp's parity so far, of the other one, of both
+    bool stop = false;
     Segment g;
     while (!stop && next_segment(a, cur, g)) {
       const bool row_in = r < g.nrows;
@@ -676,16 +714,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint4 x = __ldg(p);
           return make_uint4(x.x ^ flip, x.y ^ flip, x.z ^ flip, x.w ^ flip);
         };
-        uint4 v[24], y[12];
+        uint4 y[12];
+#pragma unroll 1
+        for (int j = 0; j < 2; ++j) {
 #pragma unroll
-        for (int k = 0; k < 24; ++k) v[k] = load(qn + 24 * half + k);
+          for (int k = 0; k < 12; ++k) y[k] = load(qn + 24 * half + 12 * j + k);
 #pragma unroll
-        for (int k = 0; k < 6; ++k) {
-          const uint32_t w[16] = {v[4 * k].x,     v[4 * k].y,     v[4 * k].z,     v[4 * k].w,
-                                  v[4 * k + 1].x, v[4 * k + 1].y, v[4 * k + 1].z, v[4 * k + 1].w,
-                                  v[4 * k + 2].x, v[4 * k + 2].y, v[4 * k + 2].z, v[4 * k + 2].w,
-                                  v[4 * k + 3].x, v[4 * k + 3].y, v[4 * k + 3].z, v[4 * k + 3].w};
-          tmem_st16(t_lane + kColQ + 96 * half + 16 * k, w);
+          for (int k = 0; k < 12; k += 4) {
+            const uint32_t w[16] = {y[k].x,     y[k].y,     y[k].z,     y[k].w,     y[k + 1].x, y[k + 1].y, y[k + 1].z, y[k + 1].w,
+                                    y[k + 2].x, y[k + 2].y, y[k + 2].z, y[k + 2].w, y[k + 3].x, y[k + 3].y, y[k + 3].z, y[k + 3].w};
+            tmem_st16(t_lane + kColQ + 96 * half + 48 * j + 4 * k, w);
+          }
         }
 #pragma unroll
         for (int k = 0; k < 12; ++k) {
@@ -695,10 +734,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int k = 0; k < 12; ++k) {
           const int c = 12 * half + k;
-          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(sbase + (c >> 3) * kQBlock + r * 128 +
-                                                                     (((c & 7) ^ (r & 7)) << 4)),
-                       "r"(y[k].x), "r"(y[k].y), "r"(y[k].z), "r"(y[k].w)
-                       : "memory");
+          sts128(sbase + (c >> 3) * kQBlock + r * 128 + (((c & 7) ^ (r & 7)) << 4), y[k].x, y[k].y, y[k].z, y[k].w);
         }
         fence_proxy_async_smem();
         tc::tmem_wait_st();
@@ -709,82 +745,66 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
       const int token = row_in ? (g.r0 + r) / a.H : 0;
       const int64_t mask_row = g.s.mask0 + (int64_t)token * g.s.keys;
-      float m = -INFINITY, M = -INFINITY;  // the row's references: of this CTA's weights, of its half of O
+      float m = -INFINITY;  // reference of the row's weights in this CTA's tiles of this parity
       // of this thread's keys: sums of the weights as P has them, and before rounding (even and odd keys)
       uint64_t l_round = 0, l_full = 0;
+      // Warps 0-3 take the row group's even tiles, 4-7 the odd ones.
 #pragma unroll 1
-      for (int t = 0; t < g.nt; ++t, ++tt) {
-        const uint32_t buf = tt & 1u;
-        if (tid == 0) tma::arrive_expect_tx(&ctl.x_full[buf], quads * (2 * 32 * 32 + 32 * 4));
-        // which of the 16 keys this row sees
-        uint32_t sees = 0xFFFFu;
+      for (int t = half; t < g.nt; t += 2, ++uses) {
+        if (lane == 0 && quad == 0) tma::arrive_expect_tx(&ctl.x_full[half], quads * (32 * kOwnKeys * 2 + 32 * 4));
+        // which of the 32 keys this row sees
+        uint32_t sees = 0xFFFFFFFFu;
         if (g.s.own) {
           sees = 0;
-          const int64_t key0 = (g.tile0 + t) * kKeys + kOwnKeys * rank + 16 * half;
-          const int64_t left = g.s.keys - key0 < 16 ? g.s.keys - key0 : 16;
+          const int64_t key0 = (g.tile0 + t) * kKeys + kOwnKeys * rank;
+          const int64_t left = g.s.keys - key0 < kOwnKeys ? g.s.keys - key0 : kOwnKeys;
           if (row_in && left > 0) {
             const int64_t bit = mask_row + key0;
             const uint8_t* p = a.mask + (bit >> 3);
             const int shift = (int)(bit & 7), bytes = (int)((shift + left + 7) >> 3);
-            uint32_t w = 0;
+            uint64_t v = 0;
 #pragma unroll
-            for (int i = 0; i < 3; ++i)
-              if (i < bytes) w |= (uint32_t)__ldg(p + i) << (8 * i);
-            sees = (w >> shift) & 0xFFFFu;
+            for (int i = 0; i < 5; ++i)
+              if (i < bytes) v |= (uint64_t)__ldg(p + i) << (8 * i);
+            sees = (uint32_t)(v >> shift);
           }
         }
-        // ---- this CTA's half of the scores, and their weights -----------------------------
-        fail |= !wait_warp(&ctl.s_full, buf, &ctl.abort, a.status);
+        // ---- the scores of this CTA's 32 keys, and their weights --------------------------
+        if (!wait_warp(&ctl.s_full[half], uses & 1u, &ctl.abort, a.status)) {
+          stop = true;
+          break;
+        }
         tc::fence_after_sync();
-        float n[16];
+        float n[32];
         if (active) {
-          tmem_ld16(t_lane + kColS + 16 * half, n);
+          tmem_ld32(t_lane + kColS + 32 * half, n);
           tc::tmem_wait_ld();
         }
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl.s_free);
-        sees &= *reinterpret_cast<const uint16_t*>(&ctl.valid[stage][2 * half]);
-        if (++stage == kOwnStages) stage = 0;
-        bool raise = false;
+        if (lane == 0) mbar_arrive(&ctl.s_free[half]);
+        uint32_t w[16];
         if (active) {
-          if (sees != 0xFFFFu) {
+          sees &= *reinterpret_cast<const uint32_t*>(ctl.valid[(tile + t) % kOwnStages]);
+          if (sees != 0xFFFFFFFFu) {
 #pragma unroll
-            for (int k = 0; k < 16; ++k) n[k] = (sees >> k) & 1u ? n[k] : -INFINITY;
+            for (int k = 0; k < 32; ++k) n[k] = (sees >> k) & 1u ? n[k] : -INFINITY;
           }
-          float top = n[0];
+          float t4[4] = {n[0], n[1], n[2], n[3]};
 #pragma unroll
-          for (int k = 1; k < 16; ++k) top = fmaxf(top, n[k]);
-          top *= scale;
-          raise = top > m + kRowHeadroom;  // (m = -inf: any key that is seen)
-          // The two warps of a quarter stay together: they leave the loop in the same place.
-          raise = or_sync(1 + quad, raise || fail);
-          if (raise) {
-            ctl.red[half][r] = top;
-            if (lane == 0) ctl.failed[half][quad] = fail ? 1 : 0;
-            named_bar_sync(1 + quad, 64);
-            top = fmaxf(top, ctl.red[half ^ 1][r]);
-            fail |= ctl.failed[half ^ 1][quad] != 0;
-            named_bar_sync(1 + quad, 64);  // (read before the next raise writes)
-            if (top > m + kRowHeadroom) {
-              const float up = ceilf(top), alpha = ratio(m, up);
-              const uint64_t alpha2 = pair(alpha, alpha);
-              l_round = fma2(l_round, alpha2, 0);
-              l_full = fma2(l_full, alpha2, 0);
-              m = up;
-            }
+          for (int k = 4; k < 32; ++k) t4[k & 3] = fmaxf(t4[k & 3], n[k]);
+          const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * scale;
+          if (top > m + kRowHeadroom) {  // (m = -inf: any key that is seen)
+            const float up = fmaf(kRefStep, ceilf((top - kRefOffset) * (1.f / kRefStep)), kRefOffset), alpha = ratio(m, up);
+            const uint64_t alpha2 = pair(alpha, alpha);
+            l_round = fma2(l_round, alpha2, 0);
+            l_full = fma2(l_full, alpha2, 0);
+            m = up;
           }
-        }
-        if (fail) {
-          stop = true;
-          break;
-        }
-        uint32_t w[8];
-        if (active) {
           const float mu = m == -INFINITY ? 0.f : -m;
           const uint64_t mu2 = pair(mu, mu);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
+          for (int k = 0; k < 16; ++k) {
             float p0, p1;
             unpair(fma2(pair(n[2 * k], n[2 * k + 1]), scale2, mu2), p0, p1);
             p0 = ex2_approx(p0);
@@ -794,84 +814,104 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             l_full = add2(l_full, pair(p0, p1));
             l_round = add2(l_round, pair(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u)));
           }
-          const uint32_t off = buf * kPBytes, bar = bar_peer + buf * 8;
-          send16(x_peer + off, bar, w[0], w[1], w[2], w[3]);
-          send16(x_peer + off + kRows * 16, bar, w[4], w[5], w[6], w[7]);
-          if (half == 0) send4(ref_peer + buf * kRows * 4, bar, m);
         }
-        // ---- both halves into P, which PV(t-1) reads until it is complete ------------------
-        if (t > 0) {
-          fail |= !wait_warp(&ctl.pv_done, (tt - 1) & 1u, &ctl.abort, a.status);  // (left at the next meeting)
-          tc::fence_after_sync();
+        // ---- to both CTAs, whose MMAs have read the weights of two tiles ago ----------------
+        // (warps without rows wait too: none may arrive twice in one phase of p_full)
+        if (uses > 0 && !wait_warp(&ctl.pv_done[half], (uses - 1) & 1u, &ctl.abort, a.status)) {
+          stop = true;
+          break;
         }
         if (active) {
-          fail |= !wait_warp(&ctl.x_full[buf], (tt >> 1) & 1u, &ctl.abort, a.status);
-          uint32_t x[8];
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
-            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                         : "=r"(x[4 * c]), "=r"(x[4 * c + 1]), "=r"(x[4 * c + 2]), "=r"(x[4 * c + 3])
-                         : "r"(x_own + buf * kPBytes + c * kRows * 16)
-                         : "memory");
-          const float mx = *reinterpret_cast<volatile float*>(&ctl.x_ref[buf][r]);
+          for (int c = 0; c < 4; ++c) send16(x_peer + c * kPPiece, bar_peer, w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+          send4(ref_peer, bar_peer, m);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) sts128(p_own + c * kPPiece, w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+          // ---- one reference for both, and for the tiles before -----------------------------
+          bool ok = wait_warp(&ctl.x_full[half], uses & 1u, &ctl.abort, a.status);
+          const uint32_t before = uses_other + (half ? (t >> 1) : (t >> 1) - 1);  // tile t - 1 among those of its parity
+          if (t > 0) ok = ok && wait_warp(&ctl.m_set[half ^ 1][quad], before & 1u, &ctl.abort, a.status);
+          if (!ok) {
+            stop = true;
+            break;
+          }
+          const float mx = *reinterpret_cast<volatile float*>(&ctl.x_ref[half][r]);
+          const float old = t > 0 ? *reinterpret_cast<volatile float*>(&ctl.m_row[r]) : -INFINITY;
           const float high = fmaxf(m, mx);
-          const bool lift = high > M + kOutHeadroom;  // (M = -inf: the first key that either CTA sees)
-          const float old = M;
-          if (lift) M = high;
-          if (t > 0 && __any_sync(0xffffffffu, lift && old != -INFINITY)) {
+          const bool lift = high > old + kOutHeadroom;  // (old = -inf: the first key that either CTA sees)
+          const float M = lift ? high : old;
+          if (__any_sync(0xffffffffu, lift && old != -INFINITY)) {
+            if (!wait_warp(&ctl.pv_done[half ^ 1], before & 1u, &ctl.abort, a.status)) {
+              stop = true;
+              break;
+            }
+            tc::fence_after_sync();
             const float alpha = lift ? ratio(old, M) : 1.f;
 #pragma unroll 1
-            for (int c = 0; c < 16; ++c) {
+            for (int c = 0; c < 32; ++c) {
               float v[8];
-              tc::tmem_ld8(t_lane + kColO + half * 128 + 8 * c, v);
+              tc::tmem_ld8(t_lane + kColO + 8 * c, v);
               tc::tmem_wait_ld();
 #pragma unroll
               for (int k = 0; k < 8; ++k) v[k] *= alpha;
-              tc::tmem_st8(t_lane + kColO + half * 128 + 8 * c, v);
+              tc::tmem_st8(t_lane + kColO + 8 * c, v);
             }
+            tc::tmem_wait_st();
           }
-          if (__any_sync(0xffffffffu, m != M || mx != M)) {
-            const uint32_t f = __float_as_uint(ratio(m, M)) >> 16, fx = __float_as_uint(ratio(mx, M)) >> 16;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              w[k] = scale_bf16x2(w[k], f | f << 16);
-              x[k] = scale_bf16x2(x[k], fx | fx << 16);
-            }
+          if (lift || t == 0) ctl.m_row[r] = M;
+          // (a reference of -inf goes with weights of 0)
+          if ((m != M && m != -INFINITY) || (mx != M && mx != -INFINITY)) {
+            scale_weights(p_own, ratio(m, M));
+            scale_weights(x_own, ratio(mx, M));
           }
-          tmem_st8u(t_lane + kColP + 8 * half, w);
-          tmem_st8u(t_lane + kColP + 16 + 8 * half, x);
-          tc::tmem_wait_st();
+          fence_proxy_async_smem();
         }
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl.p_full);
+        if (lane == 0) {
+          mbar_arrive(&ctl.p_full[half]);
+          mbar_arrive(&ctl.m_set[half][quad]);
+        }
       }
       if (stop) break;
+      tile += g.nt;
+      uses_other += half ? (g.nt + 1) >> 1 : g.nt >> 1;
       // ---- the row group's partial -----------------------------------------------------
       if (tid == 0) tma::arrive_expect_tx(&ctl.l_full, quads * 2 * 32 * 16);
-      float lr = 0.f, lf = 0.f;
       if (active) {
         float even, odd;
         unpair(l_round, even, odd);
-        lr = even + odd;
+        const float lr = even + odd;
         unpair(l_full, even, odd);
-        lf = even + odd;
+        const float lf = even + odd;
         send16(sum_peer, l_bar_peer, __float_as_uint(m), __float_as_uint(lr), __float_as_uint(lf), 0u);
-        ctl.red[half][r] = lr;
-        ctl.red2[half][r] = lf;
+        ctl.sum[half][0][r] = m;
+        ctl.sum[half][1][r] = lr;
+        ctl.sum[half][2][r] = lf;
       }
-      fail |= !wait_warp(&ctl.pv_done, (tt - 1) & 1u, &ctl.abort, a.status);
-      if (active) fail |= !wait_warp(&ctl.l_full, seg & 1u, &ctl.abort, a.status);
-      ++seg;
-      stop = active ? or_sync(1 + quad, fail) : fail;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl.l_full);
+      // The last value products of both parities; with them the other CTA's last arrivals here are in: none comes after
+      // this CTA has left.
+      stop = !wait_warp(&ctl.l_full, seg & 1u, &ctl.abort, a.status) ||
+             (uses > 0 && !wait_warp(&ctl.pv_done[half], (uses - 1) & 1u, &ctl.abort, a.status)) ||
+             (uses_other > 0 && !wait_warp(&ctl.pv_done[half ^ 1], (uses_other - 1) & 1u, &ctl.abort, a.status));
       if (stop) break;
+      ++seg;
       tc::fence_after_sync();
       if (active) {
-        const float4 x0 = ctl.x_sum[0][r], x1 = ctl.x_sum[1][r];
-        const float f = ratio(m, M), fx = ratio(x0.x, M);
-        lr = (ctl.red[0][r] + ctl.red[1][r]) * f + (x0.y + x1.y) * fx;
-        lf = (ctl.red2[0][r] + ctl.red2[1][r]) * f + (x0.z + x1.z) * fx;
-        named_bar_sync(1 + quad, 64);
+        const float M = ctl.m_row[r];
+        float lr = 0.f, lf = 0.f;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float f = ratio(ctl.sum[k][0][r], M);
+          lr += ctl.sum[k][1][r] * f;
+          lf += ctl.sum[k][2][r] * f;
+          const float4 v = ctl.x_sum[k][r];
+          const float fx = ratio(v.x, M);
+          lr += v.y * fx;
+          lf += v.z * fx;
+        }
         const int64_t at = g.place + (int64_t)kRows * cur.pair + r;
         const bool seen = !(lr <= 0.f);  // (a NaN is passed on)
         const float inv = 1.f / lr;
@@ -914,15 +954,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 }  // namespace
 
-int split_shared_smem() { return kSmem + (int)sizeof(uint32_t) * kMaxSpans; }
+int split_shared_smem() { return kSmem; }
 
 cudaError_t launch_split_shared(const SharedArgs& a, cudaStream_t stream) {
-  const int smem = kSmem + (int)sizeof(uint32_t) * (a.groups + a.batch);
-  static_assert(kSmem + sizeof(uint32_t) * kMaxSpans <= 232448, "shared memory budget exceeded");
-  cudaError_t e = cudaFuncSetAttribute(split_shared_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       split_shared_smem());
+  static_assert(kSmem <= 232448, "shared memory budget exceeded");
+  cudaError_t e = cudaFuncSetAttribute(split_shared_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  split_shared_kernel<<<2 * a.clusters, kThreads, smem, stream>>>(a);
+  split_shared_kernel<<<2 * a.clusters, kThreads, kSmem, stream>>>(a);
   return cudaGetLastError();
 }
 
