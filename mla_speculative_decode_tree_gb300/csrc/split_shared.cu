@@ -69,7 +69,7 @@ constexpr int kPPiece = kRows * 16;               // eight keys' weights of all 
 constexpr int kPBytes = 2 * (kOwnKeys / 8) * kPPiece;  // a CTA's weights of two tiles
 constexpr int kSoftmaxWarps = 8;
 constexpr int kMmaWarp = kSoftmaxWarps;  // issues the score products,
-constexpr int kOtherWarp = kMmaWarp + 1, kOtherWarps = 2;    // gather the other CTA's keys
+constexpr int kOtherWarp = kMmaWarp + 2, kOtherWarps = 1;    // gathers the other CTA's keys
 constexpr int kValueWarp = kMmaWarp + 3;                     // issues the value products
 constexpr int kGatherWarp = kMmaWarp + 4, kGatherWarps = 4;  // gather own keys (a warpgroup of their own: registers)
 constexpr int kThreads = 32 * (kGatherWarp + kGatherWarps);
@@ -426,7 +426,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int q = 0; q < 4; ++q) mbar_init(&ctl.m_set[k][q], 1);
     }
     mbar_init(&ctl.l_full, 1 + kSoftmaxWarps);
-    mbar_init(&ctl.mma_idle, 2);
+    mbar_init(&ctl.mma_idle, 3);
     ctl.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -553,7 +553,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (bad) atomicOr(a.status, kStatusBadRow);
   } else if (warp >= kMmaWarp) {
     fewer_registers<kRegsMma>();
-    if (warp == kMmaWarp || warp == kValueWarp) {
+    if (warp != kOtherWarp) {
       // ============================ MMA issue ==============================================
       // One warp issues the score products, one the value products: each product waits for its own operands, and
       // the tensor pipe has the other one's to do meanwhile.  A whole warp walks the loop and one elected lane issues,
@@ -561,47 +561,62 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const bool leader = elect_one();
       bool ok = true;
       Segment g;
-      if (warp == kMmaWarp) {
+      if (warp != kValueWarp) {
+        const int h = warp - kMmaWarp;
         constexpr uint32_t idesc = tc::idesc_bf16_f32(kRows, kOwnKeys, false, false);
         const uint64_t desc_q = tc::smem_desc(sbase, 16, 1024, tc::kSwizzle128B);
         const uint64_t desc_s = tc::smem_desc(sbase + kOffScore, 16, 1024, tc::kSwizzle128B);
         const uint64_t desc_k = tc::smem_desc(sbase + kOffOwn, 16, 1024, tc::kSwizzle128B);
-        uint32_t tile = 0, seg = 0;
-        uint32_t used = 0;  // places for scores that have been used, and (bits 2, 3) the parity of their last use
+        const uint32_t d_s = tmem + kColS + 32 * h;
+        uint32_t before = 0, seg = 0, uses = 0;  // tiles of the row groups before; tiles of this parity so far
         while (ok && next_segment(a, cur, g)) {
           if (g.nt == 0) continue;
           ok = wait_spin(&ctl.q_full, seg & 1u, &ctl.abort, a.status);
           ++seg;
-          for (int t = 0; ok && t < g.nt; ++t, ++tile) {
-            const uint32_t h = t & 1;
-            if (used >> h & 1u) ok = wait_spin(&ctl.s_free[h], used >> (2 + h) & 1u, &ctl.abort, a.status);
+          for (int t = h; ok && t < g.nt; t += 2, ++uses) {
+            const uint32_t tile = before + t;
+            if (uses > 0) ok = wait_spin(&ctl.s_free[h], (uses - 1) & 1u, &ctl.abort, a.status);
             ok = ok && wait_spin(&ctl.full[tile % kOwnStages], tile / kOwnStages & 1u, &ctl.abort, a.status);
             if (!ok) break;
-            used = used >> h & 1u ? used ^ 4u << h : used | 1u << h;
             fence_proxy_async_smem();
             tc::fence_after_sync();
             const uint64_t ds = desc_s + (tile % kScoreStages) * (uint32_t)(kScoreBytes >> 4),
                            dv = desc_k + (tile % kOwnStages) * (uint32_t)(kValueBytes >> 4);
-            const uint64_t half0 = rank == 0 ? dv : ds, half1 = rank == 0 ? ds : dv;  // latent channels 0..255, 256..511
-            const uint32_t d_s = tmem + kColS + 32 * h;
             if (leader) {
-#pragma unroll
-              for (int k = 0; k < 32; ++k) {
-                const uint64_t d = (k < 16 ? half0 : half1) + (uint32_t)((((k >> 2) & 3) * kBlockBytes + (k & 3) * 32) >> 4);
+              // What only the scores read goes first, so that its place is free for the next tile but one sooner.
+              const bool low = rank == 0;  // the values' half of the latent is channels 0..255
+              auto product = [&](uint64_t keys, int k, uint32_t accumulate) {  // latent channels 16 k .. + 15
+                const uint64_t d = keys + (uint32_t)((((k >> 2) & 3) * kBlockBytes + (k & 3) * 32) >> 4);
                 if (k < kQSteps)
-                  mma_bf16_ts(d_s, tmem + kColQ + 8 * k, d, idesc, k > 0);
+                  mma_bf16_ts(d_s, tmem + kColQ + 8 * k, d, idesc, accumulate);
                 else
-                  tc::mma_bf16_ss(d_s, desc_q + (uint32_t)((((k - kQSteps) >> 2) * kQBlock + (k & 3) * 32) >> 4), d, idesc, 1u);
+                  tc::mma_bf16_ss(d_s, desc_q + (uint32_t)((((k - kQSteps) >> 2) * kQBlock + (k & 3) * 32) >> 4), d, idesc,
+                                  accumulate);
+              };
+              if (low) {
+#pragma unroll
+                for (int k = 16; k < 32; ++k) product(ds, k, k > 16);
+              } else {
+#pragma unroll
+                for (int k = 0; k < 16; ++k) product(ds, k, k > 0);
               }
 #pragma unroll
               for (int k = 0; k < 4; ++k)
                 tc::mma_bf16_ss(d_s, desc_q + (uint32_t)((2 * kQBlock + k * 32) >> 4),
                                 ds + (uint32_t)((4 * kBlockBytes + k * 32) >> 4), idesc, 1u);
-              tc::mma_commit(&ctl.s_full[h]);
               tc::mma_commit(&ctl.empty_score[tile % kScoreStages]);
+              if (low) {
+#pragma unroll
+                for (int k = 0; k < 16; ++k) product(dv, k, 1u);
+              } else {
+#pragma unroll
+                for (int k = 16; k < 32; ++k) product(dv, k, 1u);
+              }
+              tc::mma_commit(&ctl.s_full[h]);
               mbar_arrive(&ctl.s_full[h]);
             }
           }
+          before += g.nt;
         }
       } else {
         constexpr uint32_t idesc = tc::idesc_bf16_f32(kRows, kHalfLatent, false, true);
@@ -625,12 +640,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                            dx = desc_o + (tile % kOtherStages) * (uint32_t)(kValueBytes >> 4);
             if (leader) {
 #pragma unroll
-              for (int k = 0; k < 4; ++k)  // own keys, then the other CTA's
+              for (int k = 0; k < 4; ++k) {  // own keys, then the other CTA's
                 tc::mma_bf16_ss(tmem + kColO, (k < 2 ? desc_p : desc_x) + (4 * h + 2 * (k & 1)) * (uint32_t)(kPPiece >> 4),
                                 (k < 2 ? dv : dx) + (uint32_t)((k & 1) * 2048 >> 4), idesc, t > 0 || k > 0);
+                if (k == 1) tc::mma_commit(&ctl.empty_own[tile % kOwnStages]);
+              }
               tc::mma_commit(&ctl.pv_done[h]);
               commit_to(&ctl.pv_done[h], rank ^ 1u);
-              tc::mma_commit(&ctl.empty_own[tile % kOwnStages]);
               tc::mma_commit(&ctl.empty_other[tile % kOtherStages]);
             }
           }
@@ -642,16 +658,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (uint32_t it = 0; it < (1u << 30); ++it)
         if (mbar_try_wait(&ctl.mma_idle, 0) || ((it & 63u) == 63u && global_timer_ns() - t0 > kWaitLimitNs)) break;
       __syncwarp();
-    } else if (warp < kOtherWarp + kOtherWarps) {
+    } else {
       // ==================== gather: the other CTA's keys, this CTA's half of the latent ====================
-      // A warp fills 16 keys: 128 bytes of four per instruction.
-      const int gw = warp - kOtherWarp, sub = lane >> 3, chunk = lane & 7;
+      // 128 bytes of four keys per instruction.
+      const int sub = lane >> 3, chunk = lane & 7;
       uint32_t so = 0, po = 1;
       bool stop = false;
       Segment g;
-      const uint32_t to = (16 * gw + sub) * 128, to_a = to + ((chunk ^ sub) << 4), to_b = to + ((chunk ^ (sub + 4)) << 4);
+      const uint32_t to_a = sub * 128 + ((chunk ^ sub) << 4), to_b = sub * 128 + ((chunk ^ (sub + 4)) << 4);
       while (!stop && next_segment(a, cur, g)) {
-        const int64_t key0 = g.tile0 * kKeys + kOwnKeys * (rank ^ 1u) + 16 * gw + (lane & 15);
+        const int64_t key0 = g.tile0 * kKeys + kOwnKeys * (rank ^ 1u) + lane;
         int32_t id0 = load_id(a, g, key0, 0), id1 = load_id(a, g, key0, 1);
 #pragma unroll 1
         for (int t = 0; t < g.nt; ++t) {
@@ -664,7 +680,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           const uint32_t value = sbase + kOffOther + so * kValueBytes;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
+          for (int k = 0; k < 8; ++k) {
             const int32_t r = __shfl_sync(0xffffffffu, row, 4 * k + sub);
             const __nv_bfloat16* src = a.kv_pool + (int64_t)(r < 0 ? 0 : r) * kDRow + rank * kHalfLatent + chunk * 8;
 #pragma unroll
@@ -873,6 +889,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           mbar_arrive(&ctl.m_set[half][quad]);
         }
       }
+      // Sums go where the last row group's stood: all warps of both CTAs have read those once a tile of this one has been
+      // through.  Warps without a tile wait for the other parity's.
+      if (half == 1 && g.nt == 1 && active && !stop)
+        stop = !wait_warp(&ctl.m_set[0][quad], uses_other & 1u, &ctl.abort, a.status);
       if (stop) break;
       tile += g.nt;
       uses_other += half ? (g.nt + 1) >> 1 : g.nt >> 1;

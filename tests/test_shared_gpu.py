@@ -109,8 +109,9 @@ def test_climbing_scores(step):
     c.q_rope[..., 0] = 14.0
     j = torch.arange(1500, device="cuda", dtype=torch.float32)
     c.pool[c.shared_indices.long(), 512] = (step * j / 16).to(torch.bfloat16)
-    # scores up to 14 * 20 * 94 * 0.072 = 1900, one rounding of 2^-24 of that per sum step of a k-block: 16 * 2^-24 * 1900
-    c.check(0, lse_slack=1.9e-3)
+    # Scores up to 14 * 20 * 94 * 0.072 = 1900.  The 576 channels are added up in 36 steps of 16, and a step may cut the
+    # running fp32 sum off below its last bit, 2^-23 of it: 36 * 2^-23 * 1900 = 8.2e-3, whichever channels come first.
+    c.check(0, lse_slack=8.2e-3)
 
 
 def test_one_half_far_above_the_other():
@@ -160,6 +161,24 @@ def test_repeated_calls_give_the_same_bits():
     c = Case([(3000, [(50, 2)] * 20), (100, [(1, 1)])], 16, seed=12)
     first = c.run()
     for _ in range(5):
+        again = c.run()
+        assert torch.equal(again[0], first[0]) and torch.equal(again[1], first[1])
+
+
+def test_row_groups_of_one_tile():
+    """Many own parts of one tile (and a few of more) in a row: what a row group leaves is read before the next one's."""
+    c = Case([(70, [(1 + 7 * i % 60 if i % 9 else 150, 2) for i in range(500)])], 64, seed=18)
+    c.q_rope[..., 0] = 14.0
+    c.pool[c.kv_indices.long(), 512] = (torch.arange(len(c.kv_indices), device="cuda") % 40).to(torch.bfloat16)
+    first = c.run()
+    assert first[2] == 0
+    # A weight in bf16 is off by at most 2^-8 of itself, in O's sum and its divisor alike: |dO| <= 2^-8 sum p |v - O|
+    # <= 2^-8 (max|v| + |O|), and as much as 2^-8 |O| more for O's own rounding.  32 million values: no mean hides it.
+    o, lse = c.exact()
+    v = float(c.pool[:, :512].abs().max())
+    assert bool(((first[0].double() - o).abs() <= 2.0 ** -8 * (v + 2 * o.abs())).all())
+    assert float((first[1].double() - lse).abs().max()) <= 1e-3
+    for _ in range(20):
         again = c.run()
         assert torch.equal(again[0], first[0]) and torch.equal(again[1], first[1])
 
