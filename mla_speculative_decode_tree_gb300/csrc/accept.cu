@@ -12,19 +12,26 @@
 // What has to be read is little: of a node on the path one value per child, and
 // whole rows only where the walk ends (the target row, and the draft row after a
 // rejection) or where a second child is tried after a rejection.  So what bounds
-// it is latency: tree -> the children's probabilities, fetched for all nodes at
-// once -> one pass over a row for its sum -> the search in the part that holds
-// the token.  The walk runs on shared memory, in every CTA alike; the CTAs of a
-// cluster only exchange sums.
+// a request is latency -- tree -> the children's probabilities, fetched for all
+// nodes at once -> one pass over a row for its sum -> the search in the part that
+// holds the token, about 5 us -- and, where children are rejected, the arithmetic
+// of the passes.  The walk runs on shared memory, in every CTA alike; the CTAs of
+// a cluster only exchange sums (about 1 us).
 //
 // A pass adds w(p) without 64-bit conversions, which this GPU does slowly: p *
 // 2^19 rounded to a whole number h by adding 2^23, and what that leaves, exact in
 // fp32, times 2^19 rounded the same way; w = h * 2^19 + l, since h * 2^19 is even
 // and so moves no tie.  As w never falls where p grows, min(w(p), w(q)) = w(min(p,
 // q)), and after a node's first rejection max(w(p) - w(q), 0) = w(p) - w(q) where
-// p > q: both sums need no 64-bit arithmetic per entry either.  Later rejections
-// of a node take the general way.  16 requests, trees of 9, 131,072 tokens: 50.6 ->
-// 29.8 us; 64 requests, trees of up to 16, 150,001 tokens: 199 -> 97.8.
+// p > q: both sums need no 64-bit arithmetic per entry either.  After the first
+// rejection only entries with p > q count: each warp keeps theirs in shared memory,
+// and later rejections' passes run on those, r = w(p) less the sum of the s.
+//
+// 16 requests, trees of 9, 131,072 tokens: 17.7 us (10 us for a request with one
+// rejection and a child behind it, 15 us with two); 64 requests, trees of up to 16,
+// 150,001 tokens: 47.8 us, of which the rows' 77 MB take 11.3.  In 64 bits throughout
+// these took 50.6 and 199 us, with 19-bit parts 29.8 and 97.8; what is kept, clusters
+// of 16 and a search by the whole CTA did the rest.
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -34,42 +41,35 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kMaxWarps = 32;
+constexpr int kThreads = 512, kWarps = kThreads / 32;  // two CTAs per SM (of 1024 or 256 threads: no faster)
 constexpr int kOne = 38;
-constexpr int kMaxCluster = 8;
-constexpr int kUnroll = 4;
+constexpr int kMaxCluster = 16;
+constexpr int kUnroll = 2;
 
 // (a NaN, a negative probability: 0; above 1: 1)
 __device__ __forceinline__ float clip(float p) { return fminf(fmaxf(p, 0.f), 1.f); }
 
-// Sums of weights in two parts of 19 bits; flushed before they overflow.
+// Sums of at most kMost weights in two parts of 19 bits.  Each part is the lower bits of a float with a constant on top;
+// what the constants add up to, modulo 2^32, comes off at the end.
+template <int kMost>
 struct Sum {
-  uint32_t high = 0;
-  int32_t low = 0;
-  static __device__ __forceinline__ void split(float p, uint32_t& h, int32_t& l) {
+  static_assert(kMost <= 2048, "the parts' sums have to fit 31 bits");
+  uint32_t high = 0, low = 0;
+  __device__ __forceinline__ void add(float p) {
     const float t = fmaf(p, 524288.f, 8388608.f);             // 2^23 + h
     const float rest = fmaf(p, 524288.f, -(t - 8388608.f));   // exact, at most half
-    h = __float_as_uint(t) - 0x4B000000u;
-    l = (int32_t)(__float_as_uint(fmaf(rest, 524288.f, 12582912.f)) - 0x4B400000u);
+    high += __float_as_uint(t);
+    low += __float_as_uint(fmaf(rest, 524288.f, 12582912.f));
   }
-  __device__ __forceinline__ void add(float p) {
-    uint32_t h;
-    int32_t l;
-    split(p, h, l);
-    high += h;
-    low += l;
-  }
-  __device__ __forceinline__ int64_t flush() {
-    const int64_t v = ((int64_t)high << 19) + low;
-    high = 0;
-    low = 0;
-    return v;
+  // of exactly n weights
+  __device__ __forceinline__ int64_t value(uint32_t n) const {
+    return ((int64_t)(high - n * 0x4B000000u) << 19) + (int32_t)(low - n * 0x4B400000u);
   }
 };
 __device__ __forceinline__ int64_t weight(float p) {
-  Sum s;
+  Sum<1> s;
   s.add(clip(p));
-  return s.flush();
+  return s.value(1);
 }
 __device__ __forceinline__ int64_t random24(float u) {
   return (int64_t)fminf(fmaxf(floorf(u * 16777216.f), 0.f), 16777215.f);
@@ -79,12 +79,20 @@ __device__ __forceinline__ int64_t scaled(int64_t w, int64_t Z) {
   return (int64_t)((__umul64hi((uint64_t)w, (uint64_t)Z) << (64 - kOne)) | (((uint64_t)w * (uint64_t)Z) >> kOne));
 }
 
-// The same of w = h * 2^19 + l: each shift drops what a floor drops.
-__device__ __forceinline__ int64_t scaled(uint32_t h, int32_t l, int64_t Z) {
-  const int32_t zh = (int32_t)(Z >> 19), zl = (int32_t)(Z & 0x7FFFF);
-  const int64_t mid = (int64_t)(int32_t)h * zl + (int64_t)l * zh + (((int64_t)l * zl) >> 19);
-  return (int64_t)(int32_t)h * zh + (mid >> 19);
-}
+// A weight of an entry in [0, 1] as m * 2^e, m below 2^24: what a float holds.  (From 2^-15 on the weight is the float's
+// own whole number, below a sum with 2^23 rounds it.)  Products with Z then fit 64 bits.
+struct Weight {
+  uint32_t m;
+  int e;
+  explicit __device__ __forceinline__ Weight(float p) {
+    const uint32_t bits = __float_as_uint(p);
+    const bool whole = p >= 0x1p-15f;
+    m = whole ? (bits & 0x7FFFFFu) | 0x800000u : __float_as_uint(fmaf(p, 0x1p38f, 8388608.f)) - 0x4B000000u;
+    e = whole ? (int)(bits >> 23) - 112 : 0;
+  }
+  __device__ __forceinline__ int64_t value() const { return (int64_t)((uint64_t)m << e); }
+  __device__ __forceinline__ int64_t times(int64_t Z) const { return (int64_t)(((uint64_t)Z * m) >> (kOne - e)); }
+};
 
 // Four neighbouring entries of a row; `at` is the first one's index, `fast`
 // says that their address is a multiple of 16 bytes.
@@ -108,11 +116,18 @@ struct Shared {
   int64_t z[kMaxQLen];                              // Z at each rejection of the node that the walk is at
   int32_t rejected[kMaxQLen];                       // and the tokens
   int32_t path[kMaxQLen];
-  int64_t part[kMaxWarps];
+  int64_t part[kWarps];
   int64_t all[2][kMaxCluster];  // the CTAs' sums; two in turn, so that an exchange needs one cluster barrier
   int cur, num, tried, last;    // the walk's state; last: the last child looked at
   int64_t Z;
   int ask;  // 1: the walk needs sum min(r, s) for its next child, 0: it has ended
+};
+
+// What a warp keeps, in shared memory, of a node's entries after the first rejection: p and q of those that still have r >
+// 0 (p > q).  Vectors from `from` on found no room and are read again by every pass.
+struct Kept {
+  float2* entry;
+  int room, n, from;
 };
 
 // What a pass adds up, per entry.
@@ -130,17 +145,91 @@ struct Node {
 
   // r of one entry.
   __device__ __forceinline__ int64_t left(float pv, float qv, int x) const {
-    int64_t r = weight(pv);
-    const int64_t w = kDraft && tried > 0 ? weight(qv) : 0;
-    for (int j = 0; j < tried; ++j) {
-      const int64_t s = kDraft ? (j == 0 ? w : scaled(w, z[j])) : (token[j] == x ? z[j] : 0);  // (Z is 2^38 at first)
-      r = r > s ? r - s : 0;
+    int64_t r = Weight(clip(pv)).value();
+    if (kDraft) {
+      if (tried > 0) {
+        const Weight w(clip(qv));
+        r -= w.value();  // (Z is 2^38 at first)
+        for (int j = 1; j < tried; ++j) r -= w.times(z[j]);
+        r = r > 0 ? r : 0;
+      }
+    } else {
+      for (int j = 0; j < tried; ++j) r = token[j] == x ? (r > z[j] ? r - z[j] : 0) : r;
     }
     return r;
   }
   // Vector k covers entries 4k - off .. 4k - off + 3.
   __device__ __forceinline__ float4 target(int k) const { return load4(p, 4 * k - off, vocab, true); }
   __device__ __forceinline__ float4 draft(int k) const { return load4(q, 4 * k - off, vocab, q_fast); }
+
+  // The first rejection's sum min(w(p), w(q)) over vectors begin .. end - 1, by a whole warp; what is left is kept.
+  __device__ __forceinline__ int64_t first(int begin, int end, int lane, Kept& kept) const {
+    int64_t t = 0;
+    int n = 0, from = end;
+    bool keep = kept.room > 0;
+    if (!keep) from = begin;
+#pragma unroll 1
+    for (int k0 = begin; k0 < end; k0 += 32 * kUnroll) {
+      float4 pv[kUnroll], qv[kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int k = k0 + 32 * u + lane;
+        pv[u] = qv[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k < end) {
+          pv[u] = target(k);
+          qv[u] = draft(k);
+        }
+      }
+      Sum<4 * kUnroll> less;
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const float a[4] = {pv[u].x, pv[u].y, pv[u].z, pv[u].w}, b[4] = {qv[u].x, qv[u].y, qv[u].z, qv[u].w};
+        int at = n;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float x = clip(a[i]), y = clip(b[i]);
+          less.add(fminf(x, y));
+          if (keep) {
+            const uint32_t more = __ballot_sync(0xffffffffu, x > y);
+            const int place = at + __popc(more & ((1u << lane) - 1));
+            if (x > y && place < kept.room) kept.entry[place] = make_float2(x, y);
+            at += __popc(more);
+          }
+        }
+        if (keep && at > kept.room) {
+          keep = false;
+          from = min(k0 + 32 * u, end);
+        }
+        if (keep) n = at;
+      }
+      t += less.value(4 * kUnroll);
+    }
+    kept.n = n;
+    kept.from = from;
+    __syncwarp();
+    return t;
+  }
+  // The same sums as below after two rejections or more, of the kept entries.
+  template <What kWhat>
+  __device__ __forceinline__ int64_t later(int lane, const Kept& kept) const {
+    const int n = kWhat == What::kTaken ? tried - 1 : tried;
+    const int64_t z1 = n > 1 ? z[1] : 0, zn = kWhat == What::kTaken ? z[n] : 0;
+    int64_t t = 0;
+#pragma unroll 2
+    for (int i = lane; i < kept.n; i += 32) {
+      const float2 v = kept.entry[i];
+      const Weight w(v.y);
+      int64_t r = Weight(v.x).value() - w.value() - w.times(z1);
+      for (int j = 2; j < n; ++j) r -= w.times(z[j]);
+      r = r > 0 ? r : 0;
+      if (kWhat == What::kTaken) {
+        const int64_t last = w.times(zn);
+        r = r < last ? r : last;
+      }
+      t += r;
+    }
+    return t;
+  }
 
   // Sum over vectors first, first + 32, ... below end.
   template <What kWhat>
@@ -160,7 +249,7 @@ struct Node {
           if (both) qv[u] = draft(k + 32 * u);
         }
       }
-      Sum more, less;
+      Sum<4 * kUnroll> more, less;
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
         const float a[4] = {pv[u].x, pv[u].y, pv[u].z, pv[u].w}, b[4] = {qv[u].x, qv[u].y, qv[u].z, qv[u].w};
@@ -181,30 +270,29 @@ struct Node {
             }
           } else {
             // r is what the sum of the s leaves of w(p): an r that has reached 0 stays there.
-            uint32_t h;
-            int32_t l;
-            Sum::split(y, h, l);
-            int64_t s = ((int64_t)h << 19) + l;
-            for (int j = 1; j < n; ++j) s += scaled(h, l, z[j]);
-            int64_t r = weight(x) - s;
+            const Weight w(y);
+            int64_t r = Weight(x).value() - w.value();
+            for (int j = 1; j < n; ++j) r -= w.times(z[j]);
             r = r > 0 ? r : 0;
             if (kWhat == What::kTaken) {
-              s = scaled(h, l, z[n]);
-              r = r < s ? r : s;
+              const int64_t last = w.times(z[n]);
+              r = r < last ? r : last;
             }
             t += r;
           }
         }
       }
-      t += more.flush() - less.flush();
+      if (simple || !both) {
+        t += more.value(4 * kUnroll);
+        if (both && kWhat == What::kLeft) t -= less.value(4 * kUnroll);
+      }
     }
     return t;
   }
 };
 
-template <bool kDraft, int kThreads>
-__global__ void __launch_bounds__(kThreads, 1024 / kThreads) accept_kernel(AcceptArgs a) {
-  constexpr int kWarps = kThreads / 32;
+template <bool kDraft>
+__global__ void __launch_bounds__(kThreads, 2) accept_kernel(AcceptArgs a) {
   __shared__ Shared s;
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -251,19 +339,29 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) accept_kernel(Accep
     __syncwarp();
   }
 
+  extern __shared__ float2 room[];
+  Kept kept;
+  kept.room = kDraft ? a.keep : 0;  // entries per warp
+  kept.entry = room + warp * kept.room;
+  kept.n = kept.from = 0;
+  int kept_node = -1;
   Node<kDraft> node;
   node.vocab = a.vocab;
   node.z = s.z;
   node.token = s.rejected;
-  int round = 0, w0 = 0, w1 = 0;
+  int round = 0, w0 = 0, w1 = 0;  // this warp's vectors
+  const auto w_first = [&](int w) {
+    const int vectors = (node.off + a.vocab + 3) / 4, per = (vectors + C - 1) / C, v0 = min(rank * per, vectors);
+    return min(v0 + w * ((per + kWarps - 1) / kWarps), min(v0 + per, vectors));
+  };
+  const auto w_end = [&](int w) {
+    const int vectors = (node.off + a.vocab + 3) / 4, per = (vectors + C - 1) / C, v0 = min(rank * per, vectors);
+    return min(w_first(w) + (per + kWarps - 1) / kWarps, min(v0 + per, vectors));
+  };
   // A sum over the row by warps' parts (s.part) and CTAs (s.all), all of them known to all CTAs.
   auto pass = [&](auto&& f) -> int64_t {
-    const int vectors = (node.off + a.vocab + 3) / 4;
-    const int per = (vectors + C - 1) / C;
-    const int v0 = min(rank * per, vectors), v1 = min(v0 + per, vectors);
-    const int per_warp = (per + kWarps - 1) / kWarps;
-    w0 = min(v0 + warp * per_warp, v1);
-    w1 = min(w0 + per_warp, v1);
+    w0 = w_first(warp);
+    w1 = w_end(warp);
     const int64_t t = warp_sum(f());
     if (lane == 0) s.part[warp] = t;
     __syncthreads();
@@ -341,14 +439,30 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) accept_kernel(Accep
     node.tried = s.tried;
     if (!kDraft || !s.ask) break;
     const int64_t z = s.z[s.tried - 1];
-    const int64_t taken = pass([&] { return node.template sum<What::kTaken>(w0 + lane, w1); });
+    const int64_t taken = pass([&]() -> int64_t {
+      if constexpr (kDraft) {
+        if (node.tried == 1) {
+          kept_node = s.cur;
+          return node.first(w0, w1, lane, kept);
+        }
+        const int64_t t = node.template later<What::kTaken>(lane, kept);
+        return t + node.template sum<What::kTaken>(kept.from + lane, w1);
+      }
+      return 0;
+    });
     if (tid == 0) s.Z = z > taken ? z - taken : 0;
     __syncthreads();
   }
 
   // ---- the next token -------------------------------------------------------------
   auto left_sum = [&]() -> int64_t {
-    int64_t t = node.template sum<What::kLeft>(w0 + lane, w1);
+    int64_t t = 0;
+    if (kDraft && kept_node == s.cur && node.tried > 1) {
+      t = node.template later<What::kLeft>(lane, kept);
+      t += node.template sum<What::kLeft>(kept.from + lane, w1);
+    } else {
+      t = node.template sum<What::kLeft>(w0 + lane, w1);
+    }
     if (!kDraft) {
       // Rejected tokens in this warp's part: what they lack (each token once).
       for (int j = lane; j < node.tried; j += 32) {
@@ -378,68 +492,67 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) accept_kernel(Accep
   const int64_t aim = (int64_t)__umul64hi((uint64_t)random24(u_next) << 40, (uint64_t)sum);
   int64_t mine = 0;
   for (int c = 0; c < rank; ++c) mine += s.all[round & 1][c];
-  for (int w = 0; w < warp; ++w) mine += s.part[w];
-  if (sum == 0 || aim < mine || aim >= mine + s.part[warp]) return;
-  // This warp's part holds the token.
-#pragma unroll 1
-  for (int k0 = w0; k0 < w1; k0 += 32 * kUnroll) {
-    float4 pv[kUnroll], qv[kUnroll];
+  if (sum == 0 || aim < mine || aim >= mine + s.all[round & 1][rank]) return;
+  // A warp's part in this CTA holds the token; all of the CTA looks through that part, a vector a thread.
+  const auto scan = [&](int64_t v) -> int64_t {  // over the lanes, each with those before it
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int k = k0 + 32 * u + lane;
-      pv[u] = qv[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (k < w1) {
-        pv[u] = node.target(k);
-        if (kDraft && node.tried > 0) qv[u] = node.draft(k);
-      }
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += y;
     }
+    return v;
+  };
+  int64_t parts = lane < kWarps ? s.part[lane] : 0, upto = scan(parts);
+  const int part = min(__ffs(__ballot_sync(0xffffffffu, mine + upto > aim)) - 1, kWarps - 1);
+  mine += __shfl_sync(0xffffffffu, upto - parts, part);
+  w0 = w_first(part);
+  w1 = w_end(part);
 #pragma unroll 1
-    for (int u = 0; u < kUnroll; ++u) {
-      const int k = k0 + 32 * u + lane, x = 4 * k - node.off;
-      float4 p4 = pv[0], q4 = qv[0];
-#pragma unroll
-      for (int i = 1; i < kUnroll; ++i) {
-        if (i == u) {
-          p4 = pv[i];
-          q4 = qv[i];
-        }
-      }
-      const int64_t r[4] = {node.left(p4.x, q4.x, x), node.left(p4.y, q4.y, x + 1), node.left(p4.z, q4.z, x + 2),
-                            node.left(p4.w, q4.w, x + 3)};
-      const int64_t own = (r[0] + r[1]) + (r[2] + r[3]);
-      int64_t upto = own;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += y;
-      }
-      const uint32_t past = __ballot_sync(0xffffffffu, mine + upto > aim);
-      if (past) {
-        if (lane == __ffs(past) - 1) {
-          int64_t at = mine + upto - own;
-          int i = 0;
-          while (i < 3 && (at += r[i]) <= aim) ++i;
-          a.next_tokens[b] = x + i;
-        }
-        return;
-      }
-      mine += __shfl_sync(0xffffffffu, upto, 31);
+  for (int k0 = w0; k0 < w1; k0 += kThreads) {
+    const int k = k0 + tid, x = 4 * k - node.off;
+    int64_t r[4] = {0, 0, 0, 0};
+    if (k < w1) {
+      const float4 p4 = node.target(k), q4 = kDraft && node.tried > 0 ? node.draft(k) : make_float4(0.f, 0.f, 0.f, 0.f);
+      r[0] = node.left(p4.x, q4.x, x);
+      r[1] = node.left(p4.y, q4.y, x + 1);
+      r[2] = node.left(p4.z, q4.z, x + 2);
+      r[3] = node.left(p4.w, q4.w, x + 3);
     }
+    const int64_t own = (r[0] + r[1]) + (r[2] + r[3]);
+    upto = scan(own);
+    __syncthreads();  // (the parts have been read)
+    if (lane == 31) s.part[warp] = upto;
+    __syncthreads();
+    parts = lane < kWarps ? s.part[lane] : 0;
+    const int64_t to = scan(parts), before = mine + __shfl_sync(0xffffffffu, to - parts, warp),
+                  all = __shfl_sync(0xffffffffu, to, 31);
+    if (before + upto - own <= aim && aim < before + upto) {
+      int64_t at = before + upto - own;
+      int i = 0;
+      while (i < 3 && (at += r[i]) <= aim) ++i;
+      a.next_tokens[b] = x + i;
+    }
+    mine += all;
+    if (mine > aim) return;
   }
 }
 
 }  // namespace
 
 cudaError_t launch_accept(const AcceptArgs& a, cudaStream_t stream) {
-  // As many CTAs per request as a cluster has, while each has 4096 entries: a batch is as slow as its request with the
-  // most rejections (64 requests, up to 16 nodes, 150,001 tokens: clusters of 2 / 4 / 8 take 170 / 119 / 98 us).  1024
-  // threads where a CTA has its SM to itself, else two CTAs of 512 (16 requests: 30 against 38 us; 64: 120 against 98).
+  // CTAs per request.  A batch is as slow as its request with the most rejections, whose passes are bound by arithmetic:
+  // up to 16 while each has 3500 entries (16 requests, 131,072 tokens: clusters of 4 / 8 / 16 take 38 / 21.5 / 18.7 us).
+  // But no more than twice what the GPU has room for at once, or requests queue up for their start, dependent reads of 2
+  // us (64 requests, 150,001 tokens: 8 / 16 take 46 / 56 us).  And enough of them to keep the entries of a request that is
+  // half rejected (256 requests, 131,072 tokens: 2 / 4 take 150 / 117 us).
+  const int64_t resident = 2 * 152;
   int C = 1;
-  while (C < kMaxCluster && a.vocab > 4096 * C) C *= 2;
-  const bool alone = (int64_t)a.batch * C <= 152;
+  while (C < kMaxCluster &&
+         ((a.draft && a.vocab > 32768 * C) || (a.vocab >= 7000 * C && a.batch * C <= resident)))
+    C *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.batch * C));
-  cfg.blockDim = dim3(alone ? 1024 : 512);
+  cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -447,9 +560,15 @@ cudaError_t launch_accept(const AcceptArgs& a, cudaStream_t stream) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  auto kernel = a.draft ? (alone ? accept_kernel<true, 1024> : accept_kernel<true, 512>)
-                        : (alone ? accept_kernel<false, 1024> : accept_kernel<false, 512>);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
+  // Shared memory for what is kept, of half an SM.
+  const size_t room = a.draft ? 104u * 1024u : 0;
+  AcceptArgs args = a;
+  args.keep = (int)(room / sizeof(float2)) / kWarps;
+  cfg.dynamicSmemBytes = room;
+  auto kernel = a.draft ? accept_kernel<true> : accept_kernel<false>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess && room) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)room);
+  if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, kernel, args);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -115,6 +115,7 @@ struct AcceptArgs {
   int32_t* accepted;  // [batch, T]
   int32_t* num_accepted;
   int32_t* next_tokens;
+  int32_t keep;  // entries per warp that fit the shared memory (set at the launch)
 };
 struct CommitArgs {
   PoolLayers pool;

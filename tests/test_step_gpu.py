@@ -150,6 +150,36 @@ def test_a_large_vocabulary_and_tokens_at_its_ends():
     assert got[2].tolist() == [0, 262146]
 
 
+@pytest.mark.parametrize("drawn", [True, False], ids=["drawn", "proposed"])
+@pytest.mark.parametrize("vocab", [150001, 262147])
+def test_many_rejections_in_a_large_vocabulary(drawn, vocab):
+    """Ten children of one node: a target that is nearly flat with a draft that is not (nearly all entries have p > q, more
+    than are kept), and a draft close to the target."""
+    d = Drafts([11, 11], vocab, drawn, seed=9, near=0.3)
+    d.parents = np.concatenate([[-1] + [0] * 10] * 2)
+    d.target[0] = probabilities(np.random.default_rng(1), 1, vocab, "flat")
+    if drawn:
+        d.draft[0] = probabilities(np.random.default_rng(2), 1, vocab, "sharp")
+        d.tokens[1:11] = np.argsort(d.draft[0])[-10:]
+    d.u[:] = np.float32(1 - 2.0 ** -24)
+    d.check()
+
+
+def test_weights_at_their_boundaries():
+    """Values around 2^-15, 2^-19 and 2^-39, halves of a weight's step, 1 and what is below the smallest normal float."""
+    base = [2.0 ** -15, 2.0 ** -16, 2.0 ** -19, 2.0 ** -38, 2.0 ** -39, 3 * 2.0 ** -39, 5 * 2.0 ** -39, 2.0 ** -40, 1e-40, 0.0,
+            0.25, 0.5, 1.0, 2.0 ** -14, 1 / 3, (2 ** 23 - 0.5) * 2.0 ** -38, (2 ** 22 + 0.5) * 2.0 ** -38]
+    f = np.array(base, np.float32)
+    f = np.unique(np.concatenate([f, np.nextafter(f, np.float32(2)), np.nextafter(f, np.float32(0))]))
+    for seed in range(8):
+        rng = np.random.default_rng(seed)
+        d = Drafts([5, 4, 6], 2 * f.size, True, seed=seed)
+        d.parents = np.concatenate([[-1] + [0] * 4, [-1] + [0] * 3, [-1] + [0] * 5])
+        d.target[:], d.draft[:] = rng.choice(f, d.target.shape), rng.choice(f, d.target.shape)
+        d.u[:] = np.float32(1 - 2.0 ** -24)
+        d.check()
+
+
 def test_distribution_of_the_first_new_token():
     """20,000 requests of one root and two drawn children: counts of the token behind the root within five standard
     deviations of the target's."""
