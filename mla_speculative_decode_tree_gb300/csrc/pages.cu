@@ -235,6 +235,49 @@ __global__ void __launch_bounds__(kFreeThreads, 1)
   cluster.sync();  // nobody leaves while its sums are read
 }
 
+// The same of at most kFewPages pages, by one CTA with eight counts per thread: no bits, no cluster.  2048 pages: 4.9 ->
+// 3.0 us, of which an empty launch is 1.5.
+constexpr int kFewPages = 8 * kFreeThreads;
+
+__global__ void __launch_bounds__(kFreeThreads, 1)
+    list_free_few_kernel(const int32_t* refs, int num_pages, int32_t* free_pages, int32_t* num_free) {
+  __shared__ uint32_t warp_sum[kFreeWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const bool wide = (reinterpret_cast<uintptr_t>(refs) & 15) == 0;
+  uint32_t bits = 0;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int page = 8 * tid + 4 * k;
+    if (wide && page + 4 <= num_pages) {
+      const int4 v = __ldg(reinterpret_cast<const int4*>(refs + page));
+      bits |= ((v.x == 0) | (v.y == 0) << 1 | (v.z == 0) << 2 | (v.w == 0) << 3) << (4 * k);
+    } else {
+      for (int i = 0; i < 4; ++i)
+        if (page + i < num_pages && __ldg(refs + page + i) == 0) bits |= 1u << (4 * k + i);
+    }
+  }
+  const uint32_t mine = __popc(bits);
+  uint32_t upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += y;
+  }
+  if (lane == 31) warp_sum[warp] = upto;
+  __syncthreads();
+  uint32_t ws = warp_sum[lane], wu = ws;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, wu, o);
+    if (lane >= o) wu += y;
+  }
+  int at = (int)(__shfl_sync(0xffffffffu, wu - ws, warp) + upto - mine);
+  const int total = (int)__shfl_sync(0xffffffffu, wu, 31);
+  for (; bits; bits &= bits - 1) free_pages[at++] = 8 * tid + __ffs(bits) - 1;
+  for (int i = total + tid; i < num_pages; i += kFreeThreads) free_pages[i] = -1;
+  if (tid == 0) *num_free = total;
+}
+
 // ---- fork ----------------------------------------------------------------------
 // Block (x, i): fork i's share of table entries and of rows; block (0, i) its length.
 constexpr int kForkThreads = 256;
@@ -401,11 +444,14 @@ cudaError_t launch_commit(const CommitArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_list_free(const int32_t* page_refs, int num_pages, int32_t* free_pages, int32_t* num_free,
                              cudaStream_t stream) {
+  if (num_pages <= kFewPages) {
+    list_free_few_kernel<<<1, kFreeThreads, 0, stream>>>(page_refs, num_pages, free_pages, num_free);
+    return cudaGetLastError();
+  }
   constexpr size_t smem = 2 * kFreeWords * sizeof(uint32_t);
   cudaError_t e = cudaFuncSetAttribute(list_free_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  // One CTA reads 8192 counts in one step; a second one costs the exchange.
-  int C = 1;
+  int C = 2;
   while (C < kFreeCluster && (int64_t)C * 8192 < num_pages) C *= 2;
   return launch_cluster(list_free_kernel, C, kFreeThreads, C, smem, stream, page_refs, num_pages, free_pages, num_free);
 }
