@@ -153,6 +153,8 @@ class Plan:
     def __init__(self, handle: int, params: MlaVerifyParams, workspace_bytes: int):
         self.handle = handle
         self.params = params
+        self.q_len, self.pool_rows = params.q_len, params.pool_rows  # (read at every call)
+        self.kv4 = bool(params.flags & MLA_VERIFY_KV4)
         self.workspace_bytes = workspace_bytes
 
     @property
@@ -354,13 +356,11 @@ def mla_verify_run_shared(plan: Plan, q_nope_absorbed, q_rope, kv_pool, group_in
         _check(rc, "mla_verify_run_shared")
 
 
-def _int32s(**tensors):
-    for what, x in tensors.items():
-        _int32(x, what)
-
-
-def _at_least(n: int, **tensors):
-    for what, x in tensors.items():
+def _arrays(dtype, *arrays):
+    """(tensor, least entries, name) each: contiguous and of this type."""
+    for x, n, what in arrays:
+        if x.dtype is not dtype or not x.is_contiguous():
+            raise ValueError("%s: a contiguous %s tensor expected, got %s strides %s" % (what, dtype, x.dtype, x.stride()))
         if x.numel() < n:
             raise ValueError("%s is too short: %d entries, %d needed" % (what, x.numel(), n))
 
@@ -379,22 +379,18 @@ def mla_verify_accept_drafts(plan: Plan, target_probs, draft_probs, draft_tokens
     """Draft trees against the target's probabilities (draft_probs None: proposed, not drawn; qo_indptr None: q_len nodes
     each): accepted int32 [batch, q_len], num_accepted and next_tokens int32 [batch] are written."""
     torch = _torch or _load_torch()
-    vocab = target_probs.shape[-1]
-    _int32s(draft_tokens=draft_tokens, parents=parents, accepted=accepted, num_accepted=num_accepted,
-            next_tokens=next_tokens)
-    for what, x in (("uniform", uniform), ("uniform_next", uniform_next)):
-        if x.dtype is not torch.float32 or not x.is_contiguous():
-            raise ValueError("%s: a contiguous fp32 tensor expected" % what)
-    _at_least(batch, num_accepted=num_accepted, next_tokens=next_tokens, uniform_next=uniform_next)
-    _at_least(batch * plan.params.q_len, accepted=accepted)
+    i32 = torch.int32
+    rows, vocab = target_probs.shape[0], target_probs.shape[-1]
+    nodes = 0 if qo_indptr is not None else batch * plan.q_len
+    _arrays(i32, (draft_tokens, nodes, "draft_tokens"), (parents, nodes, "parents"),
+            (accepted, batch * plan.q_len, "accepted"), (num_accepted, batch, "num_accepted"),
+            (next_tokens, batch, "next_tokens"))
+    _arrays(torch.float32, (uniform, nodes, "uniform"), (uniform_next, batch, "uniform_next"))
     if qo_indptr is not None:
-        _int32(qo_indptr, "qo_indptr")
-        _at_least(batch + 1, qo_indptr=qo_indptr)
-    else:
-        _at_least(batch * plan.params.q_len, draft_tokens=draft_tokens, parents=parents, uniform=uniform)
-        if target_probs.shape[0] < batch * plan.params.q_len:
-            raise ValueError("target_probs has too few rows")
-    if draft_probs is not None and draft_probs.shape[0] < target_probs.shape[0]:
+        _arrays(i32, (qo_indptr, batch + 1, "qo_indptr"))
+    elif rows < nodes:
+        raise ValueError("target_probs has too few rows")
+    if draft_probs is not None and draft_probs.shape[0] < rows:
         raise ValueError("draft_probs has fewer rows than target_probs")
     rc = (_lib or load()).mla_verify_accept_drafts(
         plan.handle, target_probs.data_ptr(), _prob_rows(target_probs, vocab, "target_probs"), _ptr(draft_probs),
@@ -408,39 +404,37 @@ def mla_verify_accept_drafts(plan: Plan, target_probs, draft_probs, draft_tokens
 
 def _layers_of(plan: Plan, kv_pool):
     """(layers, bytes from one to the next) of a pool [rows, row] or [layers, rows, row] of whole rows."""
-    kv4 = plan.params.flags & MLA_VERIFY_KV4
     torch = _torch or _load_torch()
-    row, dtype = (MLA_VERIFY_KV4_ROW_BYTES, torch.uint8) if kv4 else (576, torch.bfloat16)
-    if kv_pool.dtype is not dtype or kv_pool.dim() not in (2, 3) or kv_pool.shape[-2:] != (plan.params.pool_rows, row) or (
-            kv_pool.stride(-1) != 1 or (kv_pool.stride(-2) != row and kv_pool.shape[-2] > 1)):
+    row, dtype = (MLA_VERIFY_KV4_ROW_BYTES, torch.uint8) if plan.kv4 else (576, torch.bfloat16)
+    shape, stride = kv_pool.shape, kv_pool.stride()
+    if kv_pool.dtype is not dtype or len(shape) not in (2, 3) or shape[-1] != row or shape[-2] != plan.pool_rows or (
+            stride[-1] != 1 or (stride[-2] != row and shape[-2] > 1)):
         raise ValueError("kv_pool: %s [layers, %d, %d] expected, got %s %s strides %s"
-                         % (dtype, plan.params.pool_rows, row, kv_pool.dtype, tuple(kv_pool.shape), kv_pool.stride()))
-    if kv_pool.dim() == 2 or kv_pool.shape[0] == 1:
+                         % (dtype, plan.pool_rows, row, kv_pool.dtype, tuple(shape), stride))
+    if len(shape) == 2 or shape[0] == 1:
         return 1, 0
-    return kv_pool.shape[0], kv_pool.stride(0) * kv_pool.element_size()
+    return shape[0], stride[0] * (1 if plan.kv4 else 2)
 
 
 def mla_verify_commit_drafts(plan: Plan, kv_pool, qo_indptr, out_cache_loc, accepted, num_accepted, batch: int, seq_lens,
                              new_seq_lens, page_size: int, block_table, page_refs, workspace, stream=None):
     """The accepted paths' rows to the front of the new rows of kv_pool ([rows, row] or [layers, rows, row]), lengths and
     page counts (block_table int32 [>= batch, max_pages] and page_refs None: no pages)."""
-    _int32s(out_cache_loc=out_cache_loc, accepted=accepted, num_accepted=num_accepted, seq_lens=seq_lens,
-            new_seq_lens=new_seq_lens)
-    _at_least(batch, num_accepted=num_accepted, seq_lens=seq_lens, new_seq_lens=new_seq_lens)
-    _at_least(batch * plan.params.q_len, accepted=accepted)
+    i32 = (_torch or _load_torch()).int32
+    tokens = batch * plan.q_len
+    _arrays(i32, (out_cache_loc, 0 if qo_indptr is not None else tokens, "out_cache_loc"), (accepted, tokens, "accepted"),
+            (num_accepted, batch, "num_accepted"), (seq_lens, batch, "seq_lens"), (new_seq_lens, batch, "new_seq_lens"))
     if qo_indptr is not None:
-        _int32(qo_indptr, "qo_indptr")
-        _at_least(batch + 1, qo_indptr=qo_indptr)
-    else:
-        _at_least(batch * plan.params.q_len, out_cache_loc=out_cache_loc)
+        _arrays(i32, (qo_indptr, batch + 1, "qo_indptr"))
     max_pages = num_pages = 0
     if (block_table is None) != (page_refs is None):
         raise ValueError("block_table and page_refs go together")
     if block_table is not None:
-        _int32s(block_table=block_table, page_refs=page_refs)
-        if block_table.shape[0] < batch:
+        _arrays(i32, (block_table, 0, "block_table"), (page_refs, 0, "page_refs"))
+        held, max_pages = block_table.shape
+        if held < batch:
             raise ValueError("block_table has too few rows")
-        max_pages, num_pages = block_table.shape[1], page_refs.numel()
+        num_pages = page_refs.numel()
     layers, stride = _layers_of(plan, kv_pool)
     rc = (_lib or load()).mla_verify_commit_drafts(
         plan.handle, kv_pool.data_ptr(), layers, stride, _ptr(qo_indptr), out_cache_loc.data_ptr(), accepted.data_ptr(),
@@ -453,30 +447,23 @@ def mla_verify_commit_drafts(plan: Plan, kv_pool, qo_indptr, out_cache_loc, acce
 
 def mla_verify_list_free_pages(plan: Plan, page_refs, free_pages, num_free, stream=None):
     """Pages without a reference, ascending, into free_pages (-1 behind them), and their number."""
-    _int32s(page_refs=page_refs, free_pages=free_pages, num_free=num_free)
-    _at_least(page_refs.numel(), free_pages=free_pages)
-    _at_least(1, num_free=num_free)
-    rc = (_lib or load()).mla_verify_list_free_pages(plan.handle, page_refs.data_ptr(), page_refs.numel(),
-                                                     free_pages.data_ptr(), num_free.data_ptr(), _stream(stream))
+    n = page_refs.numel()
+    _arrays((_torch or _load_torch()).int32, (page_refs, 0, "page_refs"), (free_pages, n, "free_pages"),
+            (num_free, 1, "num_free"))
+    rc = (_lib or load()).mla_verify_list_free_pages(plan.handle, page_refs.data_ptr(), n, free_pages.data_ptr(),
+                                                     num_free.data_ptr(), _stream(stream))
     if rc:
         _check(rc, "mla_verify_list_free_pages")
-
-
-def _page_arrays(block_table, seq_lens, page_refs):
-    _int32s(block_table=block_table, seq_lens=seq_lens, page_refs=page_refs)
-    requests, max_pages = block_table.shape
-    _at_least(requests, seq_lens=seq_lens)
-    return requests, max_pages
 
 
 def mla_verify_fork(plan: Plan, kv_pool, src, dst, page_size: int, block_table, seq_lens, page_refs, free_pages,
                     pages_used, workspace, stream=None):
     """Requests dst become copies of requests src: full pages shared, the last one copied (all layers of kv_pool)."""
-    requests, max_pages = _page_arrays(block_table, seq_lens, page_refs)
-    _int32s(src=src, dst=dst, free_pages=free_pages, pages_used=pages_used)
+    requests, max_pages = block_table.shape
     n = src.numel()
-    _at_least(n, dst=dst)
-    _at_least(1, pages_used=pages_used)
+    _arrays((_torch or _load_torch()).int32, (block_table, 0, "block_table"), (seq_lens, requests, "seq_lens"),
+            (page_refs, 0, "page_refs"), (src, 0, "src"), (dst, n, "dst"), (free_pages, 0, "free_pages"),
+            (pages_used, 1, "pages_used"))
     layers, stride = _layers_of(plan, kv_pool)
     rc = (_lib or load()).mla_verify_fork(
         plan.handle, kv_pool.data_ptr(), layers, stride, src.data_ptr(), dst.data_ptr(), n, int(page_size),
@@ -489,8 +476,9 @@ def mla_verify_fork(plan: Plan, kv_pool, src, dst, page_size: int, block_table, 
 
 def mla_verify_release(plan: Plan, requests, page_size: int, block_table, seq_lens, page_refs, workspace, stream=None):
     """Requests let go of their pages; their lengths become 0."""
-    rows, max_pages = _page_arrays(block_table, seq_lens, page_refs)
-    _int32(requests, "requests")
+    rows, max_pages = block_table.shape
+    _arrays((_torch or _load_torch()).int32, (block_table, 0, "block_table"), (seq_lens, rows, "seq_lens"),
+            (page_refs, 0, "page_refs"), (requests, 0, "requests"))
     rc = (_lib or load()).mla_verify_release(
         plan.handle, requests.data_ptr(), requests.numel(), int(page_size), block_table.data_ptr(), rows, max_pages,
         seq_lens.data_ptr(), page_refs.data_ptr(), page_refs.numel(), workspace.data_ptr(), workspace.nbytes,
