@@ -83,8 +83,8 @@ constexpr int kColO = 0, kColQ = 256, kColS = 448;  // (S: 32 columns for a step
 constexpr float kRowHeadroom = 16.0f, kOutHeadroom = 32.0f;
 // References are 16 + a multiple of 32: those of both CTAs, and of O, are mostly the same one.
 constexpr float kRefStep = 32.0f, kRefOffset = 16.0f;
-// Start and end of a row group, in tiles.
-constexpr int kSegCost = 5;
+// Start and end of a row group, in tiles: so much and so much per 32 rows.
+constexpr int kSegCost = 5, kQuadCost = 2;
 constexpr int kMaxSpans = 2 * kMaxSharedBatch;
 constexpr int64_t kAxisEnd = 0xFFFFFFFF;  // (2^32 tiles would take half a day)
 
@@ -128,27 +128,12 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
-  uint32_t r[16];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-}
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
-}
-__device__ __forceinline__ void tmem_st8u(uint32_t taddr, const uint32_t (&r)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
-               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
 }
 // D = A*B (+ D): A from tensor memory, B from shared memory.
 __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
@@ -319,6 +304,10 @@ __device__ __forceinline__ Span span_of(const SharedArgs& a, int e) {
 __device__ __forceinline__ int64_t groups_of(const SharedArgs& a, const Span& s) {
   return ((int64_t)s.ntok * a.H + kRows - 1) / kRows;
 }
+__device__ __forceinline__ int seg_cost(const SharedArgs& a, const Span& s) {
+  const int64_t rows = (int64_t)s.ntok * a.H;
+  return kSegCost + kQuadCost * (rows < kRows ? (int)(rows + 31) / 32 : 4);
+}
 __device__ __forceinline__ int64_t tiles_of(const Span& s) { return (s.keys + kKeys - 1) / kKeys; }
 
 // Where a pair is on the axis; every role of its CTAs walks it by itself.
@@ -337,13 +326,15 @@ struct Segment {
   int nrows;
   int64_t tile0;
   int nt;
+  int turn;       // of a shared part: the run starts this many tiles behind tile0, and ends before it
   int64_t first_pair;
   int pairs;  // that have a partial of it
+  __device__ __forceinline__ int tile(int t) const { return t + turn < nt ? t + turn : t + turn - nt; }
 };
 
 // Row id of key `key` + tiles of the segment; -1 where there is no such key.
 __device__ __forceinline__ int32_t load_id(const SharedArgs& a, const Segment& g, int64_t key, int t) {
-  const int64_t j = key + (int64_t)t * kKeys;
+  const int64_t j = key + (int64_t)g.tile(t) * kKeys;
   if (t >= g.nt || j >= g.s.keys) return -1;
   return j < g.s.prefix ? __ldg((g.s.own ? a.kv_indices : a.shared_indices) + g.s.kv0 + j)
                         : __ldg(a.out_cache_loc + g.s.q0 + (j - g.s.prefix));
@@ -364,27 +355,37 @@ __device__ __forceinline__ bool next_segment(const SharedArgs& a, Cursor& c, Seg
   while (c.x < c.x_end) {
     if (c.e >= c.spans) return false;
     g.s = span_of(a, c.e);
-    const int64_t tiles = tiles_of(g.s), len = tiles + kSegCost, all = groups_of(a, g.s) * len;
+    const int cost = seg_cost(a, g.s);
+    const int64_t tiles = tiles_of(g.s), len = tiles + cost, all = groups_of(a, g.s) * len;
     if (c.start + all <= c.x) {
       c.start += all;
       c.e = next_span(c, c.e + 1);
       continue;
     }
-    const int64_t i = (c.x - c.start) / len, e0 = c.start + i * len, e1 = e0 + len;
+    // (the axis has less than 2^32 tiles)
+    const int64_t i = (uint32_t)(c.x - c.start) / (uint32_t)len, e0 = c.start + i * len, e1 = e0 + len;
     g.r0 = (int)(i * kRows);
     const int64_t left = (int64_t)g.s.ntok * a.H - g.r0;
     g.nrows = left < kRows ? (int)left : kRows;
     g.row0 = g.s.q0 * a.H + g.r0;
     g.place = g.row0 + (g.s.own ? a.rows_max : 0);
     const int64_t stop = c.x_end < e1 ? c.x_end : e1;
-    int64_t t0 = c.x - e0 - kSegCost, t1 = stop - e0 - kSegCost;
+    int64_t t0 = c.x - e0 - cost, t1 = stop - e0 - cost;
     t0 = t0 < 0 ? 0 : t0;
     const bool heads = c.x == e0;  // this pair has the row group's start on the axis
     c.x = stop;
     g.tile0 = t0;
     g.nt = t1 > t0 ? (int)(t1 - t0) : 0;
-    g.first_pair = (e0 + kSegCost) / c.piece;
-    g.pairs = tiles ? (int)((e1 - 1) / c.piece - g.first_pair + 1) : 0;
+    // Pairs at the same prefix read the same keys at the same time, as far as it goes: at its tile u a pair is at tile u
+    // modulo the piece.  (Each starting with its first tile, a prefix larger than L2 came from memory for every pair.)
+    g.turn = 0;
+    if (!g.s.own) {
+      const int64_t u = e0 + cost + t0 - c.pair * c.piece;
+      const int64_t off = (u - t0) % c.piece, turn = off < 0 ? off + c.piece : off;
+      if (turn < g.nt) g.turn = (int)turn;
+    }
+    g.first_pair = (uint32_t)(e0 + cost) / (uint32_t)c.piece;
+    g.pairs = tiles ? (int)((uint32_t)(e1 - 1) / (uint32_t)c.piece - g.first_pair + 1) : 0;
     if (g.nt > 0 || heads) return true;
   }
   return false;
@@ -444,7 +445,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int64_t v = 0;
       if (e < cur.spans) {
         const Span s = span_of(a, e);
-        v = groups_of(a, s) * (tiles_of(s) + kSegCost);
+        v = groups_of(a, s) * (tiles_of(s) + seg_cost(a, s));
       }
       const int64_t len = v;
 #pragma unroll 1
@@ -508,7 +509,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         id0 = id1;
         id1 = load_id(a, g, key0, t + 2);
         const bool ok = row >= 0 && row < a.pool_rows;
-        if (!ok && key0 + (int64_t)t * kKeys < g.s.keys) bad = 1;
+        if (!ok && key0 + (int64_t)g.tile(t) * kKeys < g.s.keys) bad = 1;
         row = ok ? row : -1;
         const uint32_t valid = __ballot_sync(0xffffffffu, ok) & 0xFFu;
         const __nv_bfloat16* src[2];
@@ -722,35 +723,62 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (g.nt == 0) continue;
       const bool active = 32 * quad < g.nrows;  // this warp's quarter has rows at all
       const uint32_t quads = (g.nrows + 31) / 32;
-      // ---- Q: channels 0..383 into tensor memory, the others into shared memory, half of each by this thread -------
+      // ---- Q: channels 0..383 into tensor memory, the others into shared memory ----------------------------------
+      // Whole sectors of a row by neighbouring lanes.  (A row is a lane of tensor memory; with each lane reading its own
+      // row, 16 bytes at a time, this took 11,000 to 15,000 cycles.)
       if (active) {
-        const uint4* qn = reinterpret_cast<const uint4*>(a.q_nope + (g.row0 + (row_in ? r : 0)) * kDLatent);
-        const uint4* qr = reinterpret_cast<const uint4*>(a.q_rope + (g.row0 + (row_in ? r : 0)) * kDRope);
-        auto load = [&](const uint4* p) {
-          const uint4 x = __ldg(p);
-          return make_uint4(x.x ^ flip, x.y ^ flip, x.z ^ flip, x.w ^ flip);
+        // 16-byte piece c of 72 of a row (rows behind the last one: that one)
+        const auto piece = [&](int row, int c) -> const uint4* {
+          row = row < g.nrows ? row : g.nrows - 1;
+          return c < 64 ? reinterpret_cast<const uint4*>(a.q_nope + (g.row0 + row) * kDLatent) + c
+                        : reinterpret_cast<const uint4*>(a.q_rope + (g.row0 + row) * kDRope) + c - 64;
         };
-        uint4 y[12];
+        // Channels 384 .. 575 of 16 of the rows: 128 bytes of four rows per instruction.
+        const int own_row = 32 * quad + 16 * half + (lane >> 3);
+        const auto place = [&](int k) {
+          const int row = own_row + 4 * (k & 3);
+          return sbase + (k >> 2) * kQBlock + row * 128 + (((lane & 7) ^ (row & 7)) << 4);
+        };
+#pragma unroll
+        for (int k = 0; k < 12; ++k) cp_async16(place(k), piece(own_row + 4 * (k & 3), 48 + 8 * (k >> 2) + (lane & 7)), 16u);
+        // Channels 192 * half .. + 191 of the quarter's rows: 64 bytes of eight rows per instruction, turned around in the
+        // place of this CTA's weights, which nobody uses between two row groups.
+        const uint32_t turn = sbase + kOffP + warp * 2048;
 #pragma unroll 1
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < 3; ++j) {
+          uint4 y[2][4];
 #pragma unroll
-          for (int k = 0; k < 12; ++k) y[k] = load(qn + 24 * half + 12 * j + k);
+          for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int k = 0; k < 12; k += 4) {
-            const uint32_t w[16] = {y[k].x,     y[k].y,     y[k].z,     y[k].w,     y[k + 1].x, y[k + 1].y, y[k + 1].z, y[k + 1].w,
-                                    y[k + 2].x, y[k + 2].y, y[k + 2].z, y[k + 2].w, y[k + 3].x, y[k + 3].y, y[k + 3].z, y[k + 3].w};
-            tmem_st16(t_lane + kColQ + 96 * half + 48 * j + 4 * k, w);
+            for (int k = 0; k < 4; ++k) y[i][k] = __ldg(piece(32 * quad + 8 * k + (lane >> 2), 24 * half + 8 * j + 4 * i + (lane & 3)));
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            __syncwarp();  // (the last ones have been read)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int row = 8 * k + (lane >> 2);
+              sts128(turn + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4), y[i][k].x ^ flip, y[i][k].y ^ flip,
+                     y[i][k].z ^ flip, y[i][k].w ^ flip);
+            }
+            __syncwarp();
+            uint32_t w[16];
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                           : "=r"(w[4 * c]), "=r"(w[4 * c + 1]), "=r"(w[4 * c + 2]), "=r"(w[4 * c + 3])
+                           : "r"(turn + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4))
+                           : "memory");
+            tmem_st16(t_lane + kColQ + 96 * half + 32 * j + 16 * i, w);
           }
         }
-#pragma unroll
-        for (int k = 0; k < 12; ++k) {
-          const int c = 12 * half + k;  // 16-byte piece of the 192 channels
-          y[k] = load(c < 16 ? qn + 48 + c : qr + c - 16);
-        }
-#pragma unroll
-        for (int k = 0; k < 12; ++k) {
-          const int c = 12 * half + k;
-          sts128(sbase + (c >> 3) * kQBlock + r * 128 + (((c & 7) ^ (r & 7)) << 4), y[k].x, y[k].y, y[k].z, y[k].w);
+        cp_async_wait_all();
+        if (flip) {
+#pragma unroll 1
+          for (int k = 0; k < 12; ++k) {
+            uint32_t x, y, z, w;
+            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(x), "=r"(y), "=r"(z), "=r"(w) : "r"(place(k)) : "memory");
+            sts128(place(k), x ^ flip, y ^ flip, z ^ flip, w ^ flip);
+          }
         }
         fence_proxy_async_smem();
         tc::tmem_wait_st();
