@@ -152,17 +152,19 @@ typedef struct {
   int32_t d_latent;   /* must be 512 */
   int32_t d_rope;     /* must be 64 */
   int32_t flags;      /* OR of MLA_VERIFY_FORCE_SIMT, MLA_VERIFY_FUSED_MERGE, MLA_VERIFY_REFETCH_VALUES,
-                       * MLA_VERIFY_KV4, MLA_VERIFY_TEST_STALL_GATHER */
+                       * MLA_VERIFY_KV4, MLA_VERIFY_SHARED, MLA_VERIFY_TEST_STALL_GATHER */
 } mla_verify_params;
 
 /* What a plan chose (for tests, benchmarks and logs). */
 typedef struct {
   int32_t kernel;        /* 1 = tcgen05 tensor-core split kernel, 0 = CUDA-core split kernel */
   int32_t rows_per_cta;  /* query rows (token x head pairs) one split CTA covers */
-  int32_t keys_per_tile; /* keys per pipeline tile (128) */
+  int32_t keys_per_tile; /* keys per pipeline tile (128; 64 for MLA_VERIFY_SHARED on the tensor-core kernel) */
   int32_t grid_x, grid_y, grid_z; /* split grid: row groups x KV chunks per request x max_batch;
-                                   * SMs x 1 x 1 for MLA_VERIFY_KV4 with nsplit = 0 */
-  int32_t merge_blocks;  /* merge grid size; 0 when the split kernel merges (MLA_VERIFY_FUSED_MERGE) */
+                                   * SMs x 1 x 1 for MLA_VERIFY_KV4 with nsplit = 0; pairs of SMs x 1 x 1
+                                   * (a CTA pair each) for MLA_VERIFY_SHARED */
+  int32_t merge_blocks;  /* merge grid size; 0 when the split kernel merges (MLA_VERIFY_FUSED_MERGE), or with
+                          * MLA_VERIFY_SHARED, where it follows the call's batch */
   int32_t smem_bytes;    /* dynamic shared memory of the split kernel */
   size_t workspace_bytes;
   int32_t resident_tile; /* 1: tensor-core kernel keeps each key tile resident (one gather per key and
@@ -180,7 +182,9 @@ typedef struct {
  * for MLA_VERIFY_FUSED_MERGE one 32-bit counter per request and row group;
  * for MLA_VERIFY_KV4 with nsplit = 0 on the tensor-core kernel, O and LSE of
  * rows_per_cta rows per SM and per request and row group, the header, and 8
- * bytes per request and row group).
+ * bytes per request and row group; for MLA_VERIFY_SHARED O and LSE of twice
+ * max_batch*q_len*num_heads rows and 128 per pair of SMs, the header, and 16 bytes
+ * per row).
  * The workspace must be 256-byte aligned and zero-filled once before its
  * first use (e.g. torch.zeros, or mla_verify_workspace_init); the library
  * keeps the header and the counters consistent afterwards (after a call that
@@ -501,8 +505,9 @@ int mla_verify_build_slots(mla_verify_plan_t plan, const int32_t* seq_lens, cons
  * Two launches.  The work of all groups and requests is cut into equal pieces,
  * one per pair of SMs, from the lengths on the device, so a captured call follows
  * new lengths.  A key whose row is outside the pool is left out for every token
- * and raises MLA_VERIFY_DEV_BAD_ROW.  Errors: EINVAL (also a plan without
- * MLA_VERIFY_SHARED), EWORKSPACE, EUNSUPPORTED, ECUDA.
+ * and raises MLA_VERIFY_DEV_BAD_ROW.  A row that sees nothing gets O = 0 and LSE =
+ * -inf; a query with an infinity or a NaN makes its own row and LSE NaN.  Errors:
+ * EINVAL (also a plan without MLA_VERIFY_SHARED), EWORKSPACE, EUNSUPPORTED, ECUDA.
  */
 int mla_verify_run_shared(mla_verify_plan_t plan, const void* q_nope_absorbed, const void* q_rope, const void* kv_pool,
                           const int32_t* group_indptr, const int32_t* shared_indptr, const int32_t* shared_indices,

@@ -442,7 +442,7 @@ int mla_verify_plan_describe(mla_verify_plan_t pl, mla_verify_plan_info* info) {
   info->grid_x = pl->pieces ? pl->pieces : pl->groups;
   info->grid_y = pl->splits;
   info->grid_z = pl->pieces ? 1 : pl->p.max_batch;
-  info->merge_blocks = pl->merge_blocks;
+  info->merge_blocks = pl->shared ? 0 : pl->merge_blocks;
   info->smem_bytes = pl->smem;
   info->min_chunk = pl->min_chunk;
   info->chunk_granule = pl->chunk_granule;

@@ -7,7 +7,7 @@
 // the MMA's M = 128, so an fp32 O of 512 latent columns would fill tensor memory
 // (128 lanes x 512 columns).  The pair shares the work of a tile: CTA c takes the
 // scores and the softmax of 32 of its keys, and half of O's columns,
-//   S_c[128 x 32]   = Q[128 x 576] . K_c^T            (36 MMAs, K = 16, N = 32)
+//   S_c[128 x 32]   = Q[128 x 576] . K_c^T             (36 MMAs, K = 16, N = 32)
 //   O_c[128 x 256] += P[128 x 64] . V[64 x 256 of 512] (4 MMAs, K = 16, N = 256)
 // and sends its half of P to the other CTA: 64 bytes per row and tile.  (Splitting
 // the latent columns in both products was built first.  It gathers a quarter less
@@ -16,32 +16,52 @@
 // there hold up every other shared-memory access.  128k keys x 2048 rows took
 // 859 us so.)
 //
-// Each CTA keeps, per row, a reference for its own weights, p = 2^(s - m), and
-// one for its half of O, M; both are whole numbers, so the weights change from one
-// to the other exactly, and neither CTA waits for the other's maximum.
+// Even and odd tiles of a row group go to two sets of four softmax warps, a thread
+// per query row and 32 keys, each with places of its own for scores and weights:
+// one set's chain -- scores, weights, the other CTA's half, about 3,000 cycles --
+// overlaps the other's.  A set keeps, per row, a reference for its weights,
+// p = 2^(s - m); the CTA keeps one for O, M, handed from tile to tile.  References
+// are 16 + a multiple of 32, so they are mostly the same one, and where they are
+// not the weights change from one to the other exactly.
+//
+// Three warps issue MMAs: even tiles' scores, odd tiles' scores, values.  (A warp
+// that has issued MMAs and a commit gets to its next wait only when they are nearly
+// done, and then needs 400 to 500 cycles up to its next MMA: one warp for all kept
+// the tensor pipe at 60 %; 128k keys x 2048 rows took 582 us.)
 //
 // A operands in tensor memory spare shared memory: with A there an MMA with N = 32
 // takes 16 cycles, with A in shared memory 40.  What fits is Q's first 384
-// channels (192 columns of bf16 pairs) and P (32 columns); the other 192 channels
-// are in shared memory.  Tensor memory: O 0..255, Q 256..447, S 448..479, P 480..511.
+// channels (192 columns of bf16 pairs); the other 192 channels and P are in shared
+// memory (with N = 256 an MMA takes 128 cycles either way).  Tensor memory: O
+// 0..255, Q 256..447, S 448..479 (even tiles) and 480..511 (odd).
 //
-// Shared memory, all in blocks of 64 columns (128 bytes) of keys or query rows,
-// 128-byte swizzled -- the K-major layout of the score product and the MN-major
-// one of the value product's B: Q's three blocks; a ring of what only the scores
-// read (of this CTA's 32 keys the other CTA's half of the latent, and the RoPE
-// columns); a ring of values (the 64 keys, this CTA's half); the other CTA's P.
+// Shared memory, in blocks of 64 columns (128 bytes) of keys or query rows, 128-byte
+// swizzled -- the K-major layout of the score product and the MN-major one of the
+// value product's B: Q's three blocks; a ring of what only the scores read (of this
+// CTA's 32 keys the other CTA's half of the latent, and the RoPE columns), which
+// the score product reads first; rings of values (this CTA's half) of its own keys
+// and of the other CTA's.  Weights, both CTAs', stand in pieces of eight keys by all
+// rows, K-major and not swizzled, so that a warp sends 512 bytes in a row: 16-byte
+// pieces of a swizzled row go between CTAs at a quarter of that rate.
 //
-// Warps: 0-7 softmax (thread = a query row and 16 of the CTA's keys; it also
-// brings its row's Q in and takes O out of tensor memory), 8 issues the MMAs, 12-15
-// gather rows with 16-byte cp.async.  The issuing warp runs QK(t+1), PV(t),
-// QK(t+2), ...: the tensor pipe has QK(t+1) to do while the softmax of tile t runs.
+// Warps: 0-7 softmax (they also bring Q in and take O out of tensor memory), 8, 9
+// and 11 issue the MMAs, 10 gathers the other CTA's keys, 12-15 own keys, with
+// 16-byte cp.async.
 //
 // Work in equal pieces: the row groups of all groups' shared parts, then of all
-// requests' own parts, each as long as its tiles and kSegCost more, form an axis;
-// pair w takes the w-th of equal pieces (every CTA sums up the lengths itself).
-// Row group with first row R (0 .. rows_max for shared parts, rows_max .. for own
-// ones) leaves pair w's partial at row R + 128 w, and the table's entry R says
-// which pairs have one.
+// requests' own parts, each as long as its tiles and what its start and end cost,
+// form an axis; pair w takes the w-th of equal pieces (every CTA sums up the lengths
+// itself).  Pairs at the same prefix go through it in step, so that its rows come
+// from L2 for all but the first.  Row group with first row R (0 .. rows_max for
+// shared parts, rows_max .. for own ones) leaves pair w's partial at row R + 128 w,
+// and the table's entry R says which pairs have one.
+//
+// What bounds it: shared memory and the tensor pipe.  A tile takes 1,650 to 1,750
+// cycles of a CTA; its MMAs alone 1,376, its 200 KB of shared-memory traffic (48 of
+// it Q, 52 the gather's) 1,560 at 128 bytes per cycle.  A row group's start and end
+// cost 20,000 cycles: Q in, the first scores, the last exchange, 131 KB of O out.
+// 2048 rows behind 128k shared keys: 440 us, 1.35 PFLOP/s (0.71 of the measured
+// peak); 9216 rows behind 8k, 160 us; 512 rows behind 32k, 65 us.
 //
 // Every wait is bounded; on a timeout the CTA raises the status bit and drains,
 // and the other CTA of the pair runs into its own limit.
@@ -68,7 +88,7 @@ constexpr int kOwnStages = 4, kOtherStages = 2, kValueBytes = 4 * kBlockBytes;
 constexpr int kPPiece = kRows * 16;               // eight keys' weights of all rows
 constexpr int kPBytes = 2 * (kOwnKeys / 8) * kPPiece;  // a CTA's weights of two tiles
 constexpr int kSoftmaxWarps = 8;
-constexpr int kMmaWarp = kSoftmaxWarps;  // issues the score products,
+constexpr int kMmaWarp = kSoftmaxWarps;                      // and the next: issue the score products
 constexpr int kOtherWarp = kMmaWarp + 2, kOtherWarps = 1;    // gathers the other CTA's keys
 constexpr int kValueWarp = kMmaWarp + 3;                     // issues the value products
 constexpr int kGatherWarp = kMmaWarp + 4, kGatherWarps = 4;  // gather own keys (a warpgroup of their own: registers)
@@ -556,9 +576,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     fewer_registers<kRegsMma>();
     if (warp != kOtherWarp) {
       // ============================ MMA issue ==============================================
-      // One warp issues the score products, one the value products: each product waits for its own operands, and
-      // the tensor pipe has the other one's to do meanwhile.  A whole warp walks the loop and one elected lane issues,
-      // so that what an MMA takes its descriptors from stays warp-uniform.
+      // Two warps issue the score products, of even and of odd tiles, one the value products: each waits for its own
+      // operands, and the tensor pipe has another one's to do meanwhile.  A whole warp walks the loop and one elected lane
+      // issues, so that what an MMA takes its descriptors from stays warp-uniform.
       const bool leader = elect_one();
       bool ok = true;
       Segment g;
@@ -653,7 +673,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
       }
-      // Drain: every MMA of both warps has completed before tensor memory is freed.
+      // Drain: every MMA of the three warps has completed before tensor memory is freed.
       if (leader) tc::mma_commit(&ctl.mma_idle);
       const uint64_t t0 = global_timer_ns();
       for (uint32_t it = 0; it < (1u << 30); ++it)
