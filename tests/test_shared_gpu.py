@@ -237,6 +237,31 @@ def test_a_captured_call_follows_lengths_and_contents():
     assert B.mla_verify_read_status(plan, ws) == 0
 
 
+def test_two_graphs_that_share_a_workspace():
+    """Replayed in turn on one stream: neither call leaves anything that the other one trips over."""
+    cases = [Case([(700, [(50, 2)] * 5), (0, [(9, 1)])], 16, seed=40).device(),
+             Case([(130, [(300, 3), (4, 1)])], 64, seed=41).device()]
+    plans = [c.plan() for c in cases]
+    ws = torch.zeros(max(p.workspace_bytes for p in plans), dtype=torch.uint8, device="cuda")
+    outs = [c.outputs() for c in cases]
+    graphs = []
+    for c, p, out in zip(cases, plans, outs):
+        c.call(p, ws, *out)
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            c.call(p, ws, *out)
+    for out in outs:
+        out[0].fill_(7), out[1].fill_(7)
+    for k in (0, 1, 1, 0, 1, 0):
+        graphs[k].replay()
+    torch.cuda.synchronize()
+    for c, out in zip(cases, outs):
+        n = int(c.qo_indptr[-1])
+        c.match(out[0][:n], out[1][:n])
+    assert B.mla_verify_read_status(plans[0], ws) == 0
+
+
 def test_two_calls_at_once_on_two_streams():
     cases = [Case([(2000 + 500 * k, [(30, 2)] * 8)], 16, seed=20 + k).device() for k in range(2)]
     plan = cases[0].plan()

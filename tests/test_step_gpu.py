@@ -202,6 +202,28 @@ def test_distribution_of_the_first_new_token():
     assert np.all(np.abs(seen - total * p) <= 5 * np.sqrt(total * p * (1 - p)) + 1)
 
 
+def test_on_another_stream():
+    """Every call on a stream that is not the current one, after work that it has to wait for."""
+    d = Drafts([5, 4], 1000, True, seed=12)
+    plan, ws = plan_ws(2, 5)
+    st = torch.cuda.Stream()
+    src, draft = torch.from_numpy(d.target).cuda(), torch.from_numpy(d.draft).cuda()
+    out = [torch.full(s, -9, dtype=torch.int32, device="cuda") for s in ((2, 5), (2,), (2,))]
+    tok, par, qo, u, un = i32(d.tokens), i32(d.parents), i32(d.qo), torch.from_numpy(d.u).cuda(), torch.from_numpy(d.u_next).cuda()
+    target, refs, free, count = torch.zeros_like(src), i32(np.ones(5000)), i32(np.zeros(5000)), i32([0])
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        torch.cuda._sleep(2_000_000)
+        target.copy_(src)
+        refs[::3] = 0
+    B.mla_verify_accept_drafts(plan, target, draft, tok, par, qo, u, un, 2, *out, ws, stream=st)
+    B.mla_verify_list_free_pages(plan, refs, free, count, stream=st)
+    st.synchronize()
+    for g, r in zip(out, d.oracle()):
+        assert np.array_equal(g.cpu().numpy(), r)
+    assert int(count) == 1667 and free[:3].tolist() == [0, 3, 6]
+
+
 def test_accept_replays_with_new_contents():
     d = [Drafts([4, 0, 6], 500, True, seed=s) for s in (10, 11)]
     d[1].counts, big = [4, 0, 6], d[0]
