@@ -27,9 +27,9 @@
 // rejection only entries with p > q count: each warp keeps theirs in shared memory,
 // and later rejections' passes run on those, r = w(p) less the sum of the s.
 //
-// 16 requests, trees of 9, 131,072 tokens: 17.7 us (10 us for a request with one
+// 16 requests, trees of 9, 131,072 tokens: 17.4 us (10 us for a request with one
 // rejection and a child behind it, 15 us with two); 64 requests, trees of up to 16,
-// 150,001 tokens: 47.8 us, of which the rows' 77 MB take 11.3.  In 64 bits throughout
+// 150,001 tokens: 45 us, of which the rows' 77 MB take 11.3.  In 64 bits throughout
 // these took 50.6 and 199 us, with 19-bit parts 29.8 and 97.8; what is kept, clusters
 // of 16 and a search by the whole CTA did the rest.
 #include <cooperative_groups.h>
@@ -47,7 +47,18 @@ constexpr int kMaxCluster = 16;
 constexpr int kUnroll = 2;
 
 // (a NaN, a negative probability: 0; above 1: 1)
-__device__ __forceinline__ float clip(float p) { return fminf(fmaxf(p, 0.f), 1.f); }
+__device__ __forceinline__ float clip(float p) { return __saturatef(p); }
+
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
 
 // Sums of at most kMost weights in two parts of 19 bits.  Each part is the lower bits of a float with a constant on top;
 // what the constants add up to, modulo 2^32, comes off at the end.
@@ -60,6 +71,15 @@ struct Sum {
     const float rest = fmaf(p, 524288.f, -(t - 8388608.f));   // exact, at most half
     high += __float_as_uint(t);
     low += __float_as_uint(fmaf(rest, 524288.f, 12582912.f));
+  }
+  // Two weights at once, in pairs of floats.
+  __device__ __forceinline__ void add(float p, float q) {
+    const uint64_t v = pair(p, q), up = pair(524288.f, 524288.f);
+    const uint64_t t = fma2(v, up, pair(8388608.f, 8388608.f));
+    const uint64_t minus = fma2(t, pair(-1.f, -1.f), pair(8388608.f, 8388608.f));  // (exact)
+    const uint64_t low2 = fma2(fma2(v, up, minus), up, pair(12582912.f, 12582912.f));
+    high += (uint32_t)t + (uint32_t)(t >> 32);
+    low += (uint32_t)low2 + (uint32_t)(low2 >> 32);
   }
   // of exactly n weights
   __device__ __forceinline__ int64_t value(uint32_t n) const {
@@ -167,6 +187,7 @@ struct Node {
     int64_t t = 0;
     int n = 0, from = end;
     bool keep = kept.room > 0;
+    const uint32_t below = (1u << lane) - 1;
     if (!keep) from = begin;
 #pragma unroll 1
     for (int k0 = begin; k0 < end; k0 += 32 * kUnroll) {
@@ -183,24 +204,26 @@ struct Node {
       Sum<4 * kUnroll> less;
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
-        const float a[4] = {pv[u].x, pv[u].y, pv[u].z, pv[u].w}, b[4] = {qv[u].x, qv[u].y, qv[u].z, qv[u].w};
-        int at = n;
+        const float a[4] = {clip(pv[u].x), clip(pv[u].y), clip(pv[u].z), clip(pv[u].w)},
+                    b[4] = {clip(qv[u].x), clip(qv[u].y), clip(qv[u].z), clip(qv[u].w)};
+        less.add(fminf(a[0], b[0]), fminf(a[1], b[1]));
+        less.add(fminf(a[2], b[2]), fminf(a[3], b[3]));
+        if (keep) {
+          int at = n;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float x = clip(a[i]), y = clip(b[i]);
-          less.add(fminf(x, y));
-          if (keep) {
-            const uint32_t more = __ballot_sync(0xffffffffu, x > y);
-            const int place = at + __popc(more & ((1u << lane) - 1));
-            if (x > y && place < kept.room) kept.entry[place] = make_float2(x, y);
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t more = __ballot_sync(0xffffffffu, a[i] > b[i]);
+            const int place = at + __popc(more & below);
+            if (a[i] > b[i] && place < kept.room) kept.entry[place] = make_float2(a[i], b[i]);
             at += __popc(more);
           }
+          if (at > kept.room) {
+            keep = false;
+            from = min(k0 + 32 * u, end);
+          } else {
+            n = at;
+          }
         }
-        if (keep && at > kept.room) {
-          keep = false;
-          from = min(k0 + 32 * u, end);
-        }
-        if (keep) n = at;
       }
       t += less.value(4 * kUnroll);
     }
@@ -252,40 +275,41 @@ struct Node {
       Sum<4 * kUnroll> more, less;
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
-        const float a[4] = {pv[u].x, pv[u].y, pv[u].z, pv[u].w}, b[4] = {qv[u].x, qv[u].y, qv[u].z, qv[u].w};
+        const float a[4] = {clip(pv[u].x), clip(pv[u].y), clip(pv[u].z), clip(pv[u].w)};
+        if (!both) {
+          more.add(a[0], a[1]);
+          more.add(a[2], a[3]);
+          continue;
+        }
+        const float b[4] = {clip(qv[u].x), clip(qv[u].y), clip(qv[u].z), clip(qv[u].w)};
+        if (simple) {  // max(w(p) - w(q), 0) = w(p) - min(w(p), w(q))
+          const float least[4] = {fminf(a[0], b[0]), fminf(a[1], b[1]), fminf(a[2], b[2]), fminf(a[3], b[3])};
+          less.add(least[0], least[1]);
+          less.add(least[2], least[3]);
+          if (kWhat == What::kLeft) {
+            more.add(a[0], a[1]);
+            more.add(a[2], a[3]);
+          }
+          continue;
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float x = clip(a[i]);
-          if (!both) {
-            more.add(x);
-            continue;
+          // r is what the sum of the s leaves of w(p): an r that has reached 0 stays there.
+          const Weight w(b[i]);
+          int64_t r = Weight(a[i]).value() - w.value();
+          for (int j = 1; j < n; ++j) r -= w.times(z[j]);
+          r = r > 0 ? r : 0;
+          if (kWhat == What::kTaken) {
+            const int64_t last = w.times(z[n]);
+            r = r < last ? r : last;
           }
-          const float y = clip(b[i]);
-          if (simple) {
-            if (kWhat == What::kTaken) {
-              more.add(fminf(x, y));
-            } else {
-              more.add(x > y ? x : 0.f);
-              less.add(x > y ? y : 0.f);
-            }
-          } else {
-            // r is what the sum of the s leaves of w(p): an r that has reached 0 stays there.
-            const Weight w(y);
-            int64_t r = Weight(x).value() - w.value();
-            for (int j = 1; j < n; ++j) r -= w.times(z[j]);
-            r = r > 0 ? r : 0;
-            if (kWhat == What::kTaken) {
-              const int64_t last = w.times(z[n]);
-              r = r < last ? r : last;
-            }
-            t += r;
-          }
+          t += r;
         }
       }
-      if (simple || !both) {
+      if (!both)
         t += more.value(4 * kUnroll);
-        if (both && kWhat == What::kLeft) t -= less.value(4 * kUnroll);
-      }
+      else if (simple)
+        t += kWhat == What::kTaken ? less.value(4 * kUnroll) : more.value(4 * kUnroll) - less.value(4 * kUnroll);
     }
     return t;
   }
