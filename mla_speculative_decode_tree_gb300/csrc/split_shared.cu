@@ -97,7 +97,7 @@ constexpr int kThreads = 32 * (kGatherWarp + kGatherWarps);
 constexpr int kRegsSoftmax = 144, kRegsMma = 112, kRegsGather = 112;
 static_assert(kThreads == 512 && 2 * kRegsSoftmax + kRegsMma + kRegsGather <= 512, "register shares");
 constexpr int kKeysPerWarp = kOwnKeys / kGatherWarps;  // own keys gathered by a warp
-constexpr int kColO = 0, kColQ = 256, kColS = 448;  // (S: 32 columns for a step's first tile, 32 for its second)
+constexpr int kColO = 0, kColQ = 256, kColS = 448;  // (S: 32 columns for even tiles, 32 for odd ones)
 // Base 2, before a reference is raised.  Weights and O are floating numbers, so a
 // reference far below the maximum costs no precision; what it must not do is overflow.
 constexpr float kRowHeadroom = 16.0f, kOutHeadroom = 32.0f;
