@@ -390,19 +390,15 @@ __global__ void __launch_bounds__(kThreads, 2) accept_kernel(AcceptArgs a) {
     if (lane == 0) s.part[warp] = t;
     __syncthreads();
     ++round;
-    if (tid < C) {
-      int64_t x = 0;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) x += s.part[w];
-      *cluster.map_shared_rank(&s.all[round & 1][rank], tid) = x;
+    if (warp == 0) {
+      const int64_t x = warp_sum(lane < kWarps ? s.part[lane] : 0);
+      if (lane < C) *cluster.map_shared_rank(&s.all[round & 1][rank], lane) = x;
     }
     if (C > 1)
       cluster.sync();
     else
       __syncthreads();
-    int64_t x = 0;
-    for (int c = 0; c < C; ++c) x += s.all[round & 1][c];
-    return x;
+    return warp_sum(lane < C ? s.all[round & 1][lane] : 0);
   };
 
   // ---- the walk, by the first warp ----------------------------------------------------
@@ -514,8 +510,7 @@ __global__ void __launch_bounds__(kThreads, 2) accept_kernel(AcceptArgs a) {
     }
   }
   const int64_t aim = (int64_t)__umul64hi((uint64_t)random24(u_next) << 40, (uint64_t)sum);
-  int64_t mine = 0;
-  for (int c = 0; c < rank; ++c) mine += s.all[round & 1][c];
+  int64_t mine = warp_sum(lane < rank ? s.all[round & 1][lane] : 0);
   if (sum == 0 || aim < mine || aim >= mine + s.all[round & 1][rank]) return;
   // A warp's part in this CTA holds the token; all of the CTA looks through that part, a vector a thread.
   const auto scan = [&](int64_t v) -> int64_t {  // over the lanes, each with those before it
