@@ -69,6 +69,8 @@ __global__ void __launch_bounds__(kCommitThreads) commit_kernel(CommitArgs a) {
   int n = a.num_accepted[b];
   bool bad = n < 0 || n > T;
   n = n < 0 ? 0 : n > T ? T : n;
+  // Read before the barriers: new_seq_lens may be seq_lens, and thread 0 writes it while other warps still move rows.
+  const int64_t P = a.seq_lens[b] > 0 ? a.seq_lens[b] : 0;
   if (tid < T) {
     slot[tid] = a.out_cache_loc[q0 + tid];
     path[tid] = a.accepted[(int64_t)b * a.T + tid];
@@ -107,7 +109,7 @@ __global__ void __launch_bounds__(kCommitThreads) commit_kernel(CommitArgs a) {
        layer += gridDim.x * (kCommitThreads / 32))
     move_rows(a.pool.base + layer * a.pool.layer_stride, a.pool.row_bytes, src, dst, moved, lane);
   if (blockIdx.x != 0) return;
-  const int64_t P = a.seq_lens[b] > 0 ? a.seq_lens[b] : 0, L = P + kept;
+  const int64_t L = P + kept;
   if (tid == 0) a.new_seq_lens[b] = (int32_t)(L > 0x7FFFFFFF ? 0x7FFFFFFF : L);
   if (a.block_table) {
     const int64_t c0 = (P + a.page_size - 1) / a.page_size;
