@@ -124,6 +124,10 @@ __device__ __forceinline__ float4 load4(const float* row, int at, int vocab, boo
   return make_float4(v[0], v[1], v[2], v[3]);
 }
 
+// Every CTA of the cluster has started: arrive first thing, wait before the first access to another CTA's shared memory.
+__device__ __forceinline__ void started_arrive() { asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory"); }
+__device__ __forceinline__ void started_wait() { asm volatile("barrier.cluster.wait;" ::: "memory"); }
+
 __device__ __forceinline__ int64_t warp_sum(int64_t v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -335,6 +339,7 @@ __global__ void __launch_bounds__(kThreads, 2) accept_kernel(AcceptArgs a) {
     }
     return;
   }
+  if (C > 1) started_arrive();
   const float u_next = a.u_next[b];
   int parent[2] = {-1, -1};  // of nodes lane, lane + 32; -1: none that the walk can come from
   if (warp < 2 && tid < n && tid > 0) {
@@ -388,6 +393,7 @@ __global__ void __launch_bounds__(kThreads, 2) accept_kernel(AcceptArgs a) {
     w1 = w_end(warp);
     const int64_t t = warp_sum(f());
     if (lane == 0) s.part[warp] = t;
+    if (C > 1 && round == 0) started_wait();
     __syncthreads();
     ++round;
     if (warp == 0) {
