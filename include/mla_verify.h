@@ -72,7 +72,7 @@ extern "C" {
 /* Device status bits (see mla_verify_read_status). */
 #define MLA_VERIFY_DEV_BAD_ROW 0x1u /* some resolved pool row was outside [0, pool_rows) */
 #define MLA_VERIFY_DEV_TIMEOUT 0x2u /* a pipeline wait gave up; that CTA's partial is invalid */
-#define MLA_VERIFY_DEV_NO_PAGE 0x4u /* a slot-map build ran out of free pages or of block-table columns */
+#define MLA_VERIFY_DEV_NO_PAGE 0x4u /* a slot-map build or a fork ran out of free pages or of block-table columns */
 #define MLA_VERIFY_DEV_CAPACITY 0x8u /* a slot map was longer than its array; the rest was not written */
 
 /* Plan flags. */
@@ -622,9 +622,12 @@ int mla_verify_list_free_pages(mla_verify_plan_t plan, const int32_t* page_refs,
  *  block_table    int32 [num_requests, max_pages]; dst's entries are written
  *  seq_lens       int32 [num_requests]; dst's are written
  *  page_refs      int32 [num_pages]: one more for a shared page, 1 for a fresh one
- *  free_pages     int32 [num_free]: fresh pages, taken from the front in the
- *                 forks' order
- *  pages_used     int32 [1] output: how many were taken
+ *  free_pages     int32 [num_free]: fresh pages, then entries of -1 up to its
+ *                 end, if any.  From the front, in the forks' order, each fork whose
+ *                 source has a last page that is not full has an entry; that of a fork
+ *                 left out for its destination is passed over and stays free
+ *  pages_used     int32 [1] output: how many pages of the list the forks went
+ *                 through, those passed over among them: the next unused ones follow
  *  workspace      the plan's workspace (only its status word is used)
  *
  * A fork from or to a request outside [0, num_requests), or into a request that

@@ -327,6 +327,19 @@ __device__ __forceinline__ int32_t load_row_id(const SplitArgs& a, int64_t q0, i
   return (j < P) ? __ldg(a.kv_indices + kv_base + j) : __ldg(a.out_cache_loc + q0 + (j - P));
 }
 
+// Where a list of pages, -1 behind them, ends among its first n entries.
+__device__ __forceinline__ int list_end(const int32_t* list, int n) {
+  int lo = 0, hi = n;
+  while (lo < hi) {
+    const int mid = (int)(((uint32_t)lo + (uint32_t)hi) >> 1);
+    if (list[mid] < 0)
+      hi = mid;
+    else
+      lo = mid + 1;
+  }
+  return lo;
+}
+
 __device__ __forceinline__ uint32_t mask_bit(const uint8_t* mask, int64_t bit) {
   return (__ldg(mask + (bit >> 3)) >> (bit & 7)) & 1u;
 }

@@ -316,12 +316,20 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(ForkArgs a) {
   const int64_t P = length(i);
   const int64_t full = P > 0 ? P / a.page_size : 0;
   const int tail = P > 0 ? (int)(P % a.page_size) : 0;
-  if (blockIdx.x == 0 && i == a.n - 1 && tid == 0) {
-    const int used = rank + (tail ? 1 : 0);
-    *a.pages_used = used < a.num_free ? used : a.num_free;
+  // The entries that the forks went through; the list may end before them.  (The last of them is read now, used at the end.)
+  const bool counts = blockIdx.x == 0 && i == a.n - 1 && tid == 0;
+  int used = 0, last_entry = 0;
+  if (counts) {
+    used = rank + (tail ? 1 : 0);
+    used = used < a.num_free ? used : a.num_free;
+    if (used > 0) last_entry = a.free_pages[used - 1];
   }
+  const auto count = [&]() {
+    if (counts) *a.pages_used = last_entry < 0 ? list_end(a.free_pages, used) : used;
+  };
   if (P < 0 || clash) {
     if (tid == 0 && blockIdx.x == 0) atomicOr(a.status, kStatusBadRow);
+    count();
     return;
   }
   const int32_t* from = a.block_table + (int64_t)a.src[i] * a.max_pages;
@@ -377,6 +385,7 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(ForkArgs a) {
     const int64_t most = (int64_t)a.max_pages * a.page_size;
     a.seq_lens[dst] = (int32_t)(len < most ? len : most);
   }
+  count();
   if (status) atomicOr(a.status, status);
 }
 

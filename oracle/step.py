@@ -123,9 +123,12 @@ def free_list(refs):
 
 
 def fork(pool, src, dst, page, table, lens, refs, free):
-    """-> (pool, table, lens, refs, pages used, status bits: 1 bad row, 4 no page)."""
+    """-> (pool, table, lens, refs, entries of the list gone through, status bits: 1 bad row, 4 no page).  A fork whose source
+    has a last page in part has an entry of the list, whether it is left out for a clash or not."""
     pool, table, lens, refs = pool.copy(), table.copy(), lens.copy(), refs.copy()
     requests, status, taken = table.shape[0], 0, 0
+    free = [int(p) for p in free]
+    free = free[:next((k for k, p in enumerate(free) if p < 0), len(free))]  # -1 ends the list
     for i, (s, d) in enumerate(zip(src.tolist(), dst.tolist())):
         if not 0 <= s < requests or not 0 <= d < requests or s == d:
             status |= 1
@@ -142,7 +145,7 @@ def fork(pool, src, dst, page, table, lens, refs, free):
             refs[table[s, c]] += 1
         lens[d] = P
         if tail:
-            fresh = int(free[mine]) if mine < free.size else -1
+            fresh = free[mine] if mine < len(free) else -1
             if not 0 <= fresh < refs.size or fresh * page + tail > pool.shape[1]:
                 status |= 4
                 table[d, full] = -1
@@ -152,7 +155,7 @@ def fork(pool, src, dst, page, table, lens, refs, free):
                 refs[fresh] = 1
                 old = int(table[s, full])
                 pool[:, fresh * page:fresh * page + tail] = pool[:, old * page:old * page + tail]
-    return pool, table, lens, refs, min(taken, free.size), status
+    return pool, table, lens, refs, min(taken, len(free)), status
 
 
 def release(which, page, table, lens, refs):
