@@ -450,7 +450,8 @@ int mla_verify_load_kv4(mla_verify_plan_t plan, const void* kv_pool, const int32
  *  block_table    int32 [batch, max_pages]: request b's first ceil(P_b / page_size)
  *                 entries are its pages; the entries of the fresh pages that
  *                 P_b + T_b tokens need are written after them
- *  free_pages     int32 [num_free]: taken from the front, in request order
+ *  free_pages     int32 [num_free]: pages, taken from the front in request order,
+ *                 then entries of -1 up to its end, if any
  *  pages_used     int32 [1] output: how many were taken
  *  kv_indptr      int32 [batch+1] output: exclusive scan of P_b
  *  kv_indices     int32 [kv_capacity] output: pool rows of the cached tokens

@@ -86,18 +86,20 @@ struct SlotsDev {
     return lo;
   }
 
-  // Pool row of position pos, which lies on `page`, the request's c-th; -1 where there is none.
-  __device__ __forceinline__ int32_t row_on(int32_t page, int64_t c, int64_t pos, uint32_t& status) const {
+  // Pool row of position pos, which lies on `page`, the request's c-th; -1 where there is none
+  // (fresh: a page of the free list, which an entry of -1 ends).
+  __device__ __forceinline__ int32_t row_on(int32_t page, int64_t c, int64_t pos, uint32_t& status, bool fresh = false) const {
     const int64_t r = (int64_t)page * a.page_size + (pos - c * a.page_size);
     if (page >= 0 && r < a.pool_rows) return (int32_t)r;
-    status |= kStatusBadRow;
+    status |= fresh && page < 0 ? kStatusNoPage : kStatusBadRow;
     return -1;
   }
 
   // Where the page of position pos of request b is written, its c-th page; null where there is none.
-  __device__ __forceinline__ const int32_t* page_at(int b, int64_t pos, int64_t& c) const {
+  __device__ __forceinline__ const int32_t* page_at(int b, int64_t pos, int64_t& c, bool& is_fresh) const {
     c = page_of(pos);
     const int64_t have = pages(cached[b]);
+    is_fresh = c >= have;
     if (c >= a.max_pages) return nullptr;
     if (c < have) return a.block_table + (int64_t)b * a.max_pages + c;
     const int64_t f = (int64_t)fresh[b] + (c - have);
@@ -207,7 +209,7 @@ __global__ void __launch_bounds__(kThreads) slots_kernel(SlotsArgs args) {
       a.qo_indptr[b] = d.qo[b];
     }
     if (threadIdx.x == 0) {
-      *a.pages_used = (int32_t)(F < a.num_free ? F : a.num_free);
+      if (F == 0 || a.num_free == 0) *a.pages_used = 0;  // (else whoever writes the last page's table entry)
       if (F > a.num_free) status |= kStatusNoPage;
       if (K > a.kv_capacity || N > a.loc_capacity) status |= kStatusCapacity;
     }
@@ -246,14 +248,16 @@ __global__ void __launch_bounds__(kThreads) slots_kernel(SlotsArgs args) {
     const int b1 = d.owner_warp(scan, first + (left < 128 ? left : 128) - 1, lane);
     const int32_t* at[kPerThread];
     int64_t pos[kPerThread], page_no[kPerThread];
+    bool fresh[kPerThread];
 #pragma unroll
     for (int k = 0; k < kPerThread; ++k) {
       at[k] = nullptr;
+      fresh[k] = false;
       if (lane + 32 * k < left) {
         const int x = first + lane + 32 * k;
         const int b = d.owner(scan, x, b0, b1);
         pos[k] = (int64_t)(x - scan[b]) + (pre ? 0 : d.cached[b]);
-        at[k] = d.page_at(b, pos[k], page_no[k]);
+        at[k] = d.page_at(b, pos[k], page_no[k], fresh[k]);
         if (!at[k]) status |= kStatusNoPage;
       }
     }
@@ -263,15 +267,22 @@ __global__ void __launch_bounds__(kThreads) slots_kernel(SlotsArgs args) {
 #pragma unroll
     for (int k = 0; k < kPerThread; ++k) {
       if (lane + 32 * k < left)
-        out[first + lane + 32 * k] = at[k] ? d.row_on(page[k], page_no[k], pos[k], status) : -1;
+        out[first + lane + 32 * k] = at[k] ? d.row_on(page[k], page_no[k], pos[k], status, fresh[k]) : -1;
     }
   }
   // The fresh pages' table entries (the last warps have the fewest chunks).
+  const int64_t last = (F < a.num_free ? F : a.num_free) - 1;
   for (int64_t f = (int64_t)(kThreads - 1 - threadIdx.x) * gridDim.x + blockIdx.x; f < F;
        f += (int64_t)gridDim.x * kThreads) {
     const int b = d.owner(d.fresh, f, 0, a.batch - 1);
     const int64_t c = d.pages(d.cached[b]) + (f - d.fresh[b]);
-    if (c < a.max_pages) a.block_table[(int64_t)b * a.max_pages + c] = f < a.num_free ? a.free_pages[f] : -1;
+    const int32_t page = f < a.num_free ? a.free_pages[f] : -1;
+    if (c < a.max_pages) a.block_table[(int64_t)b * a.max_pages + c] = page;
+    if (f == last) {  // (the list may end before it)
+      const int used = page < 0 ? list_end(a.free_pages, (int)f) : (int)f + 1;
+      *a.pages_used = used;
+      if (used < F) status |= kStatusNoPage;
+    }
   }
   if (status) atomicOr(a.status, status);
 }

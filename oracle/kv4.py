@@ -128,6 +128,8 @@ def verify(wl: dict, keys_of=None):
 def build_slots(seq_lens, new_lens, page_size, table, free_pages, pool_rows):
     """Index arrays of a step, request by request.  Returns a dict and whether (a page, a row) was missing."""
     table = np.array(table, np.int64)
+    free_pages = [int(p) for p in free_pages]
+    free_pages = free_pages[:next((k for k, p in enumerate(free_pages) if p < 0), len(free_pages))]  # -1 ends the list
     kv, qo, kv_idx, loc = [0], [0], [], []
     used = 0
     no_page = bad_row = False
@@ -137,7 +139,7 @@ def build_slots(seq_lens, new_lens, page_size, table, free_pages, pool_rows):
         for c in range(have, -(-(P + T) // page_size)):
             page = -1
             if used < len(free_pages):
-                page = int(free_pages[used])
+                page = free_pages[used]
             else:
                 no_page = True
             used += 1

@@ -9,6 +9,7 @@ pytestmark = pytest.mark.gpu
 
 from mla_speculative_decode_tree_gb300 import binding as B  # noqa: E402
 from oracle import step as S  # noqa: E402
+from test_slots_gpu import expect, run, tables  # noqa: E402
 from test_step_gpu import fork_case, run_fork  # noqa: E402
 
 
@@ -49,3 +50,23 @@ def test_entries_that_are_passed_over_stay_free():
         assert np.array_equal(g, r)
     assert got[4] == 4 and got[5] == B.MLA_VERIFY_DEV_BAD_ROW
     assert got[3][free[:4]].tolist() == [1, 1, 0, 1]
+
+
+@pytest.mark.parametrize("n,page", [(3, 4), (70, 2), (600, 16)])
+@pytest.mark.parametrize("pages", ["none", "one", "half", "one less", "all", "one more"])
+def test_slot_maps_on_a_list_that_runs_out(n, page, pages):
+    rng = np.random.default_rng(n)
+    P, T = rng.integers(0, 5 * page, n), rng.integers(0, 3 * page, n)
+    T[0] = 2 * page
+    table, free, rows = tables(P, T, page, n, spare=1)
+    want = free.size - 1
+    have = {"none": 0, "one": 1, "half": want // 2, "one less": want - 1, "all": want, "one more": want + 1}[pages]
+    padded = np.concatenate([free[:have], np.full(want + 9 - have, -1)])
+    bits = B.MLA_VERIFY_DEV_NO_PAGE if have < want else 0
+    whole, status = run(P, T, page, table, padded, rows)
+    expect(whole, status, P, T, page, table, padded, rows, bits)
+    assert whole["pages_used"][0] == min(want, have)
+    cut, status = run(P, T, page, table, free[:have], rows)
+    assert status == bits
+    for k, x in whole.items():
+        assert np.array_equal(x, cut[k]), k
