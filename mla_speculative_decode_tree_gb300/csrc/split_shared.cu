@@ -812,6 +812,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       float m = -INFINITY;  // reference of the row's weights in this CTA's tiles of this parity
       // of this thread's keys: sums of the weights as P has them, and before rounding (even and odd keys)
       uint64_t l_round = 0, l_full = 0;
+      bool saw = false;  // any of this thread's keys at all
       // Warps 0-3 take the row group's even tiles, 4-7 the odd ones.
 #pragma unroll 1
       for (int t = half; t < g.nt; t += 2, ++uses) {
@@ -850,6 +851,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         uint32_t w[16];
         if (active) {
           sees &= *reinterpret_cast<const uint32_t*>(ctl.valid[(tile + t) % kOwnStages]);
+          saw |= sees != 0;
           if (sees != 0xFFFFFFFFu) {
 #pragma unroll
             for (int k = 0; k < 32; ++k) n[k] = (sees >> k) & 1u ? n[k] : -INFINITY;
@@ -949,9 +951,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (active) {
         float even, odd;
         unpair(l_round, even, odd);
-        const float lr = even + odd;
+        float lr = even + odd;
         unpair(l_full, even, odd);
-        const float lf = even + odd;
+        float lf = even + odd;
+        // A query with an infinity may score -inf with every key: 0 over 0.
+        if (saw && m == -INFINITY) lr = lf = __int_as_float(0x7FFFFFFF);
         send16(sum_peer, l_bar_peer, __float_as_uint(m), __float_as_uint(lr), __float_as_uint(lf), 0u);
         ctl.sum[half][0][r] = m;
         ctl.sum[half][1][r] = lr;

@@ -208,7 +208,8 @@ __global__ void __launch_bounds__(32 * kSimtRowsPerCta) split_simt_kernel(SplitA
   o[2 * lane + 1] = make_float4(acc_a[4] * inv, acc_a[5] * inv, acc_a[6] * inv, acc_a[7] * inv);
   o[64 + 2 * lane] = make_float4(acc_b[0] * inv, acc_b[1] * inv, acc_b[2] * inv, acc_b[3] * inv);
   o[64 + 2 * lane + 1] = make_float4(acc_b[4] * inv, acc_b[5] * inv, acc_b[6] * inv, acc_b[7] * inv);
-  if (lane == 0) *lse_out = (m + __log2f(lsum)) * 0.69314718055994530942f;
+  // (A query that is not finite has weights that are NaN: +inf, which makes the merged row NaN.)
+  if (lane == 0) *lse_out = lsum == lsum ? (m + __log2f(lsum)) * 0.69314718055994530942f : INFINITY;
 }
 
 }  // namespace
