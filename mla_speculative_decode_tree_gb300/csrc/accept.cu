@@ -564,13 +564,13 @@ __global__ void __launch_bounds__(kThreads, 2) accept_kernel(AcceptArgs a) {
 
 }  // namespace
 
-cudaError_t launch_accept(const AcceptArgs& a, cudaStream_t stream) {
+cudaError_t launch_accept(const AcceptArgs& a, int sms, cudaStream_t stream) {
   // CTAs per request.  A batch is as slow as its request with the most rejections, whose passes are bound by arithmetic:
   // up to 16 while each has 3500 entries (16 requests, 131,072 tokens: clusters of 4 / 8 / 16 take 38 / 21.5 / 18.7 us).
   // But no more than twice what the GPU has room for at once, or requests queue up for their start, dependent reads of 2
   // us (64 requests, 150,001 tokens: 8 / 16 take 46 / 56 us).  And enough of them to keep the entries of a request that is
   // half rejected (256 requests, 131,072 tokens: 2 / 4 take 150 / 117 us).
-  const int64_t resident = 2 * 152;
+  const int64_t resident = 2 * (int64_t)sms;
   int C = 1;
   while (C < kMaxCluster &&
          ((a.draft && a.vocab > 32768 * C) || (a.vocab >= 7000 * C && a.batch * C <= resident)))

@@ -426,8 +426,9 @@ int mla_verify_plan(const mla_verify_params* params, size_t* workspace_bytes, ml
     pl->merge_rows = merge_pieces_rows(rows_max, device_sm_count());
     pl->merge_blocks = (int)((rows_b + pl->merge_rows - 1) / pl->merge_rows) * p.max_batch;
   }
+  pl->sms = device_sm_count();
   pl->shared = (p.flags & MLA_VERIFY_SHARED) != 0;
-  if (pl->shared) plan_shared(pl, device_sm_count());
+  if (pl->shared) plan_shared(pl, pl->sms);
   *workspace_bytes = pl->ws_bytes;
   *out = pl;
   return MLA_VERIFY_OK;

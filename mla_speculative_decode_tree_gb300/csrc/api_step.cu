@@ -189,7 +189,7 @@ int mla_verify_accept_drafts(mla_verify_plan_t pl, const float* target_probs, in
   if ((rc = check_device()) != MLA_VERIFY_OK) return rc;
   AcceptArgs a = {target_probs, draft_probs, target_stride, draft_stride, draft_tokens, parents, qo_indptr, uniform,
                   uniform_next, batch, pl->p.q_len, vocab, accepted, num_accepted, next_tokens};
-  return done(launch_accept(a, static_cast<cudaStream_t>(stream)));
+  return done(launch_accept(a, pl->sms, static_cast<cudaStream_t>(stream)));
 }
 
 int mla_verify_commit_drafts(mla_verify_plan_t pl, void* kv_pool, int32_t num_layers, int64_t layer_stride,

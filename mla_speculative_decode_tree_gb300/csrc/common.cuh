@@ -398,7 +398,7 @@ cudaError_t launch_slots(const SlotsArgs& a, cudaStream_t stream);
 cudaError_t launch_split_shared(const SharedArgs& a, cudaStream_t stream);
 cudaError_t launch_merge_shared(const SharedArgs& a, cudaStream_t stream);
 int split_shared_smem();
-cudaError_t launch_accept(const AcceptArgs& a, cudaStream_t stream);
+cudaError_t launch_accept(const AcceptArgs& a, int sms, cudaStream_t stream);
 cudaError_t launch_commit(const CommitArgs& a, cudaStream_t stream);
 cudaError_t launch_list_free(const int32_t* page_refs, int num_pages, int32_t* free_pages, int32_t* num_free,
                              cudaStream_t stream);

@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(128, 5) merge_shared_kernel(SharedArgs a) {
 cudaError_t launch_merge_shared(const SharedArgs& a, cudaStream_t stream) {
   // Few rows have many partials each: four warps a row, while the blocks fit two waves.
   const int64_t rows = (int64_t)a.batch * a.T * a.H;
-  if (rows <= 152 * 5 * 2)
+  if (rows <= 2 * 5 * 2 * (int64_t)a.clusters)  // (a pair of SMs each)
     merge_shared_kernel<4><<<(unsigned)rows, 128, 0, stream>>>(a);
   else
     merge_shared_kernel<1><<<(unsigned)((rows + 3) / 4), 128, 0, stream>>>(a);

@@ -13,6 +13,7 @@ using namespace mlav;
 struct mla_verify_plan_s {
   mla_verify_params p;
   int kernel;  // 1 = tcgen05, 0 = CUDA cores
+  int sms;     // of the device that the plan was made on
   int nq;      // query rows per split CTA
   bool resident;  // tensor-core kernel in resident-tile mode (each key lands once per CTA)
   int groups;  // row groups per request
