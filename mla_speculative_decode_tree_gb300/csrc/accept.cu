@@ -49,17 +49,6 @@ constexpr int kUnroll = 2;
 // (a NaN, a negative probability: 0; above 1: 1)
 __device__ __forceinline__ float clip(float p) { return __saturatef(p); }
 
-__device__ __forceinline__ uint64_t pair(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-
 // Sums of at most kMost weights in two parts of 19 bits.  Each part is the lower bits of a float with a constant on top;
 // what the constants add up to, modulo 2^32, comes off at the end.
 template <int kMost>
@@ -258,12 +247,12 @@ struct Node {
     return t;
   }
 
-  // Sum over vectors first, first + 32, ... below end.
+  // Sum over vectors first, first + 32, ... below end (kTaken: of the second rejection or a later one).
   template <What kWhat>
   __device__ __forceinline__ int64_t sum(int first, int end) const {
     const int n = kWhat == What::kTaken ? tried - 1 : tried;  // rejections before
-    const bool simple = !kDraft || n == 0 || (n == 1 && kWhat == What::kLeft);
-    const bool both = kDraft && (kWhat == What::kTaken || n > 0);
+    const bool simple = kWhat == What::kLeft && n <= 1;
+    const bool both = kDraft && n > 0;
     int64_t t = 0;
 #pragma unroll 1
     for (int k = first; k < end; k += 32 * kUnroll) {
@@ -287,13 +276,10 @@ struct Node {
         }
         const float b[4] = {clip(qv[u].x), clip(qv[u].y), clip(qv[u].z), clip(qv[u].w)};
         if (simple) {  // max(w(p) - w(q), 0) = w(p) - min(w(p), w(q))
-          const float least[4] = {fminf(a[0], b[0]), fminf(a[1], b[1]), fminf(a[2], b[2]), fminf(a[3], b[3])};
-          less.add(least[0], least[1]);
-          less.add(least[2], least[3]);
-          if (kWhat == What::kLeft) {
-            more.add(a[0], a[1]);
-            more.add(a[2], a[3]);
-          }
+          more.add(a[0], a[1]);
+          more.add(a[2], a[3]);
+          less.add(fminf(a[0], b[0]), fminf(a[1], b[1]));
+          less.add(fminf(a[2], b[2]), fminf(a[3], b[3]));
           continue;
         }
 #pragma unroll
@@ -313,7 +299,7 @@ struct Node {
       if (!both)
         t += more.value(4 * kUnroll);
       else if (simple)
-        t += kWhat == What::kTaken ? less.value(4 * kUnroll) : more.value(4 * kUnroll) - less.value(4 * kUnroll);
+        t += more.value(4 * kUnroll) - less.value(4 * kUnroll);
     }
     return t;
   }

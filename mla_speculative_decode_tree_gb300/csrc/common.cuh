@@ -327,6 +327,26 @@ __device__ __forceinline__ int32_t load_row_id(const SplitArgs& a, int64_t q0, i
   return (j < P) ? __ldg(a.kv_indices + kv_base + j) : __ldg(a.out_cache_loc + q0 + (j - P));
 }
 
+// ---- pairs of fp32 values in one instruction ---------------------------------------
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
 // Where a list of pages, -1 behind them, ends among its first n entries.
 __device__ __forceinline__ int list_end(const int32_t* list, int n) {
   int lo = 0, hi = n;

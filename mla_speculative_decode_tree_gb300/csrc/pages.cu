@@ -469,7 +469,7 @@ cudaError_t launch_list_free(const int32_t* page_refs, int num_pages, int32_t* f
 
 cudaError_t launch_fork(const ForkArgs& a, cudaStream_t stream) {
   // Enough blocks per fork for its table entries and for the rows of a full page
-  // in all layers, 2 KB of row data per warp.
+  // in all layers, 4 KB of row data (a step of the copy loop) per warp.
   const int64_t bytes = (int64_t)a.pool.layers * (a.page_size - 1) * a.pool.row_bytes;
   const int64_t by_rows = (bytes + 4096 * (kForkThreads / 32) - 1) / (4096 * (kForkThreads / 32));
   const int64_t by_pages = (a.max_pages + 4 * kForkThreads - 1) / (4 * kForkThreads);
