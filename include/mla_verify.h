@@ -545,7 +545,8 @@ int mla_verify_run_shared(mla_verify_plan_t plan, const void* q_nope_absorbed, c
  *  num_accepted   int32 [batch] output: how many (0 for a request without nodes)
  *  next_tokens    int32 [batch] output: the token drawn behind the path; -1 for a
  *                 request without nodes or with a target row of zeros
- *  workspace      the plan's workspace
+ *  workspace      the plan's workspace (of its size, as for the other calls; not
+ *                 touched, and nothing is reported in its status word)
  *
  * The arithmetic is in whole numbers, so the tokens do not depend on the order of
  * any sum: a probability is w(p) = round(p * 2^38), ties to even (outside [0, 1]

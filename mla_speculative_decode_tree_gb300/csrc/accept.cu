@@ -27,7 +27,7 @@
 // rejection only entries with p > q count: each warp keeps theirs in shared memory,
 // and later rejections' passes run on those, r = w(p) less the sum of the s.
 //
-// 16 requests, trees of 9, 131,072 tokens: 17.4 us (10 us for a request with one
+// 16 requests, trees of 9, 131,072 tokens: 17.7 us (10 us for a request with one
 // rejection and a child behind it, 15 us with two); 64 requests, trees of up to 16,
 // 150,001 tokens: 45 us, of which the rows' 77 MB take 11.3.  In 64 bits throughout
 // these took 50.6 and 199 us, with 19-bit parts 29.8 and 97.8; what is kept, clusters

@@ -61,7 +61,7 @@
 // it Q, 52 the gather's) 1,560 at 128 bytes per cycle.  A row group's start and end
 // cost 20,000 cycles: Q in, the first scores, the last exchange, 131 KB of O out.
 // 2048 rows behind 128k shared keys: 440 us, 1.35 PFLOP/s (0.71 of the measured
-// peak); 9216 rows behind 8k, 160 us; 512 rows behind 32k, 65 us.
+// peak); 9216 rows behind 8k, 161 us; 512 rows behind 32k, 66 us.
 //
 // Every wait is bounded; on a timeout the CTA raises the status bit and drains,
 // and the other CTA of the pair runs into its own limit.
