@@ -101,7 +101,7 @@ constexpr int kColO = 0, kColQ = 256, kColS = 448;  // (S: 32 columns for even t
 // Base 2, before a reference is raised.  Weights and O are floating numbers, so a
 // reference far below the maximum costs no precision; what it must not do is overflow.
 constexpr float kRowHeadroom = 16.0f, kOutHeadroom = 32.0f;
-// References are 16 + a multiple of 32: those of both CTAs, and of O, are mostly the same one.
+// References are 16 + a multiple of 32: those of both CTAs, and of O, are mostly the same one.  (Above 2^23: the largest score.)
 constexpr float kRefStep = 32.0f, kRefOffset = 16.0f;
 // Start and end of a row group, in tiles: so much and so much per 32 rows.
 constexpr int kSegCost = 5, kQuadCost = 2;
@@ -840,15 +840,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           float t4[4] = {n[0], n[1], n[2], n[3]};
 #pragma unroll
           for (int k = 4; k < 32; ++k) t4[k & 3] = fmaxf(t4[k & 3], n[k]);
-          const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * scale;
+          const float most = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])), top = most * scale;
+          const bool large = fabsf(top) >= 0x1p23f && fabsf(top) < INFINITY;
           if (top > m + kRowHeadroom) {  // (m = -inf: any key that is seen)
-            const float up = fmaf(kRefStep, ceilf((top - kRefOffset) * (1.f / kRefStep)), kRefOffset), alpha = ratio(m, up);
+            // (from 2^23 on floats are whole numbers, and too far apart for steps of 32)
+            const float up = large ? top : fmaf(kRefStep, ceilf((top - kRefOffset) * (1.f / kRefStep)), kRefOffset),
+                        alpha = ratio(m, up);
             const uint64_t alpha2 = pair(alpha, alpha);
             l_round = fma2(l_round, alpha2, 0);
             l_full = fma2(l_full, alpha2, 0);
             m = up;
           }
-          const float mu = m == -INFINITY ? 0.f : -m;
+          float mu = m == -INFINITY ? 0.f : -m;
+          if (large) {  // (what rounding the largest one's product by itself leaves out may be far from 0)
+#pragma unroll
+            for (int k = 0; k < 32; ++k) n[k] -= most;
+            mu += top;
+          }
           const uint64_t mu2 = pair(mu, mu);
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
