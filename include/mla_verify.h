@@ -182,9 +182,9 @@ typedef struct {
  * for MLA_VERIFY_FUSED_MERGE one 32-bit counter per request and row group;
  * for MLA_VERIFY_KV4 with nsplit = 0 on the tensor-core kernel, O and LSE of
  * rows_per_cta rows per SM and per request and row group, the header, and 8
- * bytes per request and row group; for MLA_VERIFY_SHARED O and LSE of twice
- * max_batch*q_len*num_heads rows and 128 per pair of SMs, the header, and 16 bytes
- * per row).
+ * bytes per request and row group; for MLA_VERIFY_SHARED on it O and LSE of
+ * twice max_batch*q_len*num_heads rows and 128 per pair of SMs, the header, and
+ * 16 bytes per row).
  * The workspace must be 256-byte aligned and zero-filled once before its
  * first use (e.g. torch.zeros, or mla_verify_workspace_init); the library
  * keeps the header and the counters consistent afterwards (after a call that
